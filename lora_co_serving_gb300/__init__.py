@@ -9,6 +9,14 @@ kernels.  PyTorch supplies device memory and streams.  The entry points mirror
     sliced_forward / sliced_backward        -> the same for a fused projection of several slices
                                                (q|k|v, gate|up) over one input
 
+and, around the layer in a fine-tuning step (``include/lora_fp8.h``, ``include/lora_preference.h``):
+
+    fp8_quantize / fp8_quantize_weight      -> e4m3 codes and their block scales
+    fp8_linear(x, w, w_scales)              -> y = x W^T of a frozen weight in 8 bits
+    swiglu_forward / swiglu_backward        -> the MLP activation with an 8-bit checkpoint of the fine-tuning rows
+    token_logprob                           -> log probability of each row's label
+    preference_forward / preference_backward-> paired log-ratio loss and the gradient of the logits
+
 ``segs`` is an int32 array (or list) of rows {start, len, adapter_id, is_train};
 ``Pool`` holds the stacked adapter factors (A blocks [r_a, K], B blocks [r_a, N])
 on the device plus their host-side offsets, ranks and scales.
@@ -18,6 +26,7 @@ fallback path.
 """
 import ctypes
 import os
+from collections import namedtuple
 
 import numpy as np
 
@@ -26,7 +35,9 @@ from . import _build
 __all__ = ["Pool", "forward", "backward", "sliced_forward", "sliced_backward", "sliced_workspace_size",
            "sliced_xa_size", "workspace_size", "xa_size", "workspace_status", "plan_describe",
            "LoraError", "LibraryNotBuilt", "library", "build", "SAVE_XA", "RECOMPUTE_XA", "ACCUMULATE_GRAD",
-           "DEBUG_CHECKS", "plan_check", "static_status", "set_wait_limit"]
+           "DEBUG_CHECKS", "plan_check", "static_status", "set_wait_limit", "fp8_quantize", "fp8_quantize_weight",
+           "fp8_linear", "fp8_workspace_size", "checkpoint_rows", "swiglu_forward", "swiglu_backward",
+           "token_logprob", "preference_forward", "preference_backward", "Preference"]
 
 SAVE_XA = 1
 RECOMPUTE_XA = 2
@@ -45,7 +56,10 @@ EXPORTED = ["lora_workspace_size", "lora_xa_size", "lora_mixed_forward", "lora_m
             "lora_selftest_wait_timeout", "lora_adamw_step", "lora_mixed_backward_flagged",
             "lora_sliced_workspace_size", "lora_sliced_xa_size", "lora_sliced_forward", "lora_sliced_backward",
             "lora_latency_terms", "lora_latency_features", "lora_latency_fit", "lora_latency_predict",
-            "lora_static_status", "lora_plan_check", "lora_set_wait_limit"]
+            "lora_static_status", "lora_plan_check", "lora_set_wait_limit", "lora_fp8_quantize",
+            "lora_fp8_quantize_weight", "lora_fp8_workspace_size", "lora_fp8_linear", "lora_checkpoint_rows",
+            "lora_swiglu_forward", "lora_swiglu_backward", "lora_token_logprob", "lora_preference_forward",
+            "lora_preference_backward"]
 
 
 class LoraError(RuntimeError):
@@ -141,6 +155,20 @@ def library(path=None):
     lib.lora_latency_fit.restype = ctypes.c_int
     lib.lora_latency_predict.argtypes = [I32, P, P]
     lib.lora_latency_predict.restype = ctypes.c_double
+    I64, F, INT = ctypes.c_int64, ctypes.c_float, ctypes.c_int
+    for name, res, args in (
+            ("lora_fp8_quantize", INT, [I32, I32, INT, P, I64, P, I64, P, P]),
+            ("lora_fp8_quantize_weight", INT, [I32, I32, INT, P, I64, P, P, P]),
+            ("lora_fp8_workspace_size", SZ, [I32, I32, I32, I32]),
+            ("lora_fp8_linear", INT, [I32, I32, I32, INT, P, I64, P, P, P, P, I64, P, SZ, P]),
+            ("lora_checkpoint_rows", I64, [I32, P, I32]),
+            ("lora_swiglu_forward", INT, [I32, I32, INT, P, I64, P, I32, P, I64, P, P, P, P]),
+            ("lora_swiglu_backward", INT, [I32, I32, INT, P, P, P, I64, P, I64, P, P]),
+            ("lora_token_logprob", INT, [I32, I32, INT, P, I64, P, P, P, P]),
+            ("lora_preference_forward", INT, [I32, I32, INT, P, I64, P, P, P, I32, F, F, P, P, P, P, P, P]),
+            ("lora_preference_backward", INT, [I32, I32, INT, P, I64, P, P, P, P, I32, P, P, I64, P])):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = res, args
     if path is None:
         _LIB = lib
     return lib
@@ -490,3 +518,241 @@ def latency_predict(model, coef, feat):
     c = np.ascontiguousarray(coef, dtype=np.float64)
     f = np.ascontiguousarray(feat, dtype=np.float64)
     return float(library().lora_latency_predict(model, _ptr(c), _ptr(f)))
+
+
+# ------------------------------------------------------------------------------------ 8-bit products and checkpoints
+FP8_BLOCK = 128     # columns (and weight rows) that share a scale
+
+
+def _blocks(n):
+    return -(-n // FP8_BLOCK)
+
+
+def _matrix(t, name, dtype=None, rows=None, cols=None, contiguous=False):
+    """Check a 2-D tensor argument (unit column stride) and return its row distance in elements."""
+    if t.dim() != 2:
+        raise ValueError("%s must have two dimensions, got %d" % (name, t.dim()))
+    r, c = t.shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError("%s must be [%s, %s], got [%d, %d]" % (name, "T" if rows is None else rows,
+                                                                "K" if cols is None else cols, r, c))
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    ld, unit = t.stride()
+    if r > 0 and c > 1 and (unit != 1 or (contiguous and ld != c and r > 1)):
+        raise ValueError("%s must %s" % (name, "be contiguous" if contiguous else "have unit column stride"))
+    return ld if r > 1 else max(ld, c)
+
+
+def _vector(t, name, dtype, n):
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s must be contiguous with %d elements, got %s" % (name, n, tuple(t.shape)))
+
+
+def fp8_quantize(x, codes=None, scales=None, stream=None):
+    """x [T, K] (bf16 or float32) -> (codes [T, K] float8_e4m3fn, scales [T, ceil(K / 128)] float32).
+
+    A scale is the smallest power of two that brings its block of 128 columns within e4m3's largest number, 448."""
+    import torch
+    code, ld = _dtype_code(x), _matrix(x, "x")
+    T, K = x.shape
+    if codes is None:
+        codes = torch.empty((T, K), dtype=torch.float8_e4m3fn, device=x.device)
+    if scales is None:
+        scales = torch.empty((T, _blocks(K)), dtype=torch.float32, device=x.device)
+    ldc = _matrix(codes, "codes", torch.float8_e4m3fn, T, K)
+    _matrix(scales, "scales", torch.float32, T, _blocks(K), contiguous=True)
+    _check(library().lora_fp8_quantize(T, K, code, _ptr(x), ld, _ptr(codes), ldc, _ptr(scales), _stream_ptr(stream)))
+    return codes, scales
+
+
+def fp8_quantize_weight(W, stream=None):
+    """W [N, K] (bf16 or float32) -> (codes [N, K] float8_e4m3fn, scales [ceil(N / 128), ceil(K / 128)]), a scale for
+    each 128 x 128 block.  For the input's gradient pass the transposed weight's (codes.t() and scales.t(), made
+    contiguous once: a block of the transposed weight is the transposed block)."""
+    import torch
+    code, ld = _dtype_code(W), _matrix(W, "W")
+    N, K = W.shape
+    codes = torch.empty((N, K), dtype=torch.float8_e4m3fn, device=W.device)
+    scales = torch.empty((_blocks(N), _blocks(K)), dtype=torch.float32, device=W.device)
+    _check(library().lora_fp8_quantize_weight(N, K, code, _ptr(W), ld, _ptr(codes), _ptr(scales),
+                                              _stream_ptr(stream)))
+    return codes, scales
+
+
+def fp8_workspace_size(T, K, N, x_fp8=False):
+    """Bytes of workspace that fp8_linear needs for these sizes (x given in 8 bits or not)."""
+    n = library().lora_fp8_workspace_size(T, K, N, 1 if x_fp8 else 0)
+    if n == 0:
+        raise LoraError(-1, library().lora_last_error().decode())
+    return int(n)
+
+
+def fp8_linear(x, w, w_scales, x_scales=None, y=None, workspace=None, stream=None, check_status=False):
+    """y [T, N] (bf16) = x W^T for a frozen weight in 8 bits (w [N, K] codes, w_scales [ceil(N/128), ceil(K/128)]).
+
+    x [T, K] is bf16 or float32 and is quantized on the way, or float8_e4m3fn codes with their x_scales
+    [T, ceil(K / 128)].  check_status: as in forward()."""
+    import torch
+    ld = _matrix(x, "x")
+    T, K = x.shape
+    N = w.shape[0]
+    _matrix(w, "w", torch.float8_e4m3fn, N, K, contiguous=True)
+    _matrix(w_scales, "w_scales", torch.float32, _blocks(N), _blocks(K), contiguous=True)
+    if x_scales is None:
+        code = _dtype_code(x)
+    else:
+        code = BF16
+        _matrix(x, "x", torch.float8_e4m3fn)
+        _matrix(x_scales, "x_scales", torch.float32, T, _blocks(K), contiguous=True)
+    if y is None:
+        y = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
+    ldy = _matrix(y, "y", torch.bfloat16, T, N)
+    if workspace is None:
+        workspace = torch.empty(fp8_workspace_size(T, K, N, x_scales is not None), dtype=torch.uint8, device=x.device)
+    _check(library().lora_fp8_linear(T, K, N, code, _ptr(x), ld, _ptr(x_scales), _ptr(w), _ptr(w_scales), _ptr(y), ldy,
+                                     _ptr(workspace), workspace.numel(), _stream_ptr(stream)))
+    if check_status:
+        workspace_status(workspace, stream)
+    return y
+
+
+def checkpoint_rows(T, segs):
+    """Rows of the 8-bit checkpoint of a segment table: the tokens of its fine-tuning segments."""
+    s = segments(segs)
+    n = library().lora_checkpoint_rows(T, _ptr(s), s.shape[0])
+    if n < 0:
+        raise LoraError(int(n), library().lora_last_error().decode())
+    return int(n)
+
+
+def swiglu_forward(gu, segs=None, checkpoint=False, fp8_out=False, h=None, h_scales=None, stream=None):
+    """h [T, I] = silu(gate) * up of gu [T, 2 I] = gate|up.
+
+    checkpoint: also keep gate|up of the fine-tuning rows of `segs` in 8 bits; returns (h, saved) with saved =
+    (codes [R, 2 I], scales [R, 2 ceil(I / 128)]), rows in increasing segment order.  fp8_out: h is (codes, scales)
+    for the next fp8_linear instead of a tensor of gu's type."""
+    import torch
+    code, ld = _dtype_code(gu), _matrix(gu, "gu")
+    T, I2 = gu.shape
+    if I2 % 2:
+        raise ValueError("gu must hold gate|up, an even number of columns; got %d" % I2)
+    I = I2 // 2
+    s = None if segs is None else segments(segs)
+    n_segs = 0 if s is None else s.shape[0]
+    ck = cs = None
+    if checkpoint:
+        if s is None:
+            raise ValueError("a checkpoint needs the batch's segment table")
+        R = checkpoint_rows(T, s)
+        ck = torch.empty((R, I2), dtype=torch.float8_e4m3fn, device=gu.device)
+        cs = torch.empty((R, 2 * _blocks(I)), dtype=torch.float32, device=gu.device)
+    out = torch.float8_e4m3fn if fp8_out else gu.dtype
+    if h is None:
+        h = torch.empty((T, I), dtype=out, device=gu.device)
+    ldh = _matrix(h, "h", out, T, I)
+    if fp8_out and h_scales is None:
+        h_scales = torch.empty((T, _blocks(I)), dtype=torch.float32, device=gu.device)
+    if fp8_out:
+        _matrix(h_scales, "h_scales", torch.float32, T, _blocks(I), contiguous=True)
+    keep = ck is not None and ck.numel() > 0
+    _check(library().lora_swiglu_forward(T, I, code, _ptr(gu), ld, _ptr(s), n_segs, _ptr(h), ldh,
+                                         _ptr(h_scales) if fp8_out else None, _ptr(ck) if keep else None,
+                                         _ptr(cs) if keep else None, _stream_ptr(stream)))
+    h = (h, h_scales) if fp8_out else h
+    return (h, (ck, cs)) if checkpoint else h
+
+
+def swiglu_backward(saved, dh, fp8_out=False, dgu=None, dgu_scales=None, stream=None):
+    """Gradient of gate|up [R, 2 I] from the checkpoint `saved` of swiglu_forward and dh [R, I], the gradient of h for
+    the checkpoint's rows.  fp8_out: (codes, scales) for the next fp8_linear (I a multiple of 128)."""
+    import torch
+    ck, cs = saved
+    code, ld = _dtype_code(dh), _matrix(dh, "dh")
+    R, I = dh.shape
+    _matrix(ck, "the checkpoint's codes", torch.float8_e4m3fn, R, 2 * I, contiguous=True)
+    _matrix(cs, "the checkpoint's scales", torch.float32, R, 2 * _blocks(I), contiguous=True)
+    out = torch.float8_e4m3fn if fp8_out else dh.dtype
+    if dgu is None:
+        dgu = torch.empty((R, 2 * I), dtype=out, device=dh.device)
+    ldo = _matrix(dgu, "dgu", out, R, 2 * I)
+    if fp8_out and dgu_scales is None:
+        dgu_scales = torch.empty((R, 2 * _blocks(I)), dtype=torch.float32, device=dh.device)
+    if fp8_out:
+        _matrix(dgu_scales, "dgu_scales", torch.float32, R, 2 * _blocks(I), contiguous=True)
+    _check(library().lora_swiglu_backward(R, I, code, _ptr(ck), _ptr(cs), _ptr(dh), ld, _ptr(dgu), ldo,
+                                          _ptr(dgu_scales) if fp8_out else None, _stream_ptr(stream)))
+    return (dgu, dgu_scales) if fp8_out else dgu
+
+
+# -------------------------------------------------------------------------------------------------- preference loss
+Preference = namedtuple("Preference", ["loss", "rewards", "logp", "lse", "coef"])
+
+
+def _pairs(pairs):
+    return np.ascontiguousarray(np.asarray(pairs, dtype=np.int32).reshape(-1, 4))
+
+
+def token_logprob(logits, labels, logp=None, lse=None, stream=None):
+    """(logp [T], lse [T]) float32: log probability of each row's label, and the row's log-sum-exp.  labels int64 [T];
+    a negative label's row is not read and gives zeros."""
+    import torch
+    code, ld = _dtype_code(logits), _matrix(logits, "logits")
+    T, V = logits.shape
+    _vector(labels, "labels", torch.int64, T)
+    if logp is None:
+        logp = torch.empty(T, dtype=torch.float32, device=logits.device)
+    if lse is None:
+        lse = torch.empty(T, dtype=torch.float32, device=logits.device)
+    _vector(logp, "logp", torch.float32, T)
+    _vector(lse, "lse", torch.float32, T)
+    _check(library().lora_token_logprob(T, V, code, _ptr(logits), ld, _ptr(labels), _ptr(logp), _ptr(lse),
+                                        _stream_ptr(stream)))
+    return logp, lse
+
+
+def preference_forward(logits, labels, ref_logp, pairs, beta=0.1, label_smoothing=0.0, stream=None):
+    """Paired log-ratio loss of a policy's logits [T, V] against a reference's ref_logp [T].
+
+    pairs: int32 rows {chosen start, chosen length, rejected start, rejected length} over the batch's rows.  Returns
+    Preference(loss [P], rewards [P, 2], logp [T], lse [T], coef [P, 2]), float32; lse and coef are the backward's."""
+    import torch
+    code, ld = _dtype_code(logits), _matrix(logits, "logits")
+    T, V = logits.shape
+    _vector(labels, "labels", torch.int64, T)
+    _vector(ref_logp, "ref_logp", torch.float32, T)
+    p = _pairs(pairs)
+    n = p.shape[0]
+    buf = torch.empty(2 * T + 5 * n, dtype=torch.float32, device=logits.device)
+    logp, lse = buf[:T], buf[T:2 * T]
+    loss, rewards = buf[2 * T:2 * T + n], buf[2 * T + n:2 * T + 3 * n].view(n, 2)
+    coef = buf[2 * T + 3 * n:].view(n, 2)
+    _check(library().lora_preference_forward(T, V, code, _ptr(logits), ld, _ptr(labels), _ptr(ref_logp), _ptr(p), n,
+                                             beta, label_smoothing, _ptr(loss), _ptr(rewards), _ptr(logp), _ptr(lse),
+                                             _ptr(coef), _stream_ptr(stream)))
+    return Preference(loss, rewards, logp, lse, coef)
+
+
+def preference_backward(logits, labels, lse, coef, pairs, dloss=None, dlogits=None, stream=None):
+    """Gradient of the logits [T, V] in their type: every row is written, zeros where a row is not counted.
+
+    dloss [P] float32: the gradient of each pair's loss (default: 1 / P each, the mean's).  dlogits may be `logits`
+    itself: the gradient then takes the logits' place."""
+    import torch
+    code, ld = _dtype_code(logits), _matrix(logits, "logits")
+    T, V = logits.shape
+    p = _pairs(pairs)
+    n = p.shape[0]
+    _vector(labels, "labels", torch.int64, T)
+    _vector(lse, "lse", torch.float32, T)
+    _vector(coef, "coef", torch.float32, 2 * n)
+    if dloss is not None:
+        _vector(dloss, "dloss", torch.float32, n)
+    if dlogits is None:
+        dlogits = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
+    ldd = _matrix(dlogits, "dlogits", logits.dtype, T, V)
+    _check(library().lora_preference_backward(T, V, code, _ptr(logits), ld, _ptr(labels), _ptr(lse), _ptr(coef),
+                                              _ptr(p), n, _ptr(dloss), _ptr(dlogits), ldd, _stream_ptr(stream)))
+    return dlogits

@@ -1,0 +1,386 @@
+// fp8.cu -- the 8-bit block format: quantizers, and the MLP activation with its 8-bit checkpoint.
+//
+// Every kernel here moves each byte once and computes little per byte: the memory rate bounds them.  A block row (128
+// columns of one row) belongs to 16 neighbouring lanes of 8 elements each, so a 16-bit row is read in 16-byte pieces,
+// the block's largest magnitude is four shuffles away, and the codes leave in 8-byte pieces, 128 bytes per block.
+#include <algorithm>
+#include <vector>
+
+#include "fp8.h"
+
+namespace lora {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnits = kThreads / kLanesPerBlock;   // block rows that a CTA holds at a time
+
+// A CTA takes `1 << log2_cols` neighbouring blocks of `kUnits >> log2_cols` rows at a time.
+struct Shape {
+    int32_t rows, cols;      // of the operand: rows, columns of one row (of one half, for gate|up)
+    int32_t n_blocks;        // blocks of a row
+    int32_t log2_cols;
+};
+
+// The width with the fewest idle lanes, the widest of equals: a row of 17 blocks taken 16 at a time would leave 15 of
+// 32 slots empty.
+Shape shape_of(int32_t rows, int32_t cols) {
+    Shape s{rows, cols, blocks_of(cols), 0};
+    int64_t best = 1ll << 62;
+    for (int l = 4; l >= 0; --l) {
+        const int64_t w = 1ll << l, slots = (s.n_blocks + w - 1) / w * w;
+        if (slots < best) { best = slots; s.log2_cols = l; }
+    }
+    return s;
+}
+dim3 grid_of(const Shape& s, int rows_per_thread) {
+    const int64_t rows_cta = (int64_t)(kUnits >> s.log2_cols) * rows_per_thread;
+    const int w = 1 << s.log2_cols;
+    return dim3((unsigned)((s.rows + rows_cta - 1) / rows_cta), (unsigned)((s.n_blocks + w - 1) / w));
+}
+
+// Row and column of this thread's i-th block row; rows of one thread lie kUnits >> log2_cols apart.
+struct Place {
+    int row0, row_step, col, block;
+    bool in;
+    __device__ __forceinline__ Place(const Shape& s, int rows_per_thread) {
+        const int unit = threadIdx.x / kLanesPerBlock, lane = threadIdx.x % kLanesPerBlock;
+        row_step = kUnits >> s.log2_cols;
+        row0 = blockIdx.x * row_step * rows_per_thread + (unit >> s.log2_cols);
+        block = (blockIdx.y << s.log2_cols) + (unit & ((1 << s.log2_cols) - 1));
+        col = block * kQBlock + lane * 8;
+        in = col < s.cols;
+    }
+};
+
+// ---------------------------------------------------------------------------------------------------- quantizers
+template <class Row8>
+__global__ void __launch_bounds__(kThreads) quantize_kernel(Shape s, const void* __restrict__ x, int64_t ld_x,
+                                                            uint8_t* __restrict__ codes, int64_t ld_codes,
+                                                            float* __restrict__ scales) {
+    const Place p(s, 1);
+    const bool in = p.in && p.row0 < s.rows;
+    Row8 r;
+    r.zero();
+    if (in) r.load(x, p.row0 * ld_x + p.col);
+    float v[8], inv;
+    r.get(v);
+    const float sc = block_scale(max_over_block(abs_bits_max(v)), &inv);
+    if (!in) return;
+    *reinterpret_cast<uint2*>(codes + p.row0 * ld_codes + p.col) = encode8(v, inv);
+    if (threadIdx.x % kLanesPerBlock == 0) scales[(int64_t)p.row0 * s.n_blocks + p.block] = sc;
+}
+
+// One 128 x 128 block of a weight per CTA; its rows stay in registers (8 per thread) between the two uses.
+template <class Row8>
+__global__ void __launch_bounds__(kThreads) quantize_weight_kernel(int32_t N, int32_t K, const void* __restrict__ W,
+                                                                   int64_t ld_w, uint8_t* __restrict__ codes,
+                                                                   float* __restrict__ scales) {
+    constexpr int kRows = kQBlock / kUnits;
+    __shared__ uint32_t warp_max[kThreads / 32];
+    const int unit = threadIdx.x / kLanesPerBlock;
+    const int col = blockIdx.x * kQBlock + (threadIdx.x % kLanesPerBlock) * 8;
+    Row8 r[kRows];
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int row = blockIdx.y * kQBlock + i * kUnits + unit;
+        r[i].zero();
+        if (row < N && col < K) r[i].load(W, row * ld_w + col);
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        float v[8];
+        r[i].get(v);
+        a = max(a, abs_bits_max(v));
+    }
+    a = __reduce_max_sync(0xffffffffu, a);
+    if (threadIdx.x % 32 == 0) warp_max[threadIdx.x / 32] = a;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w) a = max(a, warp_max[w]);
+    float inv;
+    const float sc = block_scale(a, &inv);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int row = blockIdx.y * kQBlock + i * kUnits + unit;
+        float v[8];
+        r[i].get(v);
+        if (row < N && col < K) *reinterpret_cast<uint2*>(codes + (int64_t)row * K + col) = encode8(v, inv);
+    }
+    if (threadIdx.x == 0) scales[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = sc;
+}
+
+// -------------------------------------------------------------------------------------------------------- swiglu
+// Fine-tuning segments in increasing start order: rows [start, start + len) go to checkpoint rows from `ck`.
+struct TrainRanges {
+    int32_t n;
+    int32_t start[kMaxTrainSegs], len[kMaxTrainSegs], ck[kMaxTrainSegs];
+};
+// checkpoint row of a row, -1 if it is kept nowhere
+__device__ __forceinline__ int checkpoint_row(const TrainRanges& t, int row) {
+    int lo = 0, hi = t.n;                      // the last range that starts at or before the row is lo - 1
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (t.start[mid] <= row) lo = mid + 1; else hi = mid;
+    }
+    if (lo == 0 || row - t.start[lo - 1] >= t.len[lo - 1]) return -1;
+    return t.ck[lo - 1] + row - t.start[lo - 1];
+}
+
+// 1 / (1 + e^-g).  e^-g overflows to infinity below g = -88: the quotient is then 0, as it should be.
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+
+template <class Row8, bool H8>
+__global__ void __launch_bounds__(kThreads) swiglu_forward_kernel(
+    Shape s, const void* __restrict__ gu, int64_t ld_gu, void* __restrict__ h, int64_t ld_h,
+    float* __restrict__ h_scales, uint8_t* __restrict__ ck_codes, float* __restrict__ ck_scales,
+    const __grid_constant__ TrainRanges train) {
+    const Place p(s, 1);
+    const int row = p.row0;
+    const bool in = p.in && row < s.rows;
+    Row8 rg, ru;
+    rg.zero();
+    ru.zero();
+    if (in) {
+        rg.load(gu, row * ld_gu + p.col);
+        ru.load(gu, row * ld_gu + s.cols + p.col);
+    }
+    float g[8], u[8], v[8];
+    rg.get(g);
+    ru.get(u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = g[i] * sigmoid(g[i]) * u[i];
+    const bool lead = threadIdx.x % kLanesPerBlock == 0;
+    if constexpr (H8) {
+        float inv;
+        const float sc = block_scale(max_over_block(abs_bits_max(v)), &inv);
+        if (in) {
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(h) + row * ld_h + p.col) = encode8(v, inv);
+            if (lead) h_scales[(int64_t)row * s.n_blocks + p.block] = sc;
+        }
+    } else {
+        if (in) Row8::store(h, row * ld_h + p.col, v);
+    }
+    const int ck = (train.n > 0 && row < s.rows) ? checkpoint_row(train, row) : -1;
+    if (!__any_sync(0xffffffffu, ck >= 0)) return;
+    float inv_g, inv_u;
+    const float sg = block_scale(max_over_block(abs_bits_max(g)), &inv_g);
+    const float su = block_scale(max_over_block(abs_bits_max(u)), &inv_u);
+    if (!in || ck < 0) return;
+    uint8_t* c = ck_codes + (int64_t)ck * 2 * s.cols + p.col;
+    *reinterpret_cast<uint2*>(c) = encode8(g, inv_g);
+    *reinterpret_cast<uint2*>(c + s.cols) = encode8(u, inv_u);
+    if (lead) {
+        float* z = ck_scales + (int64_t)ck * 2 * s.n_blocks + p.block;
+        z[0] = sg;
+        z[s.n_blocks] = su;
+    }
+}
+
+template <class Row8, bool D8>
+__global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(Shape s, const uint8_t* __restrict__ ck_codes,
+                                                                   const float* __restrict__ ck_scales,
+                                                                   const void* __restrict__ dh, int64_t ld_dh,
+                                                                   void* __restrict__ dgu, int64_t ld_dgu,
+                                                                   float* __restrict__ dgu_scales) {
+    const Place p(s, 1);
+    const int row = p.row0;
+    const bool in = p.in && row < s.rows;
+    Row8 rd;
+    rd.zero();
+    uint2 qg = make_uint2(0, 0), qu = qg;
+    float sg = 0.f, su = 0.f;
+    if (in) {
+        const uint8_t* c = ck_codes + (int64_t)row * 2 * s.cols + p.col;
+        const float* z = ck_scales + (int64_t)row * 2 * s.n_blocks + p.block;
+        qg = *reinterpret_cast<const uint2*>(c);
+        qu = *reinterpret_cast<const uint2*>(c + s.cols);
+        sg = z[0];
+        su = z[s.n_blocks];
+        rd.load(dh, row * ld_dh + p.col);
+    }
+    float g[8], u[8], d[8];
+    decode8(qg, sg, g);
+    decode8(qu, su, u);
+    rd.get(d);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float sig = sigmoid(g[i]);
+        const float dsig = d[i] * sig;
+        d[i] = dsig * u[i] * (1.f + g[i] * (1.f - sig));   // gate's gradient
+        u[i] = dsig * g[i];                                // up's
+    }
+    if constexpr (D8) {
+        float inv_g, inv_u;
+        const float zg = block_scale(max_over_block(abs_bits_max(d)), &inv_g);
+        const float zu = block_scale(max_over_block(abs_bits_max(u)), &inv_u);
+        if (!in) return;
+        uint8_t* c = static_cast<uint8_t*>(dgu) + row * ld_dgu + p.col;
+        *reinterpret_cast<uint2*>(c) = encode8(d, inv_g);
+        *reinterpret_cast<uint2*>(c + s.cols) = encode8(u, inv_u);
+        if (threadIdx.x % kLanesPerBlock == 0) {
+            float* z = dgu_scales + (int64_t)row * 2 * s.n_blocks + p.block;
+            z[0] = zg;
+            z[s.n_blocks] = zu;
+        }
+    } else if (in) {
+        Row8::store(dgu, row * ld_dgu + p.col, d);
+        Row8::store(dgu, row * ld_dgu + s.cols + p.col, u);
+    }
+}
+
+// Rows of at most this many columns: blocks of a row are spread over the grid's second dimension (< 65536)
+constexpr int32_t kMaxCols = 1 << 22;
+
+bool known_dtype(lora_dtype_t dt) { return dt == LORA_BF16 || dt == LORA_F32; }
+
+// The fine-tuning segments of a table that covers [0, T) once, in increasing start order; their rows, or an error
+int64_t train_ranges(const char* fn, int32_t T, const lora_segment_t* segs, int32_t n_segs, TrainRanges* out) {
+    if (n_segs < 0 || (n_segs > 0 && !segs))
+        return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": segment table is NULL or its size negative");
+    std::vector<lora_segment_t> s;
+    s.reserve(n_segs);
+    for (int32_t i = 0; i < n_segs; ++i) {
+        if (segs[i].len < 0 || segs[i].start < 0)
+            return refuse(LORA_ERR_SEGMENTS, std::string(fn) + ": negative segment start or length");
+        if (segs[i].len > 0) s.push_back(segs[i]);
+    }
+    const auto before = [](const lora_segment_t& a, const lora_segment_t& b) { return a.start < b.start; };
+    if (!std::is_sorted(s.begin(), s.end(), before)) std::sort(s.begin(), s.end(), before);
+    int64_t at = 0;
+    int32_t rows = 0;
+    out->n = 0;
+    for (const lora_segment_t& q : s) {
+        if (q.start != at)
+            return refuse(LORA_ERR_SEGMENTS, std::string(fn) + ": segments overlap or leave a gap at token " +
+                                                 std::to_string(std::min<int64_t>(at, q.start)));
+        at += q.len;
+        if (!q.is_train) continue;
+        if (out->n == kMaxTrainSegs)
+            return refuse(LORA_ERR_LIMIT, std::string(fn) + ": more than 48 fine-tuning segments");
+        out->start[out->n] = q.start;
+        out->len[out->n] = q.len;
+        out->ck[out->n++] = rows;
+        rows += q.len;
+    }
+    if (at != T) return refuse(LORA_ERR_SEGMENTS, std::string(fn) + ": segments do not cover [0, T)");
+    return rows;
+}
+
+}  // namespace
+
+void launch_quantize(int32_t T, int32_t K, lora_dtype_t dt, const void* x, int64_t ld_x, uint8_t* codes,
+                     int64_t ld_codes, float* scales, cudaStream_t stream) {
+    const Shape s = shape_of(T, K);
+    if (dt == LORA_BF16)
+        quantize_kernel<Row8Bf16><<<grid_of(s, 1), kThreads, 0, stream>>>(s, x, ld_x, codes, ld_codes, scales);
+    else
+        quantize_kernel<Row8F32><<<grid_of(s, 1), kThreads, 0, stream>>>(s, x, ld_x, codes, ld_codes, scales);
+}
+
+}  // namespace lora
+
+using namespace lora;
+
+extern "C" int lora_fp8_quantize(int32_t T, int32_t K, lora_dtype_t dt, const void* x, int64_t ld_x, void* codes,
+                                 int64_t ld_codes, float* scales, void* stream) {
+    const char* fn = "lora_fp8_quantize";
+    if (!known_dtype(dt)) return refuse(LORA_ERR_DTYPE, "unknown dtype");
+    if (T < 0 || K <= 0) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": T must be >= 0 and K > 0");
+    if (K > kMaxCols) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": more than 2^22 columns");
+    if (K % 16 != 0) return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": K must be a multiple of 16");
+    if (T == 0) return LORA_OK;
+    int rc = check_matrix(fn, "x", x, K, ld_x, elem_size(dt));
+    if (rc == LORA_OK) rc = check_matrix(fn, "codes", codes, K, ld_codes, 1);
+    if (rc != LORA_OK) return rc;
+    if (!scales) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": scales is NULL");
+    launch_quantize(T, K, dt, x, ld_x, static_cast<uint8_t*>(codes), ld_codes, scales,
+                    static_cast<cudaStream_t>(stream));
+    return launched(fn);
+}
+
+extern "C" int lora_fp8_quantize_weight(int32_t N, int32_t K, lora_dtype_t dt, const void* W, int64_t ld_w,
+                                        void* codes, float* scales, void* stream) {
+    const char* fn = "lora_fp8_quantize_weight";
+    if (!known_dtype(dt)) return refuse(LORA_ERR_DTYPE, "unknown dtype");
+    if (N <= 0 || K <= 0) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": N and K must be > 0");
+    if (K % 16 != 0) return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": K must be a multiple of 16");
+    int rc = check_matrix(fn, "W", W, K, ld_w, elem_size(dt));
+    if (rc == LORA_OK) rc = check_matrix(fn, "codes", codes, K, K, 1);
+    if (rc != LORA_OK) return rc;
+    if (!scales) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": scales is NULL");
+    if (blocks_of(N) > 65535) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": more than 65535 * 128 weight rows");
+    const dim3 grid(blocks_of(K), blocks_of(N));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dt == LORA_BF16)
+        quantize_weight_kernel<Row8Bf16>
+            <<<grid, kThreads, 0, st>>>(N, K, W, ld_w, static_cast<uint8_t*>(codes), scales);
+    else
+        quantize_weight_kernel<Row8F32>
+            <<<grid, kThreads, 0, st>>>(N, K, W, ld_w, static_cast<uint8_t*>(codes), scales);
+    return launched(fn);
+}
+
+extern "C" int64_t lora_checkpoint_rows(int32_t T, const lora_segment_t* segs, int32_t n_segs) {
+    TrainRanges t;
+    if (T < 0) return refuse(LORA_ERR_INVALID_ARG, "lora_checkpoint_rows: T must be >= 0");
+    return train_ranges("lora_checkpoint_rows", T, segs, n_segs, &t);
+}
+
+extern "C" int lora_swiglu_forward(int32_t T, int32_t I, lora_dtype_t dt, const void* gu, int64_t ld_gu,
+                                   const lora_segment_t* segs, int32_t n_segs, void* h, int64_t ld_h, float* h_scales,
+                                   void* ck_codes, float* ck_scales, void* stream) {
+    const char* fn = "lora_swiglu_forward";
+    if (!known_dtype(dt)) return refuse(LORA_ERR_DTYPE, "unknown dtype");
+    if (T < 0 || I <= 0) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": T must be >= 0 and I > 0");
+    if (I > kMaxCols) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": more than 2^22 columns");
+    if (I % 8 != 0) return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": I must be a multiple of 8");
+    TrainRanges train;
+    train.n = 0;
+    if (ck_codes || n_segs != 0) {
+        const int64_t rows = train_ranges(fn, T, segs, n_segs, &train);
+        if (rows < 0) return (int)rows;
+    }
+    if (!ck_codes) train.n = 0;
+    if (T == 0) return LORA_OK;
+    int rc = check_matrix(fn, "gu", gu, 2 * (int64_t)I, ld_gu, elem_size(dt));
+    if (rc == LORA_OK) rc = check_matrix(fn, "h", h, I, ld_h, h_scales ? 1 : elem_size(dt));
+    if (rc == LORA_OK && train.n > 0) rc = check_matrix(fn, "ck_codes", ck_codes, 2 * (int64_t)I, 2 * (int64_t)I, 1);
+    if (rc != LORA_OK) return rc;
+    if (train.n > 0 && !ck_scales) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": ck_scales is NULL");
+    const Shape s = shape_of(T, I);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    auto go = [&](auto kernel) {
+        kernel<<<grid_of(s, 1), kThreads, 0, st>>>(s, gu, ld_gu, h, ld_h, h_scales, static_cast<uint8_t*>(ck_codes),
+                                                   ck_scales, train);
+    };
+    if (dt == LORA_BF16) h_scales ? go(swiglu_forward_kernel<Row8Bf16, true>) : go(swiglu_forward_kernel<Row8Bf16, false>);
+    else h_scales ? go(swiglu_forward_kernel<Row8F32, true>) : go(swiglu_forward_kernel<Row8F32, false>);
+    return launched(fn);
+}
+
+extern "C" int lora_swiglu_backward(int32_t R, int32_t I, lora_dtype_t dt, const void* ck_codes,
+                                    const float* ck_scales, const void* dh, int64_t ld_dh, void* dgu, int64_t ld_dgu,
+                                    float* dgu_scales, void* stream) {
+    const char* fn = "lora_swiglu_backward";
+    if (!known_dtype(dt)) return refuse(LORA_ERR_DTYPE, "unknown dtype");
+    if (R < 0 || I <= 0) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": R must be >= 0 and I > 0");
+    if (I > kMaxCols) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": more than 2^22 columns");
+    if (I % 8 != 0) return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": I must be a multiple of 8");
+    if (dgu_scales && I % kQBlock != 0)
+        return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": I must be a multiple of 128 for a gradient in 8 bits");
+    if (R == 0) return LORA_OK;
+    int rc = check_matrix(fn, "ck_codes", ck_codes, 2 * (int64_t)I, 2 * (int64_t)I, 1);
+    if (rc == LORA_OK) rc = check_matrix(fn, "dh", dh, I, ld_dh, elem_size(dt));
+    if (rc == LORA_OK) rc = check_matrix(fn, "dgu", dgu, 2 * (int64_t)I, ld_dgu, dgu_scales ? 1 : elem_size(dt));
+    if (rc != LORA_OK) return rc;
+    if (!ck_scales) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": ck_scales is NULL");
+    const Shape s = shape_of(R, I);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    auto go = [&](auto kernel) {
+        kernel<<<grid_of(s, 1), kThreads, 0, st>>>(s, static_cast<const uint8_t*>(ck_codes), ck_scales, dh, ld_dh, dgu,
+                                                   ld_dgu, dgu_scales);
+    };
+    if (dt == LORA_BF16) dgu_scales ? go(swiglu_backward_kernel<Row8Bf16, true>) : go(swiglu_backward_kernel<Row8Bf16, false>);
+    else dgu_scales ? go(swiglu_backward_kernel<Row8F32, true>) : go(swiglu_backward_kernel<Row8F32, false>);
+    return launched(fn);
+}
