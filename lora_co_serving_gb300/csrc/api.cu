@@ -14,8 +14,23 @@
 #include "plan.h"
 #include "simt.h"
 #include "tc_kernel.h"
+#include "tc_prims.h"
 
 using namespace lora;
+
+EncodeTiledFn lora::encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
 
 namespace {
 
@@ -44,24 +59,6 @@ int fail(int code, const std::string& msg) {
 #ifndef LORA_L2_PROMOTION
 #define LORA_L2_PROMOTION CU_TENSOR_MAP_L2_PROMOTION_NONE
 #endif
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
 // 2-D bf16 tensor [outer, inner] with row stride `ld` elements, 128-byte swizzled boxes {box_in, box_out}.
 bool encode_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_in,
                uint32_t box_out, std::string* err, bool swizzle = true) {
@@ -567,6 +564,7 @@ int lora_set_wait_limit(uint64_t ns) {
     if (ns < 1000000ull || ns > 60000000000ull)
         return fail(LORA_ERR_INVALID_ARG, "the wait limit must lie between 1 ms and 60 s");
     CUDA_TRY(set_wait_limit_ns(ns));
+    CUDA_TRY(fp8_set_wait_limit_ns(ns));
     return LORA_OK;
 }
 

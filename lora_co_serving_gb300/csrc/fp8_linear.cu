@@ -1,63 +1,308 @@
 // fp8_linear.cu -- products with a frozen weight in 8 bits (include/lora_fp8.h):
 //     y[t,n] = sum_b sx[t,b] sw[n/128,b] sum_{k in block b} qx[t,k] qw[n,k]
+//
+// tcgen05.mma.kind::f8f6f4 multiplies the codes; a block's sum starts afresh in a TMEM accumulator and is then read
+// back, scaled and added to sums that stay in registers (a scale changes every 128 columns, and the accumulators of
+// the tensor cores cannot be rescaled in place).  Two accumulators alternate, so the MMAs of one block run while the
+// last block's sums are scaled.
+#include <cuda.h>
+
+#include <algorithm>
 #include <string>
 
 #include "fp8.h"
+#include "tc_kernel.h"
+#include "tc_prims.h"
 
 namespace lora {
 namespace {
 
-constexpr int kTile = 64;      // rows of x and of w per CTA
-constexpr int kStep = 32;      // columns staged at a time (a quarter of a block)
+// The wait without a call: a kernel that calls a function cannot move registers between its warps (setmaxnreg)
+__device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+    return mbar_try_wait(bar, parity) || wait_phase_loop(bar, parity, abort_flag, status, 0);
+}
 
-// Each thread holds 4 x 4 outputs; a block's products are summed first and then scaled once.
-__global__ void __launch_bounds__(256) linear_kernel(int32_t T, int32_t K, int32_t N, const uint8_t* __restrict__ x,
-                                                     int64_t ld_x, const float* __restrict__ xs,
-                                                     const uint8_t* __restrict__ w, const float* __restrict__ ws,
-                                                     __nv_bfloat16* __restrict__ y, int64_t ld_y) {
-    __shared__ float sx[kStep][kTile + 4], sw[kStep][kTile + 4];
-    const int t0 = blockIdx.y * kTile, n0 = blockIdx.x * kTile, nb = (K + kQBlock - 1) / kQBlock;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[4][4] = {};
-    for (int b = 0; b < nb; ++b) {
-        float part[4][4] = {};
-        for (int k0 = b * kQBlock; k0 < min(K, (b + 1) * kQBlock); k0 += kStep) {
-            const int r = threadIdx.x / 4, c = (threadIdx.x % 4) * 8;
-            float v[8], u[8];
-            const bool in = k0 + c < K;
-            decode8(in && t0 + r < T ? *reinterpret_cast<const uint2*>(x + (t0 + r) * ld_x + k0 + c) : make_uint2(0, 0),
-                    1.f, v);
-            decode8(in && n0 + r < N ? *reinterpret_cast<const uint2*>(w + (int64_t)(n0 + r) * K + k0 + c)
-                                     : make_uint2(0, 0),
-                    1.f, u);
-            __syncthreads();
-            for (int i = 0; i < 8; ++i) {
-                sx[c + i][r] = v[i];
-                sw[c + i][r] = u[i];
-            }
-            __syncthreads();
-            for (int k = 0; k < kStep; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) part[i][j] += sx[k][ty * 4 + i] * sw[k][tx * 4 + j];
-        }
-        for (int i = 0; i < 4; ++i) {
-            const int t = t0 + ty * 4 + i;
-            const float s = t < T ? xs[(int64_t)t * nb + b] * ws[(int64_t)(n0 / kQBlock) * nb + b] : 0.f;
-            for (int j = 0; j < 4; ++j) acc[i][j] += s * part[i][j];
+// kind::f8f6f4: e4m3 A and B, fp32 accumulator, both operands K-major
+__host__ __device__ constexpr uint32_t instr_desc_e4m3(int m, int n) {
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+__device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// (a.lo, a.hi) += (d0, d1) * (s.lo, s.hi).  volatile: d comes from a TMEM read and must stay behind its wait
+__device__ __forceinline__ void fma2(uint64_t& a, uint32_t d0, uint32_t d1, uint64_t s) {
+    asm volatile("{\n\t.reg .b64 d;\n\t"
+        "mov.b64 d, {%1, %2};\n\t"
+        "fma.rn.f32x2 %0, d, %3, %0;\n\t}"
+        : "+l"(a)
+        : "r"(d0), "r"(d1), "l"(s));
+}
+__device__ __forceinline__ uint64_t both(float s) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "r"(__float_as_uint(s)));
+    return r;
+}
+__device__ __forceinline__ float2 halves(uint64_t a) {
+    uint32_t lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(a));
+    return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+
+// =============================================================================================================
+// Many rows: CTA pairs, 256 rows of x by 256 outputs (rows of w).
+//
+// A pair works on one tile at a time.  CTA r holds rows [128 r, 128 r + 128) of the tile's x and of its w; the leader
+// (rank 0) issues the MMAs, which read both CTAs' shared memory and leave each CTA the accumulators of its own 128
+// rows of x by 256 outputs.  Per block each CTA moves 32 KB for 2 * 128 * 256 * 128 flops.
+//
+// 384 threads: warp 0 loads (TMA), warp 1 issues, warps 4..11 scale and add: each thread has one row of x and 128
+// outputs, which are one block of w's rows, so a block's 128 sums share one scale, sx[row] * sw[block].  The block
+// starts with 168 registers a thread (64512 in all); the first warpgroup gives up 112 of them and the adding warps,
+// whose 128 sums must not spill, take 56 more: 128 * 56 + 256 * 224 = 64512.
+// =============================================================================================================
+constexpr int kPM = 256, kPN = 256;                      // rows of x and outputs of a pair's tile
+constexpr int kOperandBytes = 128 * kQBlock;             // one CTA's 128 rows of x (or w), one block of columns
+constexpr int kPairStageBytes = 2 * kOperandBytes;
+constexpr int kPairStages = 6;
+constexpr int kPairThreads = 384;
+constexpr int kLaunchRegs = 168, kIssueRegs = 56, kAddRegs = 224;
+static_assert(128 * kIssueRegs + 256 * kAddRegs <= kPairThreads * kLaunchRegs, "register split above the launch's");
+constexpr int kAddWarps = 8;
+constexpr int kGroupM = 8;                               // tiles of x that share a sweep over w (see tile_at)
+
+struct PairParams {
+    CUtensorMap tm_x, tm_w;
+    const float* xs;
+    const float* ws;
+    __nv_bfloat16* y;
+    int64_t ld_y;
+    int32_t T, N, nb;          // nb: blocks of a row
+    int32_t tiles_m, tiles_n;
+    int32_t* status;
+};
+
+// Tiles in bands of kGroupM tiles of x: a band's columns are swept one after another, so that the tiles at work at any
+// time share few rows of x and of w.
+__device__ __forceinline__ void tile_at(const PairParams& P, int i, int* tm, int* tn) {
+    const int band = kGroupM * P.tiles_n;
+    const int m0 = i / band * kGroupM;
+    const int rows = min(kGroupM, P.tiles_m - m0);
+    const int r = i % band;
+    *tm = m0 + r % rows;
+    *tn = r / rows;
+}
+
+struct PairRing {
+    int stage = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++stage == kPairStages) { stage = 0; phase ^= 1u; }
+    }
+};
+
+struct PairBars {
+    uint32_t full, empty, tfull, tempty;       // per stage: loaded, free; per accumulator: summed, read
+    volatile int* abort_flag;
+};
+
+__device__ __forceinline__ void pair_load(const PairParams& P, const PairBars& B, uint8_t* smem, uint32_t rank) {
+    const uint32_t full_leader = mapa_shared(B.full, 0);
+    PairRing ring;
+    for (int i = blockIdx.x / 2; i < P.tiles_m * P.tiles_n; i += gridDim.x / 2) {
+        int tm, tn;
+        tile_at(P, i, &tm, &tn);
+        const int row_x = tm * kPM + 128 * (int)rank, row_w = tn * kPN + 128 * (int)rank;
+        for (int kb = 0; kb < P.nb; ++kb) {
+            if (!wait_here(B.empty + ring.stage * 8, ring.phase ^ 1u, B.abort_flag, P.status)) return;
+            if (rank == 0) mbar_expect_tx(B.full + ring.stage * 8, 2 * kPairStageBytes);
+            const uint32_t full = full_leader + ring.stage * 8;
+            const uint32_t sa = smem_u32(smem + ring.stage * kPairStageBytes);
+            tma_load_2d_pair(sa, &P.tm_x, kb * kQBlock, row_x, full);
+            tma_load_2d_pair(sa + kOperandBytes, &P.tm_w, kb * kQBlock, row_w, full);
+            ring.next();
         }
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int t = t0 + ty * 4 + i, n = n0 + tx * 4 + j;
-            if (t < T && n < N) y[t * ld_y + n] = __float2bfloat16_rn(acc[i][j]);
+}
+
+__device__ __forceinline__ void pair_issue(const PairParams& P, const PairBars& B, uint8_t* smem, uint32_t tmem) {
+    PairRing ring;
+    uint32_t use = 0;                          // blocks so far: accumulator use & 1
+    for (int i = blockIdx.x / 2; i < P.tiles_m * P.tiles_n; i += gridDim.x / 2) {
+        for (int kb = 0; kb < P.nb; ++kb, ++use) {
+            const uint32_t acc = use & 1u;
+            if (!wait_here(B.tempty + acc * 8, ((use >> 1) & 1u) ^ 1u, B.abort_flag, P.status)) return;
+            if (!wait_here(B.full + ring.stage * 8, ring.phase, B.abort_flag, P.status)) return;
+            tc_fence_after();
+            const uint32_t sa = smem_u32(smem + ring.stage * kPairStageBytes), sb = sa + kOperandBytes;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mma_e4m3_pair(tmem + acc * kPN, smem_desc(sa + k * 32, 16, 1024), smem_desc(sb + k * 32, 16, 1024),
+                              instr_desc_e4m3(kPM, kPN), k > 0);
+            mma_commit_pair(B.empty + ring.stage * 8);
+            mma_commit_pair(B.tfull + acc * 8);
+            ring.next();
         }
+    }
+}
+
+__device__ __forceinline__ void pair_add(const PairParams& P, const PairBars& B, uint32_t tmem, uint32_t rank,
+                                         int warp, int lane) {
+    const int quarter = warp & 3, half = (warp - 4) / 4;
+    const uint32_t tempty_leader = mapa_shared(B.tempty, 0);
+    const uint32_t taddr0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * 128);
+    uint32_t use = 0;
+    for (int i = blockIdx.x / 2; i < P.tiles_m * P.tiles_n; i += gridDim.x / 2) {
+        int tm, tn;
+        tile_at(P, i, &tm, &tn);
+        const int t = tm * kPM + 128 * (int)rank + quarter * 32 + lane;
+        const int n0 = tn * kPN + half * 128;
+        const bool live = t < P.T && n0 < P.N;
+        const float* xs = P.xs + (int64_t)(live ? t : 0) * P.nb;
+        const float* ws = P.ws + (int64_t)(live ? n0 / kQBlock : 0) * P.nb;
+        // scales are read two blocks ahead of their use (a read is an L2 round trip, about a block's MMAs)
+        float s0 = xs[0] * ws[0], s1 = P.nb > 1 ? xs[1] * ws[1] : 0.f;
+        uint64_t acc[64];
+#pragma unroll
+        for (int j = 0; j < 64; ++j) acc[j] = 0;
+        for (int kb = 0; kb < P.nb; ++kb, ++use) {
+            const uint64_t sc = both(s0);
+            s0 = s1;
+            if (kb + 2 < P.nb) s1 = xs[kb + 2] * ws[kb + 2];
+            const uint32_t buf = use & 1u;
+            const bool ok = wait_here(B.tfull + buf * 8, (use >> 1) & 1u, B.abort_flag, P.status);
+            if (!__all_sync(0xffffffffu, ok)) return;
+            tc_fence_after();
+            const uint32_t ta = taddr0 + buf * kPN;
+            uint32_t d[2][16];
+            tmem_ld16(ta, d[0]);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                tmem_ld_wait();
+                if (c < 7) tmem_ld16(ta + 16 * (c + 1), d[(c + 1) & 1]);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) fma2(acc[8 * c + q], d[c & 1][2 * q], d[c & 1][2 * q + 1], sc);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty_leader + buf * 8);
+        }
+        if (!live) continue;
+        __nv_bfloat16* out = P.y + t * P.ld_y + n0;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            uint32_t q[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 f = halves(acc[4 * c + k]);
+                q[k] = pack_bf16(f.x, f.y);
+            }
+            if (n0 + 8 * c < P.N) *reinterpret_cast<uint4*>(out + 8 * c) = make_uint4(q[0], q[1], q[2], q[3]);
+        }
+    }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    linear_pair_kernel(const __grid_constant__ PairParams P) {
+    extern __shared__ uint8_t dsmem[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kPairStages * kPairStageBytes);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kPairStages + 4);
+    PairBars B;
+    B.abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    B.full = smem_u32(bars);
+    B.empty = B.full + kPairStages * 8;
+    B.tfull = B.empty + kPairStages * 8;
+    B.tempty = B.tfull + 16;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_ctarank();
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            mbar_init(B.full + s * 8, 1);                    // used in the leader: its arm + both CTAs' bytes
+            mbar_init(B.empty + s * 8, 1);                   // the leader's commit
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(B.tfull + b * 8, 1);                   // the leader's commit
+            mbar_init(B.tempty + b * 8, 2 * kAddWarps);      // used in the leader: the adding warps of both CTAs
+        }
+        *B.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    grid_dep_wait();
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+        if (warp == 0 && lane == 0) pair_load(P, B, smem, rank);
+        if (warp == 1 && lane == 0 && rank == 0) pair_issue(P, B, smem, tmem);
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAddRegs));
+        pair_add(P, B, tmem, rank, warp, lane);
+    }
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+constexpr size_t kPairSmem = (size_t)kPairStages * kPairStageBytes + 1024 + 1024;
+
+// --------------------------------------------------------------------------------------------------------- host
+// [rows, K] codes, rows ld bytes apart, as 128-byte swizzled boxes of {128 columns, box_rows}; past the end reads 0
+bool encode_codes(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uint64_t ld, uint32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {K, rows};
+    cuuint64_t strides[1] = {ld};
+    cuuint32_t box[2] = {kQBlock, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Device {
+    int sms = 0;
+    bool ready = false;
+};
+// SM count of the current device; on first use its kernels' shared memory limits
+cudaError_t device_info(Device** out) {
+    static Device devs[64];
+    int d = 0;
+    cudaError_t e = cudaGetDevice(&d);
+    if (e != cudaSuccess) return e;
+    if (d >= 64) return cudaErrorInvalidDevice;
+    Device& v = devs[d];
+    if (!v.ready) {
+        e = cudaDeviceGetAttribute(&v.sms, cudaDevAttrMultiProcessorCount, d);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(linear_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
+        if (e != cudaSuccess) return e;
+        v.ready = true;
+    }
+    *out = &v;
+    return cudaSuccess;
 }
 
 // Workspace: the status word, then x's codes and scales if x is quantized on the way
 struct Scratch {
-    size_t status = 0, codes = 0, scales = 0, end = 0;
+    size_t codes = 0, scales = 0, end = 0;
 };
 Scratch layout_of(int32_t T, int32_t K, bool x_fp8) {
     auto al = [](size_t v) { return (v + 255) & ~size_t(255); };
@@ -74,10 +319,15 @@ int check_sizes(const char* fn, int32_t T, int32_t K, int32_t N) {
     if (K % 16 != 0 || N % 8 != 0)
         return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": K must be a multiple of 16 and N of 8");
     if (K > (1 << 22)) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": K above 2^22");
+    const int64_t tiles = (((int64_t)T + kPM - 1) / kPM) * (((int64_t)N + kPN - 1) / kPN);
+    if (tiles > INT32_MAX / 2) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": T x N above 2^46");
     return LORA_OK;
 }
 
 }  // namespace
+
+cudaError_t fp8_set_wait_limit_ns(uint64_t ns) { return cudaMemcpyToSymbol(g_wait_limit_ns, &ns, sizeof(ns)); }
+
 }  // namespace lora
 
 using namespace lora;
@@ -105,19 +355,33 @@ extern "C" int lora_fp8_linear(int32_t T, int32_t K, int32_t N, lora_dtype_t dt,
     if (ws_bytes < L.end)
         return refuse(LORA_ERR_WORKSPACE, "workspace too small: need " + std::to_string(L.end) + " bytes, got " +
                                               std::to_string(ws_bytes));
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
+    PairParams P{};
+    const void* xc = x_scales ? x : ws + L.codes;
+    if (!encode_codes(&P.tm_x, xc, K, T, x_scales ? ld_x : K, 128) || !encode_codes(&P.tm_w, w, K, N, K, 128))
+        return refuse(LORA_ERR_CUDA, std::string(fn) + ": cuTensorMapEncodeTiled failed");
+    Device* dev = nullptr;
+    cudaError_t e = device_info(&dev);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (e == cudaSuccess) e = cudaMemsetAsync(ws, 0, 256, st);
     if (e != cudaSuccess) return refuse(LORA_ERR_CUDA, std::string(fn) + ": " + cudaGetErrorString(e));
+    P.xs = x_scales;
     if (!x_scales) {
         float* sc = reinterpret_cast<float*>(ws + L.scales);
         launch_quantize(T, K, dt, x, ld_x, ws + L.codes, K, sc, st);
-        x = ws + L.codes;
-        ld_x = K;
-        x_scales = sc;
+        P.xs = sc;
     }
-    const dim3 grid((N + kTile - 1) / kTile, (T + kTile - 1) / kTile);
-    linear_kernel<<<grid, 256, 0, st>>>(T, K, N, static_cast<const uint8_t*>(x), ld_x, x_scales,
-                                        static_cast<const uint8_t*>(w), w_scales, static_cast<__nv_bfloat16*>(y), ld_y);
-    return launched(fn);
+    P.ws = w_scales;
+    P.y = static_cast<__nv_bfloat16*>(y);
+    P.ld_y = ld_y;
+    P.T = T;
+    P.N = N;
+    P.nb = blocks_of(K);
+    P.tiles_m = (T + kPM - 1) / kPM;
+    P.tiles_n = (N + kPN - 1) / kPN;
+    P.status = reinterpret_cast<int32_t*>(ws);
+    const int pairs = (int)std::min<int64_t>(dev->sms / 2, (int64_t)P.tiles_m * P.tiles_n);
+    e = launch_pdl(linear_pair_kernel, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, st, P);
+    if (e != cudaSuccess) return refuse(LORA_ERR_CUDA, std::string(fn) + ": " + cudaGetErrorString(e));
+    return LORA_OK;
 }

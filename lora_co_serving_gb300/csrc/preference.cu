@@ -17,7 +17,8 @@ namespace lora {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLog2eRest = (float)(1.4426950408889634 - (double)kLog2e);   // what float32 leaves of log2(e)
+constexpr float kLog2eHigh = 1.44268798828125f;        // log2(e) to 16 bits, and the rest of it
+constexpr float kLog2eLow = (float)(1.4426950408889634 - (double)kLog2eHigh);
 constexpr int kThreads = 256;
 
 // 2^x; 0 for x = -infinity, results below the smallest normal number are 0
@@ -63,8 +64,9 @@ struct RowSpan {
 
 // Running sum of e^x over what was seen, as s 2^n.  n is a whole number, the smallest not below the largest
 // x log2(e) so far: rescaling by 2^(n - n') is exact.  log2(e) is taken in two parts: its float32 value alone is
-// 1.3e-8 off, which shifts every log-sum-exp of size 12 the same way by 1.6e-7, and a sequence's sum of log ratios,
-// where random errors cancel, by that times its length.
+// 1.3e-8 off, which shifts every row's log-sum-exp the same way (by 7e-8 at a mean logit of 5), and a sequence's sum
+// of log ratios, where random errors cancel, by that times its length.  The high part has 16 bits: what the low part
+// adds is then far above a unit of the sum it is added to.
 struct ExpSum {
     float n = -INFINITY, s = 0.f;
     static __device__ __forceinline__ float weight(float from, float to) {
@@ -87,7 +89,7 @@ struct ExpSum {
         }
         const float off = n == -INFINITY ? 0.f : -n;
 #pragma unroll
-        for (int i = 0; i < N; ++i) s += exp2_fast(fmaf(x[i], kLog2eRest, fmaf(x[i], kLog2e, off)));
+        for (int i = 0; i < N; ++i) s += exp2_fast(fmaf(x[i], kLog2eLow, fmaf(x[i], kLog2eHigh, off)));
     }
     // log of the sum, in 64 bits (once per row); NaN for a row without a finite logit
     __device__ __forceinline__ double log() const {
