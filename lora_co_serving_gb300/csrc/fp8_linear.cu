@@ -26,13 +26,31 @@ __device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, volatil
 __host__ __device__ constexpr uint32_t instr_desc_e4m3(int m, int n) {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
-__device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                              uint32_t accumulate) {
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// arrive (when this CTA's issued MMAs complete) on the barrier at this offset in both CTAs of the cluster
+__device__ __forceinline__ void mma_commit_both(uint32_t bar) {
+    const uint16_t mask = 3;
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(mask)
+        : "memory");
+}
+// TMA load into the same place of both CTAs' shared memory; each CTA's barrier at this offset counts its copy's bytes
+__device__ __forceinline__ void tma_load_2d_both(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1,
+                                                 uint32_t bar) {
+    const uint16_t mask = 3;
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], "
+        "[%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "h"(mask)
         : "memory");
 }
 // (a.lo, a.hi) += (d0, d1) * (s.lo, s.hi).  volatile: d comes from a TMEM read and must stay behind its wait
@@ -55,41 +73,49 @@ __device__ __forceinline__ float2 halves(uint64_t a) {
 }
 
 // =============================================================================================================
-// Many rows: CTA pairs, 256 rows of x by 256 outputs (rows of w).
+// Many rows: clusters of two CTAs, each 128 rows of x by 256 outputs (rows of w).
 //
-// A pair works on one tile at a time.  CTA r holds rows [128 r, 128 r + 128) of the tile's x and of its w; the leader
-// (rank 0) issues the MMAs, which read both CTAs' shared memory and leave each CTA the accumulators of its own 128
-// rows of x by 256 outputs.  Per block each CTA moves 32 KB for 2 * 128 * 256 * 128 flops.
+// The CTAs of a cluster share the outputs: each loads its own 128 rows of x and half of the 256 rows of w, and the
+// halves go to both (TMA multicast), 32 KB per CTA and block for 128 * 256 * 128 products.  Everything else is the
+// CTA's own: an accumulator goes to and fro between the issuing thread and the adding warps once per block, and over
+// a CTA pair's shared MMAs that exchange takes about 1.2 us, several blocks' work.
 //
 // 384 threads: warp 0 loads (TMA), warp 1 issues, warps 4..11 scale and add: each thread has one row of x and 128
-// outputs, which are one block of w's rows, so a block's 128 sums share one scale, sx[row] * sw[block].  The block
+// outputs, which are one block of w's rows, so a block's 128 sums share one scale, sx[row] * sw[block].  The CTA
 // starts with 168 registers a thread (64512 in all); the first warpgroup gives up 112 of them and the adding warps,
 // whose 128 sums must not spill, take 56 more: 128 * 56 + 256 * 224 = 64512.
 // =============================================================================================================
-constexpr int kPM = 256, kPN = 256;                      // rows of x and outputs of a pair's tile
-constexpr int kOperandBytes = 128 * kQBlock;             // one CTA's 128 rows of x (or w), one block of columns
-constexpr int kPairStageBytes = 2 * kOperandBytes;
-constexpr int kPairStages = 6;
-constexpr int kPairThreads = 384;
+constexpr int kPM = 256, kPN = 256;                      // rows of x and outputs of a cluster's tile
+constexpr int kXBytes = 128 * kQBlock;                   // a CTA's rows of x, one block of columns
+constexpr int kWBytes = kPN * kQBlock;                   // the tile's rows of w
+constexpr int kStageBytes = kXBytes + kWBytes;
+constexpr int kStages = 4;
+constexpr int kThreads = 384;
 constexpr int kLaunchRegs = 168, kIssueRegs = 56, kAddRegs = 224;
-static_assert(128 * kIssueRegs + 256 * kAddRegs <= kPairThreads * kLaunchRegs, "register split above the launch's");
+static_assert(128 * kIssueRegs + 256 * kAddRegs <= kThreads * kLaunchRegs, "register split above the launch's");
 constexpr int kAddWarps = 8;
+constexpr int kOutBufs = 1;
+constexpr int kBars = 2 * kStages + 4;
+constexpr int kPieceBytes = 32 * 32 * 2;                 // 32 rows by 32 outputs on their way out
+constexpr int kOutBytes = kOutBufs * kPieceBytes;        // of each adding warp
+constexpr int kScaleSlots = 8;                           // blocks whose scales are at hand (kStages + 2 are needed)
+constexpr int kScaleFloats = 132;                        // 128 rows of x, two blocks of w's rows, 8 bytes unused
+static_assert(kScaleSlots >= kStages + 2, "a slot would be overwritten while it is read");
 constexpr int kGroupM = 8;                               // tiles of x that share a sweep over w (see tile_at)
 
-struct PairParams {
-    CUtensorMap tm_x, tm_w;
+struct TileParams {
+    CUtensorMap tm_x, tm_w, tm_y;
     const float* xs;
     const float* ws;
-    __nv_bfloat16* y;
-    int64_t ld_y;
     int32_t T, N, nb;          // nb: blocks of a row
+    int32_t wide_scales;       // both scales' rows are 16-byte aligned
     int32_t tiles_m, tiles_n;
     int32_t* status;
 };
 
 // Tiles in bands of kGroupM tiles of x: a band's columns are swept one after another, so that the tiles at work at any
 // time share few rows of x and of w.
-__device__ __forceinline__ void tile_at(const PairParams& P, int i, int* tm, int* tn) {
+__device__ __forceinline__ void tile_at(const TileParams& P, int i, int* tm, int* tn) {
     const int band = kGroupM * P.tiles_n;
     const int m0 = i / band * kGroupM;
     const int rows = min(kGroupM, P.tiles_m - m0);
@@ -98,147 +124,217 @@ __device__ __forceinline__ void tile_at(const PairParams& P, int i, int* tm, int
     *tn = r / rows;
 }
 
-struct PairRing {
+struct Ring {
     int stage = 0;
     uint32_t phase = 0;
     __device__ __forceinline__ void next() {
-        if (++stage == kPairStages) { stage = 0; phase ^= 1u; }
+        if (++stage == kStages) { stage = 0; phase ^= 1u; }
     }
 };
 
-struct PairBars {
+struct Bars {
     uint32_t full, empty, tfull, tempty;       // per stage: loaded, free; per accumulator: summed, read
     volatile int* abort_flag;
 };
 
-__device__ __forceinline__ void pair_load(const PairParams& P, const PairBars& B, uint8_t* smem, uint32_t rank) {
-    const uint32_t full_leader = mapa_shared(B.full, 0);
-    PairRing ring;
+__device__ __forceinline__ void tile_load(const TileParams& P, const Bars& B, uint8_t* smem, uint32_t rank) {
+    Ring ring;
     for (int i = blockIdx.x / 2; i < P.tiles_m * P.tiles_n; i += gridDim.x / 2) {
         int tm, tn;
         tile_at(P, i, &tm, &tn);
         const int row_x = tm * kPM + 128 * (int)rank, row_w = tn * kPN + 128 * (int)rank;
         for (int kb = 0; kb < P.nb; ++kb) {
+            // free in both CTAs: the half of w goes to both
             if (!wait_here(B.empty + ring.stage * 8, ring.phase ^ 1u, B.abort_flag, P.status)) return;
-            if (rank == 0) mbar_expect_tx(B.full + ring.stage * 8, 2 * kPairStageBytes);
-            const uint32_t full = full_leader + ring.stage * 8;
-            const uint32_t sa = smem_u32(smem + ring.stage * kPairStageBytes);
-            tma_load_2d_pair(sa, &P.tm_x, kb * kQBlock, row_x, full);
-            tma_load_2d_pair(sa + kOperandBytes, &P.tm_w, kb * kQBlock, row_w, full);
+            const uint32_t full = B.full + ring.stage * 8;
+            mbar_expect_tx(full, kStageBytes);
+            const uint32_t sa = smem_u32(smem + ring.stage * kStageBytes);
+            tma_load_2d(sa, &P.tm_x, kb * kQBlock, row_x, full);
+            tma_load_2d_both(sa + kXBytes + rank * (kWBytes / 2), &P.tm_w, kb * kQBlock, row_w, full);
             ring.next();
         }
     }
+    // the peer's last commits arrive on this CTA's barriers: none may be under way when the CTA ends
+    for (int s = 0; s < kStages; ++s, ring.next())
+        if (!wait_here(B.empty + ring.stage * 8, ring.phase ^ 1u, B.abort_flag, P.status)) return;
 }
 
-__device__ __forceinline__ void pair_issue(const PairParams& P, const PairBars& B, uint8_t* smem, uint32_t tmem) {
-    PairRing ring;
+__device__ __forceinline__ void tile_issue(const TileParams& P, const Bars& B, uint8_t* smem, uint32_t tmem) {
+    Ring ring;
     uint32_t use = 0;                          // blocks so far: accumulator use & 1
     for (int i = blockIdx.x / 2; i < P.tiles_m * P.tiles_n; i += gridDim.x / 2) {
         for (int kb = 0; kb < P.nb; ++kb, ++use) {
+            if (!wait_here(B.full + ring.stage * 8, ring.phase, B.abort_flag, P.status)) return;
+            const uint32_t sa = smem_u32(smem + ring.stage * kStageBytes), sb = sa + kXBytes;
             const uint32_t acc = use & 1u;
             if (!wait_here(B.tempty + acc * 8, ((use >> 1) & 1u) ^ 1u, B.abort_flag, P.status)) return;
-            if (!wait_here(B.full + ring.stage * 8, ring.phase, B.abort_flag, P.status)) return;
             tc_fence_after();
-            const uint32_t sa = smem_u32(smem + ring.stage * kPairStageBytes), sb = sa + kOperandBytes;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                mma_e4m3_pair(tmem + acc * kPN, smem_desc(sa + k * 32, 16, 1024), smem_desc(sb + k * 32, 16, 1024),
-                              instr_desc_e4m3(kPM, kPN), k > 0);
-            mma_commit_pair(B.empty + ring.stage * 8);
-            mma_commit_pair(B.tfull + acc * 8);
+                mma_e4m3(tmem + acc * kPN, smem_desc(sa + k * 32, 16, 1024), smem_desc(sb + k * 32, 16, 1024),
+                         instr_desc_e4m3(128, kPN), k > 0);
+            mma_commit_both(B.empty + ring.stage * 8);
+            mma_commit(B.tfull + acc * 8);
             ring.next();
         }
     }
 }
 
-__device__ __forceinline__ void pair_add(const PairParams& P, const PairBars& B, uint32_t tmem, uint32_t rank,
-                                         int warp, int lane) {
-    const int quarter = warp & 3, half = (warp - 4) / 4;
-    const uint32_t tempty_leader = mapa_shared(B.tempty, 0);
-    const uint32_t taddr0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * 128);
+// Warps 2 and 3 bring the scales of each block to shared memory: sx of this warp's 64 rows of x and sw of one of the
+// tile's two blocks of w's rows.  Read by the adding warps themselves, from global memory, they cost 8 % of an
+// 8192 x 8192 x 28672 product: a read under way has to end before a wait's loop is entered.
+// They arrive on the stage's barrier, so a block's MMAs, and with them its sums, come after its scales.
+// Slot kb % kScaleSlots is free once the MMAs of block kb - kStages are done, as they began after the adding warps had
+// finished with block kb - kStages - 2.
+__device__ __forceinline__ void tile_scales(const TileParams& P, const Bars& B, float* slots, uint32_t rank, int which,
+                                            int lane) {
+    Ring ring;
     uint32_t use = 0;
     for (int i = blockIdx.x / 2; i < P.tiles_m * P.tiles_n; i += gridDim.x / 2) {
         int tm, tn;
         tile_at(P, i, &tm, &tn);
-        const int t = tm * kPM + 128 * (int)rank + quarter * 32 + lane;
-        const int n0 = tn * kPN + half * 128;
-        const bool live = t < P.T && n0 < P.N;
-        const float* xs = P.xs + (int64_t)(live ? t : 0) * P.nb;
-        const float* ws = P.ws + (int64_t)(live ? n0 / kQBlock : 0) * P.nb;
-        // scales are read two blocks ahead of their use (a read is an L2 round trip, about a block's MMAs)
-        float s0 = xs[0] * ws[0], s1 = P.nb > 1 ? xs[1] * ws[1] : 0.f;
-        uint64_t acc[64];
+        const int t = tm * kPM + 128 * (int)rank + 64 * which + lane, n0 = tn * kPN + 128 * which;
+        const float* x0 = P.xs + (int64_t)min(t, P.T - 1) * P.nb;          // rows past the end: any scale will do
+        const float* x1 = P.xs + (int64_t)min(t + 32, P.T - 1) * P.nb;
+        const float* w = P.ws + (int64_t)min(n0 / kQBlock, (P.N - 1) / kQBlock) * P.nb;
+        for (int kb0 = 0; kb0 < P.nb; kb0 += 4) {
+            float a[4], b[4], c[4];
+            if (P.wide_scales) {               // rows of scales 16-byte aligned: four blocks at a time
+                const float4 va = *reinterpret_cast<const float4*>(x0 + kb0);
+                const float4 vb = *reinterpret_cast<const float4*>(x1 + kb0);
+                const float4 vc = *reinterpret_cast<const float4*>(w + kb0);
+                a[0] = va.x; a[1] = va.y; a[2] = va.z; a[3] = va.w;
+                b[0] = vb.x; b[1] = vb.y; b[2] = vb.z; b[3] = vb.w;
+                c[0] = vc.x; c[1] = vc.y; c[2] = vc.z; c[3] = vc.w;
+            } else {
 #pragma unroll
-        for (int j = 0; j < 64; ++j) acc[j] = 0;
-        for (int kb = 0; kb < P.nb; ++kb, ++use) {
-            const uint64_t sc = both(s0);
-            s0 = s1;
-            if (kb + 2 < P.nb) s1 = xs[kb + 2] * ws[kb + 2];
-            const uint32_t buf = use & 1u;
-            const bool ok = wait_here(B.tfull + buf * 8, (use >> 1) & 1u, B.abort_flag, P.status);
-            if (!__all_sync(0xffffffffu, ok)) return;
-            tc_fence_after();
-            const uint32_t ta = taddr0 + buf * kPN;
-            uint32_t d[2][16];
-            tmem_ld16(ta, d[0]);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                tmem_ld_wait();
-                if (c < 7) tmem_ld16(ta + 16 * (c + 1), d[(c + 1) & 1]);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) fma2(acc[8 * c + q], d[c & 1][2 * q], d[c & 1][2 * q + 1], sc);
+                for (int j = 0; j < 4; ++j) {
+                    const int kb = min(kb0 + j, P.nb - 1);
+                    a[j] = x0[kb];
+                    b[j] = x1[kb];
+                    c[j] = w[kb];
+                }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(tempty_leader + buf * 8);
-        }
-        if (!live) continue;
-        __nv_bfloat16* out = P.y + t * P.ld_y + n0;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-            uint32_t q[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 f = halves(acc[4 * c + k]);
-                q[k] = pack_bf16(f.x, f.y);
+            for (int j = 0; j < 4; ++j) {
+                if (kb0 + j >= P.nb) break;
+                const bool ok = wait_here(B.empty + ring.stage * 8, ring.phase ^ 1u, B.abort_flag, P.status);
+                if (!__all_sync(0xffffffffu, ok)) return;
+                float* s = slots + (use % kScaleSlots) * kScaleFloats;
+                s[64 * which + lane] = a[j];
+                s[64 * which + 32 + lane] = b[j];
+                if (lane == 0) s[128 + which] = c[j];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(B.full + ring.stage * 8);
+                ++use;
+                ring.next();
             }
-            if (n0 + 8 * c < P.N) *reinterpret_cast<uint4*>(out + 8 * c) = make_uint4(q[0], q[1], q[2], q[3]);
         }
     }
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-    linear_pair_kernel(const __grid_constant__ PairParams P) {
+__device__ __forceinline__ void tile_add(const TileParams& P, const Bars& B, uint32_t tmem, uint32_t rank, int warp,
+                                         int lane, const float* slots, uint32_t stage_out) {
+    const int quarter = warp & 3, half = (warp - 4) / 4;
+    const uint32_t taddr0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * 128;
+    uint32_t use = 0;
+    for (int i = blockIdx.x / 2; i < P.tiles_m * P.tiles_n; i += gridDim.x / 2) {
+        int tm, tn;
+        tile_at(P, i, &tm, &tn);
+        const int t0 = tm * kPM + 128 * (int)rank + quarter * 32;
+        const int n0 = tn * kPN + half * 128;
+        uint64_t acc[64];
+#pragma unroll
+        for (int j = 0; j < 64; ++j) acc[j] = 0;
+        for (int kb = 0; kb < P.nb; ++kb, ++use) {
+            const uint32_t buf = use & 1u;
+            // after a time-out no wait holds any longer: the tiles are gone through to the end, their values lost
+            wait_here(B.tfull + buf * 8, (use >> 1) & 1u, B.abort_flag, P.status);
+            __syncwarp();
+            tc_fence_after();
+            const uint32_t ta = taddr0 + buf * kPN;
+            uint32_t d[2][16];
+            tmem_ld16(ta, d[0]);
+            // written before the block's MMAs were issued (see tile_scales)
+            const float* s = slots + (use % kScaleSlots) * kScaleFloats;
+            const uint64_t sc = both(s[quarter * 32 + lane] * s[128 + half]);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                tmem_ld_wait();
+                if (c < 7) {
+                    tmem_ld16(ta + 16 * (c + 1), d[(c + 1) & 1]);
+                } else {                       // read to the end: the accumulator goes back before the last sums
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(B.tempty + buf * 8);
+                }
+#pragma unroll
+                for (int q = 0; q < 8; ++q) fma2(acc[8 * c + q], d[c & 1][2 * q], d[c & 1][2 * q + 1], sc);
+            }
+        }
+        // a warp's 32 rows leave in pieces of 32 columns, through shared memory, as one TMA store each (rows and
+        // columns past the end are cut off there)
+#pragma unroll
+        for (int piece = 0; piece < 4; ++piece) {
+            const uint32_t buf = stage_out + (piece % kOutBufs) * kPieceBytes;
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kOutBufs - 1) : "memory");   // buf's last store
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t q[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 f = halves(acc[16 * piece + 4 * c + k]);
+                    q[k] = pack_bf16(f.x, f.y);
+                }
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 64 +
+                                                                             ((c ^ ((lane >> 1) & 3)) * 16)),
+                             "r"(q[0]), "r"(q[1]), "r"(q[2]), "r"(q[3])
+                             : "memory");
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0 && t0 < P.T && n0 + 32 * piece < P.N) tma_store_2d(&P.tm_y, buf, n0 + 32 * piece, t0);
+        }
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    linear_tile_kernel(const __grid_constant__ TileParams P) {
     extern __shared__ uint8_t dsmem[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kPairStages * kPairStageBytes);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kPairStages + 4);
-    PairBars B;
+    uint8_t* out = smem + kStages * kStageBytes;
+    float* slots = reinterpret_cast<float*>(out + kAddWarps * kOutBytes);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(slots + kScaleSlots * kScaleFloats);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
+    Bars B;
     B.abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     B.full = smem_u32(bars);
-    B.empty = B.full + kPairStages * 8;
-    B.tfull = B.empty + kPairStages * 8;
+    B.empty = B.full + kStages * 8;
+    B.tfull = B.empty + kStages * 8;
     B.tempty = B.tfull + 16;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_ctarank();
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kPairStages; ++s) {
-            mbar_init(B.full + s * 8, 1);                    // used in the leader: its arm + both CTAs' bytes
-            mbar_init(B.empty + s * 8, 1);                   // the leader's commit
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(B.full + s * 8, 3);            // the arm + the bytes of both CTAs' loads; warps 2 and 3
+            mbar_init(B.empty + s * 8, 2);           // both CTAs' commits
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(B.tfull + b * 8, 1);                   // the leader's commit
-            mbar_init(B.tempty + b * 8, 2 * kAddWarps);      // used in the leader: the adding warps of both CTAs
+            mbar_init(B.tfull + b * 8, 1);
+            mbar_init(B.tempty + b * 8, kAddWarps);
         }
         *B.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot))
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot))
                      : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     cluster_sync_all();
@@ -247,21 +343,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     grid_dep_wait();
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-        if (warp == 0 && lane == 0) pair_load(P, B, smem, rank);
-        if (warp == 1 && lane == 0 && rank == 0) pair_issue(P, B, smem, tmem);
+        if (warp == 0 && lane == 0) tile_load(P, B, smem, rank);
+        if (warp == 1 && lane == 0) tile_issue(P, B, smem, tmem);
+        if (warp >= 2) tile_scales(P, B, slots, rank, warp - 2, lane);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAddRegs));
-        pair_add(P, B, tmem, rank, warp, lane);
+        tile_add(P, B, tmem, rank, warp, lane, slots, smem_u32(out) + (uint32_t)((warp - 4) * kOutBytes));
     }
     __syncwarp();
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
     if (warp == 1)
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-constexpr size_t kPairSmem = (size_t)kPairStages * kPairStageBytes + 1024 + 1024;
+constexpr size_t kTileSmem = (size_t)kStages * kStageBytes + kAddWarps * kOutBytes +
+                             kScaleSlots * kScaleFloats * 4 + (kBars + 1) * 8 + 1024;
+static_assert(kTileSmem <= 227 * 1024, "shared memory of a CTA");
 
 // --------------------------------------------------------------------------------------------------------- host
 // [rows, K] codes, rows ld bytes apart, as 128-byte swizzled boxes of {128 columns, box_rows}; past the end reads 0
@@ -274,6 +373,19 @@ bool encode_codes(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, u
     cuuint32_t estr[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// y [T, N] as 64-byte swizzled boxes of {32 columns, 32 rows}: what an adding warp stores at a time
+bool encode_y(CUtensorMap* m, const void* base, uint64_t N, uint64_t T, uint64_t ld) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {N, T};
+    cuuint64_t strides[1] = {ld * 2};
+    cuuint32_t box[2] = {32, 32};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -292,7 +404,7 @@ cudaError_t device_info(Device** out) {
     if (!v.ready) {
         e = cudaDeviceGetAttribute(&v.sms, cudaDevAttrMultiProcessorCount, d);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(linear_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
+            e = cudaFuncSetAttribute(linear_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTileSmem);
         if (e != cudaSuccess) return e;
         v.ready = true;
     }
@@ -356,9 +468,10 @@ extern "C" int lora_fp8_linear(int32_t T, int32_t K, int32_t N, lora_dtype_t dt,
         return refuse(LORA_ERR_WORKSPACE, "workspace too small: need " + std::to_string(L.end) + " bytes, got " +
                                               std::to_string(ws_bytes));
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    PairParams P{};
+    TileParams P{};
     const void* xc = x_scales ? x : ws + L.codes;
-    if (!encode_codes(&P.tm_x, xc, K, T, x_scales ? ld_x : K, 128) || !encode_codes(&P.tm_w, w, K, N, K, 128))
+    if (!encode_codes(&P.tm_x, xc, K, T, x_scales ? ld_x : K, 128) || !encode_codes(&P.tm_w, w, K, N, K, 128) ||
+        !encode_y(&P.tm_y, y, N, T, ld_y))
         return refuse(LORA_ERR_CUDA, std::string(fn) + ": cuTensorMapEncodeTiled failed");
     Device* dev = nullptr;
     cudaError_t e = device_info(&dev);
@@ -372,16 +485,15 @@ extern "C" int lora_fp8_linear(int32_t T, int32_t K, int32_t N, lora_dtype_t dt,
         P.xs = sc;
     }
     P.ws = w_scales;
-    P.y = static_cast<__nv_bfloat16*>(y);
-    P.ld_y = ld_y;
     P.T = T;
     P.N = N;
     P.nb = blocks_of(K);
+    P.wide_scales = P.nb % 4 == 0 && is_aligned(P.xs, 16) && is_aligned(P.ws, 16);
     P.tiles_m = (T + kPM - 1) / kPM;
     P.tiles_n = (N + kPN - 1) / kPN;
     P.status = reinterpret_cast<int32_t*>(ws);
     const int pairs = (int)std::min<int64_t>(dev->sms / 2, (int64_t)P.tiles_m * P.tiles_n);
-    e = launch_pdl(linear_pair_kernel, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, st, P);
+    e = launch_pdl(linear_tile_kernel, dim3(2 * pairs), dim3(kThreads), kTileSmem, st, P);
     if (e != cudaSuccess) return refuse(LORA_ERR_CUDA, std::string(fn) + ": " + cudaGetErrorString(e));
     return LORA_OK;
 }
