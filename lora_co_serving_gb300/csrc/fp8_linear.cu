@@ -110,18 +110,43 @@ struct TileParams {
     int32_t T, N, nb;          // nb: blocks of a row
     int32_t wide_scales;       // both scales' rows are 16-byte aligned
     int32_t tiles_m, tiles_n;
+    int32_t n_whole, n_split;  // tiles [0, n_whole) are whole; each of the others is cut into n_split pieces of its
+    int32_t n_items;           //   blocks, whose sums go to `part` and are added up by linear_join_kernel
+    float* part;
     int32_t* status;
+};
+
+// Item i of the grid's list: a tile, and the blocks [kb0, kb1) of it
+struct Item {
+    int tm, tn, kb0, kb1, piece;               // piece: its place in `part`, -1 for a whole tile
 };
 
 // Tiles in bands of kGroupM tiles of x: a band's columns are swept one after another, so that the tiles at work at any
 // time share few rows of x and of w.
-__device__ __forceinline__ void tile_at(const TileParams& P, int i, int* tm, int* tn) {
-    const int band = kGroupM * P.tiles_n;
+__host__ __device__ __forceinline__ void tile_at(int tiles_m, int tiles_n, int i, int* tm, int* tn) {
+    const int band = kGroupM * tiles_n;
     const int m0 = i / band * kGroupM;
-    const int rows = min(kGroupM, P.tiles_m - m0);
+    const int left = tiles_m - m0, rows = left < kGroupM ? left : kGroupM;
     const int r = i % band;
     *tm = m0 + r % rows;
     *tn = r / rows;
+}
+__device__ __forceinline__ Item item_at(const TileParams& P, int i) {
+    Item it;
+    it.kb0 = 0;
+    it.kb1 = P.nb;
+    it.piece = i - P.n_whole;
+    int tile = i;
+    if (it.piece < 0) {
+        it.piece = -1;
+    } else {
+        const int q = it.piece % P.n_split;
+        tile = P.n_whole + it.piece / P.n_split;
+        it.kb0 = (int)((int64_t)P.nb * q / P.n_split);
+        it.kb1 = (int)((int64_t)P.nb * (q + 1) / P.n_split);
+    }
+    tile_at(P.tiles_m, P.tiles_n, tile, &it.tm, &it.tn);
+    return it;
 }
 
 struct Ring {
@@ -139,11 +164,10 @@ struct Bars {
 
 __device__ __forceinline__ void tile_load(const TileParams& P, const Bars& B, uint8_t* smem, uint32_t rank) {
     Ring ring;
-    for (int i = blockIdx.x / 2; i < P.tiles_m * P.tiles_n; i += gridDim.x / 2) {
-        int tm, tn;
-        tile_at(P, i, &tm, &tn);
-        const int row_x = tm * kPM + 128 * (int)rank, row_w = tn * kPN + 128 * (int)rank;
-        for (int kb = 0; kb < P.nb; ++kb) {
+    for (int i = blockIdx.x / 2; i < P.n_items; i += gridDim.x / 2) {
+        const Item it = item_at(P, i);
+        const int row_x = it.tm * kPM + 128 * (int)rank, row_w = it.tn * kPN + 128 * (int)rank;
+        for (int kb = it.kb0; kb < it.kb1; ++kb) {
             // free in both CTAs: the half of w goes to both
             if (!wait_here(B.empty + ring.stage * 8, ring.phase ^ 1u, B.abort_flag, P.status)) return;
             const uint32_t full = B.full + ring.stage * 8;
@@ -162,8 +186,9 @@ __device__ __forceinline__ void tile_load(const TileParams& P, const Bars& B, ui
 __device__ __forceinline__ void tile_issue(const TileParams& P, const Bars& B, uint8_t* smem, uint32_t tmem) {
     Ring ring;
     uint32_t use = 0;                          // blocks so far: accumulator use & 1
-    for (int i = blockIdx.x / 2; i < P.tiles_m * P.tiles_n; i += gridDim.x / 2) {
-        for (int kb = 0; kb < P.nb; ++kb, ++use) {
+    for (int i = blockIdx.x / 2; i < P.n_items; i += gridDim.x / 2) {
+        const Item it = item_at(P, i);
+        for (int kb = it.kb0; kb < it.kb1; ++kb, ++use) {
             if (!wait_here(B.full + ring.stage * 8, ring.phase, B.abort_flag, P.status)) return;
             const uint32_t sa = smem_u32(smem + ring.stage * kStageBytes), sb = sa + kXBytes;
             const uint32_t acc = use & 1u;
@@ -190,26 +215,26 @@ __device__ __forceinline__ void tile_scales(const TileParams& P, const Bars& B, 
                                             int lane) {
     Ring ring;
     uint32_t use = 0;
-    for (int i = blockIdx.x / 2; i < P.tiles_m * P.tiles_n; i += gridDim.x / 2) {
-        int tm, tn;
-        tile_at(P, i, &tm, &tn);
-        const int t = tm * kPM + 128 * (int)rank + 64 * which + lane, n0 = tn * kPN + 128 * which;
+    for (int i = blockIdx.x / 2; i < P.n_items; i += gridDim.x / 2) {
+        const Item it = item_at(P, i);
+        const int t = it.tm * kPM + 128 * (int)rank + 64 * which + lane, n0 = it.tn * kPN + 128 * which;
         const float* x0 = P.xs + (int64_t)min(t, P.T - 1) * P.nb;          // rows past the end: any scale will do
         const float* x1 = P.xs + (int64_t)min(t + 32, P.T - 1) * P.nb;
         const float* w = P.ws + (int64_t)min(n0 / kQBlock, (P.N - 1) / kQBlock) * P.nb;
-        for (int kb0 = 0; kb0 < P.nb; kb0 += 4) {
+        for (int kb0 = it.kb0; kb0 < it.kb1; kb0 = (kb0 & ~3) + 4) {       // groups of four by block number
             float a[4], b[4], c[4];
+            const int g0 = kb0 & ~3;
             if (P.wide_scales) {               // rows of scales 16-byte aligned: four blocks at a time
-                const float4 va = *reinterpret_cast<const float4*>(x0 + kb0);
-                const float4 vb = *reinterpret_cast<const float4*>(x1 + kb0);
-                const float4 vc = *reinterpret_cast<const float4*>(w + kb0);
+                const float4 va = *reinterpret_cast<const float4*>(x0 + g0);
+                const float4 vb = *reinterpret_cast<const float4*>(x1 + g0);
+                const float4 vc = *reinterpret_cast<const float4*>(w + g0);
                 a[0] = va.x; a[1] = va.y; a[2] = va.z; a[3] = va.w;
                 b[0] = vb.x; b[1] = vb.y; b[2] = vb.z; b[3] = vb.w;
                 c[0] = vc.x; c[1] = vc.y; c[2] = vc.z; c[3] = vc.w;
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int kb = min(kb0 + j, P.nb - 1);
+                    const int kb = min(g0 + j, P.nb - 1);
                     a[j] = x0[kb];
                     b[j] = x1[kb];
                     c[j] = w[kb];
@@ -217,7 +242,7 @@ __device__ __forceinline__ void tile_scales(const TileParams& P, const Bars& B, 
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if (kb0 + j >= P.nb) break;
+                if (g0 + j < kb0 || g0 + j >= it.kb1) continue;
                 const bool ok = wait_here(B.empty + ring.stage * 8, ring.phase ^ 1u, B.abort_flag, P.status);
                 if (!__all_sync(0xffffffffu, ok)) return;
                 float* s = slots + (use % kScaleSlots) * kScaleFloats;
@@ -238,15 +263,14 @@ __device__ __forceinline__ void tile_add(const TileParams& P, const Bars& B, uin
     const int quarter = warp & 3, half = (warp - 4) / 4;
     const uint32_t taddr0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * 128;
     uint32_t use = 0;
-    for (int i = blockIdx.x / 2; i < P.tiles_m * P.tiles_n; i += gridDim.x / 2) {
-        int tm, tn;
-        tile_at(P, i, &tm, &tn);
-        const int t0 = tm * kPM + 128 * (int)rank + quarter * 32;
-        const int n0 = tn * kPN + half * 128;
+    for (int i = blockIdx.x / 2; i < P.n_items; i += gridDim.x / 2) {
+        const Item it = item_at(P, i);
+        const int t0 = it.tm * kPM + 128 * (int)rank + quarter * 32;
+        const int n0 = it.tn * kPN + half * 128;
         uint64_t acc[64];
 #pragma unroll
         for (int j = 0; j < 64; ++j) acc[j] = 0;
-        for (int kb = 0; kb < P.nb; ++kb, ++use) {
+        for (int kb = it.kb0; kb < it.kb1; ++kb, ++use) {
             const uint32_t buf = use & 1u;
             // after a time-out no wait holds any longer: the tiles are gone through to the end, their values lost
             wait_here(B.tfull + buf * 8, (use >> 1) & 1u, B.abort_flag, P.status);
@@ -271,6 +295,19 @@ __device__ __forceinline__ void tile_add(const TileParams& P, const Bars& B, uin
 #pragma unroll
                 for (int q = 0; q < 8; ++q) fma2(acc[8 * c + q], d[c & 1][2 * q], d[c & 1][2 * q + 1], sc);
             }
+        }
+        if (it.piece >= 0) {
+            // [128 rows of a CTA][256 outputs] as groups of 4 outputs: a warp writes 512 contiguous bytes per group
+            float* part = P.part + ((int64_t)it.piece * 2 + rank) * (128 * kPN) +
+                          ((int64_t)half * 32 * 128 + quarter * 32 + lane) * 4;
+            if (t0 < P.T && n0 < P.N) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const float2 f = halves(acc[2 * c]), g = halves(acc[2 * c + 1]);
+                    __stcg(reinterpret_cast<float4*>(part + c * 512), make_float4(f.x, f.y, g.x, g.y));
+                }
+            }
+            continue;
         }
         // a warp's 32 rows leave in pieces of 32 columns, through shared memory, as one TMA store each (rows and
         // columns past the end are cut off there)
@@ -358,6 +395,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
+// Adds up the pieces of each cut tile, in their order, and writes its outputs.  One CTA per 32 rows by 64 outputs of
+// a tile; each warp adds 8 columns, a lane one row, so that every read is 512 contiguous bytes.
+__global__ void __launch_bounds__(256) linear_join_kernel(const float* __restrict__ part, __nv_bfloat16* __restrict__ y,
+                                                          int64_t ld_y, int32_t T, int32_t N, int32_t tiles_m,
+                                                          int32_t tiles_n, int32_t n_whole, int32_t n_split) {
+    grid_dep_wait();
+    const int cut = blockIdx.x / 32, sub = blockIdx.x % 32;
+    int tm, tn;
+    tile_at(tiles_m, tiles_n, n_whole + cut, &tm, &tn);
+    const int row = sub / 4 * 32 + threadIdx.x % 32, col = sub % 4 * 64 + threadIdx.x / 32 * 8;
+    const int t = tm * kPM + row, n = tn * kPN + col;
+    if (t >= T || n >= N) return;
+    const float* p = part + ((int64_t)cut * n_split * 2 + row / 128) * (128 * kPN) + (int64_t)col * 128 + (row % 128) * 4;
+    float v[8] = {};
+    for (int q = 0; q < n_split; ++q, p += 2 * 128 * kPN) {
+        const float4 a = __ldcg(reinterpret_cast<const float4*>(p));
+        const float4 b = __ldcg(reinterpret_cast<const float4*>(p + 512));
+        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    }
+    *reinterpret_cast<uint4*>(y + t * ld_y + n) =
+        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+
 constexpr size_t kTileSmem = (size_t)kStages * kStageBytes + kAddWarps * kOutBytes +
                              kScaleSlots * kScaleFloats * 4 + (kBars + 1) * 8 + 1024;
 static_assert(kTileSmem <= 227 * 1024, "shared memory of a CTA");
@@ -412,19 +473,40 @@ cudaError_t device_info(Device** out) {
     return cudaSuccess;
 }
 
-// Workspace: the status word, then x's codes and scales if x is quantized on the way
-struct Scratch {
-    size_t codes = 0, scales = 0, end = 0;
+// How the tiles are spread over the clusters.  Tiles beyond the last full round are cut along K, into as many pieces
+// as clusters are left for each: a round of 4 tiles would hold 72 of 76 clusters for a tile's whole time.  At most
+// kMaxSplit pieces of at least kMinBlocks blocks: a piece's sums are written and read back (256 KB).
+constexpr int kMaxSplit = 8, kMinBlocks = 4;
+constexpr int kClusters = 76;                            // planned for (152 SMs); right on any device
+struct Spread {
+    int tiles_m, tiles_n, n_whole, n_split, n_items;
+    int n_cut() const { return tiles_m * tiles_n - n_whole; }
 };
-Scratch layout_of(int32_t T, int32_t K, bool x_fp8) {
+Spread spread_of(int32_t T, int32_t K, int32_t N) {
+    Spread s;
+    s.tiles_m = (T + kPM - 1) / kPM;
+    s.tiles_n = (N + kPN - 1) / kPN;
+    const int tiles = s.tiles_m * s.tiles_n, rest = tiles % kClusters;
+    s.n_split = rest ? std::min({kClusters / rest, kMaxSplit, blocks_of(K) / kMinBlocks}) : 0;
+    if (s.n_split < 2) s.n_split = 0;
+    s.n_whole = s.n_split ? tiles - rest : tiles;
+    s.n_items = s.n_whole + s.n_cut() * s.n_split;
+    return s;
+}
+
+// Workspace: the status word, then x's codes and scales if x is quantized on the way, then the cut tiles' sums
+struct Scratch {
+    size_t codes = 0, scales = 0, part = 0, end = 0;
+};
+Scratch layout_of(int32_t T, int32_t K, bool x_fp8, const Spread& s) {
     auto al = [](size_t v) { return (v + 255) & ~size_t(255); };
     Scratch L;
     L.codes = 256;
     L.scales = L.codes + (x_fp8 ? 0 : al((size_t)T * K));
-    L.end = L.scales + (x_fp8 ? 0 : al((size_t)T * blocks_of(K) * sizeof(float)));
+    L.part = L.scales + (x_fp8 ? 0 : al((size_t)T * blocks_of(K) * sizeof(float)));
+    L.end = L.part + (size_t)s.n_cut() * s.n_split * kPM * kPN * sizeof(float);
     return L;
 }
-
 int check_sizes(const char* fn, int32_t T, int32_t K, int32_t N) {
     if (T < 0 || K <= 0 || N <= 0)
         return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": T must be >= 0, K and N > 0");
@@ -446,7 +528,7 @@ using namespace lora;
 
 extern "C" size_t lora_fp8_workspace_size(int32_t T, int32_t K, int32_t N, int32_t x_fp8) {
     if (check_sizes("lora_fp8_workspace_size", T, K, N) != LORA_OK) return 0;
-    return layout_of(T, K, x_fp8 != 0).end;
+    return layout_of(T, K, x_fp8 != 0, spread_of(T, K, N)).end;
 }
 
 extern "C" int lora_fp8_linear(int32_t T, int32_t K, int32_t N, lora_dtype_t dt, const void* x, int64_t ld_x,
@@ -461,7 +543,8 @@ extern "C" int lora_fp8_linear(int32_t T, int32_t K, int32_t N, lora_dtype_t dt,
     if (rc == LORA_OK) rc = check_matrix(fn, "y", y, N, ld_y, 2);
     if (rc != LORA_OK) return rc;
     if (!w_scales) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": w_scales is NULL");
-    const Scratch L = layout_of(T, K, x_scales != nullptr);
+    const Spread sp = spread_of(T, K, N);
+    const Scratch L = layout_of(T, K, x_scales != nullptr, sp);
     if (!workspace) return refuse(LORA_ERR_WORKSPACE, "workspace is NULL");
     if (!is_aligned(workspace, 256)) return refuse(LORA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
     if (ws_bytes < L.end)
@@ -489,11 +572,17 @@ extern "C" int lora_fp8_linear(int32_t T, int32_t K, int32_t N, lora_dtype_t dt,
     P.N = N;
     P.nb = blocks_of(K);
     P.wide_scales = P.nb % 4 == 0 && is_aligned(P.xs, 16) && is_aligned(P.ws, 16);
-    P.tiles_m = (T + kPM - 1) / kPM;
-    P.tiles_n = (N + kPN - 1) / kPN;
+    P.tiles_m = sp.tiles_m;
+    P.tiles_n = sp.tiles_n;
+    P.n_whole = sp.n_whole;
+    P.n_split = sp.n_split;
+    P.n_items = sp.n_items;
+    P.part = reinterpret_cast<float*>(ws + L.part);
     P.status = reinterpret_cast<int32_t*>(ws);
-    const int pairs = (int)std::min<int64_t>(dev->sms / 2, (int64_t)P.tiles_m * P.tiles_n);
-    e = launch_pdl(linear_tile_kernel, dim3(2 * pairs), dim3(kThreads), kTileSmem, st, P);
+    e = launch_pdl(linear_tile_kernel, dim3(2 * std::min(dev->sms / 2, sp.n_items)), dim3(kThreads), kTileSmem, st, P);
+    if (e == cudaSuccess && sp.n_cut() > 0)
+        e = launch_pdl(linear_join_kernel, dim3(32 * sp.n_cut()), dim3(256), 0, st, static_cast<const float*>(P.part),
+                       static_cast<__nv_bfloat16*>(y), ld_y, T, N, sp.tiles_m, sp.tiles_n, sp.n_whole, sp.n_split);
     if (e != cudaSuccess) return refuse(LORA_ERR_CUDA, std::string(fn) + ": " + cudaGetErrorString(e));
     return LORA_OK;
 }
