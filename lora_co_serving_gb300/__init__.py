@@ -199,8 +199,8 @@ def _dtype_code(t):
 
 def _stream_ptr(stream):
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:      # torch.cuda.current_stream().cuda_stream without its 2.9 us of Stream object
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -530,22 +530,25 @@ def _blocks(n):
 
 def _matrix(t, name, dtype=None, rows=None, cols=None, contiguous=False):
     """Check a 2-D tensor argument (unit column stride) and return its row distance in elements."""
-    if t.dim() != 2:
-        raise ValueError("%s must have two dimensions, got %d" % (name, t.dim()))
-    r, c = t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError("%s must have two dimensions, got %d" % (name, len(shape)))
+    r, c = shape
     if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError("%s must be [%s, %s], got [%d, %d]" % (name, "T" if rows is None else rows,
                                                                 "K" if cols is None else cols, r, c))
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.is_contiguous():
+        return c
     ld, unit = t.stride()
-    if r > 0 and c > 1 and (unit != 1 or (contiguous and ld != c and r > 1)):
+    if contiguous or (unit != 1 and c > 1):
         raise ValueError("%s must %s" % (name, "be contiguous" if contiguous else "have unit column stride"))
     return ld if r > 1 else max(ld, c)
 
 
 def _vector(t, name, dtype, n):
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.numel() != n or not t.is_contiguous():
         raise ValueError("%s must be contiguous with %d elements, got %s" % (name, n, tuple(t.shape)))
@@ -590,6 +593,23 @@ def fp8_workspace_size(T, K, N, x_fp8=False):
     return int(n)
 
 
+_STATUS_BYTES = 256
+_status_workspaces = {}
+
+
+def _status_workspace(stream_ptr, device):
+    """A stream's own workspace for calls that need no more than the status word: calls on one stream run one after
+    another.  None while a CUDA graph is captured (its replays may run beside the stream's later calls)."""
+    import torch
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return None
+    key = (device.index, stream_ptr)
+    ws = _status_workspaces.get(key)
+    if ws is None:
+        ws = _status_workspaces[key] = torch.empty(_STATUS_BYTES, dtype=torch.uint8, device=device)
+    return ws
+
+
 def fp8_linear(x, w, w_scales, x_scales=None, y=None, workspace=None, stream=None, check_status=False):
     """y [T, N] (bf16) = x W^T for a frozen weight in 8 bits (w [N, K] codes, w_scales [ceil(N/128), ceil(K/128)]).
 
@@ -610,10 +630,16 @@ def fp8_linear(x, w, w_scales, x_scales=None, y=None, workspace=None, stream=Non
     if y is None:
         y = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
     ldy = _matrix(y, "y", torch.bfloat16, T, N)
+    st = _stream_ptr(stream)
     if workspace is None:
-        workspace = torch.empty(fp8_workspace_size(T, K, N, x_scales is not None), dtype=torch.uint8, device=x.device)
-    _check(library().lora_fp8_linear(T, K, N, code, _ptr(x), ld, _ptr(x_scales), _ptr(w), _ptr(w_scales), _ptr(y), ldy,
-                                     _ptr(workspace), workspace.numel(), _stream_ptr(stream)))
+        need = fp8_workspace_size(T, K, N, x_scales is not None)
+        workspace = _status_workspace(st, x.device) if need <= _STATUS_BYTES else None
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    rc = library().lora_fp8_linear(T, K, N, code, x.data_ptr(), ld, _ptr(x_scales), w.data_ptr(), w_scales.data_ptr(),
+                                   y.data_ptr(), ldy, workspace.data_ptr(), workspace.numel(), st)
+    if rc != 0:
+        _check(rc)
     if check_status:
         workspace_status(workspace, stream)
     return y
@@ -692,6 +718,7 @@ Preference = namedtuple("Preference", ["loss", "rewards", "logp", "lse", "coef"]
 
 
 def _pairs(pairs):
+    """Pairs as a contiguous int32 [n, 4] numpy array."""
     return np.ascontiguousarray(np.asarray(pairs, dtype=np.int32).reshape(-1, 4))
 
 
@@ -725,10 +752,9 @@ def preference_forward(logits, labels, ref_logp, pairs, beta=0.1, label_smoothin
     _vector(ref_logp, "ref_logp", torch.float32, T)
     p = _pairs(pairs)
     n = p.shape[0]
-    buf = torch.empty(2 * T + 5 * n, dtype=torch.float32, device=logits.device)
-    logp, lse = buf[:T], buf[T:2 * T]
-    loss, rewards = buf[2 * T:2 * T + n], buf[2 * T + n:2 * T + 3 * n].view(n, 2)
-    coef = buf[2 * T + 3 * n:].view(n, 2)
+    logp, lse = torch.empty((2, T), dtype=torch.float32, device=logits.device).unbind(0)
+    rewards, coef = torch.empty((2, n, 2), dtype=torch.float32, device=logits.device).unbind(0)
+    loss = torch.empty(n, dtype=torch.float32, device=logits.device)
     _check(library().lora_preference_forward(T, V, code, _ptr(logits), ld, _ptr(labels), _ptr(ref_logp), _ptr(p), n,
                                              beta, label_smoothing, _ptr(loss), _ptr(rewards), _ptr(logp), _ptr(lse),
                                              _ptr(coef), _stream_ptr(stream)))

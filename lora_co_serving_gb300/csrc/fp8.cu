@@ -7,6 +7,7 @@
 #include <vector>
 
 #include "fp8.h"
+#include "tc_prims.h"
 
 namespace lora {
 namespace {
@@ -57,6 +58,8 @@ template <class Row8>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(Shape s, const void* __restrict__ x, int64_t ld_x,
                                                             uint8_t* __restrict__ codes, int64_t ld_codes,
                                                             float* __restrict__ scales) {
+    asm volatile("griddepcontrol.launch_dependents;");     // a product may set itself up meanwhile
+    grid_dep_wait();
     const Place p(s, 1);
     const bool in = p.in && p.row0 < s.rows;
     Row8 r;
@@ -268,13 +271,11 @@ int64_t train_ranges(const char* fn, int32_t T, const lora_segment_t* segs, int3
 
 }  // namespace
 
-void launch_quantize(int32_t T, int32_t K, lora_dtype_t dt, const void* x, int64_t ld_x, uint8_t* codes,
-                     int64_t ld_codes, float* scales, cudaStream_t stream) {
+cudaError_t launch_quantize(int32_t T, int32_t K, lora_dtype_t dt, const void* x, int64_t ld_x, uint8_t* codes,
+                            int64_t ld_codes, float* scales, cudaStream_t stream) {
     const Shape s = shape_of(T, K);
-    if (dt == LORA_BF16)
-        quantize_kernel<Row8Bf16><<<grid_of(s, 1), kThreads, 0, stream>>>(s, x, ld_x, codes, ld_codes, scales);
-    else
-        quantize_kernel<Row8F32><<<grid_of(s, 1), kThreads, 0, stream>>>(s, x, ld_x, codes, ld_codes, scales);
+    return launch_pdl(dt == LORA_BF16 ? quantize_kernel<Row8Bf16> : quantize_kernel<Row8F32>, grid_of(s, 1),
+                      dim3(kThreads), 0, stream, s, x, ld_x, codes, ld_codes, scales);
 }
 
 }  // namespace lora
@@ -293,9 +294,10 @@ extern "C" int lora_fp8_quantize(int32_t T, int32_t K, lora_dtype_t dt, const vo
     if (rc == LORA_OK) rc = check_matrix(fn, "codes", codes, K, ld_codes, 1);
     if (rc != LORA_OK) return rc;
     if (!scales) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": scales is NULL");
-    launch_quantize(T, K, dt, x, ld_x, static_cast<uint8_t*>(codes), ld_codes, scales,
-                    static_cast<cudaStream_t>(stream));
-    return launched(fn);
+    const cudaError_t e = launch_quantize(T, K, dt, x, ld_x, static_cast<uint8_t*>(codes), ld_codes, scales,
+                                          static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return refuse(LORA_ERR_CUDA, std::string(fn) + ": " + cudaGetErrorString(e));
+    return LORA_OK;
 }
 
 extern "C" int lora_fp8_quantize_weight(int32_t N, int32_t K, lora_dtype_t dt, const void* W, int64_t ld_w,

@@ -133,7 +133,7 @@ inline int check_matrix(const char* fn, const char* name, const void* p, int64_t
 }
 
 // the quantizer behind lora_fp8_quantize (arguments checked); also lora_fp8_linear's first step
-void launch_quantize(int32_t T, int32_t K, lora_dtype_t dt, const void* x, int64_t ld_x, uint8_t* codes,
-                     int64_t ld_codes, float* scales, cudaStream_t stream);
+cudaError_t launch_quantize(int32_t T, int32_t K, lora_dtype_t dt, const void* x, int64_t ld_x, uint8_t* codes,
+                            int64_t ld_codes, float* scales, cudaStream_t stream);
 
 }  // namespace lora

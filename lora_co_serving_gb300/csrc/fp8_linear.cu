@@ -9,6 +9,7 @@
 
 #include <algorithm>
 #include <string>
+#include <type_traits>
 
 #include "fp8.h"
 #include "tc_kernel.h"
@@ -20,6 +21,15 @@ namespace {
 // The wait without a call: a kernel that calls a function cannot move registers between its warps (setmaxnreg)
 __device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
     return mbar_try_wait(bar, parity) || wait_phase_loop(bar, parity, abort_flag, status, 0);
+}
+
+// After a time-out: waits, with a limit of its own, for the loads of the last `stages` of `used` stages, so that none
+// lands in the shared memory of the SM's next CTA.
+__device__ __forceinline__ void drain_loads(uint32_t full, uint32_t used, int stages) {
+    const uint64_t t0 = global_timer(), limit = g_wait_limit_ns;
+    for (uint32_t u = used > (uint32_t)stages ? used - stages : 0; u < used; ++u)
+        while (!mbar_try_wait(full + u % stages * 8, (u / stages) & 1u))
+            if (global_timer() - t0 > limit) return;
 }
 
 // kind::f8f6f4: e4m3 A and B, fp32 accumulator, both operands K-major
@@ -66,6 +76,11 @@ __device__ __forceinline__ uint64_t both(float s) {
     asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "r"(__float_as_uint(s)));
     return r;
 }
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(__float_as_uint(lo)), "r"(__float_as_uint(hi)));
+    return r;
+}
 __device__ __forceinline__ float2 halves(uint64_t a) {
     uint32_t lo, hi;
     asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(a));
@@ -86,7 +101,8 @@ __device__ __forceinline__ float2 halves(uint64_t a) {
 // whose 128 sums must not spill, take 56 more: 128 * 56 + 256 * 224 = 64512.
 // =============================================================================================================
 constexpr int kPM = 256, kPN = 256;                      // rows of x and outputs of a cluster's tile
-constexpr int kXBytes = 128 * kQBlock;                   // a CTA's rows of x, one block of columns
+constexpr int kOperandBytes = 128 * kQBlock;             // 128 rows of x or w, one block of columns
+constexpr int kXBytes = kOperandBytes;                   // a CTA's rows of x
 constexpr int kWBytes = kPN * kQBlock;                   // the tile's rows of w
 constexpr int kStageBytes = kXBytes + kWBytes;
 constexpr int kStages = 4;
@@ -113,8 +129,8 @@ struct TileParams {
     int32_t n_whole, n_split;  // tiles [0, n_whole) are whole; each of the others is cut into n_split pieces of its
     int32_t n_items;           //   blocks, whose sums go to `part` and are added up by linear_join_kernel
     float* part;
-    int32_t* status;
-};
+    int32_t* status;           // cleared by the first CTA as it starts: a wait that runs out records that a millisecond
+};                             //   later at the soonest
 
 // Item i of the grid's list: a tile, and the blocks [kb0, kb1) of it
 struct Item {
@@ -164,18 +180,23 @@ struct Bars {
 
 __device__ __forceinline__ void tile_load(const TileParams& P, const Bars& B, uint8_t* smem, uint32_t rank) {
     Ring ring;
+    uint32_t used = 0;
     for (int i = blockIdx.x / 2; i < P.n_items; i += gridDim.x / 2) {
         const Item it = item_at(P, i);
         const int row_x = it.tm * kPM + 128 * (int)rank, row_w = it.tn * kPN + 128 * (int)rank;
         for (int kb = it.kb0; kb < it.kb1; ++kb) {
             // free in both CTAs: the half of w goes to both
-            if (!wait_here(B.empty + ring.stage * 8, ring.phase ^ 1u, B.abort_flag, P.status)) return;
+            if (!wait_here(B.empty + ring.stage * 8, ring.phase ^ 1u, B.abort_flag, P.status)) {
+                drain_loads(B.full, used, kStages);
+                return;
+            }
             const uint32_t full = B.full + ring.stage * 8;
             mbar_expect_tx(full, kStageBytes);
             const uint32_t sa = smem_u32(smem + ring.stage * kStageBytes);
             tma_load_2d(sa, &P.tm_x, kb * kQBlock, row_x, full);
             tma_load_2d_both(sa + kXBytes + rank * (kWBytes / 2), &P.tm_w, kb * kQBlock, row_w, full);
             ring.next();
+            ++used;
         }
     }
     // the peer's last commits arrive on this CTA's barriers: none may be under way when the CTA ends
@@ -356,6 +377,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t rank = cluster_ctarank();
 
     if (threadIdx.x == 0) {
+        if (blockIdx.x == 0) *P.status = 0;
         for (int s = 0; s < kStages; ++s) {
             mbar_init(B.full + s * 8, 3);            // the arm + the bytes of both CTAs' loads; warps 2 and 3
             mbar_init(B.empty + s * 8, 2);           // both CTAs' commits
@@ -423,6 +445,271 @@ constexpr size_t kTileSmem = (size_t)kStages * kStageBytes + kAddWarps * kOutByt
                              kScaleSlots * kScaleFloats * 4 + (kBars + 1) * 8 + 1024;
 static_assert(kTileSmem <= 227 * 1024, "shared memory of a CTA");
 
+// =============================================================================================================
+// Few rows (decode): 128 rows of w by all rows of x, K cut over a cluster.
+//
+// Here the weight's bytes are the work, so w's rows are the MMA's M (128 outputs a CTA) and x's rows its N, padded to
+// NT: a product costs few tensor cycles and the sums of all NT rows of x stay in one thread per output.  K is cut over
+// the CTAs of a cluster, each with its own stages in flight, and their sums meet through distributed shared memory,
+// added in rank order.  An x of 16 rows or fewer is quantized on the way, by each CTA for its own K range (the
+// rows are read from L2 once per 128 outputs), which saves a launch; more rows come quantized.
+//
+// 256 threads: warp 0 loads (TMA), warp 1 issues, warps 2 and 3 bring the scales (and quantize), warps 4..7 scale and
+// add: each thread has one output.
+// =============================================================================================================
+constexpr int kRThreads = 256;
+constexpr int kMaxCluster = 8;
+template <int NT>
+struct RowsCfg {
+    static constexpr int kStageB = kOperandBytes + NT * kQBlock;
+#ifndef FP8_RSTAGES
+#define FP8_RSTAGES 4
+#endif
+    static constexpr int kStages = FP8_RSTAGES;
+    static constexpr int kSlots = 8;                       // blocks whose scales are at hand
+    static constexpr int kSlotFloats = NT + 4;             // rows of x, one block of w's rows
+    static constexpr uint32_t kCols = 2 * NT;              // two accumulators
+    static constexpr size_t kSmem = (size_t)kStages * kStageB + kSlots * kSlotFloats * 4 + (2 * kStages + 5) * 8 + 1024;
+    static_assert(kSlots >= kStages + 2, "a slot would be overwritten while it is read");
+    static_assert(NT * 128 * 4 <= kStages * kStageB, "the sums must fit the stages");
+    // CTAs that share an SM must find their accumulators free (allocation waits, and a cluster's CTAs wait for one
+    // another): as many as fit the shared memory fit the 512 columns
+    static_assert((227 * 1024 / kSmem) * kCols <= 512, "accumulators of the CTAs on one SM");
+};
+
+struct RowsParams {
+    CUtensorMap tm_w, tm_x;        // tm_x: quantized x
+    const void* x;                 // else x itself, ld_x elements apart
+    int64_t ld_x;
+    const float* xs;
+    const float* ws;
+    __nv_bfloat16* y;
+    int64_t ld_y;
+    int32_t T, K, N, nb;
+    int32_t* status;
+};
+
+template <int NT>
+struct RowsRing {
+    int stage = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++stage == RowsCfg<NT>::kStages) { stage = 0; phase ^= 1u; }
+    }
+};
+
+// Quantizes block kb of x's NT rows into a stage (rows of 128 bytes, 16-byte pieces swizzled as the MMA reads them) and
+// its scales into a slot; two warps share the rows, two rows of a warp at a time
+template <int NT, class Row8>
+struct RowsQuant {
+    static constexpr int kSteps = NT / 4;
+    Row8 r[kSteps];
+    __device__ __forceinline__ void load(const RowsParams& P, int kb, int which, int lane) {
+        const int col = kb * kQBlock + lane % kLanesPerBlock * 8;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int t = 2 * (2 * i + which) + lane / kLanesPerBlock;
+            r[i].zero();
+            if (t < P.T && col < P.K) r[i].load(P.x, t * P.ld_x + col);
+        }
+    }
+    __device__ __forceinline__ void store(uint8_t* stage, float* slot, int which, int lane) const {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int t = 2 * (2 * i + which) + lane / kLanesPerBlock, c = lane % kLanesPerBlock;
+            float v[8], inv;
+            r[i].get(v);
+            const float sc = block_scale(max_over_block(abs_bits_max(v)), &inv);
+            *reinterpret_cast<uint2*>(stage + t * 128 + (((c >> 1) ^ (t & 7)) * 16) + (c & 1) * 8) = encode8(v, inv);
+            if (c == 0) slot[t] = sc;
+        }
+    }
+};
+
+// Row8: the type of an x that is quantized here, void for one that comes in 8 bits
+template <int NT, class Row8>
+__global__ void __launch_bounds__(kRThreads) linear_rows_kernel(const __grid_constant__ RowsParams P) {
+    using C = RowsCfg<NT>;
+    constexpr bool kQuant = !std::is_same<Row8, void>::value;
+    extern __shared__ uint8_t dsmem[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
+    float* slots = reinterpret_cast<float*>(smem + C::kStages * C::kStageB);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(slots + C::kSlots * C::kSlotFloats);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * C::kStages + 4);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const uint32_t full = smem_u32(bars), empty = full + C::kStages * 8, tfull = empty + C::kStages * 8,
+                   tempty = tfull + 16;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    uint32_t n_ranks;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n_ranks));
+    const uint32_t rank = cluster_ctarank();
+    const int n0 = (int)(blockIdx.x / n_ranks) * 128;
+    const int kb0 = (int)((int64_t)P.nb * rank / n_ranks), kb1 = (int)((int64_t)P.nb * (rank + 1) / n_ranks);
+
+    if (threadIdx.x == 0) {
+        if (blockIdx.x == 0) *P.status = 0;      // see TileParams::status
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(full + s * 8, 3);          // the arm and its bytes; warps 2 and 3
+            mbar_init(empty + s * 8, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull + b * 8, 1);
+            mbar_init(tempty + b * 8, 4);
+        }
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(C::kCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    grid_dep_wait();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            RowsRing<NT> ring;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!wait_phase(empty + ring.stage * 8, ring.phase ^ 1u, abort_flag, P.status)) {
+                    drain_loads(full, kb - kb0, C::kStages);
+                    break;
+                }
+                const uint32_t bar = full + ring.stage * 8, sa = smem_u32(smem + ring.stage * C::kStageB);
+                mbar_expect_tx(bar, kQuant ? kOperandBytes : C::kStageB);
+                tma_load_2d(sa, &P.tm_w, kb * kQBlock, n0, bar);
+                if constexpr (!kQuant) tma_load_2d(sa + kOperandBytes, &P.tm_x, kb * kQBlock, 0, bar);
+                ring.next();
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            RowsRing<NT> ring;
+            for (int kb = kb0, use = 0; kb < kb1; ++kb, ++use) {
+                const uint32_t acc = use & 1u;
+                if (!wait_phase(full + ring.stage * 8, ring.phase, abort_flag, P.status)) break;
+                if (!wait_phase(tempty + acc * 8, ((use >> 1) & 1u) ^ 1u, abort_flag, P.status)) break;
+                tc_fence_after();
+                const uint32_t sa = smem_u32(smem + ring.stage * C::kStageB), sb = sa + kOperandBytes;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_e4m3(tmem + acc * NT, smem_desc(sa + k * 32, 16, 1024), smem_desc(sb + k * 32, 16, 1024),
+                             instr_desc_e4m3(128, NT), k > 0);
+                mma_commit(empty + ring.stage * 8);
+                mma_commit(tfull + acc * 8);
+                ring.next();
+            }
+        }
+    } else if (warp < 4) {
+        const int which = warp - 2;
+        RowsRing<NT> ring;
+        const float* ws = P.ws + (int64_t)(n0 / kQBlock) * P.nb;
+        if constexpr (kQuant) {
+            RowsQuant<NT, Row8> q;
+            q.load(P, kb0, which, lane);
+            float w = ws[min(kb0, P.nb - 1)];
+            for (int kb = kb0, use = 0; kb < kb1; ++kb, ++use) {
+                const RowsQuant<NT, Row8> now = q;
+                const float w_now = w;
+                if (kb + 1 < kb1) {
+                    q.load(P, kb + 1, which, lane);
+                    w = ws[kb + 1];
+                }
+                const bool ok = wait_phase(empty + ring.stage * 8, ring.phase ^ 1u, abort_flag, P.status);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                float* slot = slots + use % C::kSlots * C::kSlotFloats;
+                now.store(smem + ring.stage * C::kStageB + kOperandBytes, slot, which, lane);
+                if (which == 0 && lane == 0) slot[NT] = w_now;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");     // the MMA reads what was stored
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full + ring.stage * 8);
+                ring.next();
+            }
+        } else {
+            // rows of x that do not exist have codes of zero (TMA) and the last row's scale
+            const int t = (NT == 64 ? 32 * which : 0) + lane;
+            const float* xs = P.xs + (int64_t)min(t, P.T - 1) * P.nb;
+            for (int kb = kb0, use = 0; kb < kb1; ++kb, ++use) {
+                const float a = xs[kb], w = ws[kb];
+                const bool ok = wait_phase(empty + ring.stage * 8, ring.phase ^ 1u, abort_flag, P.status);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                float* slot = slots + use % C::kSlots * C::kSlotFloats;
+                if (NT == 64 || (which == 0 && lane < NT)) slot[t] = a;
+                if (which == 0 && lane == 0) slot[NT] = w;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full + ring.stage * 8);
+                ring.next();
+            }
+        }
+    } else {
+        const int quarter = warp & 3;
+        const uint32_t taddr0 = tmem + ((uint32_t)(quarter * 32) << 16);
+        uint64_t acc[NT / 2];
+#pragma unroll
+        for (int j = 0; j < NT / 2; ++j) acc[j] = 0;
+        for (int kb = kb0, use = 0; kb < kb1; ++kb, ++use) {
+            const uint32_t buf = use & 1u;
+            wait_phase(tfull + buf * 8, (use >> 1) & 1u, abort_flag, P.status);    // after a time-out: on to the end
+            __syncwarp();
+            tc_fence_after();
+            const float* s = slots + use % C::kSlots * C::kSlotFloats;
+            const float w = s[NT];
+#pragma unroll
+            for (int c = 0; c < NT / 16; ++c) {
+                uint32_t d[16];
+                tmem_ld16(taddr0 + buf * NT + 16 * c, d);
+                float4 f[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) f[q] = *reinterpret_cast<const float4*>(s + 16 * c + 4 * q);
+                tmem_ld_wait();
+                if (c == NT / 16 - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(tempty + buf * 8);
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    fma2(acc[8 * c + 2 * q], d[4 * q], d[4 * q + 1], two(f[q].x * w, f[q].y * w));
+                    fma2(acc[8 * c + 2 * q + 1], d[4 * q + 2], d[4 * q + 3], two(f[q].z * w, f[q].w * w));
+                }
+            }
+        }
+        // every stage has been read: its memory takes the sums, [NT rows of x][128 outputs]
+        float* sums = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int j = 0; j < NT / 2; ++j) {
+            const float2 f = halves(acc[j]);
+            sums[(2 * j) * 128 + quarter * 32 + lane] = f.x;
+            sums[(2 * j + 1) * 128 + quarter * 32 + lane] = f.y;
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
+    // the cluster's CTAs share the rows of y out: each adds its rows' sums of all ranks, two outputs a thread
+    const int n = n0 + (threadIdx.x & 63) * 2;
+    for (int t = (int)rank + (int)n_ranks * (threadIdx.x / 64); t < P.T; t += (int)n_ranks * (kRThreads / 64)) {
+        const uint32_t at = smem_u32(smem) + (uint32_t)(t * 128 + (threadIdx.x & 63) * 2) * 4;
+        float2 v = make_float2(0.f, 0.f);
+        for (uint32_t r = 0; r < n_ranks; ++r) {
+            float a, b;
+            asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(a), "=f"(b) : "r"(mapa_shared(at, r)));
+            v.x += a;
+            v.y += b;
+        }
+        if (n < P.N) *reinterpret_cast<uint32_t*>(P.y + t * P.ld_y + n) = pack_bf16(v.x, v.y);
+    }
+    cluster_sync_all();                          // no CTA ends while another reads its sums
+}
+
 // --------------------------------------------------------------------------------------------------------- host
 // [rows, K] codes, rows ld bytes apart, as 128-byte swizzled boxes of {128 columns, box_rows}; past the end reads 0
 bool encode_codes(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uint64_t ld, uint32_t box_rows) {
@@ -464,14 +751,28 @@ cudaError_t device_info(Device** out) {
     Device& v = devs[d];
     if (!v.ready) {
         e = cudaDeviceGetAttribute(&v.sms, cudaDevAttrMultiProcessorCount, d);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(linear_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTileSmem);
+        auto allow = [&](auto kernel, size_t smem) {
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        };
+        allow(linear_tile_kernel, kTileSmem);
+        allow(linear_rows_kernel<16, Row8Bf16>, RowsCfg<16>::kSmem);
+        allow(linear_rows_kernel<16, Row8F32>, RowsCfg<16>::kSmem);
+        allow(linear_rows_kernel<16, void>, RowsCfg<16>::kSmem);
+        allow(linear_rows_kernel<32, void>, RowsCfg<32>::kSmem);
+        allow(linear_rows_kernel<64, void>, RowsCfg<64>::kSmem);
         if (e != cudaSuccess) return e;
         v.ready = true;
     }
     *out = &v;
     return cudaSuccess;
 }
+
+// Rows of x up to which a product runs on linear_rows_kernel, and up to which it quantizes them itself
+#ifndef FP8_MAX_ROWS
+#define FP8_MAX_ROWS 64
+#endif
+constexpr int kMaxRows = FP8_MAX_ROWS, kQuantRows = 16;
 
 // How the tiles are spread over the clusters.  Tiles beyond the last full round are cut along K, into as many pieces
 // as clusters are left for each: a round of 4 tiles would hold 72 of 76 clusters for a tile's whole time.  At most
@@ -483,7 +784,8 @@ struct Spread {
     int n_cut() const { return tiles_m * tiles_n - n_whole; }
 };
 Spread spread_of(int32_t T, int32_t K, int32_t N) {
-    Spread s;
+    Spread s{};
+    if (T <= kMaxRows) return s;
     s.tiles_m = (T + kPM - 1) / kPM;
     s.tiles_n = (N + kPN - 1) / kPN;
     const int tiles = s.tiles_m * s.tiles_n, rest = tiles % kClusters;
@@ -507,6 +809,36 @@ Scratch layout_of(int32_t T, int32_t K, bool x_fp8, const Spread& s) {
     L.end = L.part + (size_t)s.n_cut() * s.n_split * kPM * kPN * sizeof(float);
     return L;
 }
+// CTAs of a cluster that share a tile's K: while the launch has fewer than two CTAs per SM, as long as each keeps
+// kMinBlocks blocks
+#ifndef FP8_RTARGET
+#define FP8_RTARGET 152
+#endif
+int ranks_of(int32_t N, int32_t nb) {
+    const int tiles = (N + 127) / 128;
+    int r = 1;
+    while (r < kMaxCluster && tiles * r < FP8_RTARGET && nb / (2 * r) >= kMinBlocks) r *= 2;
+    return r;
+}
+
+template <int NT, class Row8>
+cudaError_t launch_rows(const RowsParams& P, int ranks, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((P.N + 127) / 128 * ranks));
+    cfg.blockDim = dim3(kRThreads);
+    cfg.dynamicSmemBytes = RowsCfg<NT>::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ranks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, linear_rows_kernel<NT, Row8>, P);
+}
+
 int check_sizes(const char* fn, int32_t T, int32_t K, int32_t N) {
     if (T < 0 || K <= 0 || N <= 0)
         return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": T must be >= 0, K and N > 0");
@@ -528,7 +860,7 @@ using namespace lora;
 
 extern "C" size_t lora_fp8_workspace_size(int32_t T, int32_t K, int32_t N, int32_t x_fp8) {
     if (check_sizes("lora_fp8_workspace_size", T, K, N) != LORA_OK) return 0;
-    return layout_of(T, K, x_fp8 != 0, spread_of(T, K, N)).end;
+    return layout_of(T, K, x_fp8 != 0 || T <= kQuantRows, spread_of(T, K, N)).end;
 }
 
 extern "C" int lora_fp8_linear(int32_t T, int32_t K, int32_t N, lora_dtype_t dt, const void* x, int64_t ld_x,
@@ -544,29 +876,59 @@ extern "C" int lora_fp8_linear(int32_t T, int32_t K, int32_t N, lora_dtype_t dt,
     if (rc != LORA_OK) return rc;
     if (!w_scales) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": w_scales is NULL");
     const Spread sp = spread_of(T, K, N);
-    const Scratch L = layout_of(T, K, x_scales != nullptr, sp);
+    const Scratch L = layout_of(T, K, x_scales != nullptr || T <= kQuantRows, sp);
     if (!workspace) return refuse(LORA_ERR_WORKSPACE, "workspace is NULL");
     if (!is_aligned(workspace, 256)) return refuse(LORA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
     if (ws_bytes < L.end)
         return refuse(LORA_ERR_WORKSPACE, "workspace too small: need " + std::to_string(L.end) + " bytes, got " +
                                               std::to_string(ws_bytes));
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    TileParams P{};
-    const void* xc = x_scales ? x : ws + L.codes;
-    if (!encode_codes(&P.tm_x, xc, K, T, x_scales ? ld_x : K, 128) || !encode_codes(&P.tm_w, w, K, N, K, 128) ||
-        !encode_y(&P.tm_y, y, N, T, ld_y))
-        return refuse(LORA_ERR_CUDA, std::string(fn) + ": cuTensorMapEncodeTiled failed");
     Device* dev = nullptr;
     cudaError_t e = device_info(&dev);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (e == cudaSuccess) e = cudaMemsetAsync(ws, 0, 256, st);
+    const bool quant_here = !x_scales && T <= kQuantRows;      // by the product's kernel
     if (e != cudaSuccess) return refuse(LORA_ERR_CUDA, std::string(fn) + ": " + cudaGetErrorString(e));
-    P.xs = x_scales;
-    if (!x_scales) {
-        float* sc = reinterpret_cast<float*>(ws + L.scales);
-        launch_quantize(T, K, dt, x, ld_x, ws + L.codes, K, sc, st);
-        P.xs = sc;
+    const void* xc = x;
+    const float* xs = x_scales;
+    int64_t ld_c = ld_x;
+    if (!x_scales && !quant_here) {
+        e = launch_quantize(T, K, dt, x, ld_x, ws + L.codes, K, reinterpret_cast<float*>(ws + L.scales), st);
+        if (e != cudaSuccess) return refuse(LORA_ERR_CUDA, std::string(fn) + ": " + cudaGetErrorString(e));
+        xc = ws + L.codes;
+        xs = reinterpret_cast<const float*>(ws + L.scales);
+        ld_c = K;
     }
+    if (T <= kMaxRows) {
+        RowsParams R{};
+        const int nt = T <= 16 ? 16 : T <= 32 ? 32 : 64;
+        if (!encode_codes(&R.tm_w, w, K, N, K, 128) || (!quant_here && !encode_codes(&R.tm_x, xc, K, T, ld_c, nt)))
+            return refuse(LORA_ERR_CUDA, std::string(fn) + ": cuTensorMapEncodeTiled failed");
+        R.x = x;
+        R.ld_x = ld_x;
+        R.xs = xs;
+        R.ws = w_scales;
+        R.y = static_cast<__nv_bfloat16*>(y);
+        R.ld_y = ld_y;
+        R.T = T;
+        R.K = K;
+        R.N = N;
+        R.nb = blocks_of(K);
+        R.status = reinterpret_cast<int32_t*>(ws);
+        const int ranks = ranks_of(N, R.nb);
+        if (quant_here)
+            e = dt == LORA_BF16 ? launch_rows<16, Row8Bf16>(R, ranks, st) : launch_rows<16, Row8F32>(R, ranks, st);
+        else
+            e = nt == 16   ? launch_rows<16, void>(R, ranks, st)
+                : nt == 32 ? launch_rows<32, void>(R, ranks, st)
+                           : launch_rows<64, void>(R, ranks, st);
+        if (e != cudaSuccess) return refuse(LORA_ERR_CUDA, std::string(fn) + ": " + cudaGetErrorString(e));
+        return LORA_OK;
+    }
+    TileParams P{};
+    if (!encode_codes(&P.tm_x, xc, K, T, ld_c, 128) || !encode_codes(&P.tm_w, w, K, N, K, 128) ||
+        !encode_y(&P.tm_y, y, N, T, ld_y))
+        return refuse(LORA_ERR_CUDA, std::string(fn) + ": cuTensorMapEncodeTiled failed");
+    P.xs = xs;
     P.ws = w_scales;
     P.T = T;
     P.N = N;

@@ -61,9 +61,9 @@ def test_linear(lib):
     assert f(x=None) == -1 and f(w=None) == -1 and f(ws=None) == -1 and f(y=None) == -1
     assert f(work=None) == -6 and f(work=WS + 64) == -6 and f(n=255) == -6
     assert "too small" in err(lib)
-    need = lib.lora_fp8_workspace_size(4, 64, 32, 0)
-    assert need >= 256 + 4 * 64 and f(n=need - 1) == -6
-    assert 256 <= lib.lora_fp8_workspace_size(4, 64, 32, 1) <= need
+    need = lib.lora_fp8_workspace_size(40, 64, 32, 0)
+    assert need >= 256 + 40 * 64 and f(T=40, n=need - 1) == -6       # x is quantized into the workspace
+    assert 256 <= lib.lora_fp8_workspace_size(40, 64, 32, 1) <= need
     assert lib.lora_fp8_workspace_size(0, 64, 32, 0) >= 256
     assert lib.lora_fp8_workspace_size(4, 60, 32, 0) == 0 and lib.lora_fp8_workspace_size(-1, 64, 32, 0) == 0
 
