@@ -137,6 +137,8 @@ __global__ void __launch_bounds__(kThreads) swiglu_forward_kernel(
     Shape s, const void* __restrict__ gu, int64_t ld_gu, void* __restrict__ h, int64_t ld_h,
     float* __restrict__ h_scales, uint8_t* __restrict__ ck_codes, float* __restrict__ ck_scales,
     const __grid_constant__ TrainRanges train) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    grid_dep_wait();
     const Place p(s, 1);
     const int row = p.row0;
     const bool in = p.in && row < s.rows;
@@ -185,6 +187,8 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(Shape s, cons
                                                                    const void* __restrict__ dh, int64_t ld_dh,
                                                                    void* __restrict__ dgu, int64_t ld_dgu,
                                                                    float* __restrict__ dgu_scales) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    grid_dep_wait();
     const Place p(s, 1);
     const int row = p.row0;
     const bool in = p.in && row < s.rows;
@@ -294,10 +298,8 @@ extern "C" int lora_fp8_quantize(int32_t T, int32_t K, lora_dtype_t dt, const vo
     if (rc == LORA_OK) rc = check_matrix(fn, "codes", codes, K, ld_codes, 1);
     if (rc != LORA_OK) return rc;
     if (!scales) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": scales is NULL");
-    const cudaError_t e = launch_quantize(T, K, dt, x, ld_x, static_cast<uint8_t*>(codes), ld_codes, scales,
-                                          static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return refuse(LORA_ERR_CUDA, std::string(fn) + ": " + cudaGetErrorString(e));
-    return LORA_OK;
+    return enqueued(fn, launch_quantize(T, K, dt, x, ld_x, static_cast<uint8_t*>(codes), ld_codes, scales,
+                                        static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" int lora_fp8_quantize_weight(int32_t N, int32_t K, lora_dtype_t dt, const void* W, int64_t ld_w,
@@ -319,7 +321,7 @@ extern "C" int lora_fp8_quantize_weight(int32_t N, int32_t K, lora_dtype_t dt, c
     else
         quantize_weight_kernel<Row8F32>
             <<<grid, kThreads, 0, st>>>(N, K, W, ld_w, static_cast<uint8_t*>(codes), scales);
-    return launched(fn);
+    return enqueued(fn, cudaGetLastError());
 }
 
 extern "C" int64_t lora_checkpoint_rows(int32_t T, const lora_segment_t* segs, int32_t n_segs) {
@@ -350,14 +352,15 @@ extern "C" int lora_swiglu_forward(int32_t T, int32_t I, lora_dtype_t dt, const 
     if (rc != LORA_OK) return rc;
     if (train.n > 0 && !ck_scales) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": ck_scales is NULL");
     const Shape s = shape_of(T, I);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
     auto go = [&](auto kernel) {
-        kernel<<<grid_of(s, 1), kThreads, 0, st>>>(s, gu, ld_gu, h, ld_h, h_scales, static_cast<uint8_t*>(ck_codes),
-                                                   ck_scales, train);
+        return launch_pdl(kernel, grid_of(s, 1), dim3(kThreads), 0, static_cast<cudaStream_t>(stream), s, gu, ld_gu, h,
+                          ld_h, h_scales, static_cast<uint8_t*>(ck_codes), ck_scales, train);
     };
-    if (dt == LORA_BF16) h_scales ? go(swiglu_forward_kernel<Row8Bf16, true>) : go(swiglu_forward_kernel<Row8Bf16, false>);
-    else h_scales ? go(swiglu_forward_kernel<Row8F32, true>) : go(swiglu_forward_kernel<Row8F32, false>);
-    return launched(fn);
+    if (dt == LORA_BF16)
+        return enqueued(fn, h_scales ? go(swiglu_forward_kernel<Row8Bf16, true>)
+                                     : go(swiglu_forward_kernel<Row8Bf16, false>));
+    return enqueued(fn, h_scales ? go(swiglu_forward_kernel<Row8F32, true>)
+                                 : go(swiglu_forward_kernel<Row8F32, false>));
 }
 
 extern "C" int lora_swiglu_backward(int32_t R, int32_t I, lora_dtype_t dt, const void* ck_codes,
@@ -377,12 +380,13 @@ extern "C" int lora_swiglu_backward(int32_t R, int32_t I, lora_dtype_t dt, const
     if (rc != LORA_OK) return rc;
     if (!ck_scales) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": ck_scales is NULL");
     const Shape s = shape_of(R, I);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
     auto go = [&](auto kernel) {
-        kernel<<<grid_of(s, 1), kThreads, 0, st>>>(s, static_cast<const uint8_t*>(ck_codes), ck_scales, dh, ld_dh, dgu,
-                                                   ld_dgu, dgu_scales);
+        return launch_pdl(kernel, grid_of(s, 1), dim3(kThreads), 0, static_cast<cudaStream_t>(stream), s,
+                          static_cast<const uint8_t*>(ck_codes), ck_scales, dh, ld_dh, dgu, ld_dgu, dgu_scales);
     };
-    if (dt == LORA_BF16) dgu_scales ? go(swiglu_backward_kernel<Row8Bf16, true>) : go(swiglu_backward_kernel<Row8Bf16, false>);
-    else dgu_scales ? go(swiglu_backward_kernel<Row8F32, true>) : go(swiglu_backward_kernel<Row8F32, false>);
-    return launched(fn);
+    if (dt == LORA_BF16)
+        return enqueued(fn, dgu_scales ? go(swiglu_backward_kernel<Row8Bf16, true>)
+                                       : go(swiglu_backward_kernel<Row8Bf16, false>));
+    return enqueued(fn, dgu_scales ? go(swiglu_backward_kernel<Row8F32, true>)
+                                   : go(swiglu_backward_kernel<Row8F32, false>));
 }

@@ -114,11 +114,10 @@ inline int refuse(int code, const std::string& msg) {
     set_last_error(msg.c_str());
     return code;
 }
-// after a launch
-inline int launched(const char* what) {
-    const cudaError_t e = cudaGetLastError();
+// the return code of a call that launched, or failed to
+inline int enqueued(const char* fn, cudaError_t e) {
     if (e == cudaSuccess) return LORA_OK;
-    return refuse(LORA_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+    return refuse(LORA_ERR_CUDA, std::string(fn) + ": " + cudaGetErrorString(e));
 }
 // matrix argument: non-null, 16-byte aligned, rows at least `cols` long and a multiple of 16 bytes apart
 inline int check_matrix(const char* fn, const char* name, const void* p, int64_t cols, int64_t ld, int esize) {

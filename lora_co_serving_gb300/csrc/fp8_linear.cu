@@ -887,13 +887,13 @@ extern "C" int lora_fp8_linear(int32_t T, int32_t K, int32_t N, lora_dtype_t dt,
     cudaError_t e = device_info(&dev);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool quant_here = !x_scales && T <= kQuantRows;      // by the product's kernel
-    if (e != cudaSuccess) return refuse(LORA_ERR_CUDA, std::string(fn) + ": " + cudaGetErrorString(e));
+    if (e != cudaSuccess) return enqueued(fn, e);
     const void* xc = x;
     const float* xs = x_scales;
     int64_t ld_c = ld_x;
     if (!x_scales && !quant_here) {
         e = launch_quantize(T, K, dt, x, ld_x, ws + L.codes, K, reinterpret_cast<float*>(ws + L.scales), st);
-        if (e != cudaSuccess) return refuse(LORA_ERR_CUDA, std::string(fn) + ": " + cudaGetErrorString(e));
+        if (e != cudaSuccess) return enqueued(fn, e);
         xc = ws + L.codes;
         xs = reinterpret_cast<const float*>(ws + L.scales);
         ld_c = K;
@@ -921,8 +921,7 @@ extern "C" int lora_fp8_linear(int32_t T, int32_t K, int32_t N, lora_dtype_t dt,
             e = nt == 16   ? launch_rows<16, void>(R, ranks, st)
                 : nt == 32 ? launch_rows<32, void>(R, ranks, st)
                            : launch_rows<64, void>(R, ranks, st);
-        if (e != cudaSuccess) return refuse(LORA_ERR_CUDA, std::string(fn) + ": " + cudaGetErrorString(e));
-        return LORA_OK;
+        return enqueued(fn, e);
     }
     TileParams P{};
     if (!encode_codes(&P.tm_x, xc, K, T, ld_c, 128) || !encode_codes(&P.tm_w, w, K, N, K, 128) ||
@@ -945,6 +944,5 @@ extern "C" int lora_fp8_linear(int32_t T, int32_t K, int32_t N, lora_dtype_t dt,
     if (e == cudaSuccess && sp.n_cut() > 0)
         e = launch_pdl(linear_join_kernel, dim3(32 * sp.n_cut()), dim3(256), 0, st, static_cast<const float*>(P.part),
                        static_cast<__nv_bfloat16*>(y), ld_y, T, N, sp.tiles_m, sp.tiles_n, sp.n_whole, sp.n_split);
-    if (e != cudaSuccess) return refuse(LORA_ERR_CUDA, std::string(fn) + ": " + cudaGetErrorString(e));
-    return LORA_OK;
+    return enqueued(fn, e);
 }

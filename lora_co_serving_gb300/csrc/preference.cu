@@ -9,9 +9,11 @@
 
 #include <algorithm>
 #include <string>
+#include <type_traits>
 
 #include "fp8.h"
 #include "lora_preference.h"
+#include "tc_prims.h"
 
 namespace lora {
 namespace {
@@ -19,7 +21,9 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLog2eHigh = 1.44268798828125f;        // log2(e) to 16 bits, and the rest of it
 constexpr float kLog2eLow = (float)(1.4426950408889634 - (double)kLog2eHigh);
-constexpr int kThreads = 256;
+constexpr float kLn2High = 0.693145751953125f;         // log(2) to 16 bits, and the rest
+constexpr float kLn2Low = (float)(0.6931471805599453 - (double)kLn2High);
+constexpr int kPairThreads = 256;
 
 // 2^x; 0 for x = -infinity, results below the smallest normal number are 0
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -28,37 +32,68 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-template <class T>
-__device__ __forceinline__ float to_float(T v);
-template <>
-__device__ __forceinline__ float to_float<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <class T>
-__device__ __forceinline__ T from_float(float v);
-template <>
-__device__ __forceinline__ float from_float<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-
-template <class T>
-struct Vec {                                   // 16 bytes of a row
-    static constexpr int kN = 16 / sizeof(T);
-    union {
-        uint4 q;
-        T e[kN];
-    };
-    __device__ __forceinline__ Vec() {}
+// Elements of a row, and 16-byte pieces of it
+struct Bf16 {
+    typedef __nv_bfloat16 T;
+    static constexpr int kN = 8;
+    static __device__ __forceinline__ float get(T v) { return __bfloat162float(v); }
+    static __device__ __forceinline__ T put(float v) { return __float2bfloat16_rn(v); }
+    static __device__ __forceinline__ uint4 lowest() {     // all -infinity
+        return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+    }
+    static __device__ __forceinline__ void unpack(const uint4& q, float (&x)[8]) {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+        return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+    }
+    template <int N>
+    static __device__ __forceinline__ float largest(const uint4 (&q)[N]) {
+        const __nv_bfloat162* v = reinterpret_cast<const __nv_bfloat162*>(q);
+        __nv_bfloat162 m = v[0];
+#pragma unroll
+        for (int i = 1; i < 4 * N; ++i) m = __hmax2(m, v[i]);
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+};
+struct F32 {
+    typedef float T;
+    static constexpr int kN = 4;
+    static __device__ __forceinline__ float get(T v) { return v; }
+    static __device__ __forceinline__ T put(float v) { return v; }
+    static __device__ __forceinline__ uint4 lowest() {
+        return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+    }
+    static __device__ __forceinline__ void unpack(const uint4& q, float (&x)[4]) {
+        x[0] = __uint_as_float(q.x); x[1] = __uint_as_float(q.y);
+        x[2] = __uint_as_float(q.z); x[3] = __uint_as_float(q.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    }
+    template <int N>
+    static __device__ __forceinline__ float largest(const uint4 (&q)[N]) {
+        const float* v = reinterpret_cast<const float*>(q);
+        float m = v[0];
+#pragma unroll
+        for (int i = 1; i < 4 * N; ++i) m = fmaxf(m, v[i]);
+        return m;
+    }
 };
 
 // Rows start anywhere (a row of odd length moves the next one off a 16-byte boundary): elements [0, head) come
 // before the first boundary, then `vecs` pieces of 16 bytes, then the rest.
-template <class T>
+template <class E>
 struct RowSpan {
     int head, vecs;
-    __device__ __forceinline__ RowSpan(const T* row, int V) {
-        head = min(V, (int)(((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / sizeof(T)));
-        vecs = (V - head) / Vec<T>::kN;
+    __device__ __forceinline__ RowSpan(const typename E::T* row, int V) {
+        head = min(V, (int)(((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / sizeof(typename E::T)));
+        vecs = (V - head) / E::kN;
     }
 };
 
@@ -77,72 +112,99 @@ struct ExpSum {
         s = s * weight(n, to) + s2 * weight(n2, to);
         n = to;
     }
-    template <int N>
-    __device__ __forceinline__ void add(const float (&x)[N]) {
-        float c = x[0];
-#pragma unroll
-        for (int i = 1; i < N; ++i) c = fmaxf(c, x[i]);
-        c = ceilf(c * kLog2e);
+    __device__ __forceinline__ void raise(float largest) {
+        const float c = ceilf(largest * kLog2e);
         if (c > n) {
             s *= weight(n, c);
             n = c;
         }
-        const float off = n == -INFINITY ? 0.f : -n;
-#pragma unroll
-        for (int i = 0; i < N; ++i) s += exp2_fast(fmaf(x[i], kLog2eLow, fmaf(x[i], kLog2eHigh, off)));
     }
-    // log of the sum, in 64 bits (once per row); NaN for a row without a finite logit
-    __device__ __forceinline__ double log() const {
-        return n == -INFINITY ? (double)NAN : (double)n * 0.6931471805599453 + ::log((double)s);
+    // the terms of some elements not above `raise`d ones, added pairwise: small terms are not lost to a large sum
+    template <int N>
+    __device__ __forceinline__ float terms(const float (&x)[N]) const {
+        const float off = n == -INFINITY ? 0.f : -n;
+        float e[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) e[i] = exp2_fast(fmaf(x[i], kLog2eLow, fmaf(x[i], kLog2eHigh, off)));
+#pragma unroll
+        for (int w = 1; w < N; w *= 2)
+#pragma unroll
+            for (int i = 0; i + w < N; i += 2 * w) e[i] += e[i + w];
+        return e[0];
     }
 };
 
-template <class T>
-__global__ void __launch_bounds__(kThreads) logprob_kernel(int32_t V, const T* __restrict__ logits, int64_t ld,
-                                                           const int64_t* __restrict__ labels,
+// One CTA of kThreads per row; each thread takes kAhead pieces of 16 bytes at a time.
+template <class E, int kThreads, int kAhead>
+__global__ void __launch_bounds__(kThreads) logprob_kernel(int32_t V, const typename E::T* __restrict__ logits,
+                                                           int64_t ld, const int64_t* __restrict__ labels,
                                                            float* __restrict__ logp, float* __restrict__ lse) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    grid_dep_wait();
     const int64_t t = blockIdx.x;
     const int64_t label = labels[t];
     if (label < 0) {
         if (threadIdx.x == 0) logp[t] = lse[t] = 0.f;
         return;
     }
-    const T* row = logits + t * ld;
-    const RowSpan<T> span(row, V);
+    const typename E::T* row = logits + t * ld;
+    const RowSpan<E> span(row, V);
     const uint4* q = reinterpret_cast<const uint4*>(row + span.head);
+    const float at = (threadIdx.x == 0 && label < V) ? E::get(row[label]) : NAN;
     ExpSum a;
-    for (int i = threadIdx.x; i < span.vecs; i += kThreads) {
-        Vec<T> v;
-        v.q = q[i];
-        float x[Vec<T>::kN];
+    for (int i0 = threadIdx.x; i0 < span.vecs; i0 += kThreads * kAhead) {
+        uint4 v[kAhead];
 #pragma unroll
-        for (int k = 0; k < Vec<T>::kN; ++k) x[k] = to_float(v.e[k]);
-        a.add(x);
+        for (int j = 0; j < kAhead; ++j) v[j] = i0 + j * kThreads < span.vecs ? q[i0 + j * kThreads] : E::lowest();
+        a.raise(E::largest(v));
+        float e[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            float x[E::kN];
+            E::unpack(v[j], x);
+            e[j] = a.terms(x);
+        }
+#pragma unroll
+        for (int w = 1; w < kAhead; w *= 2)
+#pragma unroll
+            for (int j = 0; j + w < kAhead; j += 2 * w) e[j] += e[j + w];
+        a.s += e[0];
     }
-    const int tail0 = span.head + span.vecs * Vec<T>::kN;
-    if ((int)threadIdx.x < span.head) {
-        const float x[1] = {to_float(row[threadIdx.x])};
-        a.add(x);
-    } else if (tail0 + (int)threadIdx.x - span.head < V) {
-        const float x[1] = {to_float(row[tail0 + threadIdx.x - span.head])};
-        a.add(x);
+    // head and tail: fewer than two pieces
+    const int loose = V - span.vecs * E::kN;
+    for (int i = threadIdx.x; i < loose; i += kThreads) {
+        const float x[1] = {E::get(row[i < span.head ? i : span.vecs * E::kN + i])};
+        a.raise(x[0]);
+        a.s += a.terms(x);
     }
-    __shared__ float sn[kThreads / 32], ss[kThreads / 32];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const float n2 = __shfl_xor_sync(0xffffffffu, a.n, o), s2 = __shfl_xor_sync(0xffffffffu, a.s, o);
         a.join(n2, s2);
     }
-    if (threadIdx.x % 32 == 0) {
-        sn[threadIdx.x / 32] = a.n;
-        ss[threadIdx.x / 32] = a.s;
+    if constexpr (kThreads > 32) {
+        constexpr int kWarps = kThreads / 32;
+        __shared__ float sn[kWarps], ss[kWarps];
+        if (threadIdx.x % 32 == 0) {
+            sn[threadIdx.x / 32] = a.n;
+            ss[threadIdx.x / 32] = a.s;
+        }
+        __syncthreads();
+        if (threadIdx.x >= 32) return;
+        a.n = threadIdx.x < kWarps ? sn[threadIdx.x] : -INFINITY;
+        a.s = threadIdx.x < kWarps ? ss[threadIdx.x] : 0.f;
+#pragma unroll
+        for (int o = kWarps / 2; o > 0; o >>= 1) {
+            const float n2 = __shfl_xor_sync(0xffffffffu, a.n, o), s2 = __shfl_xor_sync(0xffffffffu, a.s, o);
+            a.join(n2, s2);
+        }
     }
-    __syncthreads();
     if (threadIdx.x == 0) {
-        for (int w = 1; w < kThreads / 32; ++w) a.join(sn[w], ss[w]);
-        const double z = a.log();
-        lse[t] = (float)z;
-        logp[t] = label < V ? (float)((double)to_float(row[label]) - z) : NAN;
+        // log of the sum is n log(2) + log(s); x - lse is formed from its small parts, not from the rounded lse.  A row
+        // without a finite logit: NaN
+        const float r = logf(a.s) + a.n * kLn2Low;
+        lse[t] = a.n == -INFINITY ? NAN : fmaf(a.n, kLn2High, r);
+        logp[t] = a.n == -INFINITY ? NAN : fmaf(-a.n, kLn2High, at) - r;
     }
 }
 
@@ -168,93 +230,113 @@ __device__ __forceinline__ int sequence_of(const Sequences& s, int t) {
 __device__ double sum_block(double v, double* sh) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
     if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = v;
     __syncthreads();
     double r = 0.0;
-    for (int w = 0; w < kThreads / 32; ++w) r += sh[w];
+    for (int w = 0; w < kPairThreads / 32; ++w) r += sh[w];
     return r;
 }
 
-// One CTA per pair.  The differences lp - ref are small and their sums cancel: they are added up in 64 bits.
-__global__ void __launch_bounds__(kThreads) pair_loss_kernel(const __grid_constant__ Pairs pairs,
-                                                             const int64_t* __restrict__ labels,
-                                                             const float* __restrict__ logp,
-                                                             const float* __restrict__ ref, float beta, float eps,
-                                                             float* __restrict__ loss, float* __restrict__ rewards,
-                                                             float* __restrict__ coef) {
-    __shared__ double sh[kThreads / 32];
+// One CTA per pair.  The differences lp - ref are small and their sums cancel: they are added up in 64 bits.  The rest
+// is a few float32 operations (64-bit exponentials alone would take longer than the sums).
+__global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(const __grid_constant__ Pairs pairs,
+                                                                 const int64_t* __restrict__ labels,
+                                                                 const float* __restrict__ logp,
+                                                                 const float* __restrict__ ref, float beta, float eps,
+                                                                 float* __restrict__ loss, float* __restrict__ rewards,
+                                                                 float* __restrict__ coef) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    grid_dep_wait();
+    __shared__ double sh[2][kPairThreads / 32];
     const lora_pair_t p = pairs.p[blockIdx.x];
     double d[2];
     for (int side = 0; side < 2; ++side) {
         const int64_t t0 = side ? p.rejected_start : p.chosen_start;
         const int64_t t1 = t0 + (side ? p.rejected_len : p.chosen_len);
         double v = 0.0;
-        for (int64_t t = t0 + threadIdx.x; t < t1; t += kThreads)
+        for (int64_t t = t0 + threadIdx.x; t < t1; t += kPairThreads)
             if (labels[t] >= 0) v += (double)logp[t] - (double)ref[t];
-        d[side] = beta * sum_block(v, sh);
+        d[side] = beta * sum_block(v, sh[side]);
     }
     if (threadIdx.x != 0) return;
-    const double m = d[0] - d[1];
-    const double soft = log1p(exp(-fabs(m)));          // -log sig(m) = max(-m, 0) + log(1 + e^-|m|)
-    const double sig = 1.0 / (1.0 + exp(-m));
-    // a certain side (weight 0) does not meet the other's infinity
-    const double miss = (1.0 - (double)eps) * (fmax(-m, 0.0) + soft);
-    const double smooth = eps > 0.f ? (double)eps * (fmax(m, 0.0) + soft) : 0.0;
-    loss[blockIdx.x] = isnan(m) ? NAN : (float)(miss + smooth);
+    const float m = (float)(d[0] - d[1]);
+    const float e = expf(-fabsf(m)), soft = log1pf(e);     // -log sig(m) = max(-m, 0) + log(1 + e^-|m|)
+    const float small = e / (1.f + e), large = 1.f / (1.f + e);
+    const float sig = m >= 0.f ? large : small, sig_minus = m >= 0.f ? small : large;
+    // without smoothing an infinite m of the certain side adds nothing (0 times infinity)
+    const float smooth = eps > 0.f ? eps * (fmaxf(m, 0.f) + soft) : 0.f;
+    loss[blockIdx.x] = isnan(m) ? NAN : (1.f - eps) * (fmaxf(-m, 0.f) + soft) + smooth;
     rewards[2 * blockIdx.x] = (float)d[0];
     rewards[2 * blockIdx.x + 1] = (float)d[1];
-    // sig(-m) from its own exponential: 1 - sig(m) would lose it for large m
-    const double k = (double)beta * ((double)eps * sig - (1.0 - (double)eps) / (1.0 + exp(m)));
-    coef[2 * blockIdx.x] = (float)k;
-    coef[2 * blockIdx.x + 1] = (float)-k;
+    const float k = isnan(m) ? NAN : beta * (eps * sig - (1.f - eps) * sig_minus);
+    coef[2 * blockIdx.x] = k;
+    coef[2 * blockIdx.x + 1] = -k;
 }
 
-template <class T>
-__global__ void __launch_bounds__(kThreads) dlogits_kernel(int32_t V, const T* logits, int64_t ld,
+// One CTA per row, the last rows first: the forward has read them last, so L2 still holds them (logits of several
+// times its size: 100 MB of them).  What is written is not read again here and does not push them out (st.cs).
+template <class E, int kThreads, int kAhead>
+__global__ void __launch_bounds__(kThreads) dlogits_kernel(int32_t V, const typename E::T* logits, int64_t ld,
                                                            const int64_t* __restrict__ labels,
                                                            const float* __restrict__ lse,
                                                            const float* __restrict__ coef,
                                                            const __grid_constant__ Sequences seqs,
                                                            const float* __restrict__ dloss, float dloss_all,
-                                                           T* dlogits, int64_t ld_d) {
-    const int64_t t = blockIdx.x;
+                                                           typename E::T* dlogits, int64_t ld_d) {
+    grid_dep_wait();
+    const int64_t t = (int64_t)gridDim.x - 1 - blockIdx.x;
     const int64_t label = labels[t];
+    const typename E::T* row = logits + t * ld;
+    typename E::T* out = dlogits + t * ld_d;
+    const RowSpan<E> span(out, V);
     const int seq = label < 0 ? -1 : sequence_of(seqs, (int)t);
-    const T* row = logits + t * ld;
-    T* out = dlogits + t * ld_d;
-    float k = 0.f, off = 0.f;
-    if (seq >= 0) {
-        k = coef[seq] * (dloss ? dloss[seq / 2] : dloss_all);
-        if (label >= V) k = NAN;
-        off = -lse[t] * kLog2e;
+    if (seq < 0) {
+        uint4* o = reinterpret_cast<uint4*>(out + span.head);
+        for (int i = threadIdx.x; i < span.vecs; i += kThreads) __stcs(o + i, make_uint4(0, 0, 0, 0));
+        for (int i = threadIdx.x; i < V - span.vecs * E::kN; i += kThreads)
+            out[i < span.head ? i : span.vecs * E::kN + i] = E::put(0.f);
+        return;
     }
-    const int hit = label >= 0 && label < V ? (int)label : -1;
-    auto grad = [&](float x, int v) {
+    float k = coef[seq] * (dloss ? dloss[seq / 2] : dloss_all);
+    if (label >= V) k = NAN;
+    const float off = -lse[t] * kLog2e;
+    const int hit = label < V ? (int)label : -1;
+    auto grad = [&](float x, bool at) {
         const float p = exp2_fast(fmaf(x, kLog2e, off));
-        return k * ((v == hit ? 1.f : 0.f) - p);
+        return at ? k * (1.f - p) : -k * p;
     };
-    const RowSpan<T> span(out, V);
     // both rows on the same 16-byte phase: whole pieces; else element by element
     const bool whole = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
-    const int head = span.head, vecs = (whole || seq < 0) ? span.vecs : 0;
-    for (int i = threadIdx.x; i < vecs; i += kThreads) {
-        Vec<T> v;
-        const int e0 = head + i * Vec<T>::kN;
-        if (seq >= 0) {
-            v.q = *reinterpret_cast<const uint4*>(row + e0);
+    const int vecs = whole ? span.vecs : 0;
+    const uint4* q = reinterpret_cast<const uint4*>(row + span.head);
+    uint4* o = reinterpret_cast<uint4*>(out + span.head);
+    for (int i0 = threadIdx.x; i0 < vecs; i0 += kThreads * kAhead) {
+        uint4 v[kAhead];
 #pragma unroll
-            for (int j = 0; j < Vec<T>::kN; ++j) v.e[j] = from_float<T>(grad(to_float(v.e[j]), e0 + j));
-        } else {
-            v.q = make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < kAhead; ++j)
+            if (i0 + j * kThreads < vecs) v[j] = __ldcs(q + i0 + j * kThreads);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j * kThreads;
+            if (i >= vecs) break;
+            float x[E::kN];
+            E::unpack(v[j], x);
+            const int in = hit - (span.head + i * E::kN);      // the label's place in this piece, if it is in it
+            if ((unsigned)in < (unsigned)E::kN) {
+#pragma unroll
+                for (int c = 0; c < E::kN; ++c) x[c] = grad(x[c], c == in);
+            } else {
+#pragma unroll
+                for (int c = 0; c < E::kN; ++c) x[c] = grad(x[c], false);
+            }
+            __stcs(o + i, E::pack(x));
         }
-        *reinterpret_cast<uint4*>(out + e0) = v.q;
     }
-    const int tail0 = vecs > 0 ? head + vecs * Vec<T>::kN : 0;
-    if (vecs > 0 && (int)threadIdx.x < head)
-        out[threadIdx.x] = from_float<T>(seq >= 0 ? grad(to_float(row[threadIdx.x]), threadIdx.x) : 0.f);
-    for (int v = tail0 + threadIdx.x; v < V; v += kThreads)
-        out[v] = from_float<T>(seq >= 0 ? grad(to_float(row[v]), v) : 0.f);
+    const int head = vecs > 0 ? span.head : 0;
+    for (int i = threadIdx.x; i < V - vecs * E::kN; i += kThreads) {
+        const int v = i < head ? i : vecs * E::kN + i;
+        out[v] = E::put(grad(E::get(row[v]), v == hit));
+    }
 }
 
 int check_logits(const char* fn, int32_t T, int32_t V, lora_dtype_t dt, const void* logits, int64_t ld,
@@ -300,12 +382,36 @@ int check_pairs(const char* fn, int32_t T, const lora_pair_t* pairs, int32_t n_p
     return LORA_OK;
 }
 
-void launch_logprob(int32_t T, int32_t V, lora_dtype_t dt, const void* logits, int64_t ld, const int64_t* labels,
-                    float* logp, float* lse, cudaStream_t st) {
-    if (dt == LORA_BF16)
-        logprob_kernel<<<T, kThreads, 0, st>>>(V, static_cast<const __nv_bfloat16*>(logits), ld, labels, logp, lse);
-    else
-        logprob_kernel<<<T, kThreads, 0, st>>>(V, static_cast<const float*>(logits), ld, labels, logp, lse);
+// Threads per row: a warp for rows of up to four pieces a lane; for a launch of few long rows, which leaves SMs idle,
+// 1024 (60 rows of 32000: 256 threads a row take 1.9 times as long); else 256.
+template <class E, class Go>
+cudaError_t by_row_size(int32_t T, int32_t V, Go go) {
+    const int vecs = V / E::kN;
+    if (vecs <= 128) return go(std::integral_constant<int, 32>());
+    if (T <= 304 && vecs >= 1024) return go(std::integral_constant<int, 1024>());
+    return go(std::integral_constant<int, 256>());
+}
+
+template <class E>
+cudaError_t launch_logprob(int32_t T, int32_t V, const void* logits, int64_t ld, const int64_t* labels, float* logp,
+                           float* lse, cudaStream_t st) {
+    return by_row_size<E>(T, V, [&](auto threads) {
+        constexpr int kThreads = decltype(threads)::value;
+        return launch_pdl(logprob_kernel<E, kThreads, 4>, dim3(T), dim3(kThreads), 0, st, V,
+                          static_cast<const typename E::T*>(logits), ld, labels, logp, lse);
+    });
+}
+
+template <class E>
+cudaError_t launch_dlogits(int32_t T, int32_t V, const void* logits, int64_t ld, const int64_t* labels,
+                           const float* lse, const float* coef, const Sequences& seqs, const float* dloss, float all,
+                           void* dlogits, int64_t ld_d, cudaStream_t st) {
+    return by_row_size<E>(T, V, [&](auto threads) {
+        constexpr int kThreads = decltype(threads)::value;
+        return launch_pdl(dlogits_kernel<E, kThreads, 4>, dim3(T), dim3(kThreads), 0, st, V,
+                          static_cast<const typename E::T*>(logits), ld, labels, lse, coef, seqs, dloss, all,
+                          static_cast<typename E::T*>(dlogits), ld_d);
+    });
 }
 
 }  // namespace
@@ -319,8 +425,9 @@ extern "C" int lora_token_logprob(int32_t T, int32_t V, lora_dtype_t dt, const v
     const int rc = check_logits(fn, T, V, dt, logits, ld, labels);
     if (rc != LORA_OK || T == 0) return rc;
     if (!logp || !lse) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": logp or lse is NULL");
-    launch_logprob(T, V, dt, logits, ld, labels, logp, lse, static_cast<cudaStream_t>(stream));
-    return launched(fn);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return enqueued(fn, dt == LORA_BF16 ? launch_logprob<Bf16>(T, V, logits, ld, labels, logp, lse, st)
+                                        : launch_logprob<F32>(T, V, logits, ld, labels, logp, lse, st));
 }
 
 extern "C" int lora_preference_forward(int32_t T, int32_t V, lora_dtype_t dt, const void* logits, int64_t ld,
@@ -342,14 +449,17 @@ extern "C" int lora_preference_forward(int32_t T, int32_t V, lora_dtype_t dt, co
         return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": loss, rewards or coef is NULL");
     if (T == 0 && n_pairs == 0) return LORA_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (T > 0) launch_logprob(T, V, dt, logits, ld, labels, logp, lse, st);
-    if (n_pairs > 0) {
-        Pairs p{};
+    cudaError_t e = cudaSuccess;
+    if (T > 0)
+        e = dt == LORA_BF16 ? launch_logprob<Bf16>(T, V, logits, ld, labels, logp, lse, st)
+                            : launch_logprob<F32>(T, V, logits, ld, labels, logp, lse, st);
+    if (e == cudaSuccess && n_pairs > 0) {
+        Pairs p;                                 // the first n_pairs are read
         std::copy(pairs, pairs + n_pairs, p.p);
-        pair_loss_kernel<<<n_pairs, kThreads, 0, st>>>(p, labels, logp, ref_logp, beta, label_smoothing, loss, rewards,
-                                                       coef);
+        e = launch_pdl(pair_loss_kernel, dim3(n_pairs), dim3(kPairThreads), 0, st, p, labels,
+                       static_cast<const float*>(logp), ref_logp, beta, label_smoothing, loss, rewards, coef);
     }
-    return launched(fn);
+    return enqueued(fn, e);
 }
 
 extern "C" int lora_preference_backward(int32_t T, int32_t V, lora_dtype_t dt, const void* logits, int64_t ld,
@@ -371,11 +481,8 @@ extern "C" int lora_preference_backward(int32_t T, int32_t V, lora_dtype_t dt, c
         return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": in place, ld_d must be ld");
     const float all = n_pairs > 0 ? 1.f / (float)n_pairs : 0.f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dt == LORA_BF16)
-        dlogits_kernel<<<T, kThreads, 0, st>>>(V, static_cast<const __nv_bfloat16*>(logits), ld, labels, lse, coef,
-                                               seqs, dloss, all, static_cast<__nv_bfloat16*>(dlogits), ld_d);
-    else
-        dlogits_kernel<<<T, kThreads, 0, st>>>(V, static_cast<const float*>(logits), ld, labels, lse, coef, seqs,
-                                               dloss, all, static_cast<float*>(dlogits), ld_d);
-    return launched(fn);
+    return enqueued(fn, dt == LORA_BF16 ? launch_dlogits<Bf16>(T, V, logits, ld, labels, lse, coef, seqs, dloss, all,
+                                                               dlogits, ld_d, st)
+                                        : launch_dlogits<F32>(T, V, logits, ld, labels, lse, coef, seqs, dloss, all,
+                                                              dlogits, ld_d, st));
 }
