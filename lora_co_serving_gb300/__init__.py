@@ -752,12 +752,13 @@ def preference_forward(logits, labels, ref_logp, pairs, beta=0.1, label_smoothin
     _vector(ref_logp, "ref_logp", torch.float32, T)
     p = _pairs(pairs)
     n = p.shape[0]
-    logp, lse = torch.empty((2, T), dtype=torch.float32, device=logits.device).unbind(0)
-    rewards, coef = torch.empty((2, n, 2), dtype=torch.float32, device=logits.device).unbind(0)
-    loss = torch.empty(n, dtype=torch.float32, device=logits.device)
-    _check(library().lora_preference_forward(T, V, code, _ptr(logits), ld, _ptr(labels), _ptr(ref_logp), _ptr(p), n,
-                                             beta, label_smoothing, _ptr(loss), _ptr(rewards), _ptr(logp), _ptr(lse),
-                                             _ptr(coef), _stream_ptr(stream)))
+    logp, lse = torch.empty_like(ref_logp), torch.empty_like(ref_logp)
+    loss, rewards, coef = ref_logp.new_empty(n), ref_logp.new_empty((n, 2)), ref_logp.new_empty((n, 2))
+    rc = library().lora_preference_forward(T, V, code, logits.data_ptr(), ld, labels.data_ptr(), ref_logp.data_ptr(),
+                                           _ptr(p), n, beta, label_smoothing, loss.data_ptr(), rewards.data_ptr(),
+                                           logp.data_ptr(), lse.data_ptr(), coef.data_ptr(), _stream_ptr(stream))
+    if rc != 0:
+        _check(rc)
     return Preference(loss, rewards, logp, lse, coef)
 
 
