@@ -45,6 +45,11 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
 // arrive (when this CTA's issued MMAs complete) on the barrier at this offset in both CTAs of the cluster
 __device__ __forceinline__ void mma_commit_both(uint32_t bar) {
     const uint16_t mask = 3;
@@ -117,7 +122,7 @@ constexpr int kOutBytes = kOutBufs * kPieceBytes;        // of each adding warp
 constexpr int kScaleSlots = 8;                           // blocks whose scales are at hand (kStages + 2 are needed)
 constexpr int kScaleFloats = 132;                        // 128 rows of x, two blocks of w's rows, 8 bytes unused
 static_assert(kScaleSlots >= kStages + 2, "a slot would be overwritten while it is read");
-constexpr int kGroupM = 8;                               // tiles of x that share a sweep over w (see tile_at)
+constexpr int kGroupM = 16;                              // tiles of x that share a sweep over w (see tile_at)
 
 struct TileParams {
     CUtensorMap tm_x, tm_w, tm_y;
@@ -204,23 +209,33 @@ __device__ __forceinline__ void tile_load(const TileParams& P, const Bars& B, ui
         if (!wait_here(B.empty + ring.stage * 8, ring.phase ^ 1u, B.abort_flag, P.status)) return;
 }
 
+// The whole warp runs this loop, and one lane issues: what the MMAs take (descriptors, addresses) is then uniform over
+// the warp.  In a loop of one lane alone, issuing a block took 480 cycles, more than its MMAs.
 __device__ __forceinline__ void tile_issue(const TileParams& P, const Bars& B, uint8_t* smem, uint32_t tmem) {
+    const bool one = elect_one();
+    const uint64_t desc_x = smem_desc(smem_u32(smem), 16, 1024), desc_w = smem_desc(smem_u32(smem) + kXBytes, 16, 1024);
     Ring ring;
     uint32_t use = 0;                          // blocks so far: accumulator use & 1
     for (int i = blockIdx.x / 2; i < P.n_items; i += gridDim.x / 2) {
         const Item it = item_at(P, i);
         for (int kb = it.kb0; kb < it.kb1; ++kb, ++use) {
-            if (!wait_here(B.full + ring.stage * 8, ring.phase, B.abort_flag, P.status)) return;
-            const uint32_t sa = smem_u32(smem + ring.stage * kStageBytes), sb = sa + kXBytes;
             const uint32_t acc = use & 1u;
-            if (!wait_here(B.tempty + acc * 8, ((use >> 1) & 1u) ^ 1u, B.abort_flag, P.status)) return;
+            // after a time-out no wait holds any longer, here and in tile_add: the blocks are gone through to the end,
+            // their values lost
+            wait_here(B.full + ring.stage * 8, ring.phase, B.abort_flag, P.status);
+            wait_here(B.tempty + acc * 8, ((use >> 1) & 1u) ^ 1u, B.abort_flag, P.status);
+            __syncwarp();
             tc_fence_after();
+            const uint64_t at = (uint64_t)(ring.stage * (kStageBytes >> 4));
+            if (one) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                mma_e4m3(tmem + acc * kPN, smem_desc(sa + k * 32, 16, 1024), smem_desc(sb + k * 32, 16, 1024),
-                         instr_desc_e4m3(128, kPN), k > 0);
-            mma_commit_both(B.empty + ring.stage * 8);
-            mma_commit(B.tfull + acc * 8);
+                for (int k = 0; k < 4; ++k)
+                    mma_e4m3(tmem + acc * kPN, desc_x + at + 2 * k, desc_w + at + 2 * k, instr_desc_e4m3(128, kPN),
+                             k > 0);
+                mma_commit(B.tfull + acc * 8);
+                mma_commit_both(B.empty + ring.stage * 8);
+            }
+            __syncwarp();
             ring.next();
         }
     }
@@ -293,7 +308,6 @@ __device__ __forceinline__ void tile_add(const TileParams& P, const Bars& B, uin
         for (int j = 0; j < 64; ++j) acc[j] = 0;
         for (int kb = it.kb0; kb < it.kb1; ++kb, ++use) {
             const uint32_t buf = use & 1u;
-            // after a time-out no wait holds any longer: the tiles are gone through to the end, their values lost
             wait_here(B.tfull + buf * 8, (use >> 1) & 1u, B.abort_flag, P.status);
             __syncwarp();
             tc_fence_after();
@@ -403,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
         if (warp == 0 && lane == 0) tile_load(P, B, smem, rank);
-        if (warp == 1 && lane == 0) tile_issue(P, B, smem, tmem);
+        if (warp == 1) tile_issue(P, B, smem, tmem);
         if (warp >= 2) tile_scales(P, B, slots, rank, warp - 2, lane);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAddRegs));
