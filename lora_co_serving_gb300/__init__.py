@@ -628,8 +628,9 @@ def fp8_linear(x, w, w_scales, x_scales=None, y=None, workspace=None, stream=Non
         _matrix(x, "x", torch.float8_e4m3fn)
         _matrix(x_scales, "x_scales", torch.float32, T, _blocks(K), contiguous=True)
     if y is None:
-        y = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
-    ldy = _matrix(y, "y", torch.bfloat16, T, N)
+        y, ldy = torch.empty((T, N), dtype=torch.bfloat16, device=x.device), N
+    else:
+        ldy = _matrix(y, "y", torch.bfloat16, T, N)
     st = _stream_ptr(stream)
     if workspace is None:
         need = fp8_workspace_size(T, K, N, x_scales is not None)
@@ -677,16 +678,19 @@ def swiglu_forward(gu, segs=None, checkpoint=False, fp8_out=False, h=None, h_sca
         cs = torch.empty((R, 2 * _blocks(I)), dtype=torch.float32, device=gu.device)
     out = torch.float8_e4m3fn if fp8_out else gu.dtype
     if h is None:
-        h = torch.empty((T, I), dtype=out, device=gu.device)
-    ldh = _matrix(h, "h", out, T, I)
+        h, ldh = torch.empty((T, I), dtype=out, device=gu.device), I
+    else:
+        ldh = _matrix(h, "h", out, T, I)
     if fp8_out and h_scales is None:
         h_scales = torch.empty((T, _blocks(I)), dtype=torch.float32, device=gu.device)
     if fp8_out:
         _matrix(h_scales, "h_scales", torch.float32, T, _blocks(I), contiguous=True)
     keep = ck is not None and ck.numel() > 0
-    _check(library().lora_swiglu_forward(T, I, code, _ptr(gu), ld, _ptr(s), n_segs, _ptr(h), ldh,
-                                         _ptr(h_scales) if fp8_out else None, _ptr(ck) if keep else None,
-                                         _ptr(cs) if keep else None, _stream_ptr(stream)))
+    rc = library().lora_swiglu_forward(T, I, code, gu.data_ptr(), ld, _ptr(s), n_segs, h.data_ptr(), ldh,
+                                       h_scales.data_ptr() if fp8_out else None, ck.data_ptr() if keep else None,
+                                       cs.data_ptr() if keep else None, _stream_ptr(stream))
+    if rc != 0:
+        _check(rc)
     h = (h, h_scales) if fp8_out else h
     return (h, (ck, cs)) if checkpoint else h
 
@@ -702,14 +706,17 @@ def swiglu_backward(saved, dh, fp8_out=False, dgu=None, dgu_scales=None, stream=
     _matrix(cs, "the checkpoint's scales", torch.float32, R, 2 * _blocks(I), contiguous=True)
     out = torch.float8_e4m3fn if fp8_out else dh.dtype
     if dgu is None:
-        dgu = torch.empty((R, 2 * I), dtype=out, device=dh.device)
-    ldo = _matrix(dgu, "dgu", out, R, 2 * I)
+        dgu, ldo = torch.empty((R, 2 * I), dtype=out, device=dh.device), 2 * I
+    else:
+        ldo = _matrix(dgu, "dgu", out, R, 2 * I)
     if fp8_out and dgu_scales is None:
         dgu_scales = torch.empty((R, 2 * _blocks(I)), dtype=torch.float32, device=dh.device)
     if fp8_out:
         _matrix(dgu_scales, "dgu_scales", torch.float32, R, 2 * _blocks(I), contiguous=True)
-    _check(library().lora_swiglu_backward(R, I, code, _ptr(ck), _ptr(cs), _ptr(dh), ld, _ptr(dgu), ldo,
-                                          _ptr(dgu_scales) if fp8_out else None, _stream_ptr(stream)))
+    rc = library().lora_swiglu_backward(R, I, code, ck.data_ptr(), cs.data_ptr(), dh.data_ptr(), ld, dgu.data_ptr(), ldo,
+                                        dgu_scales.data_ptr() if fp8_out else None, _stream_ptr(stream))
+    if rc != 0:
+        _check(rc)
     return (dgu, dgu_scales) if fp8_out else dgu
 
 
@@ -752,14 +759,13 @@ def preference_forward(logits, labels, ref_logp, pairs, beta=0.1, label_smoothin
     _vector(ref_logp, "ref_logp", torch.float32, T)
     p = _pairs(pairs)
     n = p.shape[0]
-    logp, lse = torch.empty_like(ref_logp), torch.empty_like(ref_logp)
-    loss, rewards, coef = ref_logp.new_empty(n), ref_logp.new_empty((n, 2)), ref_logp.new_empty((n, 2))
+    logp, lse, loss, rewards, coef = ref_logp.new_empty(2 * T + 5 * n).split_with_sizes([T, T, n, 2 * n, 2 * n])
     rc = library().lora_preference_forward(T, V, code, logits.data_ptr(), ld, labels.data_ptr(), ref_logp.data_ptr(),
                                            _ptr(p), n, beta, label_smoothing, loss.data_ptr(), rewards.data_ptr(),
                                            logp.data_ptr(), lse.data_ptr(), coef.data_ptr(), _stream_ptr(stream))
     if rc != 0:
         _check(rc)
-    return Preference(loss, rewards, logp, lse, coef)
+    return Preference(loss, rewards.view(n, 2), logp, lse, coef.view(n, 2))
 
 
 def preference_backward(logits, labels, lse, coef, pairs, dloss=None, dlogits=None, stream=None):
@@ -778,8 +784,12 @@ def preference_backward(logits, labels, lse, coef, pairs, dloss=None, dlogits=No
     if dloss is not None:
         _vector(dloss, "dloss", torch.float32, n)
     if dlogits is None:
-        dlogits = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
-    ldd = _matrix(dlogits, "dlogits", logits.dtype, T, V)
-    _check(library().lora_preference_backward(T, V, code, _ptr(logits), ld, _ptr(labels), _ptr(lse), _ptr(coef),
-                                              _ptr(p), n, _ptr(dloss), _ptr(dlogits), ldd, _stream_ptr(stream)))
+        dlogits, ldd = torch.empty((T, V), dtype=logits.dtype, device=logits.device), V
+    else:
+        ldd = _matrix(dlogits, "dlogits", logits.dtype, T, V)
+    rc = library().lora_preference_backward(T, V, code, logits.data_ptr(), ld, labels.data_ptr(), lse.data_ptr(),
+                                            coef.data_ptr(), _ptr(p), n, _ptr(dloss), dlogits.data_ptr(), ldd,
+                                            _stream_ptr(stream))
+    if rc != 0:
+        _check(rc)
     return dlogits
