@@ -58,7 +58,7 @@ template <class Row8>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(Shape s, const void* __restrict__ x, int64_t ld_x,
                                                             uint8_t* __restrict__ codes, int64_t ld_codes,
                                                             float* __restrict__ scales) {
-    asm volatile("griddepcontrol.launch_dependents;");     // a product may set itself up meanwhile
+    grid_dep_launch();     // a product may set itself up meanwhile
     grid_dep_wait();
     const Place p(s, 1);
     const bool in = p.in && p.row0 < s.rows;
@@ -132,52 +132,63 @@ __device__ __forceinline__ int checkpoint_row(const TrainRanges& t, int row) {
 // 1 / (1 + e^-g).  e^-g overflows to infinity below g = -88: the quotient is then 0, as it should be.
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
 
+// Two rows a thread: 64 bytes in flight in each (one row: 162 us for the 8192 x 14336 step with 2048 rows kept, two:
+// 156 us, 95 % of the memory rate).
+constexpr int kForwardRows = 2;
+
 template <class Row8, bool H8>
 __global__ void __launch_bounds__(kThreads) swiglu_forward_kernel(
     Shape s, const void* __restrict__ gu, int64_t ld_gu, void* __restrict__ h, int64_t ld_h,
     float* __restrict__ h_scales, uint8_t* __restrict__ ck_codes, float* __restrict__ ck_scales,
     const __grid_constant__ TrainRanges train) {
-    asm volatile("griddepcontrol.launch_dependents;");
+    grid_dep_launch();
     grid_dep_wait();
-    const Place p(s, 1);
-    const int row = p.row0;
-    const bool in = p.in && row < s.rows;
-    Row8 rg, ru;
-    rg.zero();
-    ru.zero();
-    if (in) {
-        rg.load(gu, row * ld_gu + p.col);
-        ru.load(gu, row * ld_gu + s.cols + p.col);
-    }
-    float g[8], u[8], v[8];
-    rg.get(g);
-    ru.get(u);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = g[i] * sigmoid(g[i]) * u[i];
+    const Place p(s, kForwardRows);
     const bool lead = threadIdx.x % kLanesPerBlock == 0;
-    if constexpr (H8) {
-        float inv;
-        const float sc = block_scale(max_over_block(abs_bits_max(v)), &inv);
-        if (in) {
-            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(h) + row * ld_h + p.col) = encode8(v, inv);
-            if (lead) h_scales[(int64_t)row * s.n_blocks + p.block] = sc;
+    Row8 rg[kForwardRows], ru[kForwardRows];
+#pragma unroll
+    for (int k = 0; k < kForwardRows; ++k) {
+        const int row = p.row0 + k * p.row_step;
+        rg[k].zero();
+        ru[k].zero();
+        if (p.in && row < s.rows) {
+            rg[k].load(gu, row * ld_gu + p.col);
+            ru[k].load(gu, row * ld_gu + s.cols + p.col);
         }
-    } else {
-        if (in) Row8::store(h, row * ld_h + p.col, v);
     }
-    const int ck = (train.n > 0 && row < s.rows) ? checkpoint_row(train, row) : -1;
-    if (!__any_sync(0xffffffffu, ck >= 0)) return;
-    float inv_g, inv_u;
-    const float sg = block_scale(max_over_block(abs_bits_max(g)), &inv_g);
-    const float su = block_scale(max_over_block(abs_bits_max(u)), &inv_u);
-    if (!in || ck < 0) return;
-    uint8_t* c = ck_codes + (int64_t)ck * 2 * s.cols + p.col;
-    *reinterpret_cast<uint2*>(c) = encode8(g, inv_g);
-    *reinterpret_cast<uint2*>(c + s.cols) = encode8(u, inv_u);
-    if (lead) {
-        float* z = ck_scales + (int64_t)ck * 2 * s.n_blocks + p.block;
-        z[0] = sg;
-        z[s.n_blocks] = su;
+#pragma unroll
+    for (int k = 0; k < kForwardRows; ++k) {
+        const int row = p.row0 + k * p.row_step;
+        const bool in = p.in && row < s.rows;
+        float g[8], u[8], v[8];
+        rg[k].get(g);
+        ru[k].get(u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = g[i] * sigmoid(g[i]) * u[i];
+        if constexpr (H8) {
+            float inv;
+            const float sc = block_scale(max_over_block(abs_bits_max(v)), &inv);
+            if (in) {
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(h) + row * ld_h + p.col) = encode8(v, inv);
+                if (lead) h_scales[(int64_t)row * s.n_blocks + p.block] = sc;
+            }
+        } else {
+            if (in) Row8::store(h, row * ld_h + p.col, v);
+        }
+        const int ck = (train.n > 0 && row < s.rows) ? checkpoint_row(train, row) : -1;
+        if (!__any_sync(0xffffffffu, ck >= 0)) continue;
+        float inv_g, inv_u;
+        const float sg = block_scale(max_over_block(abs_bits_max(g)), &inv_g);
+        const float su = block_scale(max_over_block(abs_bits_max(u)), &inv_u);
+        if (!in || ck < 0) continue;
+        uint8_t* c = ck_codes + (int64_t)ck * 2 * s.cols + p.col;
+        *reinterpret_cast<uint2*>(c) = encode8(g, inv_g);
+        *reinterpret_cast<uint2*>(c + s.cols) = encode8(u, inv_u);
+        if (lead) {
+            float* z = ck_scales + (int64_t)ck * 2 * s.n_blocks + p.block;
+            z[0] = sg;
+            z[s.n_blocks] = su;
+        }
     }
 }
 
@@ -187,7 +198,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(Shape s, cons
                                                                    const void* __restrict__ dh, int64_t ld_dh,
                                                                    void* __restrict__ dgu, int64_t ld_dgu,
                                                                    float* __restrict__ dgu_scales) {
-    asm volatile("griddepcontrol.launch_dependents;");
+    grid_dep_launch();
     grid_dep_wait();
     const Place p(s, 1);
     const int row = p.row0;
@@ -353,7 +364,7 @@ extern "C" int lora_swiglu_forward(int32_t T, int32_t I, lora_dtype_t dt, const 
     if (train.n > 0 && !ck_scales) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": ck_scales is NULL");
     const Shape s = shape_of(T, I);
     auto go = [&](auto kernel) {
-        return launch_pdl(kernel, grid_of(s, 1), dim3(kThreads), 0, static_cast<cudaStream_t>(stream), s, gu, ld_gu, h,
+        return launch_pdl(kernel, grid_of(s, kForwardRows), dim3(kThreads), 0, static_cast<cudaStream_t>(stream), s, gu, ld_gu, h,
                           ld_h, h_scales, static_cast<uint8_t*>(ck_codes), ck_scales, train);
     };
     if (dt == LORA_BF16)

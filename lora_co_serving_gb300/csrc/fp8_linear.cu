@@ -134,7 +134,7 @@ struct TileParams {
     int32_t n_whole, n_split;  // tiles [0, n_whole) are whole; each of the others is cut into n_split pieces of its
     int32_t n_items;           //   blocks, whose sums go to `part` and are added up by linear_join_kernel
     float* part;
-    int32_t* status;           // cleared by the first CTA as it starts: a wait that runs out records that a millisecond
+    int32_t* status;           // cleared by the first CTA as it begins: a wait that runs out records that a millisecond
 };                             //   later at the soonest
 
 // Item i of the grid's list: a tile, and the blocks [kb0, kb1) of it
@@ -391,7 +391,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t rank = cluster_ctarank();
 
     if (threadIdx.x == 0) {
-        if (blockIdx.x == 0) *P.status = 0;
         for (int s = 0; s < kStages; ++s) {
             mbar_init(B.full + s * 8, 3);            // the arm + the bytes of both CTAs' loads; warps 2 and 3
             mbar_init(B.empty + s * 8, 2);           // both CTAs' commits
@@ -414,6 +413,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     grid_dep_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *P.status = 0;
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
         if (warp == 0 && lane == 0) tile_load(P, B, smem, rank);
@@ -561,7 +561,6 @@ __global__ void __launch_bounds__(kRThreads) linear_rows_kernel(const __grid_con
     const int kb0 = (int)((int64_t)P.nb * rank / n_ranks), kb1 = (int)((int64_t)P.nb * (rank + 1) / n_ranks);
 
     if (threadIdx.x == 0) {
-        if (blockIdx.x == 0) *P.status = 0;      // see TileParams::status
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(full + s * 8, 3);          // the arm and its bytes; warps 2 and 3
             mbar_init(empty + s * 8, 1);
@@ -584,7 +583,9 @@ __global__ void __launch_bounds__(kRThreads) linear_rows_kernel(const __grid_con
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    grid_dep_launch();
     grid_dep_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *P.status = 0;      // see TileParams::status
 
     if (warp == 0) {
         if (lane == 0) {
@@ -788,9 +789,12 @@ cudaError_t device_info(Device** out) {
 #endif
 constexpr int kMaxRows = FP8_MAX_ROWS, kQuantRows = 16;
 
-// How the tiles are spread over the clusters.  Tiles beyond the last full round are cut along K, into as many pieces
-// as clusters are left for each: a round of 4 tiles would hold 72 of 76 clusters for a tile's whole time.  At most
-// kMaxSplit pieces of at least kMinBlocks blocks: a piece's sums are written and read back (256 KB).
+// How the tiles are spread over the clusters.  Tiles beyond the last full round may be cut along K, into as many pieces
+// as clusters are left for each: a round of 4 tiles holds 72 of 76 clusters for a tile's whole time.  At most
+// kMaxSplit pieces of at least kMinBlocks blocks.  Cutting saves the blocks that run beside one another, 0.37 us each,
+// and costs the join: a second kernel, 3 us, and 0.04 us a piece for its sums (256 KB written and read back).  Measured
+// whole and cut: 1111 x 14336 x 4096 (4 tiles left, 8 pieces) 88 and 58 us, 65 x 2704 x 2704 (11, 5) 12.6 and 9.7 us;
+// the other way 256 x 4096 x 28672 (36, 2) 36.4 and 38.0 us, 600 x 2704 x 2704 (33, 2) 13.3 and 13.6 us.
 constexpr int kMaxSplit = 8, kMinBlocks = 4;
 constexpr int kClusters = 76;                            // planned for (152 SMs); right on any device
 struct Spread {
@@ -802,10 +806,13 @@ Spread spread_of(int32_t T, int32_t K, int32_t N) {
     if (T <= kMaxRows) return s;
     s.tiles_m = (T + kPM - 1) / kPM;
     s.tiles_n = (N + kPN - 1) / kPN;
-    const int tiles = s.tiles_m * s.tiles_n, rest = tiles % kClusters;
-    s.n_split = rest ? std::min({kClusters / rest, kMaxSplit, blocks_of(K) / kMinBlocks}) : 0;
-    if (s.n_split < 2) s.n_split = 0;
-    s.n_whole = s.n_split ? tiles - rest : tiles;
+    const int tiles = s.tiles_m * s.tiles_n, rest = tiles % kClusters, nb = blocks_of(K);
+    s.n_whole = tiles;
+    const int pieces = rest ? std::min({kClusters / rest, kMaxSplit, nb / kMinBlocks}) : 0;
+    if (pieces >= 2 && nb - (nb + pieces - 1) / pieces > 8 + rest * pieces / 9) {
+        s.n_split = pieces;
+        s.n_whole = tiles - rest;
+    }
     s.n_items = s.n_whole + s.n_cut() * s.n_split;
     return s;
 }

@@ -139,7 +139,7 @@ template <class E, int kThreads, int kAhead>
 __global__ void __launch_bounds__(kThreads) logprob_kernel(int32_t V, const typename E::T* __restrict__ logits,
                                                            int64_t ld, const int64_t* __restrict__ labels,
                                                            float* __restrict__ logp, float* __restrict__ lse) {
-    asm volatile("griddepcontrol.launch_dependents;");
+    grid_dep_launch();
     grid_dep_wait();
     const int64_t t = blockIdx.x;
     const int64_t label = labels[t];
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(const __grid_co
                                                                  const float* __restrict__ ref, float beta, float eps,
                                                                  float* __restrict__ loss, float* __restrict__ rewards,
                                                                  float* __restrict__ coef) {
-    asm volatile("griddepcontrol.launch_dependents;");
+    grid_dep_launch();
     grid_dep_wait();
     __shared__ double sh[2][kPairThreads / 32];
     const lora_pair_t p = pairs.p[blockIdx.x];

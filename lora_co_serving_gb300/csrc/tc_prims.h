@@ -116,6 +116,9 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
 // setup, TMEM allocation) while the previous one drains; this wait holds the CTA until every earlier kernel of the
 // stream has finished and its writes are visible, before anything it produced (or the caller's inputs) is read.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next kernel start once every CTA of this one has come here.  A kernel that allocates TMEM calls it after the
+// allocation: the next one's CTAs may hold TMEM of their own while they wait for this one to end.
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
