@@ -54,23 +54,32 @@ struct Place {
 };
 
 // ---------------------------------------------------------------------------------------------------- quantizers
+constexpr int kQuantRows = 2;      // rows a thread
+
 template <class Row8>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(Shape s, const void* __restrict__ x, int64_t ld_x,
                                                             uint8_t* __restrict__ codes, int64_t ld_codes,
                                                             float* __restrict__ scales) {
     grid_dep_launch();     // a product may set itself up meanwhile
     grid_dep_wait();
-    const Place p(s, 1);
-    const bool in = p.in && p.row0 < s.rows;
-    Row8 r;
-    r.zero();
-    if (in) r.load(x, p.row0 * ld_x + p.col);
-    float v[8], inv;
-    r.get(v);
-    const float sc = block_scale(max_over_block(abs_bits_max(v)), &inv);
-    if (!in) return;
-    *reinterpret_cast<uint2*>(codes + p.row0 * ld_codes + p.col) = encode8(v, inv);
-    if (threadIdx.x % kLanesPerBlock == 0) scales[(int64_t)p.row0 * s.n_blocks + p.block] = sc;
+    const Place p(s, kQuantRows);
+    Row8 r[kQuantRows];
+#pragma unroll
+    for (int k = 0; k < kQuantRows; ++k) {
+        const int row = p.row0 + k * p.row_step;
+        r[k].zero();
+        if (p.in && row < s.rows) r[k].load(x, row * ld_x + p.col);
+    }
+#pragma unroll
+    for (int k = 0; k < kQuantRows; ++k) {
+        const int row = p.row0 + k * p.row_step;
+        float v[8], inv;
+        const float sc = block_scale(max_over_block(r[k].abs_max()), &inv);
+        if (!p.in || row >= s.rows) continue;
+        r[k].get(v);
+        *reinterpret_cast<uint2*>(codes + row * ld_codes + p.col) = encode8(v, inv);
+        if (threadIdx.x % kLanesPerBlock == 0) scales[(int64_t)row * s.n_blocks + p.block] = sc;
+    }
 }
 
 // One 128 x 128 block of a weight per CTA; its rows stay in registers (8 per thread) between the two uses.
@@ -91,11 +100,7 @@ __global__ void __launch_bounds__(kThreads) quantize_weight_kernel(int32_t N, in
         if (row < N && col < K) r[i].load(W, row * ld_w + col);
     }
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        float v[8];
-        r[i].get(v);
-        a = max(a, abs_bits_max(v));
-    }
+    for (int i = 0; i < kRows; ++i) a = max(a, r[i].abs_max());
     a = __reduce_max_sync(0xffffffffu, a);
     if (threadIdx.x % 32 == 0) warp_max[threadIdx.x / 32] = a;
     __syncthreads();
@@ -178,8 +183,8 @@ __global__ void __launch_bounds__(kThreads) swiglu_forward_kernel(
         const int ck = (train.n > 0 && row < s.rows) ? checkpoint_row(train, row) : -1;
         if (!__any_sync(0xffffffffu, ck >= 0)) continue;
         float inv_g, inv_u;
-        const float sg = block_scale(max_over_block(abs_bits_max(g)), &inv_g);
-        const float su = block_scale(max_over_block(abs_bits_max(u)), &inv_u);
+        const float sg = block_scale(max_over_block(rg[k].abs_max()), &inv_g);
+        const float su = block_scale(max_over_block(ru[k].abs_max()), &inv_u);
         if (!in || ck < 0) continue;
         uint8_t* c = ck_codes + (int64_t)ck * 2 * s.cols + p.col;
         *reinterpret_cast<uint2*>(c) = encode8(g, inv_g);
@@ -289,7 +294,7 @@ int64_t train_ranges(const char* fn, int32_t T, const lora_segment_t* segs, int3
 cudaError_t launch_quantize(int32_t T, int32_t K, lora_dtype_t dt, const void* x, int64_t ld_x, uint8_t* codes,
                             int64_t ld_codes, float* scales, cudaStream_t stream) {
     const Shape s = shape_of(T, K);
-    return launch_pdl(dt == LORA_BF16 ? quantize_kernel<Row8Bf16> : quantize_kernel<Row8F32>, grid_of(s, 1),
+    return launch_pdl(dt == LORA_BF16 ? quantize_kernel<Row8Bf16> : quantize_kernel<Row8F32>, grid_of(s, kQuantRows),
                       dim3(kThreads), 0, stream, s, x, ld_x, codes, ld_codes, scales);
 }
 

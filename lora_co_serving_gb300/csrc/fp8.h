@@ -76,6 +76,14 @@ struct Row8Bf16 {
             v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
         }
     }
+    // largest magnitude as float bits, NaN above all
+    __device__ __forceinline__ uint32_t abs_max() const {
+        const uint32_t w[4] = {q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu, q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu};
+        const __nv_bfloat162* v = reinterpret_cast<const __nv_bfloat162*>(w);
+        const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(v[0], v[1]), __hmax2_nan(v[2], v[3]));
+        const uint32_t b = *reinterpret_cast<const uint32_t*>(&m);
+        return max(b << 16, b & 0xFFFF0000u);
+    }
     static __device__ __forceinline__ void store(void* p, int64_t i, const float (&v)[8]) {
         uint32_t w[4];
 #pragma unroll
@@ -97,6 +105,11 @@ struct Row8F32 {
     __device__ __forceinline__ void get(float (&v)[8]) const {
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
         v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+    __device__ __forceinline__ uint32_t abs_max() const {
+        float v[8];
+        get(v);
+        return abs_bits_max(v);
     }
     static __device__ __forceinline__ void store(void* p, int64_t i, const float (&v)[8]) {
         float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + i);

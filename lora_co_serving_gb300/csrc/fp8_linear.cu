@@ -533,7 +533,7 @@ struct RowsQuant {
             const int t = 2 * (2 * i + which) + lane / kLanesPerBlock, c = lane % kLanesPerBlock;
             float v[8], inv;
             r[i].get(v);
-            const float sc = block_scale(max_over_block(abs_bits_max(v)), &inv);
+            const float sc = block_scale(max_over_block(r[i].abs_max()), &inv);
             *reinterpret_cast<uint2*>(stage + t * 128 + (((c >> 1) ^ (t & 7)) * 16) + (c & 1) * 8) = encode8(v, inv);
             if (c == 0) slot[t] = sc;
         }
