@@ -547,6 +547,12 @@ def _matrix(t, name, dtype=None, rows=None, cols=None, contiguous=False):
     return ld if r > 1 else max(ld, c)
 
 
+def _table(rows):
+    """A table of four int32 a row as (bytes, number of rows): bytes cross the ABI without a numpy pointer object."""
+    a = np.asarray(rows, dtype=np.int32).reshape(-1, 4)
+    return a.tobytes(), a.shape[0]
+
+
 def _vector(t, name, dtype, n):
     if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
@@ -648,8 +654,7 @@ def fp8_linear(x, w, w_scales, x_scales=None, y=None, workspace=None, stream=Non
 
 def checkpoint_rows(T, segs):
     """Rows of the 8-bit checkpoint of a segment table: the tokens of its fine-tuning segments."""
-    s = segments(segs)
-    n = library().lora_checkpoint_rows(T, _ptr(s), s.shape[0])
+    n = library().lora_checkpoint_rows(T, *_table(segs))
     if n < 0:
         raise LoraError(int(n), library().lora_last_error().decode())
     return int(n)
@@ -667,13 +672,14 @@ def swiglu_forward(gu, segs=None, checkpoint=False, fp8_out=False, h=None, h_sca
     if I2 % 2:
         raise ValueError("gu must hold gate|up, an even number of columns; got %d" % I2)
     I = I2 // 2
-    s = None if segs is None else segments(segs)
-    n_segs = 0 if s is None else s.shape[0]
+    s, n_segs = (None, 0) if segs is None else _table(segs)
     ck = cs = None
     if checkpoint:
         if s is None:
             raise ValueError("a checkpoint needs the batch's segment table")
-        R = checkpoint_rows(T, s)
+        R = library().lora_checkpoint_rows(T, s, n_segs)
+        if R < 0:
+            _check(R)
         ck = torch.empty((R, I2), dtype=torch.float8_e4m3fn, device=gu.device)
         cs = torch.empty((R, 2 * _blocks(I)), dtype=torch.float32, device=gu.device)
     out = torch.float8_e4m3fn if fp8_out else gu.dtype
@@ -686,7 +692,7 @@ def swiglu_forward(gu, segs=None, checkpoint=False, fp8_out=False, h=None, h_sca
     if fp8_out:
         _matrix(h_scales, "h_scales", torch.float32, T, _blocks(I), contiguous=True)
     keep = ck is not None and ck.numel() > 0
-    rc = library().lora_swiglu_forward(T, I, code, gu.data_ptr(), ld, _ptr(s), n_segs, h.data_ptr(), ldh,
+    rc = library().lora_swiglu_forward(T, I, code, gu.data_ptr(), ld, s, n_segs, h.data_ptr(), ldh,
                                        h_scales.data_ptr() if fp8_out else None, ck.data_ptr() if keep else None,
                                        cs.data_ptr() if keep else None, _stream_ptr(stream))
     if rc != 0:
@@ -724,11 +730,6 @@ def swiglu_backward(saved, dh, fp8_out=False, dgu=None, dgu_scales=None, stream=
 Preference = namedtuple("Preference", ["loss", "rewards", "logp", "lse", "coef"])
 
 
-def _pairs(pairs):
-    """Pairs as a contiguous int32 [n, 4] numpy array."""
-    return np.ascontiguousarray(np.asarray(pairs, dtype=np.int32).reshape(-1, 4))
-
-
 def token_logprob(logits, labels, logp=None, lse=None, stream=None):
     """(logp [T], lse [T]) float32: log probability of each row's label, and the row's log-sum-exp.  labels int64 [T];
     a negative label's row is not read and gives zeros."""
@@ -757,11 +758,10 @@ def preference_forward(logits, labels, ref_logp, pairs, beta=0.1, label_smoothin
     T, V = logits.shape
     _vector(labels, "labels", torch.int64, T)
     _vector(ref_logp, "ref_logp", torch.float32, T)
-    p = _pairs(pairs)
-    n = p.shape[0]
+    p, n = _table(pairs)
     logp, lse, loss, rewards, coef = ref_logp.new_empty(2 * T + 5 * n).split_with_sizes([T, T, n, 2 * n, 2 * n])
     rc = library().lora_preference_forward(T, V, code, logits.data_ptr(), ld, labels.data_ptr(), ref_logp.data_ptr(),
-                                           _ptr(p), n, beta, label_smoothing, loss.data_ptr(), rewards.data_ptr(),
+                                           p, n, beta, label_smoothing, loss.data_ptr(), rewards.data_ptr(),
                                            logp.data_ptr(), lse.data_ptr(), coef.data_ptr(), _stream_ptr(stream))
     if rc != 0:
         _check(rc)
@@ -776,8 +776,7 @@ def preference_backward(logits, labels, lse, coef, pairs, dloss=None, dlogits=No
     import torch
     code, ld = _dtype_code(logits), _matrix(logits, "logits")
     T, V = logits.shape
-    p = _pairs(pairs)
-    n = p.shape[0]
+    p, n = _table(pairs)
     _vector(labels, "labels", torch.int64, T)
     _vector(lse, "lse", torch.float32, T)
     _vector(coef, "coef", torch.float32, 2 * n)
@@ -788,7 +787,7 @@ def preference_backward(logits, labels, lse, coef, pairs, dloss=None, dlogits=No
     else:
         ldd = _matrix(dlogits, "dlogits", logits.dtype, T, V)
     rc = library().lora_preference_backward(T, V, code, logits.data_ptr(), ld, labels.data_ptr(), lse.data_ptr(),
-                                            coef.data_ptr(), _ptr(p), n, _ptr(dloss), dlogits.data_ptr(), ldd,
+                                            coef.data_ptr(), p, n, _ptr(dloss), dlogits.data_ptr(), ldd,
                                             _stream_ptr(stream))
     if rc != 0:
         _check(rc)

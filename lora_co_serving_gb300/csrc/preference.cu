@@ -208,17 +208,22 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(int32_t V, const type
     }
 }
 
-// Sequences in increasing start order (zero-length ones left out): `id` = 2 pair + (0 chosen, 1 rejected)
+// Sequences in increasing start order (zero-length ones left out): `id` = 2 pair + (0 chosen, 1 rejected).  Tables of up
+// to kFewPairs pairs, a usual step's, travel in a smaller launch parameter than the 5 KB of the largest.
+constexpr int kFewPairs = 16;
+template <int kPairs>
 struct Sequences {
     int32_t n;
-    int32_t start[2 * LORA_MAX_PAIRS], end[2 * LORA_MAX_PAIRS];
-    int16_t id[2 * LORA_MAX_PAIRS];
+    int32_t start[2 * kPairs], end[2 * kPairs];
+    int16_t id[2 * kPairs];
 };
+template <int kPairs>
 struct Pairs {
-    lora_pair_t p[LORA_MAX_PAIRS];
+    lora_pair_t p[kPairs];
 };
 
-__device__ __forceinline__ int sequence_of(const Sequences& s, int t) {
+template <int kPairs>
+__device__ __forceinline__ int sequence_of(const Sequences<kPairs>& s, int t) {
     int lo = 0, hi = s.n;
     while (lo < hi) {
         const int mid = (lo + hi) / 2;
@@ -242,7 +247,8 @@ struct Sum2 {
 
 // One CTA per pair, half of its threads for each sequence.  The differences lp - ref are small and their sums cancel:
 // they are added up in about 48 bits (in float32 pairs: 64-bit arithmetic is slow on this GPU, 10 us against 4).
-__global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(const __grid_constant__ Pairs pairs,
+template <int kPairs>
+__global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(const __grid_constant__ Pairs<kPairs> pairs,
                                                                  const int64_t* __restrict__ labels,
                                                                  const float* __restrict__ logp,
                                                                  const float* __restrict__ ref, float beta, float eps,
@@ -294,12 +300,12 @@ __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(const __grid_co
 
 // One CTA per row, the last rows first: the forward has read them last, so L2 still holds them (logits of several
 // times its size: 100 MB of them).  What is written is not read again here and does not push them out (st.cs).
-template <class E, int kThreads, int kAhead>
+template <class E, int kThreads, int kAhead, int kPairs>
 __global__ void __launch_bounds__(kThreads) dlogits_kernel(int32_t V, const typename E::T* logits, int64_t ld,
                                                            const int64_t* __restrict__ labels,
                                                            const float* __restrict__ lse,
                                                            const float* __restrict__ coef,
-                                                           const __grid_constant__ Sequences seqs,
+                                                           const __grid_constant__ Sequences<kPairs> seqs,
                                                            const float* __restrict__ dloss, float dloss_all,
                                                            typename E::T* dlogits, int64_t ld_d) {
     grid_dep_wait();
@@ -371,7 +377,8 @@ int check_logits(const char* fn, int32_t T, int32_t V, lora_dtype_t dt, const vo
 }
 
 // The sequences inside [0, T), in increasing start order, none over another
-int check_pairs(const char* fn, int32_t T, const lora_pair_t* pairs, int32_t n_pairs, Sequences* out) {
+int check_pairs(const char* fn, int32_t T, const lora_pair_t* pairs, int32_t n_pairs,
+                Sequences<LORA_MAX_PAIRS>* out) {
     if (n_pairs < 0 || (n_pairs > 0 && !pairs))
         return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": pairs is NULL or their number negative");
     if (n_pairs > LORA_MAX_PAIRS)
@@ -422,14 +429,14 @@ cudaError_t launch_logprob(int32_t T, int32_t V, const void* logits, int64_t ld,
     });
 }
 
-template <class E>
+template <class E, int kPairs>
 cudaError_t launch_dlogits(int32_t T, int32_t V, const void* logits, int64_t ld, const int64_t* labels,
-                           const float* lse, const float* coef, const Sequences& seqs, const float* dloss, float all,
-                           void* dlogits, int64_t ld_d, cudaStream_t st) {
+                           const float* lse, const float* coef, const Sequences<kPairs>& seqs, const float* dloss,
+                           float all, void* dlogits, int64_t ld_d, cudaStream_t st) {
     // 512 threads: 263 us for the same rows (256 threads: 270 us)
     return by_row_size<E, 512>(T, V, [&](auto threads) {
         constexpr int kThreads = decltype(threads)::value;
-        return launch_pdl(dlogits_kernel<E, kThreads, 4>, dim3(T), dim3(kThreads), 0, st, V,
+        return launch_pdl(dlogits_kernel<E, kThreads, 4, kPairs>, dim3(T), dim3(kThreads), 0, st, V,
                           static_cast<const typename E::T*>(logits), ld, labels, lse, coef, seqs, dloss, all,
                           static_cast<typename E::T*>(dlogits), ld_d);
     });
@@ -461,7 +468,7 @@ extern "C" int lora_preference_forward(int32_t T, int32_t V, lora_dtype_t dt, co
     if (!(beta > 0.f) || isinf(beta) || !(label_smoothing >= 0.f && label_smoothing < 0.5f))
         return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": beta must be positive and finite, "
                                                               "label_smoothing in [0, 0.5)");
-    Sequences seqs;
+    Sequences<LORA_MAX_PAIRS> seqs;
     rc = check_pairs(fn, T, pairs, n_pairs, &seqs);
     if (rc != LORA_OK) return rc;
     if (T > 0 && (!ref_logp || !logp || !lse))
@@ -475,10 +482,13 @@ extern "C" int lora_preference_forward(int32_t T, int32_t V, lora_dtype_t dt, co
         e = dt == LORA_BF16 ? launch_logprob<Bf16>(T, V, logits, ld, labels, logp, lse, st)
                             : launch_logprob<F32>(T, V, logits, ld, labels, logp, lse, st);
     if (e == cudaSuccess && n_pairs > 0) {
-        Pairs p;                                 // the first n_pairs are read
-        std::copy(pairs, pairs + n_pairs, p.p);
-        e = launch_pdl(pair_loss_kernel, dim3(n_pairs), dim3(kPairThreads), 0, st, p, labels,
-                       static_cast<const float*>(logp), ref_logp, beta, label_smoothing, loss, rewards, coef);
+        auto go = [&](auto p) {
+            constexpr int kPairs = sizeof(p.p) / sizeof(lora_pair_t);
+            std::copy(pairs, pairs + n_pairs, p.p);      // the first n_pairs are read
+            return launch_pdl(pair_loss_kernel<kPairs>, dim3(n_pairs), dim3(kPairThreads), 0, st, p, labels,
+                              static_cast<const float*>(logp), ref_logp, beta, label_smoothing, loss, rewards, coef);
+        };
+        e = n_pairs <= kFewPairs ? go(Pairs<kFewPairs>()) : go(Pairs<LORA_MAX_PAIRS>());
     }
     return enqueued(fn, e);
 }
@@ -490,7 +500,7 @@ extern "C" int lora_preference_backward(int32_t T, int32_t V, lora_dtype_t dt, c
     const char* fn = "lora_preference_backward";
     int rc = check_logits(fn, T, V, dt, logits, ld, labels);
     if (rc != LORA_OK) return rc;
-    Sequences seqs;
+    Sequences<LORA_MAX_PAIRS> seqs;
     rc = check_pairs(fn, T, pairs, n_pairs, &seqs);
     if (rc != LORA_OK || T == 0) return rc;
     if (!lse || !dlogits || (n_pairs > 0 && !coef))
@@ -502,8 +512,16 @@ extern "C" int lora_preference_backward(int32_t T, int32_t V, lora_dtype_t dt, c
         return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": in place, ld_d must be ld");
     const float all = n_pairs > 0 ? 1.f / (float)n_pairs : 0.f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return enqueued(fn, dt == LORA_BF16 ? launch_dlogits<Bf16>(T, V, logits, ld, labels, lse, coef, seqs, dloss, all,
-                                                               dlogits, ld_d, st)
-                                        : launch_dlogits<F32>(T, V, logits, ld, labels, lse, coef, seqs, dloss, all,
-                                                              dlogits, ld_d, st));
+    auto go = [&](const auto& q) {
+        return dt == LORA_BF16
+                   ? launch_dlogits<Bf16>(T, V, logits, ld, labels, lse, coef, q, dloss, all, dlogits, ld_d, st)
+                   : launch_dlogits<F32>(T, V, logits, ld, labels, lse, coef, q, dloss, all, dlogits, ld_d, st);
+    };
+    if (n_pairs > kFewPairs) return enqueued(fn, go(seqs));
+    Sequences<kFewPairs> few;
+    few.n = seqs.n;
+    std::copy(seqs.start, seqs.start + seqs.n, few.start);
+    std::copy(seqs.end, seqs.end + seqs.n, few.end);
+    std::copy(seqs.id, seqs.id + seqs.n, few.id);
+    return enqueued(fn, go(few));
 }
