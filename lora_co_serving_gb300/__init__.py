@@ -25,6 +25,7 @@ If the compiled library is missing, calls raise ``LibraryNotBuilt``: there is no
 fallback path.
 """
 import ctypes
+import functools
 import os
 from collections import namedtuple
 
@@ -547,6 +548,28 @@ def _matrix(t, name, dtype=None, rows=None, cols=None, contiguous=False):
     return ld if r > 1 else max(ld, c)
 
 
+def _on_stream(fn):
+    """fn(..., stream=s) runs with s current, so that what it allocates belongs to s as well: memory that the caller's
+    stream has just given back, or takes again after the call, is none of it."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        import torch
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream))
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+def _one_device(*tensors):
+    d = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (d < 0 or t.get_device() != d):
+            raise ValueError("tensors must lie on one CUDA device")
+
+
 def _table(rows):
     """A table of four int32 a row as (bytes, number of rows): bytes cross the ABI without a numpy pointer object."""
     a = np.asarray(rows, dtype=np.int32).reshape(-1, 4)
@@ -560,7 +583,8 @@ def _vector(t, name, dtype, n):
         raise ValueError("%s must be contiguous with %d elements, got %s" % (name, n, tuple(t.shape)))
 
 
-def fp8_quantize(x, codes=None, scales=None, stream=None):
+@_on_stream
+def fp8_quantize(x, codes=None, scales=None):
     """x [T, K] (bf16 or float32) -> (codes [T, K] float8_e4m3fn, scales [T, ceil(K / 128)] float32).
 
     A scale is the smallest power of two that brings its block of 128 columns within e4m3's largest number, 448."""
@@ -572,22 +596,25 @@ def fp8_quantize(x, codes=None, scales=None, stream=None):
     if scales is None:
         scales = torch.empty((T, _blocks(K)), dtype=torch.float32, device=x.device)
     ldc = _matrix(codes, "codes", torch.float8_e4m3fn, T, K)
+    _one_device(x, codes, scales)
     _matrix(scales, "scales", torch.float32, T, _blocks(K), contiguous=True)
-    _check(library().lora_fp8_quantize(T, K, code, _ptr(x), ld, _ptr(codes), ldc, _ptr(scales), _stream_ptr(stream)))
+    _check(library().lora_fp8_quantize(T, K, code, _ptr(x), ld, _ptr(codes), ldc, _ptr(scales), _stream_ptr(None)))
     return codes, scales
 
 
-def fp8_quantize_weight(W, stream=None):
+@_on_stream
+def fp8_quantize_weight(W):
     """W [N, K] (bf16 or float32) -> (codes [N, K] float8_e4m3fn, scales [ceil(N / 128), ceil(K / 128)]), a scale for
     each 128 x 128 block.  For the input's gradient pass the transposed weight's (codes.t() and scales.t(), made
     contiguous once: a block of the transposed weight is the transposed block)."""
     import torch
     code, ld = _dtype_code(W), _matrix(W, "W")
+    _one_device(W)
     N, K = W.shape
     codes = torch.empty((N, K), dtype=torch.float8_e4m3fn, device=W.device)
     scales = torch.empty((_blocks(N), _blocks(K)), dtype=torch.float32, device=W.device)
     _check(library().lora_fp8_quantize_weight(N, K, code, _ptr(W), ld, _ptr(codes), _ptr(scales),
-                                              _stream_ptr(stream)))
+                                              _stream_ptr(None)))
     return codes, scales
 
 
@@ -616,7 +643,8 @@ def _status_workspace(stream_ptr, device):
     return ws
 
 
-def fp8_linear(x, w, w_scales, x_scales=None, y=None, workspace=None, stream=None, check_status=False):
+@_on_stream
+def fp8_linear(x, w, w_scales, x_scales=None, y=None, workspace=None, check_status=False):
     """y [T, N] (bf16) = x W^T for a frozen weight in 8 bits (w [N, K] codes, w_scales [ceil(N/128), ceil(K/128)]).
 
     x [T, K] is bf16 or float32 and is quantized on the way, or float8_e4m3fn codes with their x_scales
@@ -637,7 +665,8 @@ def fp8_linear(x, w, w_scales, x_scales=None, y=None, workspace=None, stream=Non
         y, ldy = torch.empty((T, N), dtype=torch.bfloat16, device=x.device), N
     else:
         ldy = _matrix(y, "y", torch.bfloat16, T, N)
-    st = _stream_ptr(stream)
+    _one_device(x, w, w_scales, x_scales, y, workspace)
+    st = _stream_ptr(None)
     if workspace is None:
         need = fp8_workspace_size(T, K, N, x_scales is not None)
         workspace = _status_workspace(st, x.device) if need <= _STATUS_BYTES else None
@@ -648,7 +677,7 @@ def fp8_linear(x, w, w_scales, x_scales=None, y=None, workspace=None, stream=Non
     if rc != 0:
         _check(rc)
     if check_status:
-        workspace_status(workspace, stream)
+        workspace_status(workspace)
     return y
 
 
@@ -660,7 +689,8 @@ def checkpoint_rows(T, segs):
     return int(n)
 
 
-def swiglu_forward(gu, segs=None, checkpoint=False, fp8_out=False, h=None, h_scales=None, stream=None):
+@_on_stream
+def swiglu_forward(gu, segs=None, checkpoint=False, fp8_out=False, h=None, h_scales=None):
     """h [T, I] = silu(gate) * up of gu [T, 2 I] = gate|up.
 
     checkpoint: also keep gate|up of the fine-tuning rows of `segs` in 8 bits; returns (h, saved) with saved =
@@ -692,16 +722,18 @@ def swiglu_forward(gu, segs=None, checkpoint=False, fp8_out=False, h=None, h_sca
     if fp8_out:
         _matrix(h_scales, "h_scales", torch.float32, T, _blocks(I), contiguous=True)
     keep = ck is not None and ck.numel() > 0
+    _one_device(gu, h, h_scales)
     rc = library().lora_swiglu_forward(T, I, code, gu.data_ptr(), ld, s, n_segs, h.data_ptr(), ldh,
                                        h_scales.data_ptr() if fp8_out else None, ck.data_ptr() if keep else None,
-                                       cs.data_ptr() if keep else None, _stream_ptr(stream))
+                                       cs.data_ptr() if keep else None, _stream_ptr(None))
     if rc != 0:
         _check(rc)
     h = (h, h_scales) if fp8_out else h
     return (h, (ck, cs)) if checkpoint else h
 
 
-def swiglu_backward(saved, dh, fp8_out=False, dgu=None, dgu_scales=None, stream=None):
+@_on_stream
+def swiglu_backward(saved, dh, fp8_out=False, dgu=None, dgu_scales=None):
     """Gradient of gate|up [R, 2 I] from the checkpoint `saved` of swiglu_forward and dh [R, I], the gradient of h for
     the checkpoint's rows.  fp8_out: (codes, scales) for the next fp8_linear (I a multiple of 128)."""
     import torch
@@ -719,8 +751,9 @@ def swiglu_backward(saved, dh, fp8_out=False, dgu=None, dgu_scales=None, stream=
         dgu_scales = torch.empty((R, 2 * _blocks(I)), dtype=torch.float32, device=dh.device)
     if fp8_out:
         _matrix(dgu_scales, "dgu_scales", torch.float32, R, 2 * _blocks(I), contiguous=True)
+    _one_device(dh, ck, cs, dgu, dgu_scales)
     rc = library().lora_swiglu_backward(R, I, code, ck.data_ptr(), cs.data_ptr(), dh.data_ptr(), ld, dgu.data_ptr(), ldo,
-                                        dgu_scales.data_ptr() if fp8_out else None, _stream_ptr(stream))
+                                        dgu_scales.data_ptr() if fp8_out else None, _stream_ptr(None))
     if rc != 0:
         _check(rc)
     return (dgu, dgu_scales) if fp8_out else dgu
@@ -730,7 +763,8 @@ def swiglu_backward(saved, dh, fp8_out=False, dgu=None, dgu_scales=None, stream=
 Preference = namedtuple("Preference", ["loss", "rewards", "logp", "lse", "coef"])
 
 
-def token_logprob(logits, labels, logp=None, lse=None, stream=None):
+@_on_stream
+def token_logprob(logits, labels, logp=None, lse=None):
     """(logp [T], lse [T]) float32: log probability of each row's label, and the row's log-sum-exp.  labels int64 [T];
     a negative label's row is not read and gives zeros."""
     import torch
@@ -743,12 +777,14 @@ def token_logprob(logits, labels, logp=None, lse=None, stream=None):
         lse = torch.empty(T, dtype=torch.float32, device=logits.device)
     _vector(logp, "logp", torch.float32, T)
     _vector(lse, "lse", torch.float32, T)
+    _one_device(logits, labels, logp, lse)
     _check(library().lora_token_logprob(T, V, code, _ptr(logits), ld, _ptr(labels), _ptr(logp), _ptr(lse),
-                                        _stream_ptr(stream)))
+                                        _stream_ptr(None)))
     return logp, lse
 
 
-def preference_forward(logits, labels, ref_logp, pairs, beta=0.1, label_smoothing=0.0, stream=None):
+@_on_stream
+def preference_forward(logits, labels, ref_logp, pairs, beta=0.1, label_smoothing=0.0):
     """Paired log-ratio loss of a policy's logits [T, V] against a reference's ref_logp [T].
 
     pairs: int32 rows {chosen start, chosen length, rejected start, rejected length} over the batch's rows.  Returns
@@ -758,17 +794,19 @@ def preference_forward(logits, labels, ref_logp, pairs, beta=0.1, label_smoothin
     T, V = logits.shape
     _vector(labels, "labels", torch.int64, T)
     _vector(ref_logp, "ref_logp", torch.float32, T)
+    _one_device(logits, labels, ref_logp)
     p, n = _table(pairs)
     logp, lse, loss, rewards, coef = ref_logp.new_empty(2 * T + 5 * n).split_with_sizes([T, T, n, 2 * n, 2 * n])
     rc = library().lora_preference_forward(T, V, code, logits.data_ptr(), ld, labels.data_ptr(), ref_logp.data_ptr(),
                                            p, n, beta, label_smoothing, loss.data_ptr(), rewards.data_ptr(),
-                                           logp.data_ptr(), lse.data_ptr(), coef.data_ptr(), _stream_ptr(stream))
+                                           logp.data_ptr(), lse.data_ptr(), coef.data_ptr(), _stream_ptr(None))
     if rc != 0:
         _check(rc)
     return Preference(loss, rewards.view(n, 2), logp, lse, coef.view(n, 2))
 
 
-def preference_backward(logits, labels, lse, coef, pairs, dloss=None, dlogits=None, stream=None):
+@_on_stream
+def preference_backward(logits, labels, lse, coef, pairs, dloss=None, dlogits=None):
     """Gradient of the logits [T, V] in their type: every row is written, zeros where a row is not counted.
 
     dloss [P] float32: the gradient of each pair's loss (default: 1 / P each, the mean's).  dlogits may be `logits`
@@ -786,9 +824,10 @@ def preference_backward(logits, labels, lse, coef, pairs, dloss=None, dlogits=No
         dlogits, ldd = torch.empty((T, V), dtype=logits.dtype, device=logits.device), V
     else:
         ldd = _matrix(dlogits, "dlogits", logits.dtype, T, V)
+    _one_device(logits, labels, lse, coef, dloss, dlogits)
     rc = library().lora_preference_backward(T, V, code, logits.data_ptr(), ld, labels.data_ptr(), lse.data_ptr(),
                                             coef.data_ptr(), p, n, _ptr(dloss), dlogits.data_ptr(), ldd,
-                                            _stream_ptr(stream))
+                                            _stream_ptr(None))
     if rc != 0:
         _check(rc)
     return dlogits

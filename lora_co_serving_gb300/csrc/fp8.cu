@@ -260,23 +260,28 @@ bool known_dtype(lora_dtype_t dt) { return dt == LORA_BF16 || dt == LORA_F32; }
 int64_t train_ranges(const char* fn, int32_t T, const lora_segment_t* segs, int32_t n_segs, TrainRanges* out) {
     if (n_segs < 0 || (n_segs > 0 && !segs))
         return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": segment table is NULL or its size negative");
-    std::vector<lora_segment_t> s;
-    s.reserve(n_segs);
-    for (int32_t i = 0; i < n_segs; ++i) {
-        if (segs[i].len < 0 || segs[i].start < 0)
-            return refuse(LORA_ERR_SEGMENTS, std::string(fn) + ": negative segment start or length");
-        if (segs[i].len > 0) s.push_back(segs[i]);
+    std::vector<lora_segment_t> copy;          // in increasing start order, made only if the table is not
+    const auto before = [](const lora_segment_t& a, const lora_segment_t& b) {
+        return a.start != b.start ? a.start < b.start : a.len < b.len;      // empty ones first
+    };
+    if (!std::is_sorted(segs, segs + n_segs, before)) {
+        copy.assign(segs, segs + n_segs);
+        std::sort(copy.begin(), copy.end(), before);
+        segs = copy.data();
     }
-    const auto before = [](const lora_segment_t& a, const lora_segment_t& b) { return a.start < b.start; };
-    if (!std::is_sorted(s.begin(), s.end(), before)) std::sort(s.begin(), s.end(), before);
     int64_t at = 0;
     int32_t rows = 0;
     out->n = 0;
-    for (const lora_segment_t& q : s) {
+    for (int32_t i = 0; i < n_segs; ++i) {
+        const lora_segment_t& q = segs[i];
+        if (q.len < 0 || q.start < 0)
+            return refuse(LORA_ERR_SEGMENTS, std::string(fn) + ": negative segment start or length");
+        if (q.len == 0) continue;
         if (q.start != at)
             return refuse(LORA_ERR_SEGMENTS, std::string(fn) + ": segments overlap or leave a gap at token " +
                                                  std::to_string(std::min<int64_t>(at, q.start)));
         at += q.len;
+        if (at > T) break;
         if (!q.is_train) continue;
         if (out->n == kMaxTrainSegs)
             return refuse(LORA_ERR_LIMIT, std::string(fn) + ": more than 48 fine-tuning segments");
@@ -304,105 +309,118 @@ using namespace lora;
 
 extern "C" int lora_fp8_quantize(int32_t T, int32_t K, lora_dtype_t dt, const void* x, int64_t ld_x, void* codes,
                                  int64_t ld_codes, float* scales, void* stream) {
-    const char* fn = "lora_fp8_quantize";
-    if (!known_dtype(dt)) return refuse(LORA_ERR_DTYPE, "unknown dtype");
-    if (T < 0 || K <= 0) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": T must be >= 0 and K > 0");
-    if (K > kMaxCols) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": more than 2^22 columns");
-    if (K % 16 != 0) return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": K must be a multiple of 16");
-    if (T == 0) return LORA_OK;
-    int rc = check_matrix(fn, "x", x, K, ld_x, elem_size(dt));
-    if (rc == LORA_OK) rc = check_matrix(fn, "codes", codes, K, ld_codes, 1);
-    if (rc != LORA_OK) return rc;
-    if (!scales) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": scales is NULL");
-    return enqueued(fn, launch_quantize(T, K, dt, x, ld_x, static_cast<uint8_t*>(codes), ld_codes, scales,
-                                        static_cast<cudaStream_t>(stream)));
+    return guarded([&]() -> int {
+        const char* fn = "lora_fp8_quantize";
+        if (!known_dtype(dt)) return refuse(LORA_ERR_DTYPE, "unknown dtype");
+        if (T < 0 || K <= 0) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": T must be >= 0 and K > 0");
+        if (K > kMaxCols) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": more than 2^22 columns");
+        if (T > kMaxRowsOfX) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": T above 2^31 - 1025");
+        if (K % 16 != 0) return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": K must be a multiple of 16");
+        if (T == 0) return LORA_OK;
+        int rc = check_matrix(fn, "x", x, K, ld_x, elem_size(dt));
+        if (rc == LORA_OK) rc = check_matrix(fn, "codes", codes, K, ld_codes, 1);
+        if (rc != LORA_OK) return rc;
+        if (!scales) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": scales is NULL");
+        return enqueued(fn, launch_quantize(T, K, dt, x, ld_x, static_cast<uint8_t*>(codes), ld_codes, scales,
+                                            static_cast<cudaStream_t>(stream)));
+    });
 }
 
 extern "C" int lora_fp8_quantize_weight(int32_t N, int32_t K, lora_dtype_t dt, const void* W, int64_t ld_w,
                                         void* codes, float* scales, void* stream) {
-    const char* fn = "lora_fp8_quantize_weight";
-    if (!known_dtype(dt)) return refuse(LORA_ERR_DTYPE, "unknown dtype");
-    if (N <= 0 || K <= 0) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": N and K must be > 0");
-    if (K % 16 != 0) return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": K must be a multiple of 16");
-    int rc = check_matrix(fn, "W", W, K, ld_w, elem_size(dt));
-    if (rc == LORA_OK) rc = check_matrix(fn, "codes", codes, K, K, 1);
-    if (rc != LORA_OK) return rc;
-    if (!scales) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": scales is NULL");
-    if (blocks_of(N) > 65535) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": more than 65535 * 128 weight rows");
-    const dim3 grid(blocks_of(K), blocks_of(N));
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dt == LORA_BF16)
-        quantize_weight_kernel<Row8Bf16>
-            <<<grid, kThreads, 0, st>>>(N, K, W, ld_w, static_cast<uint8_t*>(codes), scales);
-    else
-        quantize_weight_kernel<Row8F32>
-            <<<grid, kThreads, 0, st>>>(N, K, W, ld_w, static_cast<uint8_t*>(codes), scales);
-    return enqueued(fn, cudaGetLastError());
+    return guarded([&]() -> int {
+        const char* fn = "lora_fp8_quantize_weight";
+        if (!known_dtype(dt)) return refuse(LORA_ERR_DTYPE, "unknown dtype");
+        if (N <= 0 || K <= 0) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": N and K must be > 0");
+        if (K % 16 != 0) return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": K must be a multiple of 16");
+        int rc = check_matrix(fn, "W", W, K, ld_w, elem_size(dt));
+        if (rc == LORA_OK) rc = check_matrix(fn, "codes", codes, K, K, 1);
+        if (rc != LORA_OK) return rc;
+        if (!scales) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": scales is NULL");
+        if (blocks_of(N) > 65535) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": more than 65535 * 128 weight rows");
+        const dim3 grid(blocks_of(K), blocks_of(N));
+        cudaStream_t st = static_cast<cudaStream_t>(stream);
+        if (dt == LORA_BF16)
+            quantize_weight_kernel<Row8Bf16>
+                <<<grid, kThreads, 0, st>>>(N, K, W, ld_w, static_cast<uint8_t*>(codes), scales);
+        else
+            quantize_weight_kernel<Row8F32>
+                <<<grid, kThreads, 0, st>>>(N, K, W, ld_w, static_cast<uint8_t*>(codes), scales);
+        return enqueued(fn, cudaGetLastError());
+    });
 }
 
 extern "C" int64_t lora_checkpoint_rows(int32_t T, const lora_segment_t* segs, int32_t n_segs) {
-    TrainRanges t;
-    if (T < 0) return refuse(LORA_ERR_INVALID_ARG, "lora_checkpoint_rows: T must be >= 0");
-    return train_ranges("lora_checkpoint_rows", T, segs, n_segs, &t);
+    return guarded([&]() -> int64_t {
+        TrainRanges t;
+        if (T < 0) return refuse(LORA_ERR_INVALID_ARG, "lora_checkpoint_rows: T must be >= 0");
+        return train_ranges("lora_checkpoint_rows", T, segs, n_segs, &t);
+    });
 }
 
 extern "C" int lora_swiglu_forward(int32_t T, int32_t I, lora_dtype_t dt, const void* gu, int64_t ld_gu,
                                    const lora_segment_t* segs, int32_t n_segs, void* h, int64_t ld_h, float* h_scales,
                                    void* ck_codes, float* ck_scales, void* stream) {
-    const char* fn = "lora_swiglu_forward";
-    if (!known_dtype(dt)) return refuse(LORA_ERR_DTYPE, "unknown dtype");
-    if (T < 0 || I <= 0) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": T must be >= 0 and I > 0");
-    if (I > kMaxCols) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": more than 2^22 columns");
-    if (I % 8 != 0) return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": I must be a multiple of 8");
-    TrainRanges train;
-    train.n = 0;
-    if (ck_codes || n_segs != 0) {
-        const int64_t rows = train_ranges(fn, T, segs, n_segs, &train);
-        if (rows < 0) return (int)rows;
-    }
-    if (!ck_codes) train.n = 0;
-    if (T == 0) return LORA_OK;
-    int rc = check_matrix(fn, "gu", gu, 2 * (int64_t)I, ld_gu, elem_size(dt));
-    if (rc == LORA_OK) rc = check_matrix(fn, "h", h, I, ld_h, h_scales ? 1 : elem_size(dt));
-    if (rc == LORA_OK && train.n > 0) rc = check_matrix(fn, "ck_codes", ck_codes, 2 * (int64_t)I, 2 * (int64_t)I, 1);
-    if (rc != LORA_OK) return rc;
-    if (train.n > 0 && !ck_scales) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": ck_scales is NULL");
-    const Shape s = shape_of(T, I);
-    auto go = [&](auto kernel) {
-        return launch_pdl(kernel, grid_of(s, kForwardRows), dim3(kThreads), 0, static_cast<cudaStream_t>(stream), s, gu, ld_gu, h,
-                          ld_h, h_scales, static_cast<uint8_t*>(ck_codes), ck_scales, train);
-    };
-    if (dt == LORA_BF16)
-        return enqueued(fn, h_scales ? go(swiglu_forward_kernel<Row8Bf16, true>)
-                                     : go(swiglu_forward_kernel<Row8Bf16, false>));
-    return enqueued(fn, h_scales ? go(swiglu_forward_kernel<Row8F32, true>)
-                                 : go(swiglu_forward_kernel<Row8F32, false>));
+    return guarded([&]() -> int {
+        const char* fn = "lora_swiglu_forward";
+        if (!known_dtype(dt)) return refuse(LORA_ERR_DTYPE, "unknown dtype");
+        if (T < 0 || I <= 0) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": T must be >= 0 and I > 0");
+        if (I > kMaxCols) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": more than 2^22 columns");
+        if (T > kMaxRowsOfX) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": T above 2^31 - 1025");
+        if (I % 8 != 0) return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": I must be a multiple of 8");
+        TrainRanges train;
+        train.n = 0;
+        if (ck_codes || n_segs != 0) {
+            const int64_t rows = train_ranges(fn, T, segs, n_segs, &train);
+            if (rows < 0) return (int)rows;
+        }
+        if (!ck_codes) train.n = 0;
+        if (T == 0) return LORA_OK;
+        int rc = check_matrix(fn, "gu", gu, 2 * (int64_t)I, ld_gu, elem_size(dt));
+        if (rc == LORA_OK) rc = check_matrix(fn, "h", h, I, ld_h, h_scales ? 1 : elem_size(dt));
+        if (rc == LORA_OK && train.n > 0) rc = check_matrix(fn, "ck_codes", ck_codes, 2 * (int64_t)I, 2 * (int64_t)I, 1);
+        if (rc != LORA_OK) return rc;
+        if (train.n > 0 && !ck_scales) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": ck_scales is NULL");
+        const Shape s = shape_of(T, I);
+        auto go = [&](auto kernel) {
+            return launch_pdl(kernel, grid_of(s, kForwardRows), dim3(kThreads), 0, static_cast<cudaStream_t>(stream), s, gu, ld_gu, h,
+                              ld_h, h_scales, static_cast<uint8_t*>(ck_codes), ck_scales, train);
+        };
+        if (dt == LORA_BF16)
+            return enqueued(fn, h_scales ? go(swiglu_forward_kernel<Row8Bf16, true>)
+                                         : go(swiglu_forward_kernel<Row8Bf16, false>));
+        return enqueued(fn, h_scales ? go(swiglu_forward_kernel<Row8F32, true>)
+                                     : go(swiglu_forward_kernel<Row8F32, false>));
+    });
 }
 
 extern "C" int lora_swiglu_backward(int32_t R, int32_t I, lora_dtype_t dt, const void* ck_codes,
                                     const float* ck_scales, const void* dh, int64_t ld_dh, void* dgu, int64_t ld_dgu,
                                     float* dgu_scales, void* stream) {
-    const char* fn = "lora_swiglu_backward";
-    if (!known_dtype(dt)) return refuse(LORA_ERR_DTYPE, "unknown dtype");
-    if (R < 0 || I <= 0) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": R must be >= 0 and I > 0");
-    if (I > kMaxCols) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": more than 2^22 columns");
-    if (I % 8 != 0) return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": I must be a multiple of 8");
-    if (dgu_scales && I % kQBlock != 0)
-        return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": I must be a multiple of 128 for a gradient in 8 bits");
-    if (R == 0) return LORA_OK;
-    int rc = check_matrix(fn, "ck_codes", ck_codes, 2 * (int64_t)I, 2 * (int64_t)I, 1);
-    if (rc == LORA_OK) rc = check_matrix(fn, "dh", dh, I, ld_dh, elem_size(dt));
-    if (rc == LORA_OK) rc = check_matrix(fn, "dgu", dgu, 2 * (int64_t)I, ld_dgu, dgu_scales ? 1 : elem_size(dt));
-    if (rc != LORA_OK) return rc;
-    if (!ck_scales) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": ck_scales is NULL");
-    const Shape s = shape_of(R, I);
-    auto go = [&](auto kernel) {
-        return launch_pdl(kernel, grid_of(s, 1), dim3(kThreads), 0, static_cast<cudaStream_t>(stream), s,
-                          static_cast<const uint8_t*>(ck_codes), ck_scales, dh, ld_dh, dgu, ld_dgu, dgu_scales);
-    };
-    if (dt == LORA_BF16)
-        return enqueued(fn, dgu_scales ? go(swiglu_backward_kernel<Row8Bf16, true>)
-                                       : go(swiglu_backward_kernel<Row8Bf16, false>));
-    return enqueued(fn, dgu_scales ? go(swiglu_backward_kernel<Row8F32, true>)
-                                   : go(swiglu_backward_kernel<Row8F32, false>));
+    return guarded([&]() -> int {
+        const char* fn = "lora_swiglu_backward";
+        if (!known_dtype(dt)) return refuse(LORA_ERR_DTYPE, "unknown dtype");
+        if (R < 0 || I <= 0) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": R must be >= 0 and I > 0");
+        if (I > kMaxCols) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": more than 2^22 columns");
+        if (R > kMaxRowsOfX) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": R above 2^31 - 1025");
+        if (I % 8 != 0) return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": I must be a multiple of 8");
+        if (dgu_scales && I % kQBlock != 0)
+            return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": I must be a multiple of 128 for a gradient in 8 bits");
+        if (R == 0) return LORA_OK;
+        int rc = check_matrix(fn, "ck_codes", ck_codes, 2 * (int64_t)I, 2 * (int64_t)I, 1);
+        if (rc == LORA_OK) rc = check_matrix(fn, "dh", dh, I, ld_dh, elem_size(dt));
+        if (rc == LORA_OK) rc = check_matrix(fn, "dgu", dgu, 2 * (int64_t)I, ld_dgu, dgu_scales ? 1 : elem_size(dt));
+        if (rc != LORA_OK) return rc;
+        if (!ck_scales) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": ck_scales is NULL");
+        const Shape s = shape_of(R, I);
+        auto go = [&](auto kernel) {
+            return launch_pdl(kernel, grid_of(s, 1), dim3(kThreads), 0, static_cast<cudaStream_t>(stream), s,
+                              static_cast<const uint8_t*>(ck_codes), ck_scales, dh, ld_dh, dgu, ld_dgu, dgu_scales);
+        };
+        if (dt == LORA_BF16)
+            return enqueued(fn, dgu_scales ? go(swiglu_backward_kernel<Row8Bf16, true>)
+                                           : go(swiglu_backward_kernel<Row8Bf16, false>));
+        return enqueued(fn, dgu_scales ? go(swiglu_backward_kernel<Row8F32, true>)
+                                       : go(swiglu_backward_kernel<Row8F32, false>));
+    });
 }

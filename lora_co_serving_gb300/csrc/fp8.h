@@ -127,6 +127,20 @@ inline int refuse(int code, const std::string& msg) {
     set_last_error(msg.c_str());
     return code;
 }
+// A C entry's body: nothing it throws (host memory running out) leaves it
+template <class Body>
+auto guarded(Body body) -> decltype(body()) {
+    try {
+        return body();
+    } catch (...) {
+        set_last_error("out of host memory");
+        return LORA_ERR_LIMIT;
+    }
+}
+
+// Rows that a call takes: tiles are counted in 32 bits, past the last row by a tile's height at the most
+constexpr int32_t kMaxRowsOfX = INT32_MAX - 1024;
+
 // the return code of a call that launched, or failed to
 inline int enqueued(const char* fn, cudaError_t e) {
     if (e == cudaSuccess) return LORA_OK;

@@ -8,8 +8,10 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <mutex>
 #include <string>
 #include <type_traits>
+#include <vector>
 
 #include "fp8.h"
 #include "tc_kernel.h"
@@ -752,20 +754,18 @@ bool encode_y(CUtensorMap* m, const void* base, uint64_t N, uint64_t T, uint64_t
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-struct Device {
-    int sms = 0;
-    bool ready = false;
-};
-// SM count of the current device; on first use its kernels' shared memory limits
-cudaError_t device_info(Device** out) {
-    static Device devs[64];
+// SM count of the current device; on a device's first use its kernels' shared memory limits are raised
+cudaError_t device_sms(int* sms) {
+    static std::mutex mu;
+    static std::vector<int> known;             // by device, 0: not used yet
     int d = 0;
     cudaError_t e = cudaGetDevice(&d);
     if (e != cudaSuccess) return e;
-    if (d >= 64) return cudaErrorInvalidDevice;
-    Device& v = devs[d];
-    if (!v.ready) {
-        e = cudaDeviceGetAttribute(&v.sms, cudaDevAttrMultiProcessorCount, d);
+    std::lock_guard<std::mutex> lock(mu);
+    if ((int)known.size() <= d) known.resize(d + 1, 0);
+    if (known[d] == 0) {
+        int n = 0;
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d);
         auto allow = [&](auto kernel, size_t smem) {
             if (e == cudaSuccess)
                 e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -777,9 +777,9 @@ cudaError_t device_info(Device** out) {
         allow(linear_rows_kernel<32, void>, RowsCfg<32>::kSmem);
         allow(linear_rows_kernel<64, void>, RowsCfg<64>::kSmem);
         if (e != cudaSuccess) return e;
-        v.ready = true;
+        known[d] = n;
     }
-    *out = &v;
+    *sms = known[d];
     return cudaSuccess;
 }
 
@@ -866,6 +866,7 @@ int check_sizes(const char* fn, int32_t T, int32_t K, int32_t N) {
     if (K % 16 != 0 || N % 8 != 0)
         return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": K must be a multiple of 16 and N of 8");
     if (K > (1 << 22)) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": K above 2^22");
+    if (T > kMaxRowsOfX) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": T above 2^31 - 1025");
     const int64_t tiles = (((int64_t)T + kPM - 1) / kPM) * (((int64_t)N + kPN - 1) / kPN);
     if (tiles > INT32_MAX / 2) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": T x N above 2^46");
     return LORA_OK;
@@ -887,83 +888,92 @@ extern "C" size_t lora_fp8_workspace_size(int32_t T, int32_t K, int32_t N, int32
 extern "C" int lora_fp8_linear(int32_t T, int32_t K, int32_t N, lora_dtype_t dt, const void* x, int64_t ld_x,
                                const float* x_scales, const void* w, const float* w_scales, void* y, int64_t ld_y,
                                void* workspace, size_t ws_bytes, void* stream) {
-    const char* fn = "lora_fp8_linear";
-    if (!x_scales && dt != LORA_BF16 && dt != LORA_F32) return refuse(LORA_ERR_DTYPE, "unknown dtype");
-    int rc = check_sizes(fn, T, K, N);
-    if (rc != LORA_OK || T == 0) return rc;
-    rc = check_matrix(fn, "x", x, K, ld_x, x_scales ? 1 : elem_size(dt));
-    if (rc == LORA_OK) rc = check_matrix(fn, "w", w, K, K, 1);
-    if (rc == LORA_OK) rc = check_matrix(fn, "y", y, N, ld_y, 2);
-    if (rc != LORA_OK) return rc;
-    if (!w_scales) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": w_scales is NULL");
-    const Spread sp = spread_of(T, K, N);
-    const Scratch L = layout_of(T, K, x_scales != nullptr || T <= kQuantRows, sp);
-    if (!workspace) return refuse(LORA_ERR_WORKSPACE, "workspace is NULL");
-    if (!is_aligned(workspace, 256)) return refuse(LORA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-    if (ws_bytes < L.end)
-        return refuse(LORA_ERR_WORKSPACE, "workspace too small: need " + std::to_string(L.end) + " bytes, got " +
-                                              std::to_string(ws_bytes));
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    Device* dev = nullptr;
-    cudaError_t e = device_info(&dev);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool quant_here = !x_scales && T <= kQuantRows;      // by the product's kernel
-    if (e != cudaSuccess) return enqueued(fn, e);
-    const void* xc = x;
-    const float* xs = x_scales;
-    int64_t ld_c = ld_x;
-    if (!x_scales && !quant_here) {
-        e = launch_quantize(T, K, dt, x, ld_x, ws + L.codes, K, reinterpret_cast<float*>(ws + L.scales), st);
+    return guarded([&]() -> int {
+        const char* fn = "lora_fp8_linear";
+        if (!x_scales && dt != LORA_BF16 && dt != LORA_F32) return refuse(LORA_ERR_DTYPE, "unknown dtype");
+        int rc = check_sizes(fn, T, K, N);
+        if (rc != LORA_OK || T == 0) return rc;
+        rc = check_matrix(fn, "x", x, K, ld_x, x_scales ? 1 : elem_size(dt));
+        if (rc == LORA_OK) rc = check_matrix(fn, "w", w, K, K, 1);
+        if (rc == LORA_OK) rc = check_matrix(fn, "y", y, N, ld_y, 2);
+        if (rc != LORA_OK) return rc;
+        if (!w_scales) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": w_scales is NULL");
+        if (!is_aligned(w_scales, 4) || !is_aligned(x_scales, 4))
+            return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": scales must be aligned to a float");
+        const Spread sp = spread_of(T, K, N);
+        const Scratch L = layout_of(T, K, x_scales != nullptr || T <= kQuantRows, sp);
+        if (!workspace) return refuse(LORA_ERR_WORKSPACE, "workspace is NULL");
+        if (!is_aligned(workspace, 256)) return refuse(LORA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+        if (ws_bytes < L.end)
+            return refuse(LORA_ERR_WORKSPACE, "workspace too small: need " + std::to_string(L.end) + " bytes, got " +
+                                                  std::to_string(ws_bytes));
+        uint8_t* ws = static_cast<uint8_t*>(workspace);
+        int sms = 0;
+        cudaError_t e = device_sms(&sms);
         if (e != cudaSuccess) return enqueued(fn, e);
-        xc = ws + L.codes;
-        xs = reinterpret_cast<const float*>(ws + L.scales);
-        ld_c = K;
-    }
-    if (T <= kMaxRows) {
-        RowsParams R{};
-        const int nt = T <= 16 ? 16 : T <= 32 ? 32 : 64;
-        if (!encode_codes(&R.tm_w, w, K, N, K, 128) || (!quant_here && !encode_codes(&R.tm_x, xc, K, T, ld_c, nt)))
-            return refuse(LORA_ERR_CUDA, std::string(fn) + ": cuTensorMapEncodeTiled failed");
-        R.x = x;
-        R.ld_x = ld_x;
-        R.xs = xs;
-        R.ws = w_scales;
-        R.y = static_cast<__nv_bfloat16*>(y);
-        R.ld_y = ld_y;
-        R.T = T;
-        R.K = K;
-        R.N = N;
-        R.nb = blocks_of(K);
-        R.status = reinterpret_cast<int32_t*>(ws);
-        const int ranks = ranks_of(N, R.nb);
-        if (quant_here)
-            e = dt == LORA_BF16 ? launch_rows<16, Row8Bf16>(R, ranks, st) : launch_rows<16, Row8F32>(R, ranks, st);
-        else
-            e = nt == 16   ? launch_rows<16, void>(R, ranks, st)
-                : nt == 32 ? launch_rows<32, void>(R, ranks, st)
-                           : launch_rows<64, void>(R, ranks, st);
+        cudaStream_t st = static_cast<cudaStream_t>(stream);
+        const bool quant_here = !x_scales && T <= kQuantRows;      // by the product's kernel
+        const bool quant_first = !x_scales && !quant_here;
+        const void* xc = quant_first ? ws + L.codes : x;
+        const float* xs = quant_first ? reinterpret_cast<const float*>(ws + L.scales) : x_scales;
+        const int64_t ld_c = quant_first ? K : ld_x;
+        // every tensor map before the first launch
+        auto bad_map = [&] { return refuse(LORA_ERR_CUDA, std::string(fn) + ": cuTensorMapEncodeTiled failed"); };
+        auto quantize = [&] {
+            return quant_first ? launch_quantize(T, K, dt, x, ld_x, ws + L.codes, K, reinterpret_cast<float*>(ws + L.scales),
+                                                 st)
+                               : cudaSuccess;
+        };
+        if (T <= kMaxRows) {
+            RowsParams R{};
+            const int nt = T <= 16 ? 16 : T <= 32 ? 32 : 64;
+            if (!encode_codes(&R.tm_w, w, K, N, K, 128) || (!quant_here && !encode_codes(&R.tm_x, xc, K, T, ld_c, nt)))
+                return bad_map();
+            R.x = x;
+            R.ld_x = ld_x;
+            R.xs = xs;
+            R.ws = w_scales;
+            R.y = static_cast<__nv_bfloat16*>(y);
+            R.ld_y = ld_y;
+            R.T = T;
+            R.K = K;
+            R.N = N;
+            R.nb = blocks_of(K);
+            R.status = reinterpret_cast<int32_t*>(ws);
+            const int ranks = ranks_of(N, R.nb);
+            e = quantize();
+            if (e != cudaSuccess) return enqueued(fn, e);
+            if (quant_here)
+                e = dt == LORA_BF16 ? launch_rows<16, Row8Bf16>(R, ranks, st) : launch_rows<16, Row8F32>(R, ranks, st);
+            else
+                e = nt == 16   ? launch_rows<16, void>(R, ranks, st)
+                    : nt == 32 ? launch_rows<32, void>(R, ranks, st)
+                               : launch_rows<64, void>(R, ranks, st);
+            return enqueued(fn, e);
+        }
+        TileParams P{};
+        if (!encode_codes(&P.tm_x, xc, K, T, ld_c, 128) || !encode_codes(&P.tm_w, w, K, N, K, 128) ||
+            !encode_y(&P.tm_y, y, N, T, ld_y))
+            return bad_map();
+        P.xs = xs;
+        P.ws = w_scales;
+        P.T = T;
+        P.N = N;
+        P.nb = blocks_of(K);
+        P.wide_scales = P.nb % 4 == 0 && is_aligned(P.xs, 16) && is_aligned(P.ws, 16);
+        P.tiles_m = sp.tiles_m;
+        P.tiles_n = sp.tiles_n;
+        P.n_whole = sp.n_whole;
+        P.n_split = sp.n_split;
+        P.n_items = sp.n_items;
+        P.part = reinterpret_cast<float*>(ws + L.part);
+        P.status = reinterpret_cast<int32_t*>(ws);
+        e = quantize();
+        if (e == cudaSuccess)
+            e = launch_pdl(linear_tile_kernel, dim3(2 * std::min(sms / 2, sp.n_items)), dim3(kThreads), kTileSmem, st, P);
+        if (e == cudaSuccess && sp.n_cut() > 0)
+            e = launch_pdl(linear_join_kernel, dim3(32 * sp.n_cut()), dim3(256), 0, st, static_cast<const float*>(P.part),
+                           static_cast<__nv_bfloat16*>(y), ld_y, T, N, sp.tiles_m, sp.tiles_n, sp.n_whole, sp.n_split);
         return enqueued(fn, e);
-    }
-    TileParams P{};
-    if (!encode_codes(&P.tm_x, xc, K, T, ld_c, 128) || !encode_codes(&P.tm_w, w, K, N, K, 128) ||
-        !encode_y(&P.tm_y, y, N, T, ld_y))
-        return refuse(LORA_ERR_CUDA, std::string(fn) + ": cuTensorMapEncodeTiled failed");
-    P.xs = xs;
-    P.ws = w_scales;
-    P.T = T;
-    P.N = N;
-    P.nb = blocks_of(K);
-    P.wide_scales = P.nb % 4 == 0 && is_aligned(P.xs, 16) && is_aligned(P.ws, 16);
-    P.tiles_m = sp.tiles_m;
-    P.tiles_n = sp.tiles_n;
-    P.n_whole = sp.n_whole;
-    P.n_split = sp.n_split;
-    P.n_items = sp.n_items;
-    P.part = reinterpret_cast<float*>(ws + L.part);
-    P.status = reinterpret_cast<int32_t*>(ws);
-    e = launch_pdl(linear_tile_kernel, dim3(2 * std::min(dev->sms / 2, sp.n_items)), dim3(kThreads), kTileSmem, st, P);
-    if (e == cudaSuccess && sp.n_cut() > 0)
-        e = launch_pdl(linear_join_kernel, dim3(32 * sp.n_cut()), dim3(256), 0, st, static_cast<const float*>(P.part),
-                       static_cast<__nv_bfloat16*>(y), ld_y, T, N, sp.tiles_m, sp.tiles_n, sp.n_whole, sp.n_split);
-    return enqueued(fn, e);
+    });
 }

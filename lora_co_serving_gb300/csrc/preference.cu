@@ -199,12 +199,28 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(int32_t V, const type
             a.join(n2, s2);
         }
     }
+    // logits of 2^30 and beyond (a mask of the type's lowest value over the whole row) lose their differences in
+    // x log2(e) - n: one warp takes such a row again, from its largest logit
+    constexpr float kFar = 1073741824.f;
+    if (!(fabsf(__shfl_sync(0xffffffffu, a.n, 0)) < kFar)) {
+        float m = -INFINITY, s = 0.f;
+        for (int i = threadIdx.x; i < V; i += 32) m = fmaxf(m, E::get(row[i]));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int i = threadIdx.x; i < V; i += 32) s += __expf(E::get(row[i]) - m);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (threadIdx.x == 0) {                  // no finite logit: -infinity less itself, NaN
+            lse[t] = m + logf(s);
+            logp[t] = (at - m) - logf(s);
+        }
+        return;
+    }
     if (threadIdx.x == 0) {
-        // log of the sum is n log(2) + log(s); x - lse is formed from its small parts, not from the rounded lse.  A row
-        // without a finite logit: NaN
+        // log of the sum is n log(2) + log(s); x - lse is formed from its small parts, not from the rounded lse
         const float r = logf(a.s) + a.n * kLn2Low;
-        lse[t] = a.n == -INFINITY ? NAN : fmaf(a.n, kLn2High, r);
-        logp[t] = a.n == -INFINITY ? NAN : fmaf(-a.n, kLn2High, at) - r;
+        lse[t] = fmaf(a.n, kLn2High, r);
+        logp[t] = fmaf(-a.n, kLn2High, at) - r;
     }
 }
 
@@ -324,10 +340,11 @@ __global__ void __launch_bounds__(kThreads) dlogits_kernel(int32_t V, const type
     }
     float k = coef[seq] * (dloss ? dloss[seq / 2] : dloss_all);
     if (label >= V) k = NAN;
-    const float off = -lse[t] * kLog2e;
+    // x log2(e) - lse log2(e); for a far row (see logprob_kernel) x - lse first
+    const float z = lse[t], base = fabsf(z) < 1048576.f ? 0.f : z, off = base == 0.f ? -z * kLog2e : 0.f;
     const int hit = label < V ? (int)label : -1;
     auto grad = [&](float x, bool at) {
-        const float p = exp2_fast(fmaf(x, kLog2e, off));
+        const float p = exp2_fast(fmaf(x - base, kLog2e, off));
         return at ? k * (1.f - p) : -k * p;
     };
     // both rows on the same 16-byte phase: whole pieces; else element by element
@@ -449,79 +466,85 @@ using namespace lora;
 
 extern "C" int lora_token_logprob(int32_t T, int32_t V, lora_dtype_t dt, const void* logits, int64_t ld,
                                   const int64_t* labels, float* logp, float* lse, void* stream) {
-    const char* fn = "lora_token_logprob";
-    const int rc = check_logits(fn, T, V, dt, logits, ld, labels);
-    if (rc != LORA_OK || T == 0) return rc;
-    if (!logp || !lse) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": logp or lse is NULL");
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return enqueued(fn, dt == LORA_BF16 ? launch_logprob<Bf16>(T, V, logits, ld, labels, logp, lse, st)
-                                        : launch_logprob<F32>(T, V, logits, ld, labels, logp, lse, st));
+    return guarded([&]() -> int {
+        const char* fn = "lora_token_logprob";
+        const int rc = check_logits(fn, T, V, dt, logits, ld, labels);
+        if (rc != LORA_OK || T == 0) return rc;
+        if (!logp || !lse) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": logp or lse is NULL");
+        cudaStream_t st = static_cast<cudaStream_t>(stream);
+        return enqueued(fn, dt == LORA_BF16 ? launch_logprob<Bf16>(T, V, logits, ld, labels, logp, lse, st)
+                                            : launch_logprob<F32>(T, V, logits, ld, labels, logp, lse, st));
+    });
 }
 
 extern "C" int lora_preference_forward(int32_t T, int32_t V, lora_dtype_t dt, const void* logits, int64_t ld,
                                        const int64_t* labels, const float* ref_logp, const lora_pair_t* pairs,
                                        int32_t n_pairs, float beta, float label_smoothing, float* loss,
                                        float* rewards, float* logp, float* lse, float* coef, void* stream) {
-    const char* fn = "lora_preference_forward";
-    int rc = check_logits(fn, T, V, dt, logits, ld, labels);
-    if (rc != LORA_OK) return rc;
-    if (!(beta > 0.f) || isinf(beta) || !(label_smoothing >= 0.f && label_smoothing < 0.5f))
-        return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": beta must be positive and finite, "
-                                                              "label_smoothing in [0, 0.5)");
-    Sequences<LORA_MAX_PAIRS> seqs;
-    rc = check_pairs(fn, T, pairs, n_pairs, &seqs);
-    if (rc != LORA_OK) return rc;
-    if (T > 0 && (!ref_logp || !logp || !lse))
-        return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": ref_logp, logp or lse is NULL");
-    if (n_pairs > 0 && (!loss || !rewards || !coef))
-        return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": loss, rewards or coef is NULL");
-    if (T == 0 && n_pairs == 0) return LORA_OK;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaSuccess;
-    if (T > 0)
-        e = dt == LORA_BF16 ? launch_logprob<Bf16>(T, V, logits, ld, labels, logp, lse, st)
-                            : launch_logprob<F32>(T, V, logits, ld, labels, logp, lse, st);
-    if (e == cudaSuccess && n_pairs > 0) {
-        auto go = [&](auto p) {
-            constexpr int kPairs = sizeof(p.p) / sizeof(lora_pair_t);
-            std::copy(pairs, pairs + n_pairs, p.p);      // the first n_pairs are read
-            return launch_pdl(pair_loss_kernel<kPairs>, dim3(n_pairs), dim3(kPairThreads), 0, st, p, labels,
-                              static_cast<const float*>(logp), ref_logp, beta, label_smoothing, loss, rewards, coef);
-        };
-        e = n_pairs <= kFewPairs ? go(Pairs<kFewPairs>()) : go(Pairs<LORA_MAX_PAIRS>());
-    }
-    return enqueued(fn, e);
+    return guarded([&]() -> int {
+        const char* fn = "lora_preference_forward";
+        int rc = check_logits(fn, T, V, dt, logits, ld, labels);
+        if (rc != LORA_OK) return rc;
+        if (!(beta > 0.f) || isinf(beta) || !(label_smoothing >= 0.f && label_smoothing < 0.5f))
+            return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": beta must be positive and finite, "
+                                                                  "label_smoothing in [0, 0.5)");
+        Sequences<LORA_MAX_PAIRS> seqs;
+        rc = check_pairs(fn, T, pairs, n_pairs, &seqs);
+        if (rc != LORA_OK) return rc;
+        if (T > 0 && (!ref_logp || !logp || !lse))
+            return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": ref_logp, logp or lse is NULL");
+        if (n_pairs > 0 && (!loss || !rewards || !coef))
+            return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": loss, rewards or coef is NULL");
+        if (T == 0 && n_pairs == 0) return LORA_OK;
+        cudaStream_t st = static_cast<cudaStream_t>(stream);
+        cudaError_t e = cudaSuccess;
+        if (T > 0)
+            e = dt == LORA_BF16 ? launch_logprob<Bf16>(T, V, logits, ld, labels, logp, lse, st)
+                                : launch_logprob<F32>(T, V, logits, ld, labels, logp, lse, st);
+        if (e == cudaSuccess && n_pairs > 0) {
+            auto go = [&](auto p) {
+                constexpr int kPairs = sizeof(p.p) / sizeof(lora_pair_t);
+                std::copy(pairs, pairs + n_pairs, p.p);      // the first n_pairs are read
+                return launch_pdl(pair_loss_kernel<kPairs>, dim3(n_pairs), dim3(kPairThreads), 0, st, p, labels,
+                                  static_cast<const float*>(logp), ref_logp, beta, label_smoothing, loss, rewards, coef);
+            };
+            e = n_pairs <= kFewPairs ? go(Pairs<kFewPairs>()) : go(Pairs<LORA_MAX_PAIRS>());
+        }
+        return enqueued(fn, e);
+    });
 }
 
 extern "C" int lora_preference_backward(int32_t T, int32_t V, lora_dtype_t dt, const void* logits, int64_t ld,
                                         const int64_t* labels, const float* lse, const float* coef,
                                         const lora_pair_t* pairs, int32_t n_pairs, const float* dloss, void* dlogits,
                                         int64_t ld_d, void* stream) {
-    const char* fn = "lora_preference_backward";
-    int rc = check_logits(fn, T, V, dt, logits, ld, labels);
-    if (rc != LORA_OK) return rc;
-    Sequences<LORA_MAX_PAIRS> seqs;
-    rc = check_pairs(fn, T, pairs, n_pairs, &seqs);
-    if (rc != LORA_OK || T == 0) return rc;
-    if (!lse || !dlogits || (n_pairs > 0 && !coef))
-        return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": lse, coef or dlogits is NULL");
-    if (ld_d < V) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": rows of dlogits overlap (ld_d < V)");
-    if (!is_aligned(dlogits, elem_size(dt)))
-        return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": dlogits must be aligned to an element");
-    if (dlogits == logits && ld_d != ld)
-        return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": in place, ld_d must be ld");
-    const float all = n_pairs > 0 ? 1.f / (float)n_pairs : 0.f;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    auto go = [&](const auto& q) {
-        return dt == LORA_BF16
-                   ? launch_dlogits<Bf16>(T, V, logits, ld, labels, lse, coef, q, dloss, all, dlogits, ld_d, st)
-                   : launch_dlogits<F32>(T, V, logits, ld, labels, lse, coef, q, dloss, all, dlogits, ld_d, st);
-    };
-    if (n_pairs > kFewPairs) return enqueued(fn, go(seqs));
-    Sequences<kFewPairs> few;
-    few.n = seqs.n;
-    std::copy(seqs.start, seqs.start + seqs.n, few.start);
-    std::copy(seqs.end, seqs.end + seqs.n, few.end);
-    std::copy(seqs.id, seqs.id + seqs.n, few.id);
-    return enqueued(fn, go(few));
+    return guarded([&]() -> int {
+        const char* fn = "lora_preference_backward";
+        int rc = check_logits(fn, T, V, dt, logits, ld, labels);
+        if (rc != LORA_OK) return rc;
+        Sequences<LORA_MAX_PAIRS> seqs;
+        rc = check_pairs(fn, T, pairs, n_pairs, &seqs);
+        if (rc != LORA_OK || T == 0) return rc;
+        if (!lse || !dlogits || (n_pairs > 0 && !coef))
+            return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": lse, coef or dlogits is NULL");
+        if (ld_d < V) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": rows of dlogits overlap (ld_d < V)");
+        if (!is_aligned(dlogits, elem_size(dt)))
+            return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": dlogits must be aligned to an element");
+        if (dlogits == logits && ld_d != ld)
+            return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": in place, ld_d must be ld");
+        const float all = n_pairs > 0 ? 1.f / (float)n_pairs : 0.f;
+        cudaStream_t st = static_cast<cudaStream_t>(stream);
+        auto go = [&](const auto& q) {
+            return dt == LORA_BF16
+                       ? launch_dlogits<Bf16>(T, V, logits, ld, labels, lse, coef, q, dloss, all, dlogits, ld_d, st)
+                       : launch_dlogits<F32>(T, V, logits, ld, labels, lse, coef, q, dloss, all, dlogits, ld_d, st);
+        };
+        if (n_pairs > kFewPairs) return enqueued(fn, go(seqs));
+        Sequences<kFewPairs> few;
+        few.n = seqs.n;
+        std::copy(seqs.start, seqs.start + seqs.n, few.start);
+        std::copy(seqs.end, seqs.end + seqs.n, few.end);
+        std::copy(seqs.id, seqs.id + seqs.n, few.id);
+        return enqueued(fn, go(few));
+    });
 }

@@ -238,6 +238,38 @@ def test_large_logits_and_certain_rows():
     assert (np.abs(down(f[0]) - want) <= 2.0 ** -22 * np.abs(lse) + 2.0 ** -17).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [5, 1000, 9001])
+def test_rows_masked_with_a_finite_value(V, dtype):
+    """A mask of the type's lowest value (or -1e9) over most of a row leaves the rest as it is; over the whole row every
+    entry is as likely as any other, and the gradient stays finite."""
+    import torch
+    import lora_co_serving_gb300 as lm
+    low = float(torch.finfo({"bf16": torch.bfloat16, "f32": torch.float32}[dtype]).min)
+    x = up(np.random.default_rng(V).standard_normal((8, V)), dtype)
+    plain = x.clone()
+    keep = 3
+    x[0, keep:], plain[0, keep:] = low, float("-inf")
+    x[1, keep:], plain[1, keep:] = -1e9, float("-inf")
+    x[2] = low
+    x[3] = -1e9
+    x[4], x[4, 1] = low, low / 2
+    x[5] = 3e38
+    labels = np.array([1, 2, 0, V - 1, 1, 2, 0, 1])
+    lp, lse = lm.token_logprob(x, lab(labels))
+    same = lm.token_logprob(plain, lab(labels))
+    f = lm.preference_forward(x, lab(labels), up(np.zeros(8)), [(0, 4, 4, 4)])
+    d = lm.preference_backward(x, lab(labels), f.lse, f.coef, [(0, 4, 4, 4)])
+    torch.cuda.synchronize()
+    for t in (0, 1, 6, 7):
+        assert lp[t] == same[0][t] and lse[t] == same[1][t]
+    # far rows: logarithms of sums of exact exponentials (0 or 1), a few units in the last place; at -1e9 the row's
+    # exponent n is a number near 2^30.4, n log(2) is cut at 2^-24 of n (log(2) - its high part) = 2^11: 2^-12
+    assert np.abs(down(lp)[[2, 3, 5]] + np.log(V)).max() <= 2.0 ** -11
+    assert abs(down(lp)[4]) <= 2.0 ** -20
+    assert np.isfinite(down(f.loss)).all() and np.isfinite(down(d)).all()
+
+
 def test_offsets_past_32_bits():
     import torch
     import lora_co_serving_gb300 as lm

@@ -58,6 +58,8 @@ def test_linear(lib):
     assert f(ldx=60) == -1 and f(ldy=24) == -1
     assert f(ldx=68) == -5 and f(ldy=36) == -5
     assert f(xs=R, ldx=72) == -5                                     # codes' rows 72 bytes apart
+    assert f(ws=R + 2) == -5 and f(xs=R + 1) == -5
+    assert f(T=2 ** 31 - 1) == -10 and f(K=(1 << 22) + 16, ldx=BIG) == -10
     assert f(x=None) == -1 and f(w=None) == -1 and f(ws=None) == -1 and f(y=None) == -1
     assert f(work=None) == -6 and f(work=WS + 64) == -6 and f(n=255) == -6
     assert "too small" in err(lib)
@@ -166,6 +168,12 @@ def test_binding_checks_shapes():
     with pytest.raises(ValueError, match="coef"):
         lm.preference_backward(torch.zeros(4, 8), torch.zeros(4, dtype=torch.int64), torch.zeros(4), torch.zeros(4),
                                [(0, 2, 2, 2)])
+    for call in (lambda: lm.fp8_linear(x, w, ws), lambda: lm.fp8_quantize(x), lambda: lm.swiglu_forward(x),
+                 lambda: lm.fp8_quantize_weight(x),
+                 lambda: lm.token_logprob(torch.zeros(4, 8), torch.zeros(4, dtype=torch.int64)),
+                 lambda: lm.preference_forward(torch.zeros(4, 8), torch.zeros(4, dtype=torch.int64), torch.zeros(4), [])):
+        with pytest.raises(ValueError, match="one CUDA device"):     # host memory never reaches a kernel
+            call()
     with pytest.raises(lm.LoraError, match="segments"):
         lm.checkpoint_rows(4, [(0, 3, 0, 1)])
     assert lm.checkpoint_rows(4, [(0, 4, 0, 1)]) == 4
