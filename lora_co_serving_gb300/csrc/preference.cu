@@ -23,6 +23,10 @@ constexpr float kLog2eHigh = 1.44268798828125f;        // log2(e) to 16 bits, an
 constexpr float kLog2eLow = (float)(1.4426950408889634 - (double)kLog2eHigh);
 constexpr float kLn2High = 0.693145751953125f;         // log(2) to 16 bits, and the rest
 constexpr float kLn2Low = (float)(0.6931471805599453 - (double)kLn2High);
+// ex2.approx lies low by about this much on average: the mean error of 4096 rows' log-sum-exp was 2.4e-8 to 5.6e-8 over
+// vocabularies of 500 to 128256 and standard deviations of the logits from 1 to 3.  It is nothing against a row's own
+// rounding, 2e-7, but the same in every token of a sequence's sum.
+constexpr float kExp2Low = 4e-8f;
 constexpr int kPairThreads = 512;
 
 // 2^x; 0 for x = -infinity, results below the smallest normal number are 0
@@ -217,10 +221,13 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(int32_t V, const type
         return;
     }
     if (threadIdx.x == 0) {
-        // log of the sum is n log(2) + log(s); x - lse is formed from its small parts, not from the rounded lse
-        const float r = logf(a.s) + a.n * kLn2Low;
-        lse[t] = fmaf(a.n, kLn2High, r);
-        logp[t] = fmaf(-a.n, kLn2High, at) - r;
+        // log of the sum is n log(2) + log(s), with s brought to [1, 2) first; x - lse is formed from its small parts,
+        // not from the rounded lse.  (frexpf leaves a NaN as it is)
+        int e;
+        const float m = 2.f * frexpf(a.s, &e), n = a.n + (float)(e - 1);
+        const float r = logf(m) + fmaf(n, kLn2Low, kExp2Low);
+        lse[t] = fmaf(n, kLn2High, r);
+        logp[t] = fmaf(-n, kLn2High, at) - r;
     }
 }
 
