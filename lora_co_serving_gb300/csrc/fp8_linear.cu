@@ -99,8 +99,13 @@ __device__ __forceinline__ float2 halves(uint64_t a) {
 //
 // The CTAs of a cluster share the outputs: each loads its own 128 rows of x and half of the 256 rows of w, and the
 // halves go to both (TMA multicast), 32 KB per CTA and block for 128 * 256 * 128 products.  Everything else is the
-// CTA's own: an accumulator goes to and fro between the issuing thread and the adding warps once per block, and over
-// a CTA pair's shared MMAs that exchange takes about 1.2 us, several blocks' work.
+// CTA's own: an accumulator goes to and fro between the issuing warp and the adding warps once per block, and where the
+// leader of a CTA pair issues for both (cta_group::2) that exchange crosses SMs: 8192 x 8192 x 28672 then takes 2.9 ms.
+//
+// What bounds it: a block's MMAs are 512 cycles of tensor work, but its 48 KB are written to shared memory once and
+// read once, 750 cycles at 128 bytes a cycle; scaling and adding takes an accumulator about 550 cycles, of which 256
+// are its 128 x 256 multiply-adds.  Two accumulators hide most of that: a block takes about 770 cycles (clock counts
+// in the kernel), 0.37 us, and 8192 x 8192 x 28672 1.45 ms, 2650 TFLOP/s, under the power limit.
 //
 // 384 threads: warp 0 loads (TMA), warp 1 issues, warps 4..11 scale and add: each thread has one row of x and 128
 // outputs, which are one block of w's rows, so a block's 128 sums share one scale, sx[row] * sw[block].  The CTA
@@ -117,10 +122,8 @@ constexpr int kThreads = 384;
 constexpr int kLaunchRegs = 168, kIssueRegs = 56, kAddRegs = 224;
 static_assert(128 * kIssueRegs + 256 * kAddRegs <= kThreads * kLaunchRegs, "register split above the launch's");
 constexpr int kAddWarps = 8;
-constexpr int kOutBufs = 1;
 constexpr int kBars = 2 * kStages + 4;
-constexpr int kPieceBytes = 32 * 32 * 2;                 // 32 rows by 32 outputs on their way out
-constexpr int kOutBytes = kOutBufs * kPieceBytes;        // of each adding warp
+constexpr int kPieceBytes = 32 * 32 * 2;                 // an adding warp's 32 rows by 32 outputs on their way out
 constexpr int kScaleSlots = 8;                           // blocks whose scales are at hand (kStages + 2 are needed)
 constexpr int kScaleFloats = 132;                        // 128 rows of x, two blocks of w's rows, 8 bytes unused
 static_assert(kScaleSlots >= kStages + 2, "a slot would be overwritten while it is read");
@@ -350,8 +353,7 @@ __device__ __forceinline__ void tile_add(const TileParams& P, const Bars& B, uin
         // columns past the end are cut off there)
 #pragma unroll
         for (int piece = 0; piece < 4; ++piece) {
-            const uint32_t buf = stage_out + (piece % kOutBufs) * kPieceBytes;
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kOutBufs - 1) : "memory");   // buf's last store
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");      // the last piece is out
             __syncwarp();
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -361,14 +363,14 @@ __device__ __forceinline__ void tile_add(const TileParams& P, const Bars& B, uin
                     const float2 f = halves(acc[16 * piece + 4 * c + k]);
                     q[k] = pack_bf16(f.x, f.y);
                 }
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 64 +
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage_out + lane * 64 +
                                                                              ((c ^ ((lane >> 1) & 3)) * 16)),
                              "r"(q[0]), "r"(q[1]), "r"(q[2]), "r"(q[3])
                              : "memory");
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0 && t0 < P.T && n0 + 32 * piece < P.N) tma_store_2d(&P.tm_y, buf, n0 + 32 * piece, t0);
+            if (lane == 0 && t0 < P.T && n0 + 32 * piece < P.N) tma_store_2d(&P.tm_y, stage_out, n0 + 32 * piece, t0);
         }
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -380,7 +382,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t dsmem[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
     uint8_t* out = smem + kStages * kStageBytes;
-    float* slots = reinterpret_cast<float*>(out + kAddWarps * kOutBytes);
+    float* slots = reinterpret_cast<float*>(out + kAddWarps * kPieceBytes);
     uint64_t* bars = reinterpret_cast<uint64_t*>(slots + kScaleSlots * kScaleFloats);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
     Bars B;
@@ -423,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (warp >= 2) tile_scales(P, B, slots, rank, warp - 2, lane);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAddRegs));
-        tile_add(P, B, tmem, rank, warp, lane, slots, smem_u32(out) + (uint32_t)((warp - 4) * kOutBytes));
+        tile_add(P, B, tmem, rank, warp, lane, slots, smem_u32(out) + (uint32_t)((warp - 4) * kPieceBytes));
     }
     __syncwarp();
     tc_fence_before();
@@ -457,7 +459,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const float* __restric
         make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
-constexpr size_t kTileSmem = (size_t)kStages * kStageBytes + kAddWarps * kOutBytes +
+constexpr size_t kTileSmem = (size_t)kStages * kStageBytes + kAddWarps * kPieceBytes +
                              kScaleSlots * kScaleFloats * 4 + (kBars + 1) * 8 + 1024;
 static_assert(kTileSmem <= 227 * 1024, "shared memory of a CTA");
 
@@ -467,8 +469,8 @@ static_assert(kTileSmem <= 227 * 1024, "shared memory of a CTA");
 // Here the weight's bytes are the work, so w's rows are the MMA's M (128 outputs a CTA) and x's rows its N, padded to
 // NT: a product costs few tensor cycles and the sums of all NT rows of x stay in one thread per output.  K is cut over
 // the CTAs of a cluster, each with its own stages in flight, and their sums meet through distributed shared memory,
-// added in rank order.  An x of 16 rows or fewer is quantized on the way, by each CTA for its own K range (the
-// rows are read from L2 once per 128 outputs), which saves a launch; more rows come quantized.
+// added in rank order.  An x of few rows may be quantized on the way, by each CTA for its own K range (see
+// quantized_on_the_way); else it comes quantized.
 //
 // 256 threads: warp 0 loads (TMA), warp 1 issues, warps 2 and 3 bring the scales (and quantize), warps 4..7 scale and
 // add: each thread has one output.
@@ -478,10 +480,7 @@ constexpr int kMaxCluster = 8;
 template <int NT>
 struct RowsCfg {
     static constexpr int kStageB = kOperandBytes + NT * kQBlock;
-#ifndef FP8_RSTAGES
-#define FP8_RSTAGES 4
-#endif
-    static constexpr int kStages = FP8_RSTAGES;
+    static constexpr int kStages = 4;                      // 3 CTAs of 16 rows to an SM, 2 of 32 and of 64
     static constexpr int kSlots = 8;                       // blocks whose scales are at hand
     static constexpr int kSlotFloats = NT + 4;             // rows of x, one block of w's rows
     static constexpr uint32_t kCols = 2 * NT;              // two accumulators
@@ -515,7 +514,8 @@ struct RowsRing {
 };
 
 // Quantizes block kb of x's NT rows into a stage (rows of 128 bytes, 16-byte pieces swizzled as the MMA reads them) and
-// its scales into a slot; two warps share the rows, two rows of a warp at a time
+// its scales into a slot; two warps share the rows, two rows of a warp at a time.  Rows past the last one keep whatever
+// the stage and the slot hold: their sums are stored nowhere.
 template <int NT, class Row8>
 struct RowsQuant {
     static constexpr int kSteps = NT / 4;
@@ -529,10 +529,11 @@ struct RowsQuant {
             if (t < P.T && col < P.K) r[i].load(P.x, t * P.ld_x + col);
         }
     }
-    __device__ __forceinline__ void store(uint8_t* stage, float* slot, int which, int lane) const {
+    __device__ __forceinline__ void store(int T, uint8_t* stage, float* slot, int which, int lane) const {
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             const int t = 2 * (2 * i + which) + lane / kLanesPerBlock, c = lane % kLanesPerBlock;
+            if (t - lane / kLanesPerBlock >= T) break;
             float v[8], inv;
             r[i].get(v);
             const float sc = block_scale(max_over_block(r[i].abs_max()), &inv);
@@ -605,22 +606,27 @@ __global__ void __launch_bounds__(kRThreads) linear_rows_kernel(const __grid_con
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            RowsRing<NT> ring;
-            for (int kb = kb0, use = 0; kb < kb1; ++kb, ++use) {
-                const uint32_t acc = use & 1u;
-                if (!wait_phase(full + ring.stage * 8, ring.phase, abort_flag, P.status)) break;
-                if (!wait_phase(tempty + acc * 8, ((use >> 1) & 1u) ^ 1u, abort_flag, P.status)) break;
-                tc_fence_after();
-                const uint32_t sa = smem_u32(smem + ring.stage * C::kStageB), sb = sa + kOperandBytes;
+        // the whole warp, so that descriptors are uniform (see tile_issue)
+        const bool one = elect_one();
+        const uint64_t desc_w = smem_desc(smem_u32(smem), 16, 1024);
+        const uint64_t desc_x = smem_desc(smem_u32(smem) + kOperandBytes, 16, 1024);
+        RowsRing<NT> ring;
+        for (int kb = kb0, use = 0; kb < kb1; ++kb, ++use) {
+            const uint32_t acc = use & 1u;
+            wait_here(full + ring.stage * 8, ring.phase, abort_flag, P.status);    // after a time-out: on to the end
+            wait_here(tempty + acc * 8, ((use >> 1) & 1u) ^ 1u, abort_flag, P.status);
+            __syncwarp();
+            tc_fence_after();
+            const uint64_t at = (uint64_t)(ring.stage * (C::kStageB >> 4));
+            if (one) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    mma_e4m3(tmem + acc * NT, smem_desc(sa + k * 32, 16, 1024), smem_desc(sb + k * 32, 16, 1024),
-                             instr_desc_e4m3(128, NT), k > 0);
-                mma_commit(empty + ring.stage * 8);
+                    mma_e4m3(tmem + acc * NT, desc_w + at + 2 * k, desc_x + at + 2 * k, instr_desc_e4m3(128, NT), k > 0);
                 mma_commit(tfull + acc * 8);
-                ring.next();
+                mma_commit(empty + ring.stage * 8);
             }
+            __syncwarp();
+            ring.next();
         }
     } else if (warp < 4) {
         const int which = warp - 2;
@@ -640,7 +646,7 @@ __global__ void __launch_bounds__(kRThreads) linear_rows_kernel(const __grid_con
                 const bool ok = wait_phase(empty + ring.stage * 8, ring.phase ^ 1u, abort_flag, P.status);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 float* slot = slots + use % C::kSlots * C::kSlotFloats;
-                now.store(smem + ring.stage * C::kStageB + kOperandBytes, slot, which, lane);
+                now.store(P.T, smem + ring.stage * C::kStageB + kOperandBytes, slot, which, lane);
                 if (which == 0 && lane == 0) slot[NT] = w_now;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");     // the MMA reads what was stored
                 __syncwarp();
@@ -783,11 +789,13 @@ cudaError_t device_sms(int* sms) {
     return cudaSuccess;
 }
 
-// Rows of x up to which a product runs on linear_rows_kernel, and up to which it quantizes them itself
-#ifndef FP8_MAX_ROWS
-#define FP8_MAX_ROWS 64
-#endif
-constexpr int kMaxRows = FP8_MAX_ROWS, kQuantRows = 16;
+// Rows of x up to which a product runs on linear_rows_kernel: 64 x 4096 x 14336 takes 18 us there and 20 us on tiles,
+// 128 x 4096 x 28672 66 and 37 us.
+constexpr int kMaxRows = 64;
+// Whether that kernel quantizes x itself: a launch less, but a part of every 128 outputs' work.  For 16 rows and weights
+// of up to 32 MB: 16 x 4096 x 4096 takes 8.1 us of a program's time so (quantized first: 10.5 us, the host's part of two
+// launches), 16 x 4096 x 14336 20 us (14 us).
+bool quantized_on_the_way(int32_t T, int32_t K, int32_t N) { return T <= 16 && (int64_t)K * N <= (1 << 25); }
 
 // How the tiles are spread over the clusters.  Tiles beyond the last full round may be cut along K, into as many pieces
 // as clusters are left for each: a round of 4 tiles holds 72 of 76 clusters for a tile's whole time.  At most
@@ -830,15 +838,13 @@ Scratch layout_of(int32_t T, int32_t K, bool x_fp8, const Spread& s) {
     L.end = L.part + (size_t)s.n_cut() * s.n_split * kPM * kPN * sizeof(float);
     return L;
 }
-// CTAs of a cluster that share a tile's K: while the launch has fewer than two CTAs per SM, as long as each keeps
-// kMinBlocks blocks
-#ifndef FP8_RTARGET
-#define FP8_RTARGET 152
-#endif
+// CTAs of a cluster that share 128 outputs' K: more while the launch has fewer than one per SM and each keeps
+// kMinBlocks blocks.  Up to two per SM cost 64 x 4096 x 14336 22 us instead of 18 (another round of CTAs, each with its
+// set-up), and gained 16 x 8192 x 28672 1 us of 43.
 int ranks_of(int32_t N, int32_t nb) {
     const int tiles = (N + 127) / 128;
     int r = 1;
-    while (r < kMaxCluster && tiles * r < FP8_RTARGET && nb / (2 * r) >= kMinBlocks) r *= 2;
+    while (r < kMaxCluster && tiles * r < 2 * kClusters && nb / (2 * r) >= kMinBlocks) r *= 2;
     return r;
 }
 
@@ -882,7 +888,7 @@ using namespace lora;
 
 extern "C" size_t lora_fp8_workspace_size(int32_t T, int32_t K, int32_t N, int32_t x_fp8) {
     if (check_sizes("lora_fp8_workspace_size", T, K, N) != LORA_OK) return 0;
-    return layout_of(T, K, x_fp8 != 0 || T <= kQuantRows, spread_of(T, K, N)).end;
+    return layout_of(T, K, x_fp8 != 0 || quantized_on_the_way(T, K, N), spread_of(T, K, N)).end;
 }
 
 extern "C" int lora_fp8_linear(int32_t T, int32_t K, int32_t N, lora_dtype_t dt, const void* x, int64_t ld_x,
@@ -901,7 +907,7 @@ extern "C" int lora_fp8_linear(int32_t T, int32_t K, int32_t N, lora_dtype_t dt,
         if (!is_aligned(w_scales, 4) || !is_aligned(x_scales, 4))
             return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": scales must be aligned to a float");
         const Spread sp = spread_of(T, K, N);
-        const Scratch L = layout_of(T, K, x_scales != nullptr || T <= kQuantRows, sp);
+        const Scratch L = layout_of(T, K, x_scales != nullptr || quantized_on_the_way(T, K, N), sp);
         if (!workspace) return refuse(LORA_ERR_WORKSPACE, "workspace is NULL");
         if (!is_aligned(workspace, 256)) return refuse(LORA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
         if (ws_bytes < L.end)
@@ -912,7 +918,7 @@ extern "C" int lora_fp8_linear(int32_t T, int32_t K, int32_t N, lora_dtype_t dt,
         cudaError_t e = device_sms(&sms);
         if (e != cudaSuccess) return enqueued(fn, e);
         cudaStream_t st = static_cast<cudaStream_t>(stream);
-        const bool quant_here = !x_scales && T <= kQuantRows;      // by the product's kernel
+        const bool quant_here = !x_scales && quantized_on_the_way(T, K, N);
         const bool quant_first = !x_scales && !quant_here;
         const void* xc = quant_first ? ws + L.codes : x;
         const float* xs = quant_first ? reinterpret_cast<const float*>(ws + L.scales) : x_scales;
