@@ -109,25 +109,36 @@ __device__ __forceinline__ float2 halves(uint64_t a) {
 //
 // 384 threads: warp 0 loads (TMA), warp 1 issues, warps 4..11 scale and add: each thread has one row of x and 128
 // outputs, which are one block of w's rows, so a block's 128 sums share one scale, sx[row] * sw[block].  The CTA
-// starts with 168 registers a thread (64512 in all); the first warpgroup gives up 112 of them and the adding warps,
-// whose 128 sums must not spill, take 56 more: 128 * 56 + 256 * 224 = 64512.
+// starts with 168 registers a thread (64512 in all); the first warpgroup gives up 96 of them and the adding warps,
+// whose 128 sums must not spill, take 48 more: 128 * 72 + 256 * 216 = 64512.
 // =============================================================================================================
-constexpr int kPM = 256, kPN = 256;                      // rows of x and outputs of a cluster's tile
 constexpr int kOperandBytes = 128 * kQBlock;             // 128 rows of x or w, one block of columns
-constexpr int kXBytes = kOperandBytes;                   // a CTA's rows of x
-constexpr int kWBytes = kPN * kQBlock;                   // the tile's rows of w
-constexpr int kStageBytes = kXBytes + kWBytes;
-constexpr int kStages = 4;
 constexpr int kThreads = 384;
-constexpr int kLaunchRegs = 168, kIssueRegs = 56, kAddRegs = 224;
-static_assert(128 * kIssueRegs + 256 * kAddRegs <= kThreads * kLaunchRegs, "register split above the launch's");
+constexpr int kLaunchRegs = 168;
 constexpr int kAddWarps = 8;
-constexpr int kBars = 2 * kStages + 4;
 constexpr int kPieceBytes = 32 * 32 * 2;                 // an adding warp's 32 rows by 32 outputs on their way out
 constexpr int kScaleSlots = 8;                           // blocks whose scales are at hand (kStages + 2 are needed)
-constexpr int kScaleFloats = 132;                        // 128 rows of x, two blocks of w's rows, 8 bytes unused
-static_assert(kScaleSlots >= kStages + 2, "a slot would be overwritten while it is read");
-constexpr int kGroupM = 16;                              // tiles of x that share a sweep over w (see tile_at)
+constexpr int kScaleFloats = 132;                        // 128 rows of x, up to two blocks of w's rows
+constexpr int kGroupRows = 4096;                         // rows of x that share a sweep over w (see tile_at)
+
+// The shapes: kCtas CTAs of a cluster, 128 rows of x each, by kPN outputs.  {2, 256} moves and reads the least per
+// product; {2, 128} has twice the tiles, for products whose tiles of 256 leave clusters idle; {1, .} is for x of up to
+// 128 rows, which leave a cluster's second CTA nothing.  spread_of() weighs them.
+template <int kCtas_, int kPN_>
+struct TileCfg {
+    static constexpr int kCtas = kCtas_, kPN = kPN_, kPM = 128 * kCtas;
+    static constexpr int kWBytes = kPN * kQBlock;        // the tile's rows of w
+    static constexpr int kStageBytes = kOperandBytes + kWBytes;
+    static constexpr int kStages = kPN == 256 ? 4 : 6;
+    static constexpr int kCols = kPN / 2;                // outputs of an adding thread
+    static constexpr int kIssueRegs = kPN == 256 ? 72 : 104, kAddRegs = kPN == 256 ? 216 : 200;
+    static_assert(128 * kIssueRegs + 256 * kAddRegs <= kThreads * kLaunchRegs, "register split above the launch's");
+    static constexpr int kBars = 2 * kStages + 4;
+    static constexpr size_t kSmem = (size_t)kStages * kStageBytes + kAddWarps * kPieceBytes +
+                                    kScaleSlots * kScaleFloats * 4 + (kBars + 1) * 8 + 1024;
+    static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+    static_assert(kScaleSlots >= kStages + 2, "a slot would be overwritten while it is read");
+};
 
 struct TileParams {
     CUtensorMap tm_x, tm_w, tm_y;
@@ -147,16 +158,19 @@ struct Item {
     int tm, tn, kb0, kb1, piece;               // piece: its place in `part`, -1 for a whole tile
 };
 
-// Tiles in bands of kGroupM tiles of x: a band's columns are swept one after another, so that the tiles at work at any
+// Tiles in bands of kGroupRows rows of x: a band's columns are swept one after another, so that the tiles at work at any
 // time share few rows of x and of w.
+template <class C>
 __host__ __device__ __forceinline__ void tile_at(int tiles_m, int tiles_n, int i, int* tm, int* tn) {
-    const int band = kGroupM * tiles_n;
-    const int m0 = i / band * kGroupM;
-    const int left = tiles_m - m0, rows = left < kGroupM ? left : kGroupM;
+    constexpr int kGroup = kGroupRows / C::kPM;
+    const int band = kGroup * tiles_n;
+    const int m0 = i / band * kGroup;
+    const int left = tiles_m - m0, rows = left < kGroup ? left : kGroup;
     const int r = i % band;
     *tm = m0 + r % rows;
     *tn = r / rows;
 }
+template <class C>
 __device__ __forceinline__ Item item_at(const TileParams& P, int i) {
     Item it;
     it.kb0 = 0;
@@ -171,11 +185,12 @@ __device__ __forceinline__ Item item_at(const TileParams& P, int i) {
         it.kb0 = (int)((int64_t)P.nb * q / P.n_split);
         it.kb1 = (int)((int64_t)P.nb * (q + 1) / P.n_split);
     }
-    tile_at(P.tiles_m, P.tiles_n, tile, &it.tm, &it.tn);
+    tile_at<C>(P.tiles_m, P.tiles_n, tile, &it.tm, &it.tn);
     return it;
 }
 
-struct Ring {
+template <int kStages>
+struct StageRing {
     int stage = 0;
     uint32_t phase = 0;
     __device__ __forceinline__ void next() {
@@ -188,41 +203,47 @@ struct Bars {
     volatile int* abort_flag;
 };
 
+template <class C>
 __device__ __forceinline__ void tile_load(const TileParams& P, const Bars& B, uint8_t* smem, uint32_t rank) {
-    Ring ring;
+    StageRing<C::kStages> ring;
     uint32_t used = 0;
-    for (int i = blockIdx.x / 2; i < P.n_items; i += gridDim.x / 2) {
-        const Item it = item_at(P, i);
-        const int row_x = it.tm * kPM + 128 * (int)rank, row_w = it.tn * kPN + 128 * (int)rank;
+    for (int i = blockIdx.x / C::kCtas; i < P.n_items; i += gridDim.x / C::kCtas) {
+        const Item it = item_at<C>(P, i);
+        const int row_x = it.tm * C::kPM + 128 * (int)rank;
+        const int row_w = it.tn * C::kPN + C::kPN / C::kCtas * (int)rank;
         for (int kb = it.kb0; kb < it.kb1; ++kb) {
             // free in both CTAs: the half of w goes to both
             if (!wait_here(B.empty + ring.stage * 8, ring.phase ^ 1u, B.abort_flag, P.status)) {
-                drain_loads(B.full, used, kStages);
+                drain_loads(B.full, used, C::kStages);
                 return;
             }
             const uint32_t full = B.full + ring.stage * 8;
-            mbar_expect_tx(full, kStageBytes);
-            const uint32_t sa = smem_u32(smem + ring.stage * kStageBytes);
+            mbar_expect_tx(full, C::kStageBytes);
+            const uint32_t sa = smem_u32(smem + ring.stage * C::kStageBytes);
             tma_load_2d(sa, &P.tm_x, kb * kQBlock, row_x, full);
-            tma_load_2d_both(sa + kXBytes + rank * (kWBytes / 2), &P.tm_w, kb * kQBlock, row_w, full);
+            if constexpr (C::kCtas == 2)
+                tma_load_2d_both(sa + kOperandBytes + rank * (C::kWBytes / 2), &P.tm_w, kb * kQBlock, row_w, full);
+            else
+                tma_load_2d(sa + kOperandBytes, &P.tm_w, kb * kQBlock, row_w, full);
             ring.next();
             ++used;
         }
     }
     // the peer's last commits arrive on this CTA's barriers: none may be under way when the CTA ends
-    for (int s = 0; s < kStages; ++s, ring.next())
+    for (int s = 0; s < C::kStages; ++s, ring.next())
         if (!wait_here(B.empty + ring.stage * 8, ring.phase ^ 1u, B.abort_flag, P.status)) return;
 }
 
 // The whole warp runs this loop, and one lane issues: what the MMAs take (descriptors, addresses) is then uniform over
 // the warp.  In a loop of one lane alone, issuing a block took 480 cycles, more than its MMAs.
+template <class C>
 __device__ __forceinline__ void tile_issue(const TileParams& P, const Bars& B, uint8_t* smem, uint32_t tmem) {
     const bool one = elect_one();
-    const uint64_t desc_x = smem_desc(smem_u32(smem), 16, 1024), desc_w = smem_desc(smem_u32(smem) + kXBytes, 16, 1024);
-    Ring ring;
+    const uint64_t desc_x = smem_desc(smem_u32(smem), 16, 1024), desc_w = smem_desc(smem_u32(smem) + kOperandBytes, 16, 1024);
+    StageRing<C::kStages> ring;
     uint32_t use = 0;                          // blocks so far: accumulator use & 1
-    for (int i = blockIdx.x / 2; i < P.n_items; i += gridDim.x / 2) {
-        const Item it = item_at(P, i);
+    for (int i = blockIdx.x / C::kCtas; i < P.n_items; i += gridDim.x / C::kCtas) {
+        const Item it = item_at<C>(P, i);
         for (int kb = it.kb0; kb < it.kb1; ++kb, ++use) {
             const uint32_t acc = use & 1u;
             // after a time-out no wait holds any longer, here and in tile_add: the blocks are gone through to the end,
@@ -231,14 +252,17 @@ __device__ __forceinline__ void tile_issue(const TileParams& P, const Bars& B, u
             wait_here(B.tempty + acc * 8, ((use >> 1) & 1u) ^ 1u, B.abort_flag, P.status);
             __syncwarp();
             tc_fence_after();
-            const uint64_t at = (uint64_t)(ring.stage * (kStageBytes >> 4));
+            const uint64_t at = (uint64_t)(ring.stage * (C::kStageBytes >> 4));
             if (one) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    mma_e4m3(tmem + acc * kPN, desc_x + at + 2 * k, desc_w + at + 2 * k, instr_desc_e4m3(128, kPN),
-                             k > 0);
+                    mma_e4m3(tmem + acc * C::kPN, desc_x + at + 2 * k, desc_w + at + 2 * k,
+                             instr_desc_e4m3(128, C::kPN), k > 0);
                 mma_commit(B.tfull + acc * 8);
-                mma_commit_both(B.empty + ring.stage * 8);
+                if constexpr (C::kCtas == 2)
+                    mma_commit_both(B.empty + ring.stage * 8);
+                else
+                    mma_commit(B.empty + ring.stage * 8);
             }
             __syncwarp();
             ring.next();
@@ -252,13 +276,14 @@ __device__ __forceinline__ void tile_issue(const TileParams& P, const Bars& B, u
 // They arrive on the stage's barrier, so a block's MMAs, and with them its sums, come after its scales.
 // Slot kb % kScaleSlots is free once the MMAs of block kb - kStages are done, as they began after the adding warps had
 // finished with block kb - kStages - 2.
+template <class C>
 __device__ __forceinline__ void tile_scales(const TileParams& P, const Bars& B, float* slots, uint32_t rank, int which,
                                             int lane) {
-    Ring ring;
+    StageRing<C::kStages> ring;
     uint32_t use = 0;
-    for (int i = blockIdx.x / 2; i < P.n_items; i += gridDim.x / 2) {
-        const Item it = item_at(P, i);
-        const int t = it.tm * kPM + 128 * (int)rank + 64 * which + lane, n0 = it.tn * kPN + 128 * which;
+    for (int i = blockIdx.x / C::kCtas; i < P.n_items; i += gridDim.x / C::kCtas) {
+        const Item it = item_at<C>(P, i);
+        const int t = it.tm * C::kPM + 128 * (int)rank + 64 * which + lane, n0 = it.tn * C::kPN + (C::kPN == 256 ? 128 * which : 0);
         const float* x0 = P.xs + (int64_t)min(t, P.T - 1) * P.nb;          // rows past the end: any scale will do
         const float* x1 = P.xs + (int64_t)min(t + 32, P.T - 1) * P.nb;
         const float* w = P.ws + (int64_t)min(n0 / kQBlock, (P.N - 1) / kQBlock) * P.nb;
@@ -299,33 +324,34 @@ __device__ __forceinline__ void tile_scales(const TileParams& P, const Bars& B, 
     }
 }
 
+template <class C>
 __device__ __forceinline__ void tile_add(const TileParams& P, const Bars& B, uint32_t tmem, uint32_t rank, int warp,
                                          int lane, const float* slots, uint32_t stage_out) {
     const int quarter = warp & 3, half = (warp - 4) / 4;
-    const uint32_t taddr0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * 128;
+    const uint32_t taddr0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * C::kCols;
     uint32_t use = 0;
-    for (int i = blockIdx.x / 2; i < P.n_items; i += gridDim.x / 2) {
-        const Item it = item_at(P, i);
-        const int t0 = it.tm * kPM + 128 * (int)rank + quarter * 32;
-        const int n0 = it.tn * kPN + half * 128;
-        uint64_t acc[64];
+    for (int i = blockIdx.x / C::kCtas; i < P.n_items; i += gridDim.x / C::kCtas) {
+        const Item it = item_at<C>(P, i);
+        const int t0 = it.tm * C::kPM + 128 * (int)rank + quarter * 32;
+        const int n0 = it.tn * C::kPN + half * C::kCols;
+        uint64_t acc[C::kCols / 2];
 #pragma unroll
-        for (int j = 0; j < 64; ++j) acc[j] = 0;
+        for (int j = 0; j < C::kCols / 2; ++j) acc[j] = 0;
         for (int kb = it.kb0; kb < it.kb1; ++kb, ++use) {
             const uint32_t buf = use & 1u;
             wait_here(B.tfull + buf * 8, (use >> 1) & 1u, B.abort_flag, P.status);
             __syncwarp();
             tc_fence_after();
-            const uint32_t ta = taddr0 + buf * kPN;
+            const uint32_t ta = taddr0 + buf * C::kPN;
             uint32_t d[2][16];
             tmem_ld16(ta, d[0]);
             // written before the block's MMAs were issued (see tile_scales)
             const float* s = slots + (use % kScaleSlots) * kScaleFloats;
-            const uint64_t sc = both(s[quarter * 32 + lane] * s[128 + half]);
+            const uint64_t sc = both(s[quarter * 32 + lane] * s[128 + half * C::kCols / 128]);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 0; c < C::kCols / 16; ++c) {
                 tmem_ld_wait();
-                if (c < 7) {
+                if (c < C::kCols / 16 - 1) {
                     tmem_ld16(ta + 16 * (c + 1), d[(c + 1) & 1]);
                 } else {                       // read to the end: the accumulator goes back before the last sums
                     tc_fence_before();
@@ -337,12 +363,12 @@ __device__ __forceinline__ void tile_add(const TileParams& P, const Bars& B, uin
             }
         }
         if (it.piece >= 0) {
-            // [128 rows of a CTA][256 outputs] as groups of 4 outputs: a warp writes 512 contiguous bytes per group
-            float* part = P.part + ((int64_t)it.piece * 2 + rank) * (128 * kPN) +
-                          ((int64_t)half * 32 * 128 + quarter * 32 + lane) * 4;
+            // [128 rows of a CTA][kPN outputs] as groups of 4 outputs: a warp writes 512 contiguous bytes per group
+            float* part = P.part + ((int64_t)it.piece * C::kCtas + rank) * (128 * C::kPN) +
+                          ((int64_t)half * (C::kCols / 4) * 128 + quarter * 32 + lane) * 4;
             if (t0 < P.T && n0 < P.N) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
+                for (int c = 0; c < C::kCols / 4; ++c) {
                     const float2 f = halves(acc[2 * c]), g = halves(acc[2 * c + 1]);
                     __stcg(reinterpret_cast<float4*>(part + c * 512), make_float4(f.x, f.y, g.x, g.y));
                 }
@@ -352,7 +378,7 @@ __device__ __forceinline__ void tile_add(const TileParams& P, const Bars& B, uin
         // a warp's 32 rows leave in pieces of 32 columns, through shared memory, as one TMA store each (rows and
         // columns past the end are cut off there)
 #pragma unroll
-        for (int piece = 0; piece < 4; ++piece) {
+        for (int piece = 0; piece < C::kCols / 32; ++piece) {
             if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");      // the last piece is out
             __syncwarp();
 #pragma unroll
@@ -377,27 +403,27 @@ __device__ __forceinline__ void tile_add(const TileParams& P, const Bars& B, uin
     __syncwarp();
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    linear_tile_kernel(const __grid_constant__ TileParams P) {
+template <class C>
+__global__ void __launch_bounds__(kThreads, 1) linear_tile_kernel(const __grid_constant__ TileParams P) {
     extern __shared__ uint8_t dsmem[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
-    uint8_t* out = smem + kStages * kStageBytes;
+    uint8_t* out = smem + C::kStages * C::kStageBytes;
     float* slots = reinterpret_cast<float*>(out + kAddWarps * kPieceBytes);
     uint64_t* bars = reinterpret_cast<uint64_t*>(slots + kScaleSlots * kScaleFloats);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
     Bars B;
     B.abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     B.full = smem_u32(bars);
-    B.empty = B.full + kStages * 8;
-    B.tfull = B.empty + kStages * 8;
+    B.empty = B.full + C::kStages * 8;
+    B.tfull = B.empty + C::kStages * 8;
     B.tempty = B.tfull + 16;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_ctarank();
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < C::kStages; ++s) {
             mbar_init(B.full + s * 8, 3);            // the arm + the bytes of both CTAs' loads; warps 2 and 3
-            mbar_init(B.empty + s * 8, 2);           // both CTAs' commits
+            mbar_init(B.empty + s * 8, C::kCtas);    // every CTA's commit
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(B.tfull + b * 8, 1);
@@ -408,7 +434,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot))
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(2 * C::kPN)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -419,37 +446,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grid_dep_wait();
     if (blockIdx.x == 0 && threadIdx.x == 0) *P.status = 0;
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-        if (warp == 0 && lane == 0) tile_load(P, B, smem, rank);
-        if (warp == 1) tile_issue(P, B, smem, tmem);
-        if (warp >= 2) tile_scales(P, B, slots, rank, warp - 2, lane);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
+        if (warp == 0 && lane == 0) tile_load<C>(P, B, smem, rank);
+        if (warp == 1) tile_issue<C>(P, B, smem, tmem);
+        if (warp >= 2) tile_scales<C>(P, B, slots, rank, warp - 2, lane);
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAddRegs));
-        tile_add(P, B, tmem, rank, warp, lane, slots, smem_u32(out) + (uint32_t)((warp - 4) * kPieceBytes));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kAddRegs));
+        tile_add<C>(P, B, tmem, rank, warp, lane, slots, smem_u32(out) + (uint32_t)((warp - 4) * kPieceBytes));
     }
     __syncwarp();
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
     if (warp == 1)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * C::kPN) : "memory");
 }
 
 // Adds up the pieces of each cut tile, in their order, and writes its outputs.  One CTA per 32 rows by 64 outputs of
 // a tile; each warp adds 8 columns, a lane one row, so that every read is 512 contiguous bytes.
+template <class C>
 __global__ void __launch_bounds__(256) linear_join_kernel(const float* __restrict__ part, __nv_bfloat16* __restrict__ y,
                                                           int64_t ld_y, int32_t T, int32_t N, int32_t tiles_m,
                                                           int32_t tiles_n, int32_t n_whole, int32_t n_split) {
     grid_dep_wait();
-    const int cut = blockIdx.x / 32, sub = blockIdx.x % 32;
+    constexpr int kPerRow = C::kPN / 64, kPerTile = C::kPM / 32 * kPerRow;
+    const int cut = blockIdx.x / kPerTile, sub = blockIdx.x % kPerTile;
     int tm, tn;
-    tile_at(tiles_m, tiles_n, n_whole + cut, &tm, &tn);
-    const int row = sub / 4 * 32 + threadIdx.x % 32, col = sub % 4 * 64 + threadIdx.x / 32 * 8;
-    const int t = tm * kPM + row, n = tn * kPN + col;
+    tile_at<C>(tiles_m, tiles_n, n_whole + cut, &tm, &tn);
+    const int row = sub / kPerRow * 32 + threadIdx.x % 32, col = sub % kPerRow * 64 + threadIdx.x / 32 * 8;
+    const int t = tm * C::kPM + row, n = tn * C::kPN + col;
     if (t >= T || n >= N) return;
-    const float* p = part + ((int64_t)cut * n_split * 2 + row / 128) * (128 * kPN) + (int64_t)col * 128 + (row % 128) * 4;
+    const float* p = part + ((int64_t)cut * n_split * C::kCtas + row / 128) * (128 * C::kPN) + (int64_t)col * 128 + (row % 128) * 4;
     float v[8] = {};
-    for (int q = 0; q < n_split; ++q, p += 2 * 128 * kPN) {
+    for (int q = 0; q < n_split; ++q, p += C::kCtas * 128 * C::kPN) {
         const float4 a = __ldcg(reinterpret_cast<const float4*>(p));
         const float4 b = __ldcg(reinterpret_cast<const float4*>(p + 512));
         v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
@@ -458,10 +487,6 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const float* __restric
     *reinterpret_cast<uint4*>(y + t * ld_y + n) =
         make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
-
-constexpr size_t kTileSmem = (size_t)kStages * kStageBytes + kAddWarps * kPieceBytes +
-                             kScaleSlots * kScaleFloats * 4 + (kBars + 1) * 8 + 1024;
-static_assert(kTileSmem <= 227 * 1024, "shared memory of a CTA");
 
 // =============================================================================================================
 // Few rows (decode): 128 rows of w by all rows of x, K cut over a cluster.
@@ -502,15 +527,6 @@ struct RowsParams {
     int64_t ld_y;
     int32_t T, K, N, nb;
     int32_t* status;
-};
-
-template <int NT>
-struct RowsRing {
-    int stage = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next() {
-        if (++stage == RowsCfg<NT>::kStages) { stage = 0; phase ^= 1u; }
-    }
 };
 
 // Quantizes block kb of x's NT rows into a stage (rows of 128 bytes, 16-byte pieces swizzled as the MMA reads them) and
@@ -592,7 +608,7 @@ __global__ void __launch_bounds__(kRThreads) linear_rows_kernel(const __grid_con
 
     if (warp == 0) {
         if (lane == 0) {
-            RowsRing<NT> ring;
+            StageRing<C::kStages> ring;
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!wait_phase(empty + ring.stage * 8, ring.phase ^ 1u, abort_flag, P.status)) {
                     drain_loads(full, kb - kb0, C::kStages);
@@ -610,7 +626,7 @@ __global__ void __launch_bounds__(kRThreads) linear_rows_kernel(const __grid_con
         const bool one = elect_one();
         const uint64_t desc_w = smem_desc(smem_u32(smem), 16, 1024);
         const uint64_t desc_x = smem_desc(smem_u32(smem) + kOperandBytes, 16, 1024);
-        RowsRing<NT> ring;
+        StageRing<C::kStages> ring;
         for (int kb = kb0, use = 0; kb < kb1; ++kb, ++use) {
             const uint32_t acc = use & 1u;
             wait_here(full + ring.stage * 8, ring.phase, abort_flag, P.status);    // after a time-out: on to the end
@@ -630,7 +646,7 @@ __global__ void __launch_bounds__(kRThreads) linear_rows_kernel(const __grid_con
         }
     } else if (warp < 4) {
         const int which = warp - 2;
-        RowsRing<NT> ring;
+        StageRing<C::kStages> ring;
         const float* ws = P.ws + (int64_t)(n0 / kQBlock) * P.nb;
         if constexpr (kQuant) {
             RowsQuant<NT, Row8> q;
@@ -776,7 +792,10 @@ cudaError_t device_sms(int* sms) {
             if (e == cudaSuccess)
                 e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         };
-        allow(linear_tile_kernel, kTileSmem);
+        allow(linear_tile_kernel<TileCfg<2, 256>>, TileCfg<2, 256>::kSmem);
+        allow(linear_tile_kernel<TileCfg<2, 128>>, TileCfg<2, 128>::kSmem);
+        allow(linear_tile_kernel<TileCfg<1, 256>>, TileCfg<1, 256>::kSmem);
+        allow(linear_tile_kernel<TileCfg<1, 128>>, TileCfg<1, 128>::kSmem);
         allow(linear_rows_kernel<16, Row8Bf16>, RowsCfg<16>::kSmem);
         allow(linear_rows_kernel<16, Row8F32>, RowsCfg<16>::kSmem);
         allow(linear_rows_kernel<16, void>, RowsCfg<16>::kSmem);
@@ -789,40 +808,65 @@ cudaError_t device_sms(int* sms) {
     return cudaSuccess;
 }
 
-// Rows of x up to which a product runs on linear_rows_kernel: 64 x 4096 x 14336 takes 18 us there and 20 us on tiles,
-// 128 x 4096 x 28672 66 and 37 us.
-constexpr int kMaxRows = 64;
+// Whether a product runs on linear_rows_kernel: up to 32 rows, and up to 64 where the weight is small (32 MB):
+// 40 x 2704 x 2704 takes 7.4 us there (9.1 us on tiles), 64 x 4096 x 28672 27.6 us (25.2 us).
+constexpr int64_t kSmallWeight = 1 << 25;
+bool few_rows(int32_t T, int32_t K, int32_t N) { return T <= 32 || (T <= 64 && (int64_t)K * N <= kSmallWeight); }
 // Whether that kernel quantizes x itself: a launch less, but a part of every 128 outputs' work.  For 16 rows and weights
 // of up to 32 MB: 16 x 4096 x 4096 takes 8.1 us of a program's time so (quantized first: 10.5 us, the host's part of two
 // launches), 16 x 4096 x 14336 20 us (14 us).
-bool quantized_on_the_way(int32_t T, int32_t K, int32_t N) { return T <= 16 && (int64_t)K * N <= (1 << 25); }
+bool quantized_on_the_way(int32_t T, int32_t K, int32_t N) { return T <= 16 && (int64_t)K * N <= kSmallWeight; }
 
-// How the tiles are spread over the clusters.  Tiles beyond the last full round may be cut along K, into as many pieces
-// as clusters are left for each: a round of 4 tiles holds 72 of 76 clusters for a tile's whole time.  At most
-// kMaxSplit pieces of at least kMinBlocks blocks.  Cutting saves the blocks that run beside one another, 0.37 us each,
-// and costs the join: a second kernel, 3 us, and 0.04 us a piece for its sums (256 KB written and read back).  Measured
-// whole and cut: 1111 x 14336 x 4096 (4 tiles left, 8 pieces) 88 and 58 us, 65 x 2704 x 2704 (11, 5) 12.6 and 9.7 us;
-// the other way 256 x 4096 x 28672 (36, 2) 36.4 and 38.0 us, 600 x 2704 x 2704 (33, 2) 13.3 and 13.6 us.
+// A product's shape, and how its tiles are spread over the clusters.  Tiles beyond the last full round may be cut along
+// K, into as many pieces as clusters are left for each, at most kMaxSplit, of at least kMinBlocks blocks: a round of 4
+// tiles holds 72 of 76 clusters for a tile's whole time.  The choice is by an estimate from measured times: a block of a
+// tile of 256 outputs takes 0.345 us, of 128 outputs 0.273 us and the whole 1 us less; a join takes 1.6 us and 0.05 us
+// for each 256 KB of sums.  Measured, the other choice in brackets:
+//   whole or cut: 1111 x 14336 x 4096, 4 tiles left in 8 pieces, 58 us (whole 89), 65 x 2704 x 2704 8.2 us (10.7);
+//                 1000 x 2704 x 2704 whole, 44 tiles;
+//   128 outputs:  600 x 2704 x 2704 11.0 us (13.4), 300 x 512 x 2704 5.4 us (6.4); not 2000 x 2704 x 2704 22 us (25.6),
+//                 8192 x 8192 x 28672 1.43 ms (1.85);
+//   one CTA:      128 x 4096 x 28672 27 us (two: 35).
+// With one row of tiles the whole weight comes from memory, whose latency the six smaller stages of 128 outputs cover
+// better: 256 x 4096 x 28672 34.9 us (36.6), hence a factor of 0.85 there.
 constexpr int kMaxSplit = 8, kMinBlocks = 4;
-constexpr int kClusters = 76;                            // planned for (152 SMs); right on any device
+constexpr int kSms = 152;                                // planned for; right on any device
 struct Spread {
+    int ctas, pn;                                        // TileCfg
     int tiles_m, tiles_n, n_whole, n_split, n_items;
+    double us;                                           // estimate
     int n_cut() const { return tiles_m * tiles_n - n_whole; }
 };
-Spread spread_of(int32_t T, int32_t K, int32_t N) {
+Spread spread_as(int32_t T, int32_t K, int32_t N, int ctas, int pn) {
+    const double block = pn == 256 ? 0.345 : 0.273;
     Spread s{};
-    if (T <= kMaxRows) return s;
-    s.tiles_m = (T + kPM - 1) / kPM;
-    s.tiles_n = (N + kPN - 1) / kPN;
-    const int tiles = s.tiles_m * s.tiles_n, rest = tiles % kClusters, nb = blocks_of(K);
+    s.ctas = ctas;
+    s.pn = pn;
+    s.tiles_m = (int)(((int64_t)T + 128 * ctas - 1) / (128 * ctas));
+    s.tiles_n = (N + pn - 1) / pn;
+    const int clusters = kSms / ctas, tiles = s.tiles_m * s.tiles_n, rest = tiles % clusters, nb = blocks_of(K);
+    const int rounds = tiles / clusters;
     s.n_whole = tiles;
-    const int pieces = rest ? std::min({kClusters / rest, kMaxSplit, nb / kMinBlocks}) : 0;
-    if (pieces >= 2 && nb - (nb + pieces - 1) / pieces > 8 + rest * pieces / 9) {
-        s.n_split = pieces;
-        s.n_whole = tiles - rest;
+    s.us = (double)(rounds + (rest > 0)) * nb * block;
+    const int pieces = rest ? std::min({clusters / rest, kMaxSplit, nb / kMinBlocks}) : 0;
+    if (pieces >= 2) {
+        const double sums = (double)rest * pieces * ctas * pn / 512.0;
+        const double cut = ((double)rounds * nb + (nb + pieces - 1) / pieces) * block + 1.6 + 0.05 * sums;
+        if (cut < s.us) {
+            s.us = cut;
+            s.n_split = pieces;
+            s.n_whole = tiles - rest;
+        }
     }
+    if (pn == 128) s.us = (s.us - 1.0) * (s.tiles_m == 1 ? 0.85 : 1.0);
     s.n_items = s.n_whole + s.n_cut() * s.n_split;
     return s;
+}
+Spread spread_of(int32_t T, int32_t K, int32_t N) {
+    if (few_rows(T, K, N)) return Spread{};
+    const int ctas = T <= 128 ? 1 : 2;
+    const Spread wide = spread_as(T, K, N, ctas, 256), narrow = spread_as(T, K, N, ctas, 128);
+    return narrow.us < wide.us ? narrow : wide;
 }
 
 // Workspace: the status word, then x's codes and scales if x is quantized on the way, then the cut tiles' sums
@@ -835,7 +879,7 @@ Scratch layout_of(int32_t T, int32_t K, bool x_fp8, const Spread& s) {
     L.codes = 256;
     L.scales = L.codes + (x_fp8 ? 0 : al((size_t)T * K));
     L.part = L.scales + (x_fp8 ? 0 : al((size_t)T * blocks_of(K) * sizeof(float)));
-    L.end = L.part + (size_t)s.n_cut() * s.n_split * kPM * kPN * sizeof(float);
+    L.end = L.part + (size_t)s.n_cut() * s.n_split * (128 * s.ctas) * s.pn * sizeof(float);
     return L;
 }
 // CTAs of a cluster that share 128 outputs' K: more while the launch has fewer than one per SM and each keeps
@@ -844,7 +888,7 @@ Scratch layout_of(int32_t T, int32_t K, bool x_fp8, const Spread& s) {
 int ranks_of(int32_t N, int32_t nb) {
     const int tiles = (N + 127) / 128;
     int r = 1;
-    while (r < kMaxCluster && tiles * r < 2 * kClusters && nb / (2 * r) >= kMinBlocks) r *= 2;
+    while (r < kMaxCluster && tiles * r < kSms && nb / (2 * r) >= kMinBlocks) r *= 2;
     return r;
 }
 
@@ -866,6 +910,29 @@ cudaError_t launch_rows(const RowsParams& P, int ranks, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, linear_rows_kernel<NT, Row8>, P);
 }
 
+template <class C>
+cudaError_t launch_tiles(const TileParams& P, const Spread& sp, int sms, __nv_bfloat16* y, int64_t ld_y,
+                         cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(C::kCtas * std::min(sms / C::kCtas, sp.n_items)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C::kCtas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_tile_kernel<C>, P);
+    if (e != cudaSuccess || sp.n_cut() == 0) return e;
+    return launch_pdl(linear_join_kernel<C>, dim3((unsigned)(C::kPM / 32 * (C::kPN / 64) * sp.n_cut())), dim3(256), 0, st,
+                      static_cast<const float*>(P.part), y, ld_y, P.T, P.N, sp.tiles_m, sp.tiles_n, sp.n_whole,
+                      sp.n_split);
+}
+
 int check_sizes(const char* fn, int32_t T, int32_t K, int32_t N) {
     if (T < 0 || K <= 0 || N <= 0)
         return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": T must be >= 0, K and N > 0");
@@ -873,8 +940,8 @@ int check_sizes(const char* fn, int32_t T, int32_t K, int32_t N) {
         return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": K must be a multiple of 16 and N of 8");
     if (K > (1 << 22)) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": K above 2^22");
     if (T > kMaxRowsOfX) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": T above 2^31 - 1025");
-    const int64_t tiles = (((int64_t)T + kPM - 1) / kPM) * (((int64_t)N + kPN - 1) / kPN);
-    if (tiles > INT32_MAX / 2) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": T x N above 2^46");
+    const int64_t tiles = (((int64_t)T + 127) / 128) * (((int64_t)N + 127) / 128);
+    if (tiles > INT32_MAX / 2) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": T x N above 2^44");
     return LORA_OK;
 }
 
@@ -930,7 +997,7 @@ extern "C" int lora_fp8_linear(int32_t T, int32_t K, int32_t N, lora_dtype_t dt,
                                                  st)
                                : cudaSuccess;
         };
-        if (T <= kMaxRows) {
+        if (few_rows(T, K, N)) {
             RowsParams R{};
             const int nt = T <= 16 ? 16 : T <= 32 ? 32 : 64;
             if (!encode_codes(&R.tm_w, w, K, N, K, 128) || (!quant_here && !encode_codes(&R.tm_x, xc, K, T, ld_c, nt)))
@@ -958,7 +1025,7 @@ extern "C" int lora_fp8_linear(int32_t T, int32_t K, int32_t N, lora_dtype_t dt,
             return enqueued(fn, e);
         }
         TileParams P{};
-        if (!encode_codes(&P.tm_x, xc, K, T, ld_c, 128) || !encode_codes(&P.tm_w, w, K, N, K, 128) ||
+        if (!encode_codes(&P.tm_x, xc, K, T, ld_c, 128) || !encode_codes(&P.tm_w, w, K, N, K, sp.pn / sp.ctas) ||
             !encode_y(&P.tm_y, y, N, T, ld_y))
             return bad_map();
         P.xs = xs;
@@ -975,11 +1042,14 @@ extern "C" int lora_fp8_linear(int32_t T, int32_t K, int32_t N, lora_dtype_t dt,
         P.part = reinterpret_cast<float*>(ws + L.part);
         P.status = reinterpret_cast<int32_t*>(ws);
         e = quantize();
-        if (e == cudaSuccess)
-            e = launch_pdl(linear_tile_kernel, dim3(2 * std::min(sms / 2, sp.n_items)), dim3(kThreads), kTileSmem, st, P);
-        if (e == cudaSuccess && sp.n_cut() > 0)
-            e = launch_pdl(linear_join_kernel, dim3(32 * sp.n_cut()), dim3(256), 0, st, static_cast<const float*>(P.part),
-                           static_cast<__nv_bfloat16*>(y), ld_y, T, N, sp.tiles_m, sp.tiles_n, sp.n_whole, sp.n_split);
+        if (e != cudaSuccess) return enqueued(fn, e);
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(y);
+        if (sp.ctas == 2)
+            e = sp.pn == 256 ? launch_tiles<TileCfg<2, 256>>(P, sp, sms, out, ld_y, st)
+                             : launch_tiles<TileCfg<2, 128>>(P, sp, sms, out, ld_y, st);
+        else
+            e = sp.pn == 256 ? launch_tiles<TileCfg<1, 256>>(P, sp, sms, out, ld_y, st)
+                             : launch_tiles<TileCfg<1, 128>>(P, sp, sms, out, ld_y, st);
         return enqueued(fn, e);
     });
 }
