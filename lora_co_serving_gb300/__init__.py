@@ -618,6 +618,7 @@ def fp8_quantize_weight(W):
     return codes, scales
 
 
+@functools.lru_cache(maxsize=4096)
 def fp8_workspace_size(T, K, N, x_fp8=False):
     """Bytes of workspace that fp8_linear needs for these sizes (x given in 8 bits or not)."""
     n = library().lora_fp8_workspace_size(T, K, N, 1 if x_fp8 else 0)
