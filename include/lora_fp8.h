@@ -20,7 +20,8 @@
  * The conventions of lora_mixed.h hold: device pointers unless marked HOST; the caller owns every buffer; everything
  * is validated on the host, and a call that returns an error has launched and written nothing; work is enqueued on
  * `stream` and nothing is waited for.  All matrices are row-major with unit column stride; ld_* is the distance of
- * two rows in elements.  A size of zero rows is valid and launches nothing.  Limits: K, I <= 2^22 (LORA_ERR_LIMIT).
+ * two rows in elements.  A size of zero rows is valid and launches nothing.  Limits: K, I <= 2^22, T <= 2^31 -
+ * 1025, and for lora_fp8_linear T x N <= 2^44 (LORA_ERR_LIMIT).
  */
 #ifndef LORA_FP8_H
 #define LORA_FP8_H
@@ -40,7 +41,7 @@ int lora_fp8_quantize(int32_t T, int32_t K, lora_dtype_t dt, const void* x, int6
                       int64_t ld_codes, float* scales, void* stream);
 
 /* W [N,K] (element type dt, ld_w) -> codes [N,K] (contiguous) and scales [ceil(N/128), ceil(K/128)].  Done once for a
- * frozen weight.  K a multiple of 16; alignment as lora_fp8_quantize. */
+ * frozen weight.  K a multiple of 16, N <= 65535 * 128; alignment as lora_fp8_quantize. */
 int lora_fp8_quantize_weight(int32_t N, int32_t K, lora_dtype_t dt, const void* W, int64_t ld_w, void* codes,
                              float* scales, void* stream);
 

@@ -99,13 +99,16 @@ __device__ __forceinline__ float2 halves(uint64_t a) {
 //
 // The CTAs of a cluster share the outputs: each loads its own 128 rows of x and half of the 256 rows of w, and the
 // halves go to both (TMA multicast), 32 KB per CTA and block for 128 * 256 * 128 products.  Everything else is the
-// CTA's own: an accumulator goes to and fro between the issuing warp and the adding warps once per block, and where the
-// leader of a CTA pair issues for both (cta_group::2) that exchange crosses SMs: 8192 x 8192 x 28672 then takes 2.9 ms.
+// CTA's own: an accumulator goes to and fro between the issuing warp and the adding warps once per block.  A CTA pair
+// whose leader issues for both (cta_group::2) would halve w's share of shared memory, but gains nothing: accumulators
+// handed back by arrivals with release at cluster scope took 8192 x 8192 x 28672 to 2.9 ms, relaxed ones with a barrier
+// of the scales' own to 1.45 ms (this kernel beside it: 1.43 ms), and the adding warps' chain remains.
 //
-// What bounds it: a block's MMAs are 512 cycles of tensor work, but its 48 KB are written to shared memory once and
-// read once, 750 cycles at 128 bytes a cycle; scaling and adding takes an accumulator about 550 cycles, of which 256
-// are its 128 x 256 multiply-adds.  Two accumulators hide most of that: a block takes about 770 cycles (clock counts
-// in the kernel), 0.37 us, and 8192 x 8192 x 28672 1.45 ms, 2650 TFLOP/s, under the power limit.
+// What bounds it: a block's MMAs are 512 cycles of tensor work; its 48 KB are written to shared memory once and read
+// once, 750 cycles at 128 bytes a cycle; scaling and adding takes an accumulator about 550 cycles, of which 256 are its
+// 128 x 256 multiply-adds, and handing it over and back comes on top.  Two accumulators hide part of that: a block takes
+// about 770 cycles (clock counts in the kernel), 0.37 us, and 8192 x 8192 x 28672 1.45 ms, 2650 TFLOP/s, under the power
+// limit.  Shared memory alone is not the bound: a pair's 512 cycles of it gave the same time.
 //
 // 384 threads: warp 0 loads (TMA), warp 1 issues, warps 4..11 scale and add: each thread has one row of x and 128
 // outputs, which are one block of w's rows, so a block's 128 sums share one scale, sx[row] * sw[block].  The CTA
