@@ -347,11 +347,10 @@ __global__ void __launch_bounds__(kThreads) dlogits_kernel(int32_t V, const type
     }
     float k = coef[seq] * (dloss ? dloss[seq / 2] : dloss_all);
     if (label >= V) k = NAN;
-    // x log2(e) - lse log2(e); for a far row (see logprob_kernel) x - lse first
-    const float z = lse[t], base = fabsf(z) < 1048576.f ? 0.f : z, off = base == 0.f ? -z * kLog2e : 0.f;
+    const float z = lse[t];
     const int hit = label < V ? (int)label : -1;
     auto grad = [&](float x, bool at) {
-        const float p = exp2_fast(fmaf(x - base, kLog2e, off));
+        const float p = exp2_fast((x - z) * kLog2e);
         return at ? k * (1.f - p) : -k * p;
     };
     // both rows on the same 16-byte phase: whole pieces; else element by element
