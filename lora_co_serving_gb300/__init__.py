@@ -797,13 +797,14 @@ def preference_forward(logits, labels, ref_logp, pairs, beta=0.1, label_smoothin
     _vector(ref_logp, "ref_logp", torch.float32, T)
     _one_device(logits, labels, ref_logp)
     p, n = _table(pairs)
-    logp, lse, loss, rewards, coef = ref_logp.new_empty(2 * T + 5 * n).split_with_sizes([T, T, n, 2 * n, 2 * n])
+    new = ref_logp.new_empty
+    logp, lse, loss, rewards, coef = new(T), new(T), new(n), new((n, 2)), new((n, 2))
     rc = library().lora_preference_forward(T, V, code, logits.data_ptr(), ld, labels.data_ptr(), ref_logp.data_ptr(),
                                            p, n, beta, label_smoothing, loss.data_ptr(), rewards.data_ptr(),
                                            logp.data_ptr(), lse.data_ptr(), coef.data_ptr(), _stream_ptr(None))
     if rc != 0:
         _check(rc)
-    return Preference(loss, rewards.view(n, 2), logp, lse, coef.view(n, 2))
+    return Preference(loss, rewards, logp, lse, coef)
 
 
 @_on_stream
