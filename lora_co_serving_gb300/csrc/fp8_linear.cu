@@ -125,8 +125,9 @@ constexpr int kScaleFloats = 132;                        // 128 rows of x, up to
 constexpr int kGroupRows = 4096;                         // rows of x that share a sweep over w (see tile_at)
 
 // The shapes: kCtas CTAs of a cluster, 128 rows of x each, by kPN outputs.  {2, 256} moves and reads the least per
-// product; {2, 128} has twice the tiles, for products whose tiles of 256 leave clusters idle; {1, .} is for x of up to
-// 128 rows, which leave a cluster's second CTA nothing.  spread_of() weighs them.
+// product; {2, 128} has twice the tiles, for products whose tiles of 256 leave clusters idle; {1, .} cuts x into 128 rows
+// for each SM by itself: 9 tiles where clusters need 10 for 1111 rows, and any one of 152 places for each.  spread_of()
+// weighs them.
 template <int kCtas_, int kPN_>
 struct TileCfg {
     static constexpr int kCtas = kCtas_, kPN = kPN_, kPM = 128 * kCtas;
@@ -822,16 +823,18 @@ bool quantized_on_the_way(int32_t T, int32_t K, int32_t N) { return T <= 16 && (
 
 // A product's shape, and how its tiles are spread over the clusters.  Tiles beyond the last full round may be cut along
 // K, into as many pieces as clusters are left for each, at most kMaxSplit, of at least kMinBlocks blocks: a round of 4
-// tiles holds 72 of 76 clusters for a tile's whole time.  The choice is by an estimate from measured times: a block of a
-// tile of 256 outputs takes 0.345 us, of 128 outputs 0.273 us and the whole 1 us less; a join takes 1.6 us and 0.05 us
-// for each 256 KB of sums.  Measured, the other choice in brackets:
-//   whole or cut: 1111 x 14336 x 4096, 4 tiles left in 8 pieces, 58 us (whole 89), 65 x 2704 x 2704 8.2 us (10.7);
-//                 1000 x 2704 x 2704 whole, 44 tiles;
-//   128 outputs:  600 x 2704 x 2704 11.0 us (13.4), 300 x 512 x 2704 5.4 us (6.4); not 2000 x 2704 x 2704 22 us (25.6),
-//                 8192 x 8192 x 28672 1.43 ms (1.85);
-//   one CTA:      128 x 4096 x 28672 27 us (two: 35).
-// With one row of tiles the whole weight comes from memory, whose latency the six smaller stages of 128 outputs cover
-// better: 256 x 4096 x 28672 34.9 us (36.6), hence a factor of 0.85 there.
+// tiles holds 72 of 76 clusters for a tile's whole time.  The choice is by an estimate, whose numbers were fitted to 120
+// products of 80 to 3000 rows timed in all four shapes (K and N from 512 to 28672): the estimate is 8 % off (rms), the
+// shape it takes 0.7 % slower than the best of the four, 9 % at the worst (500 x 5120 x 5120).  Measured, us:
+//                              2 x 256   2 x 128   1 x 256   1 x 128
+//    300 x   512 x  2704           6.6       5.7       6.5       5.5
+//    256 x  4096 x 28672          38.5      35.2      38.1      34.9
+//    600 x  2704 x  2704          14.2      11.3      18.2      12.8
+//   1500 x  2704 x  2704          15.7      18.9      17.8      21.9
+//    777 x  5120 x  5120          28.6      34.1      21.6      28.8   44 wide tiles of two CTAs, one round of 140 of one
+//   1111 x 14336 x  4096          60.2      77.3      49.8      69.2   76 wide tiles and 4 more; one round of 144 of one
+//   2048 x 28672 x  8192           370                 388
+//   8192 x  8192 x 28672          1430      1850      1520      1900
 constexpr int kMaxSplit = 8, kMinBlocks = 4;
 constexpr int kSms = 152;                                // planned for; right on any device
 struct Spread {
@@ -841,7 +844,10 @@ struct Spread {
     int n_cut() const { return tiles_m * tiles_n - n_whole; }
 };
 Spread spread_as(int32_t T, int32_t K, int32_t N, int ctas, int pn) {
-    const double block = pn == 256 ? 0.345 : 0.273;
+    // a block; a tile's outputs on their way out, while no sums are added up; a join, and each 256 KB that it reads
+    double block = pn == 256 ? 0.40 : 0.29;
+    const double out = pn == 256 ? 1.5 : 0.8, join = 2.6, join_sums = 0.06;
+    if (ctas == 1) block *= 1.04;                        // w is read from L2 once per CTA
     Spread s{};
     s.ctas = ctas;
     s.pn = pn;
@@ -850,26 +856,36 @@ Spread spread_as(int32_t T, int32_t K, int32_t N, int ctas, int pn) {
     const int clusters = kSms / ctas, tiles = s.tiles_m * s.tiles_n, rest = tiles % clusters, nb = blocks_of(K);
     const int rounds = tiles / clusters;
     s.n_whole = tiles;
-    s.us = (double)(rounds + (rest > 0)) * nb * block;
+    s.us = (double)(rounds + (rest > 0)) * (nb * block + out);
     const int pieces = rest ? std::min({clusters / rest, kMaxSplit, nb / kMinBlocks}) : 0;
     if (pieces >= 2) {
         const double sums = (double)rest * pieces * ctas * pn / 512.0;
-        const double cut = ((double)rounds * nb + (nb + pieces - 1) / pieces) * block + 1.6 + 0.05 * sums;
+        const double cut = (double)rounds * (nb * block + out) + (double)((nb + pieces - 1) / pieces) * block + join +
+                           join_sums * sums;
         if (cut < s.us) {
             s.us = cut;
             s.n_split = pieces;
             s.n_whole = tiles - rest;
         }
     }
-    if (pn == 128) s.us = (s.us - 1.0) * (s.tiles_m == 1 ? 0.85 : 1.0);
+    // with one row of tiles the whole weight comes from memory, whose latency the narrow shapes' six smaller stages
+    // cover better than four
+    if (pn == 128 && s.tiles_m == 1) s.us *= 0.9;
     s.n_items = s.n_whole + s.n_cut() * s.n_split;
     return s;
 }
 Spread spread_of(int32_t T, int32_t K, int32_t N) {
     if (few_rows(T, K, N)) return Spread{};
-    const int ctas = T <= 128 ? 1 : 2;
-    const Spread wide = spread_as(T, K, N, ctas, 256), narrow = spread_as(T, K, N, ctas, 128);
-    return narrow.us < wide.us ? narrow : wide;
+    Spread best = spread_as(T, K, N, 1, 256);
+    auto weigh = [&](const Spread& s) {
+        if (s.us < best.us) best = s;
+    };
+    weigh(spread_as(T, K, N, 1, 128));
+    if (T > 128) {                                       // else a cluster's second CTA has no rows
+        weigh(spread_as(T, K, N, 2, 256));
+        weigh(spread_as(T, K, N, 2, 128));
+    }
+    return best;
 }
 
 // Workspace: the status word, then x's codes and scales if x is quantized on the way, then the cut tiles' sums

@@ -168,6 +168,21 @@ def test_linear(T, K, N, dtype):
     assert (np.abs(down(y) - ref) <= tol).all(), np.max(np.abs(down(y) - ref) / tol)
 
 
+# tiles of one CTA and of two, of 128 outputs and of 256, in one round and in several, whole and cut along K
+@pytest.mark.parametrize("T,K,N", [(300, 1552, 136), (2100, 144, 2056), (777, 5136, 2712),       # 1 CTA, 128
+                                   (300, 144, 12296), (2100, 144, 4104), (300, 5136, 2056), (777, 2064, 6152),  # 1, 256
+                                   (129, 1552, 136), (385, 144, 12296), (300, 2704, 2704),       # 2, 128
+                                   (129, 144, 12296), (777, 144, 9224), (385, 2704, 12296)])     # 2, 256
+def test_linear_tile_shapes(T, K, N):
+    import torch
+    import lora_co_serving_gb300 as lm
+    (args, kw), *vals = product(T + K + N, T, K, N, "fp8")
+    y = lm.fp8_linear(*args, check_status=True, **kw)
+    ref, tol = expect(*vals)
+    assert (np.abs(down(y) - ref) <= tol).all(), np.max(np.abs(down(y) - ref) / tol)
+    assert torch.equal(y, lm.fp8_linear(*args, **kw))
+
+
 @pytest.mark.parametrize("T", [1, 5, 40, 130, 300])
 def test_linear_strides_and_edges(T):
     """Rows of x and y lie apart; nothing beyond y's columns is written; another stream; repeated calls agree."""
