@@ -129,7 +129,7 @@ constexpr int kThreads = 384;
 constexpr int kLaunchRegs = 168;
 constexpr int kAddWarps = 8;
 constexpr int kPieceBytes = 32 * 32 * 2;                 // an adding warp's 32 rows by 32 outputs on their way out
-constexpr int kScaleSlots = 8;                           // blocks whose scales are at hand (kStages + 2 are needed)
+constexpr int kScaleSlots = 16;                          // blocks whose scales are at hand (see TileCfg)
 constexpr int kScaleFloats = 132;                        // 128 rows of x, up to two blocks of w's rows
 constexpr int kGroupRows = 4096;                         // rows of x that share a sweep over w (see tile_at)
 
@@ -141,8 +141,13 @@ template <int kCtas_, int kPN_>
 struct TileCfg {
     static constexpr int kCtas = kCtas_, kPN = kPN_, kPM = 128 * kCtas;
     static constexpr int kWBytes = kPN * kQBlock;        // the tile's rows of w
-    static constexpr int kStageBytes = kOperandBytes + kWBytes;
-    static constexpr int kStages = kPN == 256 ? 4 : 6;
+    // What passes the barriers at a time: one block, or two of 128 outputs, whose MMAs take 256 cycles each: issuing a
+    // block (two barrier tests, four MMAs, two commits: about 400 cycles) would take longer.  500 x 4096 x 4096 takes
+    // 11.7 us so, 13.2 us a block at a time.
+    static constexpr int kStep = 256 / kPN;
+    static constexpr int kBlockBytes = kOperandBytes + kWBytes, kStageBytes = kStep * kBlockBytes;
+    static constexpr int kStages = kPN == 256 ? 4 : 3;
+    static constexpr int kAccCols = kStep * kPN;
     static constexpr int kCols = kPN / 2;                // outputs of an adding thread
     static constexpr int kIssueRegs = kPN == 256 ? 72 : 104, kAddRegs = kPN == 256 ? 216 : 200;
     static_assert(128 * kIssueRegs + 256 * kAddRegs <= kThreads * kLaunchRegs, "register split above the launch's");
@@ -150,7 +155,7 @@ struct TileCfg {
     static constexpr size_t kSmem = (size_t)kStages * kStageBytes + kAddWarps * kPieceBytes +
                                     kScaleSlots * kScaleFloats * 4 + (kBars + 1) * 8 + 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
-    static_assert(kScaleSlots >= kStages + 2, "a slot would be overwritten while it is read");
+    static_assert(kScaleSlots >= kStep * (kStages + 2), "a slot would be overwritten while it is read");
 };
 
 struct TileParams {
@@ -195,8 +200,8 @@ __device__ __forceinline__ Item item_at(const TileParams& P, int i) {
     } else {
         const int q = it.piece % P.n_split;
         tile = P.n_whole + it.piece / P.n_split;
-        it.kb0 = (int)((int64_t)P.nb * q / P.n_split);
-        it.kb1 = (int)((int64_t)P.nb * (q + 1) / P.n_split);
+        it.kb0 = (int)((int64_t)P.nb * q / P.n_split) / C::kStep * C::kStep;
+        if (q + 1 < P.n_split) it.kb1 = (int)((int64_t)P.nb * (q + 1) / P.n_split) / C::kStep * C::kStep;
     }
     tile_at<C>(P.tiles_m, P.tiles_n, tile, &it.tm, &it.tn);
     return it;
@@ -226,21 +231,27 @@ __device__ __forceinline__ void tile_load(const TileParams& P, const Bars& B, ui
         const Item it = item_at<C>(P, i);
         const int row_x = it.tm * C::kPM + 128 * (int)rank;
         const int row_w = it.tn * C::kPN + C::kPN / C::kCtas * (int)rank;
-        for (int kb = it.kb0; kb < it.kb1; ++kb) {
+        for (int kb = it.kb0; kb < it.kb1; kb += C::kStep) {
             // free in both CTAs: the half of w goes to both
             const bool ok = wait_here(B.empty + ring.stage * 8, ring.phase ^ 1u, B.abort_flag, P.status);
             if (!__all_sync(0xffffffffu, ok)) {
                 drain_loads(B.full, used, C::kStages);
                 return;
             }
+            const int n = min(C::kStep, it.kb1 - kb);
             const uint32_t full = B.full + ring.stage * 8, sa = smem_u32(smem + ring.stage * C::kStageBytes);
             if (one) {
-                mbar_expect_tx(full, C::kStageBytes);
-                tma_load_2d(sa, &P.tm_x, kb * kQBlock, row_x, full);
-                if constexpr (C::kCtas == 2)
-                    tma_load_2d_both(sa + kOperandBytes + rank * (C::kWBytes / 2), &P.tm_w, kb * kQBlock, row_w, full);
-                else
-                    tma_load_2d(sa + kOperandBytes, &P.tm_w, kb * kQBlock, row_w, full);
+                mbar_expect_tx(full, n * C::kBlockBytes);
+#pragma unroll
+                for (int g = 0; g < C::kStep; ++g) {
+                    if (g >= n) break;
+                    const uint32_t sx = sa + g * C::kBlockBytes, sw = sx + kOperandBytes;
+                    tma_load_2d(sx, &P.tm_x, (kb + g) * kQBlock, row_x, full);
+                    if constexpr (C::kCtas == 2)
+                        tma_load_2d_both(sw + rank * (C::kWBytes / 2), &P.tm_w, (kb + g) * kQBlock, row_w, full);
+                    else
+                        tma_load_2d(sw, &P.tm_w, (kb + g) * kQBlock, row_w, full);
+                }
             }
             __syncwarp();
             ring.next();
@@ -259,10 +270,10 @@ __device__ __forceinline__ void tile_issue(const TileParams& P, const Bars& B, u
     const bool one = elect_one();
     const uint64_t desc_x = smem_desc(smem_u32(smem), 16, 1024), desc_w = smem_desc(smem_u32(smem) + kOperandBytes, 16, 1024);
     StageRing<C::kStages> ring;
-    uint32_t use = 0;                          // blocks so far: accumulator use & 1
+    uint32_t use = 0;                          // steps so far: accumulator use & 1
     for (int i = blockIdx.x / C::kCtas; i < P.n_items; i += gridDim.x / C::kCtas) {
         const Item it = item_at<C>(P, i);
-        for (int kb = it.kb0; kb < it.kb1; ++kb, ++use) {
+        for (int kb = it.kb0; kb < it.kb1; kb += C::kStep, ++use) {
             const uint32_t acc = use & 1u;
             // after a time-out no wait holds any longer, here and in tile_add: the blocks are gone through to the end,
             // their values lost
@@ -273,9 +284,13 @@ __device__ __forceinline__ void tile_issue(const TileParams& P, const Bars& B, u
             const uint64_t at = (uint64_t)(ring.stage * (C::kStageBytes >> 4));
             if (one) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_e4m3(tmem + acc * C::kPN, desc_x + at + 2 * k, desc_w + at + 2 * k,
-                             instr_desc_e4m3(128, C::kPN), k > 0);
+                for (int g = 0; g < C::kStep; ++g) {
+                    if (kb + g >= it.kb1) break;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_e4m3(tmem + acc * C::kAccCols + g * C::kPN, desc_x + at + g * (C::kBlockBytes >> 4) + 2 * k,
+                                 desc_w + at + g * (C::kBlockBytes >> 4) + 2 * k, instr_desc_e4m3(128, C::kPN), k > 0);
+                }
                 mma_commit(B.tfull + acc * 8);
                 if constexpr (C::kCtas == 2)
                     mma_commit_both(B.empty + ring.stage * 8);
@@ -327,16 +342,20 @@ __device__ __forceinline__ void tile_scales(const TileParams& P, const Bars& B, 
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if (g0 + j < kb0 || g0 + j >= it.kb1) continue;
-                const bool ok = wait_here(B.empty + ring.stage * 8, ring.phase ^ 1u, B.abort_flag, P.status);
-                if (!__all_sync(0xffffffffu, ok)) return;
-                float* s = slots + (use % kScaleSlots) * kScaleFloats;
+                if (j % C::kStep == 0) {       // items start with a step
+                    const bool ok = wait_here(B.empty + ring.stage * 8, ring.phase ^ 1u, B.abort_flag, P.status);
+                    if (!__all_sync(0xffffffffu, ok)) return;
+                }
+                float* s = slots + (use * C::kStep + j % C::kStep) % kScaleSlots * kScaleFloats;
                 s[64 * which + lane] = a[j];
                 s[64 * which + 32 + lane] = b[j];
                 if (lane == 0) s[128 + which] = c[j];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(B.full + ring.stage * 8);
-                ++use;
-                ring.next();
+                if (j % C::kStep == C::kStep - 1 || g0 + j == it.kb1 - 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(B.full + ring.stage * 8);
+                    ++use;
+                    ring.next();
+                }
             }
         }
     }
@@ -355,29 +374,36 @@ __device__ __forceinline__ void tile_add(const TileParams& P, const Bars& B, uin
         uint64_t acc[C::kCols / 2];
 #pragma unroll
         for (int j = 0; j < C::kCols / 2; ++j) acc[j] = 0;
-        for (int kb = it.kb0; kb < it.kb1; ++kb, ++use) {
+        for (int kb = it.kb0; kb < it.kb1; kb += C::kStep, ++use) {
             const uint32_t buf = use & 1u;
             wait_here(B.tfull + buf * 8, (use >> 1) & 1u, B.abort_flag, P.status);
             __syncwarp();
             tc_fence_after();
-            const uint32_t ta = taddr0 + buf * C::kPN;
+            const uint32_t ta = taddr0 + buf * C::kAccCols;
             uint32_t d[2][16];
             tmem_ld16(ta, d[0]);
-            // written before the block's MMAs were issued (see tile_scales)
-            const float* s = slots + (use % kScaleSlots) * kScaleFloats;
-            const uint64_t sc = both(s[quarter * 32 + lane] * s[128 + half * C::kCols / 128]);
+            // written before the step's MMAs were issued (see tile_scales); of a block past the end: any value
+            uint64_t sc[C::kStep];
 #pragma unroll
-            for (int c = 0; c < C::kCols / 16; ++c) {
+            for (int g = 0; g < C::kStep; ++g) {
+                const float* s = slots + (use * C::kStep + g) % kScaleSlots * kScaleFloats;
+                sc[g] = both(s[quarter * 32 + lane] * s[128 + half * C::kCols / 128]);
+            }
+            constexpr int kChunks = C::kCols / 16;
+#pragma unroll
+            for (int i = 0; i < C::kStep * kChunks; ++i) {
+                const int g = i / kChunks, c = i % kChunks;
+                if (kb + g >= it.kb1) break;
                 tmem_ld_wait();
-                if (c < C::kCols / 16 - 1) {
-                    tmem_ld16(ta + 16 * (c + 1), d[(c + 1) & 1]);
+                if (c < kChunks - 1 || (g < C::kStep - 1 && kb + g + 1 < it.kb1)) {
+                    tmem_ld16(ta + (i + 1) / kChunks * C::kPN + (i + 1) % kChunks * 16, d[(i + 1) & 1]);
                 } else {                       // read to the end: the accumulator goes back before the last sums
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(B.tempty + buf * 8);
                 }
 #pragma unroll
-                for (int q = 0; q < 8; ++q) fma2(acc[8 * c + q], d[c & 1][2 * q], d[c & 1][2 * q + 1], sc);
+                for (int q = 0; q < 8; ++q) fma2(acc[8 * c + q], d[i & 1][2 * q], d[i & 1][2 * q + 1], sc[g]);
             }
         }
         if (it.piece >= 0) {
@@ -453,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tile_kernel(const __grid_c
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                     "r"(2 * C::kPN)
+                     "r"(2 * C::kAccCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -477,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tile_kernel(const __grid_c
     cluster_sync_all();
     tc_fence_after();
     if (warp == 1)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * C::kPN) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * C::kAccCols) : "memory");
 }
 
 // Adds up the pieces of each cut tile, in their order, and writes its outputs.  One CTA per 32 rows by 64 outputs of
@@ -840,17 +866,18 @@ bool quantized_on_the_way(int32_t T, int32_t K, int32_t N) { return T <= 16 && (
 
 // A product's shape, and how its tiles are spread over the clusters.  Tiles beyond the last full round may be cut along
 // K, into as many pieces as clusters are left for each, at most kMaxSplit, of at least kMinBlocks blocks: a round of 4
-// tiles holds 72 of 76 clusters for a tile's whole time.  The choice is by an estimate, whose numbers were fitted to 120
-// products of 80 to 3000 rows timed in all four shapes (K and N from 512 to 28672): the estimate is 8 % off (rms), the
-// shape it takes 0.7 % slower than the best of the four, 9 % at the worst (500 x 5120 x 5120).  Measured, us:
+// tiles holds 72 of 76 clusters for a tile's whole time.  The choice is by an estimate, whose numbers were fitted to 167
+// products of 68 to 3000 rows timed in all four shapes (K and N from 512 to 28672): the estimate is 8 % off (rms), the
+// shape it takes 0.5 % slower than the best of the four, 9 % at the worst (777 x 512 x 2704).  Measured, us:
 //                              2 x 256   2 x 128   1 x 256   1 x 128
-//    300 x   512 x  2704           6.6       5.7       6.5       5.5
-//    256 x  4096 x 28672          38.5      35.2      38.1      34.9
-//    600 x  2704 x  2704          14.2      11.3      18.2      12.8
-//   1500 x  2704 x  2704          15.7      18.9      17.8      21.9
-//    777 x  5120 x  5120          28.6      34.1      21.6      28.8   44 wide tiles of two CTAs, one round of 140 of one
-//   1111 x 14336 x  4096          60.2      77.3      49.8      69.2   76 wide tiles and 4 more; one round of 144 of one
-//   2048 x 28672 x  8192           370                 388
+//    300 x   512 x  2704           6.7       5.6       6.4       5.5
+//    256 x  4096 x 28672          37.7      33.9      37.6      34.3
+//    600 x  2704 x  2704          13.9      10.9      15.3      12.9
+//   1500 x  2704 x  2704          14.2      17.8      17.6      21.7
+//    300 x  5120 x  5120          20.4      19.5      18.1      14.6   120 narrow tiles of one CTA, one round
+//    777 x  5120 x  5120          28.4      28.9      21.1      24.3   80 wide tiles of two CTAs, one round of 140 of one
+//   1111 x 14336 x  4096          59.2      65.6      48.7      60.3   80 wide tiles of two CTAs, one round of 144 of one
+//   2048 x 28672 x  8192           365                 388
 //   8192 x  8192 x 28672          1430      1850      1520      1900
 constexpr int kMaxSplit = 8, kMinBlocks = 4;
 constexpr int kSms = 152;                                // planned for; right on any device
@@ -862,9 +889,9 @@ struct Spread {
 };
 Spread spread_as(int32_t T, int32_t K, int32_t N, int ctas, int pn) {
     // a block; a tile's outputs on their way out, while no sums are added up; a join, and each 256 KB that it reads
-    double block = pn == 256 ? 0.40 : 0.29;
-    const double out = pn == 256 ? 1.5 : 0.8, join = 2.6, join_sums = 0.06;
-    if (ctas == 1) block *= 1.04;                        // w is read from L2 once per CTA
+    double block = pn == 256 ? 0.415 : 0.243;
+    const double out = pn == 256 ? 1.3 : 0.8, join = 2.7, join_sums = 0.05;
+    if (ctas == 1) block *= 1.05;                        // w is read from L2 once per CTA
     Spread s{};
     s.ctas = ctas;
     s.pn = pn;
@@ -885,9 +912,6 @@ Spread spread_as(int32_t T, int32_t K, int32_t N, int ctas, int pn) {
             s.n_whole = tiles - rest;
         }
     }
-    // with one row of tiles the whole weight comes from memory, whose latency the narrow shapes' six smaller stages
-    // cover better than four
-    if (pn == 128 && s.tiles_m == 1) s.us *= 0.9;
     s.n_items = s.n_whole + s.n_cut() * s.n_split;
     return s;
 }

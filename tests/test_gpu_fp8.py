@@ -168,11 +168,13 @@ def test_linear(T, K, N, dtype):
     assert (np.abs(down(y) - ref) <= tol).all(), np.max(np.abs(down(y) - ref) / tol)
 
 
-# tiles of one CTA and of two, of 128 outputs and of 256, in one round and in several, whole and cut along K
-@pytest.mark.parametrize("T,K,N", [(300, 1552, 136), (2100, 144, 2056), (777, 5136, 2712),       # 1 CTA, 128
-                                   (300, 144, 12296), (2100, 144, 4104), (300, 5136, 2056), (777, 2064, 6152),  # 1, 256
-                                   (129, 1552, 136), (385, 144, 12296), (300, 2704, 2704),       # 2, 128
-                                   (129, 144, 12296), (777, 144, 9224), (385, 2704, 12296)])     # 2, 256
+# tiles of one CTA and of two, of 128 outputs and of 256, in one round and in several, whole and cut along K, with an
+# even and an odd number of blocks
+@pytest.mark.parametrize("T,K,N", [(300, 1552, 136), (2100, 144, 2056), (777, 5136, 2712), (70, 1552, 136),
+                                   (300, 144, 12296), (2100, 144, 4104), (300, 5136, 2056), (777, 2064, 6152),
+                                   (300, 8208, 2056), (777, 4112, 6152), (129, 1552, 136), (129, 1680, 136),
+                                   (385, 144, 12296), (300, 2704, 2704), (900, 4112, 2712), (129, 144, 12296),
+                                   (777, 144, 9224), (385, 2704, 12296), (129, 8208, 6152), (385, 4112, 12296)])
 def test_linear_tile_shapes(T, K, N):
     import torch
     import lora_co_serving_gb300 as lm
