@@ -855,14 +855,14 @@ cudaError_t device_sms(int* sms) {
     return cudaSuccess;
 }
 
-// Whether a product runs on linear_rows_kernel: up to 32 rows, and up to 64 where the weight is small (32 MB):
-// 40 x 2704 x 2704 takes 7.4 us there (9.1 us on tiles), 64 x 4096 x 28672 27.6 us (25.2 us).
-constexpr int64_t kSmallWeight = 1 << 25;
-bool few_rows(int32_t T, int32_t K, int32_t N) { return T <= 32 || (T <= 64 && (int64_t)K * N <= kSmallWeight); }
-// Whether that kernel quantizes x itself: a launch less, but a part of every 128 outputs' work.  For 16 rows and weights
-// of up to 32 MB: 16 x 4096 x 4096 takes 8.1 us of a program's time so (quantized first: 10.5 us, the host's part of two
-// launches), 16 x 4096 x 14336 20 us (14 us).
-bool quantized_on_the_way(int32_t T, int32_t K, int32_t N) { return T <= 16 && (int64_t)K * N <= kSmallWeight; }
+// Whether a product runs on linear_rows_kernel: up to 32 rows, and up to 64 where K is long enough to be cut and N does not
+// fill the SMs by itself.  64 x 8192 x 8192 takes 16.8 us there (19.1 us on tiles), 64 x 2704 x 2704 7.7 us (8.5 us);
+// 64 x 512 x 2704 7.0 us (5.1 us), 64 x 4096 x 28672 27.8 us (25.1 us); 32 x 4096 x 28672 24.3 us (24.7 us).
+bool few_rows(int32_t T, int32_t K, int32_t N) { return T <= 32 || (T <= 64 && K > 1024 && N <= 8192); }
+// Whether that kernel quantizes x itself: a launch less, but a part of every 128 outputs' work, so for few products.  In a
+// program's loop 16 x 4096 x 4096 takes 8.0 us so (quantized first: 9.6 us, the host's part of two launches), 1 x 4096 x
+// 28672 24.6 us (24.8 us), 16 x 5120 x 5120 13.2 us (9.6 us).
+bool quantized_on_the_way(int32_t T, int32_t K, int32_t N) { return T <= 16 && (int64_t)T * K * N <= (1 << 28); }
 
 // A product's shape, and how its tiles are spread over the clusters.  Tiles beyond the last full round may be cut along
 // K, into as many pieces as clusters are left for each, at most kMaxSplit, of at least kMinBlocks blocks: a round of 4
