@@ -116,8 +116,9 @@ __device__ __forceinline__ float2 halves(uint64_t a) {
 // What bounds it: a block's MMAs are 512 cycles of tensor work; its 48 KB are written to shared memory once and read
 // once, 750 cycles at 128 bytes a cycle; scaling and adding takes an accumulator about 550 cycles, of which 256 are its
 // 128 x 256 multiply-adds, and handing it over and back comes on top.  Two accumulators hide part of that: a block takes
-// about 770 cycles (clock counts in the kernel), 0.37 us, and 8192 x 8192 x 28672 1.45 ms, 2650 TFLOP/s, under the power
-// limit.  With the multiply-adds left out it takes 1.35 ms, with the TMEM reads left out too 1.27 ms (a pair: 1.18 ms).
+// 730 to 770 cycles (clock counts in the kernel), and 8192 x 8192 x 28672 1.45 ms, 2650 TFLOP/s, at the 1.57 GHz that the
+// power limit leaves of 2.07.  With the multiply-adds left out it takes 1.35 ms, with the TMEM reads left out too 1.27 ms
+// (a pair: 1.18 ms).
 //
 // 384 threads: warp 0 loads (TMA), warp 1 issues, warps 4..11 scale and add: each thread has one row of x and 128
 // outputs, which are one block of w's rows, so a block's 128 sums share one scale, sx[row] * sw[block].  The CTA
