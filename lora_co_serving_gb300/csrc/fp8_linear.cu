@@ -269,7 +269,8 @@ __device__ __forceinline__ void tile_load(const TileParams& P, const Bars& B, ui
 template <class C>
 __device__ __forceinline__ void tile_issue(const TileParams& P, const Bars& B, uint8_t* smem, uint32_t tmem) {
     const bool one = elect_one();
-    const uint64_t desc_x = smem_desc(smem_u32(smem), 16, 1024), desc_w = smem_desc(smem_u32(smem) + kOperandBytes, 16, 1024);
+    const uint64_t desc_x = smem_desc(smem_u32(smem), 16, 1024);
+    const uint64_t desc_w = smem_desc(smem_u32(smem) + kOperandBytes, 16, 1024);
     StageRing<C::kStages> ring;
     uint32_t use = 0;                          // steps so far: accumulator use & 1
     for (int i = blockIdx.x / C::kCtas; i < P.n_items; i += gridDim.x / C::kCtas) {
@@ -317,7 +318,8 @@ __device__ __forceinline__ void tile_scales(const TileParams& P, const Bars& B, 
     uint32_t use = 0;
     for (int i = blockIdx.x / C::kCtas; i < P.n_items; i += gridDim.x / C::kCtas) {
         const Item it = item_at<C>(P, i);
-        const int t = it.tm * C::kPM + 128 * (int)rank + 64 * which + lane, n0 = it.tn * C::kPN + (C::kPN == 256 ? 128 * which : 0);
+        const int t = it.tm * C::kPM + 128 * (int)rank + 64 * which + lane;
+        const int n0 = it.tn * C::kPN + (C::kPN == 256 ? 128 * which : 0);
         const float* x0 = P.xs + (int64_t)min(t, P.T - 1) * P.nb;          // rows past the end: any scale will do
         const float* x1 = P.xs + (int64_t)min(t + 32, P.T - 1) * P.nb;
         const float* w = P.ws + (int64_t)min(n0 / kQBlock, (P.N - 1) / kQBlock) * P.nb;
@@ -521,7 +523,8 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const float* __restric
     const int row = sub / kPerRow * 32 + threadIdx.x % 32, col = sub % kPerRow * 64 + threadIdx.x / 32 * 8;
     const int t = tm * C::kPM + row, n = tn * C::kPN + col;
     if (t >= T || n >= N) return;
-    const float* p = part + ((int64_t)cut * n_split * C::kCtas + row / 128) * (128 * C::kPN) + (int64_t)col * 128 + (row % 128) * 4;
+    const float* p = part + ((int64_t)cut * n_split * C::kCtas + row / 128) * (128 * C::kPN) + (int64_t)col * 128 +
+                     (row % 128) * 4;
     float v[8] = {};
     for (int q = 0; q < n_split; ++q, p += C::kCtas * 128 * C::kPN) {
         const float4 a = __ldcg(reinterpret_cast<const float4*>(p));

@@ -151,7 +151,7 @@ __device__ __forceinline__ uint64_t l2_policy(bool keep) {
 }
 __device__ __forceinline__ uint4 load_hinted(const uint4* p, uint64_t policy) {
     uint4 v;
-    asm volatile("ld.global.nc.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+    asm volatile("ld.global.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p), "l"(policy));
     return v;
