@@ -57,9 +57,9 @@ struct Place {
 constexpr int kQuantRows = 2;      // rows a thread
 
 template <class Row8>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(Shape s, const void* __restrict__ x, int64_t ld_x,
-                                                            uint8_t* __restrict__ codes, int64_t ld_codes,
-                                                            float* __restrict__ scales) {
+__global__ void __launch_bounds__(kThreads) quantize_kernel(Shape s, const void* x, int64_t ld_x,
+                                                            uint8_t* codes, int64_t ld_codes,
+                                                            float* scales) {
     grid_dep_launch();     // a product may set itself up meanwhile
     grid_dep_wait();
     const Place p(s, kQuantRows);
@@ -143,8 +143,8 @@ constexpr int kForwardRows = 2;
 
 template <class Row8, bool H8>
 __global__ void __launch_bounds__(kThreads) swiglu_forward_kernel(
-    Shape s, const void* __restrict__ gu, int64_t ld_gu, void* __restrict__ h, int64_t ld_h,
-    float* __restrict__ h_scales, uint8_t* __restrict__ ck_codes, float* __restrict__ ck_scales,
+    Shape s, const void* gu, int64_t ld_gu, void* h, int64_t ld_h,
+    float* h_scales, uint8_t* ck_codes, float* ck_scales,
     const __grid_constant__ TrainRanges train) {
     grid_dep_launch();
     grid_dep_wait();
@@ -198,11 +198,11 @@ __global__ void __launch_bounds__(kThreads) swiglu_forward_kernel(
 }
 
 template <class Row8, bool D8>
-__global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(Shape s, const uint8_t* __restrict__ ck_codes,
-                                                                   const float* __restrict__ ck_scales,
-                                                                   const void* __restrict__ dh, int64_t ld_dh,
-                                                                   void* __restrict__ dgu, int64_t ld_dgu,
-                                                                   float* __restrict__ dgu_scales) {
+__global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(Shape s, const uint8_t* ck_codes,
+                                                                   const float* ck_scales,
+                                                                   const void* dh, int64_t ld_dh,
+                                                                   void* dgu, int64_t ld_dgu,
+                                                                   float* dgu_scales) {
     grid_dep_launch();
     grid_dep_wait();
     const Place p(s, 1);

@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tile_kernel(const __grid_c
 // Adds up the pieces of each cut tile, in their order, and writes its outputs.  One CTA per 32 rows by 64 outputs of
 // a tile; each warp adds 8 columns, a lane one row, so that every read is 512 contiguous bytes.
 template <class C>
-__global__ void __launch_bounds__(256) linear_join_kernel(const float* __restrict__ part, __nv_bfloat16* __restrict__ y,
+__global__ void __launch_bounds__(256) linear_join_kernel(const float* part, __nv_bfloat16* y,
                                                           int64_t ld_y, int32_t T, int32_t N, int32_t tiles_m,
                                                           int32_t tiles_n, int32_t n_whole, int32_t n_split) {
     grid_dep_wait();

@@ -159,9 +159,9 @@ __device__ __forceinline__ uint4 load_hinted(const uint4* p, uint64_t policy) {
 
 // One CTA of kThreads per row; each thread takes kAhead pieces of 16 bytes at a time.
 template <class E, int kThreads, int kAhead>
-__global__ void __launch_bounds__(kThreads) logprob_kernel(int32_t V, const typename E::T* __restrict__ logits,
-                                                           int64_t ld, const int64_t* __restrict__ labels,
-                                                           float* __restrict__ logp, float* __restrict__ lse) {
+__global__ void __launch_bounds__(kThreads) logprob_kernel(int32_t V, const typename E::T* logits,
+                                                           int64_t ld, const int64_t* labels,
+                                                           float* logp, float* lse) {
     grid_dep_launch();
     grid_dep_wait();
     const int64_t t = blockIdx.x;
@@ -292,11 +292,11 @@ struct Sum2 {
 // they are added up in about 48 bits (in float32 pairs: 64-bit arithmetic is slow on this GPU, 10 us against 4).
 template <int kPairs>
 __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(const __grid_constant__ Pairs<kPairs> pairs,
-                                                                 const int64_t* __restrict__ labels,
-                                                                 const float* __restrict__ logp,
-                                                                 const float* __restrict__ ref, float beta, float eps,
-                                                                 float* __restrict__ loss, float* __restrict__ rewards,
-                                                                 float* __restrict__ coef) {
+                                                                 const int64_t* labels,
+                                                                 const float* logp,
+                                                                 const float* ref, float beta, float eps,
+                                                                 float* loss, float* rewards,
+                                                                 float* coef) {
     grid_dep_launch();
     grid_dep_wait();
     constexpr int kHalf = kPairThreads / 2, kWarps = kHalf / 32;
@@ -346,11 +346,11 @@ __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(const __grid_co
 // here and does not push them out (st.cs).
 template <class E, int kThreads, int kAhead, int kPairs>
 __global__ void __launch_bounds__(kThreads) dlogits_kernel(int32_t V, const typename E::T* logits, int64_t ld,
-                                                           const int64_t* __restrict__ labels,
-                                                           const float* __restrict__ lse,
-                                                           const float* __restrict__ coef,
+                                                           const int64_t* labels,
+                                                           const float* lse,
+                                                           const float* coef,
                                                            const __grid_constant__ Sequences<kPairs> seqs,
-                                                           const float* __restrict__ dloss, float dloss_all,
+                                                           const float* dloss, float dloss_all,
                                                            typename E::T* dlogits, int64_t ld_d) {
     grid_dep_wait();
     const int64_t t = blockIdx.x % 2 == 0 ? (int64_t)gridDim.x - 1 - blockIdx.x / 2 : blockIdx.x / 2;

@@ -965,9 +965,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // Sums the fp32 partials of every split output tile in split order and writes the tile's rows of the output.
 // One block per (split tile, CTA half, row quarter, 64-column group); warp w sums 8 columns, lane = tile row, so
 // every partial load is one coalesced 128-byte row of the column-major partial.
-__global__ void __launch_bounds__(256) main_reduce_kernel(const SplitTile* __restrict__ splits,
-                                                          const int32_t* __restrict__ rowmap,
-                                                          const float* __restrict__ part, __nv_bfloat16* out,
+__global__ void __launch_bounds__(256) main_reduce_kernel(const SplitTile* splits,
+                                                          const int32_t* rowmap,
+                                                          const float* part, __nv_bfloat16* out,
                                                           int32_t out_ld, int32_t out_cols, int32_t debug,
                                                           int32_t* status, int64_t out_rows, int64_t main_slots) {
     grid_dep_wait();

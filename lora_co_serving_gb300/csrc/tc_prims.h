@@ -115,6 +115,8 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
 // Programmatic dependent launch: the kernels of a call are launched so that each may start (its prologue: barrier
 // setup, TMEM allocation) while the previous one drains; this wait holds the CTA until every earlier kernel of the
 // stream has finished and its writes are visible, before anything it produced (or the caller's inputs) is read.
+// Such a kernel's arguments carry no __restrict__: it promises that nobody writes the data while the kernel runs, which
+// holds after this wait only, and would let reads be moved ahead of it or take the cache that is not kept coherent.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Lets the next kernel start once every CTA of this one has come here.  A kernel that allocates TMEM calls it after the
 // allocation: the next one's CTAs may hold TMEM of their own while they wait for this one to end.

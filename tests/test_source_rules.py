@@ -1,0 +1,46 @@
+"""Rules that the CUDA sources keep and that no run can show broken (no GPU is touched)."""
+import glob
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "lora_co_serving_gb300", "csrc")
+
+
+def source(path):
+    """A file's text without its comments."""
+    with open(path) as f:
+        return re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
+
+
+FILES = {os.path.basename(p): source(p) for p in sorted(glob.glob(os.path.join(CSRC, "*.cu")) +
+                                                        glob.glob(os.path.join(CSRC, "*.h")))}
+
+
+def kernels():
+    """(file, name, parameter list, body) of every kernel."""
+    for name, text in FILES.items():
+        for m in re.finditer(r"__global__\s+void\s+(?:__\w+__\s*\([^()]*\)\s*|__cluster_dims__\s*\([^()]*\)\s*)*(\w+)\s*\(", text):
+            at, depth = m.end(), 1
+            while depth:
+                depth += {"(": 1, ")": -1}.get(text[at], 0)
+                at += 1
+            args, at = text[m.end():at - 1], text.index("{", at) + 1
+            start, depth = at, 1
+            while depth:
+                depth += {"{": 1, "}": -1}.get(text[at], 0)
+                at += 1
+            yield name, m.group(1), args, text[start:at]
+
+
+def test_kernels_are_found():
+    assert len(list(kernels())) == sum(len(re.findall(r"__global__\s+void", t)) for t in FILES.values()) > 15
+
+
+@pytest.mark.parametrize("file,name,args,body", [pytest.param(*k, id=k[1]) for k in kernels() if "grid_dep_wait" in k[3]])
+def test_early_kernels_promise_nothing_about_their_arguments(file, name, args, body):
+    """A kernel that waits for the launch before it starts while that launch may still write what it is going to read.
+    A __restrict__ argument promises that nobody writes the data while the kernel runs: the compiler may then read it
+    through the cache that is not kept coherent, and ahead of the wait."""
+    assert "__restrict__" not in args and "__ldg" not in body and "ld.global.nc" not in body
