@@ -61,24 +61,6 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
     return one != 0;
 }
-// arrive (when this CTA's issued MMAs complete) on the barrier at this offset in both CTAs of the cluster
-__device__ __forceinline__ void mma_commit_both(uint32_t bar) {
-    const uint16_t mask = 3;
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(mask)
-        : "memory");
-}
-// TMA load into the same place of both CTAs' shared memory; each CTA's barrier at this offset counts its copy's bytes
-__device__ __forceinline__ void tma_load_2d_both(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1,
-                                                 uint32_t bar) {
-    const uint16_t mask = 3;
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], "
-        "[%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "h"(mask)
-        : "memory");
-}
 // (a.lo, a.hi) += (d0, d1) * (s.lo, s.hi).  volatile: d comes from a TMEM read and must stay behind its wait
 __device__ __forceinline__ void fma2(uint64_t& a, uint32_t d0, uint32_t d1, uint64_t s) {
     asm volatile("{\n\t.reg .b64 d;\n\t"
@@ -104,21 +86,18 @@ __device__ __forceinline__ float2 halves(uint64_t a) {
 }
 
 // =============================================================================================================
-// Many rows: clusters of two CTAs, each 128 rows of x by 256 outputs (rows of w).
+// Many rows: one CTA's tile is 128 rows of x by 256 outputs (rows of w), or by 128.
 //
-// The CTAs of a cluster share the outputs: each loads its own 128 rows of x and half of the 256 rows of w, and the
-// halves go to both (TMA multicast), 32 KB per CTA and block for 128 * 256 * 128 products.  Everything else is the
-// CTA's own: an accumulator goes to and fro between the issuing warp and the adding warps once per block.  A CTA pair
-// whose leader issues for both (cta_group::2) would halve w's share of shared memory, but gains nothing: accumulators
-// handed back by arrivals with release at cluster scope took 8192 x 8192 x 28672 to 2.9 ms, relaxed ones with a barrier
-// of the scales' own to 1.45 ms (this kernel beside it: 1.43 ms), and the adding warps' chain remains.
+// The CTA loads its rows of x and of w, 48 KB a block for 128 * 256 * 128 products; an accumulator goes to and fro
+// between the issuing warp and the adding warps once per block.
 //
 // What bounds it: a block's MMAs are 512 cycles of tensor work; its 48 KB are written to shared memory once and read
 // once, 750 cycles at 128 bytes a cycle; scaling and adding takes an accumulator about 550 cycles, of which 256 are its
-// 128 x 256 multiply-adds, and handing it over and back comes on top.  Two accumulators hide part of that: a block takes
-// 730 to 770 cycles (clock counts in the kernel), and 8192 x 8192 x 28672 1.45 ms, 2650 TFLOP/s, at the 1.57 GHz that the
-// power limit leaves of 2.07.  With the multiply-adds left out it takes 1.35 ms, with the TMEM reads left out too 1.27 ms
-// (a pair: 1.18 ms).
+// 128 x 256 multiply-adds, and handing it over and back comes on top.  Two accumulators hide part of that.  8192 x 8192 x 28672 takes 1.455 ms (2640
+// TFLOP/s) in runs of a few milliseconds, at 2.07 GHz; longer ones meet the power limit, which lowers the clock:
+// 2048 x 28672 x 8192 takes 336 us at first and 373 us, at 1.63 GHz, when it runs for half a second.
+//
+// Neighbouring CTAs load the same rows of w, each for itself, from L2.
 //
 // 384 threads: warp 0 loads (TMA), warp 1 issues, warps 4..11 scale and add: each thread has one row of x and 128
 // outputs, which are one block of w's rows, so a block's 128 sums share one scale, sx[row] * sw[block].  The CTA
@@ -134,13 +113,11 @@ constexpr int kScaleSlots = 16;                          // blocks whose scales 
 constexpr int kScaleFloats = 132;                        // 128 rows of x, up to two blocks of w's rows
 constexpr int kGroupRows = 4096;                         // rows of x that share a sweep over w (see tile_at)
 
-// The shapes: kCtas CTAs of a cluster, 128 rows of x each, by kPN outputs.  {2, 256} moves and reads the least per
-// product; {2, 128} has twice the tiles, for products whose tiles of 256 leave clusters idle; {1, .} cuts x into 128 rows
-// for each SM by itself: 9 tiles where clusters need 10 for 1111 rows, and any one of 152 places for each.  spread_of()
-// weighs them.
-template <int kCtas_, int kPN_>
+// The shapes: a tile is 128 rows of x by kPN outputs.  256 moves and reads the least per product; 128 has twice the tiles,
+// for products whose tiles of 256 leave SMs idle.  spread_of() weighs them.
+template <int kPN_>
 struct TileCfg {
-    static constexpr int kCtas = kCtas_, kPN = kPN_, kPM = 128 * kCtas;
+    static constexpr int kPN = kPN_;
     static constexpr int kWBytes = kPN * kQBlock;        // the tile's rows of w
     // What passes the barriers at a time: one block, or two of 128 outputs, whose MMAs take 256 cycles each: issuing a
     // block (two barrier tests, four MMAs, two commits: about 400 cycles) would take longer.  500 x 4096 x 4096 takes
@@ -179,9 +156,8 @@ struct Item {
 
 // Tiles in bands of kGroupRows rows of x: a band's columns are swept one after another, so that the tiles at work at any
 // time share few rows of x and of w.
-template <class C>
 __host__ __device__ __forceinline__ void tile_at(int tiles_m, int tiles_n, int i, int* tm, int* tn) {
-    constexpr int kGroup = kGroupRows / C::kPM;
+    constexpr int kGroup = kGroupRows / 128;
     const int band = kGroup * tiles_n;
     const int m0 = i / band * kGroup;
     const int left = tiles_m - m0, rows = left < kGroup ? left : kGroup;
@@ -204,7 +180,7 @@ __device__ __forceinline__ Item item_at(const TileParams& P, int i) {
         it.kb0 = (int)((int64_t)P.nb * q / P.n_split) / C::kStep * C::kStep;
         if (q + 1 < P.n_split) it.kb1 = (int)((int64_t)P.nb * (q + 1) / P.n_split) / C::kStep * C::kStep;
     }
-    tile_at<C>(P.tiles_m, P.tiles_n, tile, &it.tm, &it.tn);
+    tile_at(P.tiles_m, P.tiles_n, tile, &it.tm, &it.tn);
     return it;
 }
 
@@ -224,16 +200,14 @@ struct Bars {
 
 // The whole warp runs this loop too (see tile_issue): 600 x 2704 x 2704 10.7 us so, 11.0 us in a loop of one lane
 template <class C>
-__device__ __forceinline__ void tile_load(const TileParams& P, const Bars& B, uint8_t* smem, uint32_t rank) {
+__device__ __forceinline__ void tile_load(const TileParams& P, const Bars& B, uint8_t* smem) {
     const bool one = elect_one();
     StageRing<C::kStages> ring;
     uint32_t used = 0;
-    for (int i = blockIdx.x / C::kCtas; i < P.n_items; i += gridDim.x / C::kCtas) {
+    for (int i = blockIdx.x; i < P.n_items; i += gridDim.x) {
         const Item it = item_at<C>(P, i);
-        const int row_x = it.tm * C::kPM + 128 * (int)rank;
-        const int row_w = it.tn * C::kPN + C::kPN / C::kCtas * (int)rank;
+        const int row_x = it.tm * 128, row_w = it.tn * C::kPN;
         for (int kb = it.kb0; kb < it.kb1; kb += C::kStep) {
-            // free in both CTAs: the half of w goes to both
             const bool ok = wait_here(B.empty + ring.stage * 8, ring.phase ^ 1u, B.abort_flag, P.status);
             if (!__all_sync(0xffffffffu, ok)) {
                 drain_loads(B.full, used, C::kStages);
@@ -248,10 +222,7 @@ __device__ __forceinline__ void tile_load(const TileParams& P, const Bars& B, ui
                     if (g >= n) break;
                     const uint32_t sx = sa + g * C::kBlockBytes, sw = sx + kOperandBytes;
                     tma_load_2d(sx, &P.tm_x, (kb + g) * kQBlock, row_x, full);
-                    if constexpr (C::kCtas == 2)
-                        tma_load_2d_both(sw + rank * (C::kWBytes / 2), &P.tm_w, (kb + g) * kQBlock, row_w, full);
-                    else
-                        tma_load_2d(sw, &P.tm_w, (kb + g) * kQBlock, row_w, full);
+                    tma_load_2d(sw, &P.tm_w, (kb + g) * kQBlock, row_w, full);
                 }
             }
             __syncwarp();
@@ -259,7 +230,7 @@ __device__ __forceinline__ void tile_load(const TileParams& P, const Bars& B, ui
             ++used;
         }
     }
-    // the peer's last commits arrive on this CTA's barriers: none may be under way when the CTA ends
+    // the last commits arrive on this CTA's barriers: none may be under way when it ends
     for (int s = 0; s < C::kStages; ++s, ring.next())
         if (!wait_here(B.empty + ring.stage * 8, ring.phase ^ 1u, B.abort_flag, P.status)) return;
 }
@@ -273,7 +244,7 @@ __device__ __forceinline__ void tile_issue(const TileParams& P, const Bars& B, u
     const uint64_t desc_w = smem_desc(smem_u32(smem) + kOperandBytes, 16, 1024);
     StageRing<C::kStages> ring;
     uint32_t use = 0;                          // steps so far: accumulator use & 1
-    for (int i = blockIdx.x / C::kCtas; i < P.n_items; i += gridDim.x / C::kCtas) {
+    for (int i = blockIdx.x; i < P.n_items; i += gridDim.x) {
         const Item it = item_at<C>(P, i);
         for (int kb = it.kb0; kb < it.kb1; kb += C::kStep, ++use) {
             const uint32_t acc = use & 1u;
@@ -294,10 +265,7 @@ __device__ __forceinline__ void tile_issue(const TileParams& P, const Bars& B, u
                                  desc_w + at + g * (C::kBlockBytes >> 4) + 2 * k, instr_desc_e4m3(128, C::kPN), k > 0);
                 }
                 mma_commit(B.tfull + acc * 8);
-                if constexpr (C::kCtas == 2)
-                    mma_commit_both(B.empty + ring.stage * 8);
-                else
-                    mma_commit(B.empty + ring.stage * 8);
+                mma_commit(B.empty + ring.stage * 8);
             }
             __syncwarp();
             ring.next();
@@ -312,13 +280,12 @@ __device__ __forceinline__ void tile_issue(const TileParams& P, const Bars& B, u
 // Slot kb % kScaleSlots is free once the MMAs of block kb - kStages are done, as they began after the adding warps had
 // finished with block kb - kStages - 2.
 template <class C>
-__device__ __forceinline__ void tile_scales(const TileParams& P, const Bars& B, float* slots, uint32_t rank, int which,
-                                            int lane) {
+__device__ __forceinline__ void tile_scales(const TileParams& P, const Bars& B, float* slots, int which, int lane) {
     StageRing<C::kStages> ring;
     uint32_t use = 0;
-    for (int i = blockIdx.x / C::kCtas; i < P.n_items; i += gridDim.x / C::kCtas) {
+    for (int i = blockIdx.x; i < P.n_items; i += gridDim.x) {
         const Item it = item_at<C>(P, i);
-        const int t = it.tm * C::kPM + 128 * (int)rank + 64 * which + lane;
+        const int t = it.tm * 128 + 64 * which + lane;
         const int n0 = it.tn * C::kPN + (C::kPN == 256 ? 128 * which : 0);
         const float* x0 = P.xs + (int64_t)min(t, P.T - 1) * P.nb;          // rows past the end: any scale will do
         const float* x1 = P.xs + (int64_t)min(t + 32, P.T - 1) * P.nb;
@@ -365,14 +332,14 @@ __device__ __forceinline__ void tile_scales(const TileParams& P, const Bars& B, 
 }
 
 template <class C>
-__device__ __forceinline__ void tile_add(const TileParams& P, const Bars& B, uint32_t tmem, uint32_t rank, int warp,
-                                         int lane, const float* slots, uint32_t stage_out) {
+__device__ __forceinline__ void tile_add(const TileParams& P, const Bars& B, uint32_t tmem, int warp, int lane,
+                                         const float* slots, uint32_t stage_out) {
     const int quarter = warp & 3, half = (warp - 4) / 4;
     const uint32_t taddr0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * C::kCols;
     uint32_t use = 0;
-    for (int i = blockIdx.x / C::kCtas; i < P.n_items; i += gridDim.x / C::kCtas) {
+    for (int i = blockIdx.x; i < P.n_items; i += gridDim.x) {
         const Item it = item_at<C>(P, i);
-        const int t0 = it.tm * C::kPM + 128 * (int)rank + quarter * 32;
+        const int t0 = it.tm * 128 + quarter * 32;
         const int n0 = it.tn * C::kPN + half * C::kCols;
         uint64_t acc[C::kCols / 2];
 #pragma unroll
@@ -410,8 +377,8 @@ __device__ __forceinline__ void tile_add(const TileParams& P, const Bars& B, uin
             }
         }
         if (it.piece >= 0) {
-            // [128 rows of a CTA][kPN outputs] as groups of 4 outputs: a warp writes 512 contiguous bytes per group
-            float* part = P.part + ((int64_t)it.piece * C::kCtas + rank) * (128 * C::kPN) +
+            // [128 rows][kPN outputs] as groups of 4 outputs: a warp writes 512 contiguous bytes per group
+            float* part = P.part + (int64_t)it.piece * (128 * C::kPN) +
                           ((int64_t)half * (C::kCols / 4) * 128 + quarter * 32 + lane) * 4;
             if (t0 < P.T && n0 < P.N) {
 #pragma unroll
@@ -465,12 +432,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tile_kernel(const __grid_c
     B.tfull = B.empty + C::kStages * 8;
     B.tempty = B.tfull + 16;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint32_t rank = cluster_ctarank();
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(B.full + s * 8, 3);            // the arm + the bytes of both CTAs' loads; warps 2 and 3
-            mbar_init(B.empty + s * 8, C::kCtas);    // every CTA's commit
+            mbar_init(B.full + s * 8, 3);            // the arm and its bytes; warps 2 and 3
+            mbar_init(B.empty + s * 8, 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(B.tfull + b * 8, 1);
@@ -487,23 +453,23 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tile_kernel(const __grid_c
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
-    cluster_sync_all();
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     grid_dep_wait();
     if (blockIdx.x == 0 && threadIdx.x == 0) *P.status = 0;
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
-        if (warp == 0) tile_load<C>(P, B, smem, rank);
+        if (warp == 0) tile_load<C>(P, B, smem);
         if (warp == 1) tile_issue<C>(P, B, smem, tmem);
-        if (warp >= 2) tile_scales<C>(P, B, slots, rank, warp - 2, lane);
+        if (warp >= 2) tile_scales<C>(P, B, slots, warp - 2, lane);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kAddRegs));
-        tile_add<C>(P, B, tmem, rank, warp, lane, slots, smem_u32(out) + (uint32_t)((warp - 4) * kPieceBytes));
+        tile_add<C>(P, B, tmem, warp, lane, slots, smem_u32(out) + (uint32_t)((warp - 4) * kPieceBytes));
     }
     __syncwarp();
     tc_fence_before();
-    cluster_sync_all();
+    __syncthreads();
     tc_fence_after();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * C::kAccCols) : "memory");
@@ -516,17 +482,16 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const float* part, __n
                                                           int64_t ld_y, int32_t T, int32_t N, int32_t tiles_m,
                                                           int32_t tiles_n, int32_t n_whole, int32_t n_split) {
     grid_dep_wait();
-    constexpr int kPerRow = C::kPN / 64, kPerTile = C::kPM / 32 * kPerRow;
+    constexpr int kPerRow = C::kPN / 64, kPerTile = 4 * kPerRow;
     const int cut = blockIdx.x / kPerTile, sub = blockIdx.x % kPerTile;
     int tm, tn;
-    tile_at<C>(tiles_m, tiles_n, n_whole + cut, &tm, &tn);
+    tile_at(tiles_m, tiles_n, n_whole + cut, &tm, &tn);
     const int row = sub / kPerRow * 32 + threadIdx.x % 32, col = sub % kPerRow * 64 + threadIdx.x / 32 * 8;
-    const int t = tm * C::kPM + row, n = tn * C::kPN + col;
+    const int t = tm * 128 + row, n = tn * C::kPN + col;
     if (t >= T || n >= N) return;
-    const float* p = part + ((int64_t)cut * n_split * C::kCtas + row / 128) * (128 * C::kPN) + (int64_t)col * 128 +
-                     (row % 128) * 4;
+    const float* p = part + (int64_t)cut * n_split * (128 * C::kPN) + (int64_t)col * 128 + row * 4;
     float v[8] = {};
-    for (int q = 0; q < n_split; ++q, p += C::kCtas * 128 * C::kPN) {
+    for (int q = 0; q < n_split; ++q, p += 128 * C::kPN) {
         const float4 a = __ldcg(reinterpret_cast<const float4*>(p));
         const float4 b = __ldcg(reinterpret_cast<const float4*>(p + 512));
         v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
@@ -843,10 +808,8 @@ cudaError_t device_sms(int* sms) {
             if (e == cudaSuccess)
                 e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         };
-        allow(linear_tile_kernel<TileCfg<2, 256>>, TileCfg<2, 256>::kSmem);
-        allow(linear_tile_kernel<TileCfg<2, 128>>, TileCfg<2, 128>::kSmem);
-        allow(linear_tile_kernel<TileCfg<1, 256>>, TileCfg<1, 256>::kSmem);
-        allow(linear_tile_kernel<TileCfg<1, 128>>, TileCfg<1, 128>::kSmem);
+        allow(linear_tile_kernel<TileCfg<256>>, TileCfg<256>::kSmem);
+        allow(linear_tile_kernel<TileCfg<128>>, TileCfg<128>::kSmem);
         allow(linear_rows_kernel<16, Row8Bf16>, RowsCfg<16>::kSmem);
         allow(linear_rows_kernel<16, Row8F32>, RowsCfg<16>::kSmem);
         allow(linear_rows_kernel<16, void>, RowsCfg<16>::kSmem);
@@ -868,46 +831,44 @@ bool few_rows(int32_t T, int32_t K, int32_t N) { return T <= 32 || (T <= 64 && K
 // 28672 24.6 us (24.8 us), 16 x 5120 x 5120 13.2 us (9.6 us).
 bool quantized_on_the_way(int32_t T, int32_t K, int32_t N) { return T <= 16 && (int64_t)T * K * N <= (1 << 28); }
 
-// A product's shape, and how its tiles are spread over the clusters.  Tiles beyond the last full round may be cut along
-// K, into as many pieces as clusters are left for each, at most kMaxSplit, of at least kMinBlocks blocks: a round of 4
-// tiles holds 72 of 76 clusters for a tile's whole time.  The choice is by an estimate, whose numbers were fitted to 167
-// products of 68 to 3000 rows timed in all four shapes (K and N from 512 to 28672): the estimate is 8 % off (rms), the
-// shape it takes 0.5 % slower than the best of the four, 9 % at the worst (777 x 512 x 2704).  Measured, us:
-//                              2 x 256   2 x 128   1 x 256   1 x 128
-//    300 x   512 x  2704           6.7       5.6       6.4       5.5
-//    256 x  4096 x 28672          37.7      33.9      37.6      34.3
-//    600 x  2704 x  2704          13.9      10.9      15.3      12.9
-//   1500 x  2704 x  2704          14.2      17.8      17.6      21.7
-//    300 x  5120 x  5120          20.4      19.5      18.1      14.6   120 narrow tiles of one CTA, one round
-//    777 x  5120 x  5120          28.4      28.9      21.1      24.3   80 wide tiles of two CTAs, one round of 140 of one
-//   1111 x 14336 x  4096          59.2      65.6      48.7      60.3   80 wide tiles of two CTAs, one round of 144 of one
-//   2048 x 28672 x  8192           365                 388
-//   8192 x  8192 x 28672          1430      1850      1520      1900
+// A product's shape, and how its tiles are spread over the SMs.  Tiles beyond the last full round may be cut along K, into
+// as many pieces as SMs are left for each, at most kMaxSplit, of at least kMinBlocks blocks: a round of 8 tiles holds 144
+// of 152 SMs for a tile's whole time.  The choice is by an estimate whose numbers were fitted to measured products.  For 169
+// products of 68 to 8192 rows (K and N from 512 to 28672) it is 11 % off (rms; the 3 us that every launch takes are left
+// out of it), the shape it takes 0.2 % slower than the better of the two, 10 % at the worst (384 x 2704 x 2704).
+// Measured in us, x in 8 bits, weights of fp8_quantize_weight, three in turn, in replayed graphs of a few milliseconds:
+//                               256     128
+//    300 x   512 x  2704        5.4     4.5
+//    500 x  4096 x  4096       15.6    10.8
+//    256 x  4096 x 28672       37.4    33.6
+//    600 x  2704 x  2704       14.4    12.7
+//   1500 x  2704 x  2704       16.6    20.6
+//    300 x  5120 x  5120       17.2    13.5   120 narrow tiles in one round
+//    777 x  5120 x  5120       20.3    23.3   140 wide tiles in one round
+//   1111 x 14336 x  4096       48.5    60.7   144 wide tiles in one round (54 us in a long run, at 1.78 GHz)
+//   2048 x 28672 x  8192        334     428
+//   8192 x  8192 x 28672       1455    1630
 constexpr int kMaxSplit = 8, kMinBlocks = 4;
 constexpr int kSms = 152;                                // planned for; right on any device
 struct Spread {
-    int ctas, pn;                                        // TileCfg
+    int pn;                                              // TileCfg
     int tiles_m, tiles_n, n_whole, n_split, n_items;
     double us;                                           // estimate
     int n_cut() const { return tiles_m * tiles_n - n_whole; }
 };
-Spread spread_as(int32_t T, int32_t K, int32_t N, int ctas, int pn) {
+Spread spread_as(int32_t T, int32_t K, int32_t N, int pn) {
     // a block; a tile's outputs on their way out, while no sums are added up; a join, and each 256 KB that it reads
-    double block = pn == 256 ? 0.415 : 0.243;
-    const double out = pn == 256 ? 1.3 : 0.8, join = 2.7, join_sums = 0.05;
-    if (ctas == 1) block *= 1.05;                        // w is read from L2 once per CTA
+    const double block = pn == 256 ? 0.436 : 0.255, out = pn == 256 ? 1.3 : 0.8, join = 2.7, join_sums = 0.05;
     Spread s{};
-    s.ctas = ctas;
     s.pn = pn;
-    s.tiles_m = (int)(((int64_t)T + 128 * ctas - 1) / (128 * ctas));
+    s.tiles_m = (int)(((int64_t)T + 127) / 128);
     s.tiles_n = (N + pn - 1) / pn;
-    const int clusters = kSms / ctas, tiles = s.tiles_m * s.tiles_n, rest = tiles % clusters, nb = blocks_of(K);
-    const int rounds = tiles / clusters;
+    const int tiles = s.tiles_m * s.tiles_n, rest = tiles % kSms, nb = blocks_of(K), rounds = tiles / kSms;
     s.n_whole = tiles;
     s.us = (double)(rounds + (rest > 0)) * (nb * block + out);
-    const int pieces = rest ? std::min({clusters / rest, kMaxSplit, nb / kMinBlocks}) : 0;
+    const int pieces = rest ? std::min({kSms / rest, kMaxSplit, nb / kMinBlocks}) : 0;
     if (pieces >= 2) {
-        const double sums = (double)rest * pieces * ctas * pn / 512.0;
+        const double sums = (double)rest * pieces * pn / 512.0;
         const double cut = (double)rounds * (nb * block + out) + (double)((nb + pieces - 1) / pieces) * block + join +
                            join_sums * sums;
         if (cut < s.us) {
@@ -921,16 +882,8 @@ Spread spread_as(int32_t T, int32_t K, int32_t N, int ctas, int pn) {
 }
 Spread spread_of(int32_t T, int32_t K, int32_t N) {
     if (few_rows(T, K, N)) return Spread{};
-    Spread best = spread_as(T, K, N, 1, 256);
-    auto weigh = [&](const Spread& s) {
-        if (s.us < best.us) best = s;
-    };
-    weigh(spread_as(T, K, N, 1, 128));
-    if (T > 128) {                                       // else a cluster's second CTA has no rows
-        weigh(spread_as(T, K, N, 2, 256));
-        weigh(spread_as(T, K, N, 2, 128));
-    }
-    return best;
+    const Spread wide = spread_as(T, K, N, 256), narrow = spread_as(T, K, N, 128);
+    return narrow.us < wide.us ? narrow : wide;
 }
 
 // Workspace: the status word, then x's codes and scales if x is quantized on the way, then the cut tiles' sums
@@ -943,7 +896,7 @@ Scratch layout_of(int32_t T, int32_t K, bool x_fp8, const Spread& s) {
     L.codes = 256;
     L.scales = L.codes + (x_fp8 ? 0 : al((size_t)T * K));
     L.part = L.scales + (x_fp8 ? 0 : al((size_t)T * blocks_of(K) * sizeof(float)));
-    L.end = L.part + (size_t)s.n_cut() * s.n_split * (128 * s.ctas) * s.pn * sizeof(float);
+    L.end = L.part + (size_t)s.n_cut() * s.n_split * 128 * s.pn * sizeof(float);
     return L;
 }
 // CTAs of a cluster that share 128 outputs' K: more while the launch has fewer than one per SM and each keeps
@@ -977,22 +930,10 @@ cudaError_t launch_rows(const RowsParams& P, int ranks, cudaStream_t st) {
 template <class C>
 cudaError_t launch_tiles(const TileParams& P, const Spread& sp, int sms, __nv_bfloat16* y, int64_t ld_y,
                          cudaStream_t st) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(C::kCtas * std::min(sms / C::kCtas, sp.n_items)));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = C::kCtas;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_tile_kernel<C>, P);
+    const cudaError_t e = launch_pdl(linear_tile_kernel<C>, dim3((unsigned)std::min(sms, sp.n_items)), dim3(kThreads),
+                                     C::kSmem, st, P);
     if (e != cudaSuccess || sp.n_cut() == 0) return e;
-    return launch_pdl(linear_join_kernel<C>, dim3((unsigned)(C::kPM / 32 * (C::kPN / 64) * sp.n_cut())), dim3(256), 0, st,
+    return launch_pdl(linear_join_kernel<C>, dim3((unsigned)(4 * (C::kPN / 64) * sp.n_cut())), dim3(256), 0, st,
                       static_cast<const float*>(P.part), y, ld_y, P.T, P.N, sp.tiles_m, sp.tiles_n, sp.n_whole,
                       sp.n_split);
 }
@@ -1089,7 +1030,7 @@ extern "C" int lora_fp8_linear(int32_t T, int32_t K, int32_t N, lora_dtype_t dt,
             return enqueued(fn, e);
         }
         TileParams P{};
-        if (!encode_codes(&P.tm_x, xc, K, T, ld_c, 128) || !encode_codes(&P.tm_w, w, K, N, K, sp.pn / sp.ctas) ||
+        if (!encode_codes(&P.tm_x, xc, K, T, ld_c, 128) || !encode_codes(&P.tm_w, w, K, N, K, sp.pn) ||
             !encode_y(&P.tm_y, y, N, T, ld_y))
             return bad_map();
         P.xs = xs;
@@ -1108,12 +1049,8 @@ extern "C" int lora_fp8_linear(int32_t T, int32_t K, int32_t N, lora_dtype_t dt,
         e = quantize();
         if (e != cudaSuccess) return enqueued(fn, e);
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(y);
-        if (sp.ctas == 2)
-            e = sp.pn == 256 ? launch_tiles<TileCfg<2, 256>>(P, sp, sms, out, ld_y, st)
-                             : launch_tiles<TileCfg<2, 128>>(P, sp, sms, out, ld_y, st);
-        else
-            e = sp.pn == 256 ? launch_tiles<TileCfg<1, 256>>(P, sp, sms, out, ld_y, st)
-                             : launch_tiles<TileCfg<1, 128>>(P, sp, sms, out, ld_y, st);
+        e = sp.pn == 256 ? launch_tiles<TileCfg<256>>(P, sp, sms, out, ld_y, st)
+                         : launch_tiles<TileCfg<128>>(P, sp, sms, out, ld_y, st);
         return enqueued(fn, e);
     });
 }

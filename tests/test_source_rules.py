@@ -44,3 +44,11 @@ def test_early_kernels_promise_nothing_about_their_arguments(file, name, args, b
     A __restrict__ argument promises that nobody writes the data while the kernel runs: the compiler may then read it
     through the cache that is not kept coherent, and ahead of the wait."""
     assert "__restrict__" not in args and "__ldg" not in body and "ld.global.nc" not in body
+
+
+def test_no_load_is_multicast_over_a_cluster():
+    """The library also runs where several GPUs see one another's memory; a bulk load that lands in several CTAs is kept
+    out of it.  (Commits of tensor-core work may arrive on both CTAs of a pair: they move no data.)"""
+    for name, text in FILES.items():
+        for m in re.finditer(r"cp\.async\.bulk[^;]*", text):
+            assert "multicast" not in m.group(0), name
