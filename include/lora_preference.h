@@ -53,7 +53,10 @@ int lora_preference_forward(int32_t T, int32_t V, lora_dtype_t dt, const void* l
 
 /* dlogits [T,V] (element type dt, ld_d): every row is written, with zeros where it is not counted or in no sequence.
  *   lse, coef: the forward's.   dloss [n_pairs]: the gradient of each pair's loss; NULL: 1 / n_pairs each (the mean).
- * dlogits may be the logits buffer itself (same ld): the gradient then takes the logits' place. */
+ * dlogits may be the logits buffer itself (same ld): the gradient then takes the logits' place.
+ * Probabilities are e^(x - lse).  Where |lse| >= 256, so that its rounding to float32 would show in them, the row is
+ * summed up again; an lse that differs from that sum by more than 2^-21 of itself (a part of a vocabulary, with the whole
+ * one's) is taken as given. */
 int lora_preference_backward(int32_t T, int32_t V, lora_dtype_t dt, const void* logits, int64_t ld,
                              const int64_t* labels, const float* lse, const float* coef,
                              const lora_pair_t* pairs /* HOST */, int32_t n_pairs, const float* dloss, void* dlogits,

@@ -341,6 +341,46 @@ __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(const __grid_co
     coef[2 * blockIdx.x + 1] = -k;
 }
 
+// The backward's probabilities are e^(x - lse), and lse is one float32 number: half a unit of it, 2^-25 of its size, is
+// every probability's relative error.  From kFarLse on that is 2^-17 and more (all of a probability where every logit is
+// the type's lowest value), so the row is summed up once more, from its largest logit, and the probabilities are taken
+// from there.  An lse that is not the row's own, by more than roundings, is the caller's and stays.
+constexpr float kFarLse = 256.f;
+struct RowBase {
+    float from, less;                          // a probability is 2^((x - from) log2(e) - less)
+};
+template <class E, int kThreads>
+__device__ __noinline__ RowBase far_row(const typename E::T* row, int V, float z) {
+    constexpr int kWarps = kThreads / 32;
+    __shared__ float sh[kWarps][3];
+    const int warp = threadIdx.x / 32;
+    float m = -INFINITY;
+    for (int i = threadIdx.x; i < V; i += kThreads) m = fmaxf(m, E::get(row[i]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (threadIdx.x % 32 == 0) sh[warp][0] = m;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sh[w][0]);
+    Sum2 s;
+    for (int i = threadIdx.x; i < V; i += kThreads) s.add(exp2_fast((E::get(row[i]) - m) * kLog2e));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float hi = __shfl_xor_sync(0xffffffffu, s.hi, o), lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
+        s.add(hi, lo);
+    }
+    if (threadIdx.x % 32 == 0) {
+        sh[warp][1] = s.hi;
+        sh[warp][2] = s.lo;
+    }
+    __syncthreads();                           // in place: the row is written after this
+    Sum2 all;
+    for (int w = 0; w < kWarps; ++w) all.add(sh[w][1], sh[w][2]);
+    const float sum = all.value();
+    // the forward's lse is a few units off at most
+    const bool own = fabsf(m + logf(sum) - z) <= 4.7683716e-7f * fabsf(z);       // 2^-21
+    return own ? RowBase{m, log2f(sum)} : RowBase{z, 0.f};
+}
+
 // One CTA per row; rows are taken from the end and from the start in turn, so that the rows that L2 still holds from
 // the forward (see kKept) and those that come from memory are read side by side.  What is written is not read again
 // here and does not push them out (st.cs).
@@ -368,10 +408,11 @@ __global__ void __launch_bounds__(kThreads) dlogits_kernel(int32_t V, const type
     }
     float k = coef[seq] * (dloss ? dloss[seq / 2] : dloss_all);
     if (label >= V) k = NAN;
-    const float z = lse[t];
+    RowBase base{lse[t], 0.f};
+    if (fabsf(base.from) >= kFarLse && fabsf(base.from) < INFINITY) base = far_row<E, kThreads>(row, V, base.from);
     const int hit = label < V ? (int)label : -1;
     auto grad = [&](float x, bool at) {
-        const float p = exp2_fast((x - z) * kLog2e);
+        const float p = exp2_fast(fmaf(x - base.from, kLog2e, -base.less));
         return at ? k * (1.f - p) : -k * p;
     };
     // both rows on the same 16-byte phase: whole pieces; else element by element
