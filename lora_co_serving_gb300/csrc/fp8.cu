@@ -4,6 +4,7 @@
 // columns of one row) belongs to 16 neighbouring lanes of 8 elements each, so a 16-bit row is read in 16-byte pieces,
 // the block's largest magnitude is four shuffles away, and the codes leave in 8-byte pieces, 128 bytes per block.
 #include <algorithm>
+#include <type_traits>
 #include <vector>
 
 #include "fp8.h"
@@ -134,8 +135,31 @@ __device__ __forceinline__ int checkpoint_row(const TrainRanges& t, int row) {
     return t.ck[lo - 1] + row - t.start[lo - 1];
 }
 
-// 1 / (1 + e^-g).  e^-g overflows to infinity below g = -88: the quotient is then 0, as it should be.
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+// sig(g) = 1 / (1 + e^-g) and sig(-g).
+// kFull, where the result leaves as float32: from e^-|g|, which cannot overflow, by the full exponential and quotient; each
+// is a few units of 2^-24 off.
+// Else the result is rounded to 16 bits or 8: the fast forms, with numerator and denominator scaled by 2^-32, so that the
+// denominator passes 2^126, where the fast reciprocal ends, only for gates below -109, whose sigmoid float32 cannot hold.
+// The exponent is off by |g| 2^-24 at the most: 2^-17 where the sigmoid is next to nothing.  sig(-g) is 1 - sig(g), 2^-24
+// off; it is added to 1 after a product with g.  (The full forms take the bf16 step's forward from 113 to 124 us for
+// 8192 x 14336, and float32 to 8 bits from 164 to 188 us; float32 to float32 takes 211 us with either.)
+struct Sigmoid {
+    float pos, neg;
+};
+template <bool kFull>
+__device__ __forceinline__ Sigmoid sigmoid(float g) {
+    if constexpr (kFull) {
+        const float e = expf(-fabsf(g)), large = 1.f / (1.f + e), small = e * large;
+        return g < 0.f ? Sigmoid{small, large} : Sigmoid{large, small};
+    } else {
+        constexpr float kLog2e = 1.4426950408889634f, kUnit = 0x1p-32f;
+        float e, r;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(g, -kLog2e, -32.f)));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(kUnit + e));
+        const float sig = kUnit * r;
+        return Sigmoid{sig, 1.f - sig};
+    }
+}
 
 // Two rows a thread: 64 bytes in flight in each (one row: 162 us for the 8192 x 14336 step with 2048 rows kept, two:
 // 156 us, 95 % of the memory rate).
@@ -148,6 +172,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_forward_kernel(
     const __grid_constant__ TrainRanges train) {
     grid_dep_launch();
     grid_dep_wait();
+    constexpr bool kFull = std::is_same<Row8, Row8F32>::value && !H8;
     const Place p(s, kForwardRows);
     const bool lead = threadIdx.x % kLanesPerBlock == 0;
     Row8 rg[kForwardRows], ru[kForwardRows];
@@ -169,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_forward_kernel(
         rg[k].get(g);
         ru[k].get(u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = g[i] * sigmoid(g[i]) * u[i];
+        for (int i = 0; i < 8; ++i) v[i] = g[i] * sigmoid<kFull>(g[i]).pos * u[i];
         if constexpr (H8) {
             float inv;
             const float sc = block_scale(max_over_block(abs_bits_max(v)), &inv);
@@ -205,6 +230,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(Shape s, cons
                                                                    float* dgu_scales) {
     grid_dep_launch();
     grid_dep_wait();
+    constexpr bool kFull = std::is_same<Row8, Row8F32>::value && !D8;
     const Place p(s, 1);
     const int row = p.row0;
     const bool in = p.in && row < s.rows;
@@ -227,9 +253,9 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(Shape s, cons
     rd.get(d);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float sig = sigmoid(g[i]);
-        const float dsig = d[i] * sig;
-        d[i] = dsig * u[i] * (1.f + g[i] * (1.f - sig));   // gate's gradient
+        const Sigmoid sig = sigmoid<kFull>(g[i]);
+        const float dsig = d[i] * sig.pos;
+        d[i] = dsig * u[i] * (1.f + g[i] * sig.neg);       // gate's gradient
         u[i] = dsig * g[i];                                // up's
     }
     if constexpr (D8) {
