@@ -58,7 +58,8 @@ size_t lora_fp8_workspace_size(int32_t T, int32_t K, int32_t N, int32_t x_fp8);
  * The gradient of the input is the same call on the transposed weight's codes (K and N exchanged, scales
  * transposed).  K a multiple of 16, N a multiple of 8; x, w and y 16-byte aligned, ld_x * element size and ld_y * 2
  * multiples of 16 bytes.  workspace: 256-byte aligned, >= lora_fp8_workspace_size bytes; its status word is read by
- * lora_workspace_status.  Sums are taken in a fixed order: repeated calls give identical bits. */
+ * lora_workspace_status (a call of zero rows leaves it as it was).  Sums are taken in a fixed order: repeated calls
+ * give identical bits. */
 int lora_fp8_linear(int32_t T, int32_t K, int32_t N, lora_dtype_t dt, const void* x, int64_t ld_x,
                     const float* x_scales, const void* w, const float* w_scales, void* y, int64_t ld_y,
                     void* workspace, size_t ws_bytes, void* stream);
