@@ -632,8 +632,8 @@ _status_workspaces = {}
 
 
 def _status_workspace(stream_ptr, device):
-    """A stream's own workspace for calls that need no more than the status word: calls on one stream run one after
-    another.  None while a CUDA graph is captured (its replays may run beside the stream's later calls)."""
+    """A stream's own workspace for calls that need no more than the status word and do not read it: calls on one stream
+    run one after another, but a thread's call may clear the word before another thread has read it.  None while a CUDA graph is captured (its replays may run beside the stream's later calls)."""
     import torch
     if torch._C._cuda_isCurrentStreamCapturing():
         return None
@@ -670,7 +670,7 @@ def fp8_linear(x, w, w_scales, x_scales=None, y=None, workspace=None, check_stat
     st = _stream_ptr(None)
     if workspace is None:
         need = fp8_workspace_size(T, K, N, x_scales is not None)
-        workspace = _status_workspace(st, x.device) if need <= _STATUS_BYTES else None
+        workspace = _status_workspace(st, x.device) if need <= _STATUS_BYTES and not check_status else None
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     rc = library().lora_fp8_linear(T, K, N, code, x.data_ptr(), ld, _ptr(x_scales), w.data_ptr(), w_scales.data_ptr(),

@@ -1,4 +1,4 @@
-"""The status word of fp8_linear: calls without rows."""
+"""The status word of fp8_linear: calls without rows, and calls that ask for it beside others on their stream."""
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -32,3 +32,20 @@ def test_a_call_without_rows_has_no_failure():
     y = lm.fp8_linear(codes, *w, x_scales=torch.empty(0, 4, device="cuda"), check_status=True,
                       workspace=torch.full((4096,), 255, dtype=torch.uint8, device="cuda"))
     assert y.shape == (0, 256)
+
+
+def test_a_checked_call_reads_a_status_of_its_own():
+    """Calls of a stream share a status word that nobody reads; one that is read must not be cleared by another call."""
+    import torch
+    import lora_co_serving_gb300 as lm
+    w, x = weight(), torch.randn(3, 512, device="cuda").bfloat16()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    want = lm.fp8_linear(x, *w, stream=side)
+    kept = lm._status_workspaces[(x.device.index, side.cuda_stream)]
+    side.synchronize()
+    kept.fill_(255)
+    torch.cuda.synchronize()
+    y = lm.fp8_linear(x, *w, stream=side, check_status=True)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and bool((kept == 255).all())
