@@ -564,10 +564,15 @@ def _on_stream(fn):
 
 
 def _one_device(*tensors):
+    """Refuse tensors off the current device: the launch goes to its stream, which no other device's work waits for."""
+    import torch
     d = tensors[0].get_device()
     for t in tensors:
         if t is not None and (d < 0 or t.get_device() != d):
             raise ValueError("tensors must lie on one CUDA device")
+    if d != torch._C._cuda_getDevice():
+        raise ValueError("tensors must lie on one CUDA device, the current one: they lie on cuda:%d, cuda:%d is current"
+                         % (d, torch._C._cuda_getDevice()))
 
 
 def _table(rows):
