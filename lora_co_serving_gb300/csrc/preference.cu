@@ -345,40 +345,66 @@ __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(const __grid_co
 // every probability's relative error.  From kFarLse on that is 2^-17 and more (all of a probability where every logit is
 // the type's lowest value), so the row is summed up once more, from its largest logit, and the probabilities are taken
 // from there.  An lse that is not the row's own, by more than roundings, is the caller's and stays.
+// 4096 rows of 32000 in 16 bits: 105 us where all of them are summed up again, 78 us where none is (without the one pass
+// in 16-byte pieces: 169 us).
 constexpr float kFarLse = 256.f;
 struct RowBase {
     float from, less;                          // a probability is 2^((x - from) log2(e) - less)
 };
 template <class E, int kThreads>
 __device__ __noinline__ RowBase far_row(const typename E::T* row, int V, float z) {
-    constexpr int kWarps = kThreads / 32;
-    __shared__ float sh[kWarps][3];
-    const int warp = threadIdx.x / 32;
-    float m = -INFINITY;
-    for (int i = threadIdx.x; i < V; i += kThreads) m = fmaxf(m, E::get(row[i]));
+    constexpr int kWarps = kThreads / 32, kAhead = 4;
+    __shared__ float sm[kWarps], ss[kWarps];
+    const RowSpan<E> span(row, V);
+    const uint4* q = reinterpret_cast<const uint4*>(row + span.head);
+    float m = -INFINITY, s = 0.f;              // the largest logit so far, and the sum of e^(x - m)
+    // (from == to: -infinity on both sides, an empty sum)
+    auto weight = [](float from, float to) { return from == to ? 1.f : exp2_fast((from - to) * kLog2e); };
+    auto take = [&](const auto& x, int n, float largest) {
+        const float to = fmaxf(m, largest);
+        s *= weight(m, to);
+        m = to;
+        float sum = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (threadIdx.x % 32 == 0) sh[warp][0] = m;
-    __syncthreads();
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sh[w][0]);
-    Sum2 s;
-    for (int i = threadIdx.x; i < V; i += kThreads) s.add(exp2_fast((E::get(row[i]) - m) * kLog2e));
+        for (int i = 0; i < n; ++i) sum += x[i] == -INFINITY ? 0.f : exp2_fast((x[i] - m) * kLog2e);
+        s += sum;
+    };
+    for (int i0 = threadIdx.x; i0 < span.vecs; i0 += kThreads * kAhead) {
+        uint4 v[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) v[j] = i0 + j * kThreads < span.vecs ? q[i0 + j * kThreads] : E::lowest();
+        const float largest = E::largest(v);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            float x[E::kN];
+            E::unpack(v[j], x);
+            take(x, E::kN, largest);
+        }
+    }
+    for (int i = threadIdx.x; i < V - span.vecs * E::kN; i += kThreads) {
+        const float x[1] = {E::get(row[i < span.head ? i : span.vecs * E::kN + i])};
+        take(x, 1, x[0]);
+    }
+    auto join = [&](float m2, float s2) {
+        const float to = fmaxf(m, m2);
+        s = s * weight(m, to) + s2 * weight(m2, to);
+        m = to;
+    };
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        const float hi = __shfl_xor_sync(0xffffffffu, s.hi, o), lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
-        s.add(hi, lo);
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+        join(m2, s2);
     }
     if (threadIdx.x % 32 == 0) {
-        sh[warp][1] = s.hi;
-        sh[warp][2] = s.lo;
+        sm[threadIdx.x / 32] = m;
+        ss[threadIdx.x / 32] = s;
     }
     __syncthreads();                           // in place: the row is written after this
-    Sum2 all;
-    for (int w = 0; w < kWarps; ++w) all.add(sh[w][1], sh[w][2]);
-    const float sum = all.value();
+    m = -INFINITY, s = 0.f;
+    for (int w = 0; w < kWarps; ++w) join(sm[w], ss[w]);       // in one order for every thread
     // the forward's lse is a few units off at most
-    const bool own = fabsf(m + logf(sum) - z) <= 4.7683716e-7f * fabsf(z);       // 2^-21
-    return own ? RowBase{m, log2f(sum)} : RowBase{z, 0.f};
+    const bool own = fabsf(m + logf(s) - z) <= 4.7683716e-7f * fabsf(z);         // 2^-21
+    return own ? RowBase{m, log2f(s)} : RowBase{z, 0.f};
 }
 
 // One CTA per row; rows are taken from the end and from the start in turn, so that the rows that L2 still holds from
