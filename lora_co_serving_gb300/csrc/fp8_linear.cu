@@ -43,6 +43,23 @@ __device__ __forceinline__ void drain_loads(uint32_t full, uint32_t used, int st
             if (global_timer() - t0 > limit) return;
 }
 
+template <int kStages>
+struct StageRing {
+    int stage = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++stage == kStages) { stage = 0; phase ^= 1u; }
+    }
+};
+// The last commits arrive on the stages' barriers (`empty`): none may be under way when the CTA ends and its shared memory
+// goes to another.  `ring`: after the last load.
+template <int kStages>
+__device__ __forceinline__ void await_commits(StageRing<kStages> ring, uint32_t empty, volatile int* abort_flag,
+                                              int32_t* status) {
+    for (int s = 0; s < kStages; ++s, ring.next())
+        if (!wait_here(empty + ring.stage * 8, ring.phase ^ 1u, abort_flag, status)) return;
+}
+
 // kind::f8f6f4: e4m3 A and B, fp32 accumulator, both operands K-major
 __host__ __device__ constexpr uint32_t instr_desc_e4m3(int m, int n) {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
@@ -184,15 +201,6 @@ __device__ __forceinline__ Item item_at(const TileParams& P, int i) {
     return it;
 }
 
-template <int kStages>
-struct StageRing {
-    int stage = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next() {
-        if (++stage == kStages) { stage = 0; phase ^= 1u; }
-    }
-};
-
 struct Bars {
     uint32_t full, empty, tfull, tempty;       // per stage: loaded, free; per accumulator: summed, read
     volatile int* abort_flag;
@@ -230,9 +238,7 @@ __device__ __forceinline__ void tile_load(const TileParams& P, const Bars& B, ui
             ++used;
         }
     }
-    // the last commits arrive on this CTA's barriers: none may be under way when it ends
-    for (int s = 0; s < C::kStages; ++s, ring.next())
-        if (!wait_here(B.empty + ring.stage * 8, ring.phase ^ 1u, B.abort_flag, P.status)) return;
+    await_commits(ring, B.empty, B.abort_flag, P.status);
 }
 
 // The whole warp runs this loop, and one lane issues: what the MMAs take (descriptors, addresses) is then uniform over
@@ -638,6 +644,7 @@ __global__ void __launch_bounds__(kRThreads) linear_rows_kernel(const __grid_con
             __syncwarp();
             ring.next();
         }
+        await_commits(ring, empty, abort_flag, P.status);
     } else if (warp == 1) {
         // the whole warp, so that descriptors are uniform (see tile_issue)
         const bool one = elect_one();

@@ -52,3 +52,16 @@ def test_no_load_is_multicast_over_a_cluster():
     for name, text in FILES.items():
         for m in re.finditer(r"cp\.async\.bulk[^;]*", text):
             assert "multicast" not in m.group(0), name
+
+
+@pytest.mark.parametrize("file,name,args,body", [pytest.param(*k, id=k[1]) for k in kernels()
+                                                 if k[0] == "fp8_linear.cu" and "tcgen05.alloc" in k[3]])
+def test_commits_of_the_products_end_before_their_cta(file, name, args, body):
+    """Commits of tensor-core work arrive on barriers in shared memory, whoever owns that by then: each kernel of the 8-bit
+    products waits for those that no other role waits for (the stages' last ones)."""
+    called = set(re.findall(r"(\w+)(?:<[^<>;]*>)?\s*\(", body))
+    text = body
+    for m in re.finditer(r"__device__ __forceinline__ void (\w+)\([^)]*\) \{(.*?)\n\}\n", FILES[file], flags=re.S):
+        if m.group(1) in called:
+            text += m.group(2)
+    assert "mma_commit(" in text and "await_commits(ring" in text
