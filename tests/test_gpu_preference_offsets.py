@@ -90,3 +90,20 @@ def test_a_given_log_sum_exp_is_kept():
     want = -np.array([[1.0], [-1.0]]) * np.exp(down(part) - down(whole)[:, None])
     want[[0, 1], [5, 700]] += [1.0, -1.0]
     assert (np.abs(down(d) - want) <= 2.0 ** -16 * np.abs(want) + 2.0 ** -16 * (np.abs(want) > 0.5)).all()
+
+
+def test_log_sum_exp_has_no_mean_error():
+    """A sequence's sum of log ratios adds up thousands of log probabilities: their mean error counts, not a row's own.
+
+    The fast exponential lies low by 4e-8 on average, which the kernel takes out; what is left is within half of that
+    over vocabularies and spreads (4096 rows of 3e-7 each leave 5e-9 to chance, the mean of nine 2e-9)."""
+    import torch
+    import lora_co_serving_gb300 as lm
+    T, off = 4096, []
+    for V in (500, 4000, 32000):
+        for sd in (1.0, 2.0, 3.0):
+            x = torch.randn(T, V, device="cuda", generator=torch.Generator(device="cuda").manual_seed(V + int(sd))) * sd
+            _, lse = lm.token_logprob(x, torch.zeros(T, dtype=torch.int64, device="cuda"))
+            ref = torch.cat([torch.logsumexp(c.double(), 1) for c in x.split(256)])
+            off.append(float((lse.double() - ref).mean()))
+    assert abs(np.mean(off)) <= 2e-8 and max(map(abs, off)) <= 4e-8, off
