@@ -140,9 +140,9 @@ __device__ __forceinline__ int checkpoint_row(const TrainRanges& t, int row) {
 // is a few units of 2^-24 off.
 // Else the result is rounded to 16 bits or 8: the fast forms, with numerator and denominator scaled by 2^-32, so that the
 // denominator passes 2^126, where the fast reciprocal ends, only for gates below -109, whose sigmoid float32 cannot hold.
-// The exponent is off by |g| 2^-24 at the most: 2^-17 where the sigmoid is next to nothing.  sig(-g) is 1 - sig(g), 2^-24
-// off; it is added to 1 after a product with g.  (The full forms take the bf16 step's forward from 113 to 124 us for
-// 8192 x 14336, and float32 to 8 bits from 164 to 188 us; float32 to float32 takes 211 us with either.)
+// e^-g is the square of e^(-g / 2), which stays finite there; it is off by |g| 2^-24 and a few units, 2^-17 where the
+// sigmoid is next to nothing.  (Shifting the exponent by 32 instead rounds it at 2^-19 for every gate.)  sig(-g) is
+// 1 - sig(g), 2^-24 off; it is added to 1 after a product with g.
 struct Sigmoid {
     float pos, neg;
 };
@@ -152,21 +152,21 @@ __device__ __forceinline__ Sigmoid sigmoid(float g) {
         const float e = expf(-fabsf(g)), large = 1.f / (1.f + e), small = e * large;
         return g < 0.f ? Sigmoid{small, large} : Sigmoid{large, small};
     } else {
-        constexpr float kLog2e = 1.4426950408889634f, kUnit = 0x1p-32f;
+        constexpr float kHalfLog2e = 0.7213475204444817f, kUnit = 0x1p-32f;
         float e, r;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(g, -kLog2e, -32.f)));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(kUnit + e));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -kHalfLog2e));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(e * kUnit, e, kUnit)));
         const float sig = kUnit * r;
         return Sigmoid{sig, 1.f - sig};
     }
 }
 
-// Two rows a thread: 64 bytes in flight in each (one row: 162 us for the 8192 x 14336 step with 2048 rows kept, two:
-// 156 us, 95 % of the memory rate).
+// Two rows a thread: 64 bytes in flight in each.  16 bits, 8192 x 14336 with 2048 rows kept: 112 us, the memory rate (one
+// row a thread: 133 us; two with 58 registers, four CTAs to an SM for five: 121 us).
 constexpr int kForwardRows = 2;
 
 template <class Row8, bool H8>
-__global__ void __launch_bounds__(kThreads) swiglu_forward_kernel(
+__global__ void __launch_bounds__(kThreads, std::is_same<Row8, Row8Bf16>::value && !H8 ? 5 : 4) swiglu_forward_kernel(
     Shape s, const void* gu, int64_t ld_gu, void* h, int64_t ld_h,
     float* h_scales, uint8_t* ck_codes, float* ck_scales,
     const __grid_constant__ TrainRanges train) {
@@ -222,12 +222,12 @@ __global__ void __launch_bounds__(kThreads) swiglu_forward_kernel(
     }
 }
 
+// Eight CTAs to an SM keep enough reads in flight, which takes 32 registers a thread; the full forms of float32 need 40, and
+// gain from them (2048 x 14336: 63 us, 64 with the fast forms and 32).
 template <class Row8, bool D8>
-__global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(Shape s, const uint8_t* ck_codes,
-                                                                   const float* ck_scales,
-                                                                   const void* dh, int64_t ld_dh,
-                                                                   void* dgu, int64_t ld_dgu,
-                                                                   float* dgu_scales) {
+__global__ void __launch_bounds__(kThreads, std::is_same<Row8, Row8F32>::value && !D8 ? 6 : 8) swiglu_backward_kernel(
+    Shape s, const uint8_t* ck_codes, const float* ck_scales, const void* dh, int64_t ld_dh, void* dgu, int64_t ld_dgu,
+    float* dgu_scales) {
     grid_dep_launch();
     grid_dep_wait();
     constexpr bool kFull = std::is_same<Row8, Row8F32>::value && !D8;
