@@ -182,7 +182,7 @@ def peaks():
 
 def kernel_hash():
     h = hashlib.sha256()
-    for f in ("tc_kernel.cu", "tc_kernel.h", "common.h"):
+    for f in ("tc_kernel.cu", "tc_kernel.h", "tc_prims.h", "common.h"):
         h.update(open(os.path.join(ROOT, "lora_co_serving_gb300", "csrc", f), "rb").read())
     return h.hexdigest()[:16]
 

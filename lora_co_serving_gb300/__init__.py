@@ -638,7 +638,8 @@ _status_workspaces = {}
 
 def _status_workspace(stream_ptr, device):
     """A stream's own workspace for calls that need no more than the status word and do not read it: calls on one stream
-    run one after another, but a thread's call may clear the word before another thread has read it.  None while a CUDA graph is captured (its replays may run beside the stream's later calls)."""
+    run one after another, but a thread's call may clear the word before another thread has read it.  None while a CUDA
+    graph is captured (its replays may run beside the stream's later calls)."""
     import torch
     if torch._C._cuda_isCurrentStreamCapturing():
         return None

@@ -26,7 +26,7 @@ __device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, volatil
 }
 
 // Two waits whose first tests are under way together: a test takes about 80 cycles, on the chain of every block that is
-// issued (256 x 4096 x 28672 33.6 us so, 34.8 us one after the other)
+// issued (500 x 4096 x 4096 10.8 us so, 11.0 us one after the other; 256 x 4096 x 28672 33.7 and 33.9)
 __device__ __forceinline__ void wait_both(uint32_t bar, uint32_t parity, uint32_t bar2, uint32_t parity2,
                                           volatile int* abort_flag, int32_t* status) {
     const bool ok = mbar_try_wait(bar, parity), ok2 = mbar_try_wait(bar2, parity2);
@@ -138,7 +138,7 @@ struct TileCfg {
     static constexpr int kWBytes = kPN * kQBlock;        // the tile's rows of w
     // What passes the barriers at a time: one block, or two of 128 outputs, whose MMAs take 256 cycles each: issuing a
     // block (two barrier tests, four MMAs, two commits: about 400 cycles) would take longer.  500 x 4096 x 4096 takes
-    // 11.7 us so, 13.2 us a block at a time.
+    // 10.8 us so, 12.1 us a block at a time (300 x 5120 x 5120: 13.6 and 14.4; 256 x 4096 x 28672: 33.7 and 32.9).
     static constexpr int kStep = 256 / kPN;
     static constexpr int kBlockBytes = kOperandBytes + kWBytes, kStageBytes = kStep * kBlockBytes;
     static constexpr int kStages = kPN == 256 ? 4 : 3;
@@ -206,7 +206,7 @@ struct Bars {
     volatile int* abort_flag;
 };
 
-// The whole warp runs this loop too (see tile_issue): 600 x 2704 x 2704 10.7 us so, 11.0 us in a loop of one lane
+// The whole warp runs this loop too (see tile_issue); in a loop of one lane 600 x 2704 x 2704 took 3 % longer
 template <class C>
 __device__ __forceinline__ void tile_load(const TileParams& P, const Bars& B, uint8_t* smem) {
     const bool one = elect_one();
@@ -830,12 +830,14 @@ cudaError_t device_sms(int* sms) {
 }
 
 // Whether a product runs on linear_rows_kernel: up to 32 rows, and up to 64 where K is long enough to be cut and N does not
-// fill the SMs by itself.  64 x 8192 x 8192 takes 16.8 us there (19.1 us on tiles), 64 x 2704 x 2704 7.7 us (8.5 us);
-// 64 x 512 x 2704 7.0 us (5.1 us), 64 x 4096 x 28672 27.8 us (25.1 us); 32 x 4096 x 28672 24.3 us (24.7 us).
+// fill the SMs by itself.  64 x 8192 x 8192 takes 17.0 us there (17.9 us on tiles), 64 x 2704 x 2704 7.8 us (7.8 us);
+// 64 x 512 x 2704 7.1 us (4.3 us), 64 x 4096 x 28672 28.7 us (24.6 us); 32 x 4096 x 4096 6.5 us (7.2 us), 32 x 4096 x
+// 28672 23.9 us (23.8 us).  The rule loses where K is of middling length: 48 x 4096 x 4096 8.4 us (7.4 us).
 bool few_rows(int32_t T, int32_t K, int32_t N) { return T <= 32 || (T <= 64 && K > 1024 && N <= 8192); }
-// Whether that kernel quantizes x itself: a launch less, but a part of every 128 outputs' work, so for few products.  In a
-// program's loop 16 x 4096 x 4096 takes 8.0 us so (quantized first: 9.6 us, the host's part of two launches), 1 x 4096 x
-// 28672 24.6 us (24.8 us), 16 x 5120 x 5120 13.2 us (9.6 us).
+// Whether that kernel quantizes x itself: a launch less, but a part of every 128 outputs' work, so for few products.  From
+// a program's loop, which two launches and a workspace hold up, and replayed from a graph: 16 x 4096 x 4096 takes 13 and
+// 7.7 us so (quantized first: 18 and 6.9 us), 1 x 4096 x 28672 24.5 and 24.0 us (24.6 and 23.2 us), 16 x 5120 x 5120 13.3
+// and 12.7 us (18 and 8.2 us).
 bool quantized_on_the_way(int32_t T, int32_t K, int32_t N) { return T <= 16 && (int64_t)T * K * N <= (1 << 28); }
 
 // A product's shape, and how its tiles are spread over the SMs.  Tiles beyond the last full round may be cut along K, into

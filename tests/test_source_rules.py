@@ -65,3 +65,17 @@ def test_commits_of_the_products_end_before_their_cta(file, name, args, body):
         if m.group(1) in called:
             text += m.group(2)
     assert "mma_commit(" in text and "await_commits(ring" in text
+
+
+def test_the_benchmark_has_the_main_pass_traffic_of_these_sources():
+    """The benchmark reports the DRAM bytes of a committed profile only while it belongs to the sources, all of them."""
+    import json
+    import bench
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "profiles", "fwd_main_traffic.json")) as f:
+        cfg = json.load(f)["config"]
+    assert bench.profiled_traffic(cfg) is not None
+    named = re.findall(r'#include "(\w+\.h)"', open(os.path.join(CSRC, "tc_kernel.cu")).read())
+    with open(os.path.join(root, "bench.py")) as f:
+        hashed = re.search(r"def kernel_hash.*?\n\n", f.read(), flags=re.S).group(0)
+    assert "tc_prims.h" in named and all(n in hashed for n in named)
