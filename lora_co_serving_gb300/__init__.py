@@ -818,7 +818,8 @@ def preference_backward(logits, labels, lse, coef, pairs, dloss=None, dlogits=No
     """Gradient of the logits [T, V] in their type: every row is written, zeros where a row is not counted.
 
     dloss [P] float32: the gradient of each pair's loss (default: 1 / P each, the mean's).  dlogits may be `logits`
-    itself: the gradient then takes the logits' place."""
+    itself: the gradient then takes the logits' place.  Rows whose |lse| is 256 or more are read twice: one float32 number
+    no longer holds it well enough for their probabilities."""
     import torch
     code, ld = _dtype_code(logits), _matrix(logits, "logits")
     T, V = logits.shape

@@ -841,8 +841,8 @@ bool few_rows(int32_t T, int32_t K, int32_t N) { return T <= 32 || (T <= 64 && K
 bool quantized_on_the_way(int32_t T, int32_t K, int32_t N) { return T <= 16 && (int64_t)T * K * N <= (1 << 28); }
 
 // A product's shape, and how its tiles are spread over the SMs.  Tiles beyond the last full round may be cut along K, into
-// as many pieces as SMs are left for each, at most kMaxSplit, of at least kMinBlocks blocks: a round of 8 tiles holds 144
-// of 152 SMs for a tile's whole time.  The choice is by an estimate whose numbers were fitted to measured products.  For 169
+// as many pieces as SMs are left for each, at most kMaxSplit, of at least kMinBlocks blocks: a last round of 8 tiles would
+// leave 144 of 152 SMs idle for a tile's whole time.  The choice is by an estimate whose numbers were fitted.  For 169
 // products of 68 to 8192 rows (K and N from 512 to 28672) it is 11 % off (rms; the 3 us that every launch takes are left
 // out of it), the shape it takes 0.2 % slower than the better of the two, 10 % at the worst (384 x 2704 x 2704).
 // Measured in us, x in 8 bits, weights of fp8_quantize_weight, three in turn, in replayed graphs of a few milliseconds:
