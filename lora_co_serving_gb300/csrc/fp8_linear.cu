@@ -110,9 +110,10 @@ __device__ __forceinline__ float2 halves(uint64_t a) {
 //
 // What bounds it: a block's MMAs are 512 cycles of tensor work; its 48 KB are written to shared memory once and read
 // once, 750 cycles at 128 bytes a cycle; scaling and adding takes an accumulator about 550 cycles, of which 256 are its
-// 128 x 256 multiply-adds, and handing it over and back comes on top.  Two accumulators hide part of that.  8192 x 8192 x 28672 takes 1.455 ms (2640
-// TFLOP/s) in runs of a few milliseconds, at 2.07 GHz; longer ones meet the power limit, which lowers the clock:
-// 2048 x 28672 x 8192 takes 336 us at first and 373 us, at 1.63 GHz, when it runs for half a second.
+// 128 x 256 multiply-adds, and handing it over and back comes on top.  Two accumulators hide part of that.
+// 8192 x 8192 x 28672 takes 1.455 ms (2640 TFLOP/s) in runs of a few milliseconds, at 2.07 GHz; longer ones meet the power
+// limit, which lowers the clock: 2048 x 28672 x 8192 takes 336 us at first and 373 us, at 1.63 GHz, when it runs for half a
+// second.
 //
 // Neighbouring CTAs load the same rows of w, each for itself, from L2.
 //
