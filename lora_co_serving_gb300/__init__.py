@@ -17,6 +17,13 @@ and, around the layer in a fine-tuning step (``include/lora_fp8.h``, ``include/l
     token_logprob                           -> log probability of each row's label
     preference_forward / preference_backward-> paired log-ratio loss and the gradient of the logits
 
+and, between the q|k|v projection and the output projection (``include/lora_attention.h``):
+
+    rotary_turns, kv_cache                  -> rotary frequencies; an empty paged cache, in 16 bits or 8
+    rotary_forward / rotary_backward        -> norm and rotary positions of query and key heads, keys and values cached
+    cache_write / cache_read                -> rows into the paged cache, quantized on the way, and back
+    decode_attention                        -> attention of one new token of each sequence over the paged cache
+
 ``segs`` is an int32 array (or list) of rows {start, len, adapter_id, is_train};
 ``Pool`` holds the stacked adapter factors (A blocks [r_a, K], B blocks [r_a, N])
 on the device plus their host-side offsets, ranks and scales.
@@ -26,7 +33,9 @@ fallback path.
 """
 import ctypes
 import functools
+import math
 import os
+import struct
 from collections import namedtuple
 
 import numpy as np
@@ -38,7 +47,9 @@ __all__ = ["Pool", "forward", "backward", "sliced_forward", "sliced_backward", "
            "LoraError", "LibraryNotBuilt", "library", "build", "SAVE_XA", "RECOMPUTE_XA", "ACCUMULATE_GRAD",
            "DEBUG_CHECKS", "plan_check", "static_status", "set_wait_limit", "fp8_quantize", "fp8_quantize_weight",
            "fp8_linear", "fp8_workspace_size", "checkpoint_rows", "swiglu_forward", "swiglu_backward",
-           "token_logprob", "preference_forward", "preference_backward", "Preference"]
+           "token_logprob", "preference_forward", "preference_backward", "Preference", "KVCache", "kv_cache",
+           "rotary_turns", "rotary_forward", "rotary_backward", "cache_write", "cache_read", "decode_attention",
+           "decode_workspace_size"]
 
 SAVE_XA = 1
 RECOMPUTE_XA = 2
@@ -60,7 +71,8 @@ EXPORTED = ["lora_workspace_size", "lora_xa_size", "lora_mixed_forward", "lora_m
             "lora_static_status", "lora_plan_check", "lora_set_wait_limit", "lora_fp8_quantize",
             "lora_fp8_quantize_weight", "lora_fp8_workspace_size", "lora_fp8_linear", "lora_checkpoint_rows",
             "lora_swiglu_forward", "lora_swiglu_backward", "lora_token_logprob", "lora_preference_forward",
-            "lora_preference_backward"]
+            "lora_preference_backward", "lora_rotary_forward", "lora_rotary_workspace_size", "lora_rotary_backward",
+            "lora_cache_write", "lora_cache_read", "lora_decode_workspace_size", "lora_decode_attention"]
 
 
 class LoraError(RuntimeError):
@@ -167,7 +179,14 @@ def library(path=None):
             ("lora_swiglu_backward", INT, [I32, I32, INT, P, P, P, I64, P, I64, P, P]),
             ("lora_token_logprob", INT, [I32, I32, INT, P, I64, P, P, P, P]),
             ("lora_preference_forward", INT, [I32, I32, INT, P, I64, P, P, P, I32, F, F, P, P, P, P, P, P]),
-            ("lora_preference_backward", INT, [I32, I32, INT, P, I64, P, P, P, P, I32, P, P, I64, P])):
+            ("lora_preference_backward", INT, [I32, I32, INT, P, I64, P, P, P, P, I32, P, P, I64, P]),
+            ("lora_rotary_forward", INT, [I32, INT, P, P, I64, P, P, I64, P, I64, P, P, I32, P]),
+            ("lora_rotary_workspace_size", SZ, [I32, P]),
+            ("lora_rotary_backward", INT, [I32, INT, P, P, I64, P, P, I64, P, I64, P, P, P, SZ, P]),
+            ("lora_cache_write", INT, [I32, INT, P, I64, P, I64, P, P, P]),
+            ("lora_cache_read", INT, [I32, INT, P, P, P, I64, P, I64, P]),
+            ("lora_decode_workspace_size", SZ, [I32, P]),
+            ("lora_decode_attention", INT, [I32, I32, P, I64, P, P, I64, I32, P, I32, F, F, P, I64, P, P, SZ, P])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
     if path is None:
@@ -840,3 +859,294 @@ def preference_backward(logits, labels, lse, coef, pairs, dloss=None, dlogits=No
     if rc != 0:
         _check(rc)
     return dlogits
+
+
+# -------------------------------------------------------------------------------------- rotary positions, paged cache
+KVCache = namedtuple("KVCache", ["k", "v", "k_scales", "v_scales"], defaults=[None, None])
+KVCache.__doc__ = """A paged key-value cache: k and v [pages, kv heads, rows of a page, head size] (bf16, or float8_e4m3fn with
+float32 scales k_scales and v_scales [pages, kv heads, rows of a page]).  Pages, heads and rows may lie in any order in
+memory (a transposed view, halves of one buffer), k and v alike.  A row's slot is page * rows of a page + row."""
+
+
+def kv_cache(n_pages, n_kv_heads, page_size, head_dim, dtype=None, device="cuda"):
+    """An empty paged cache of bf16 (the default) or float8_e4m3fn."""
+    import torch
+    dtype = torch.bfloat16 if dtype is None else dtype
+    shape = (n_pages, n_kv_heads, page_size, head_dim)
+    if dtype is torch.bfloat16:
+        return KVCache(*(torch.zeros(shape, dtype=dtype, device=device) for _ in range(2)))
+    if dtype is not torch.float8_e4m3fn:
+        raise TypeError("a cache holds bfloat16 or float8_e4m3fn, got %s" % dtype)
+    return KVCache(*(torch.zeros(shape, dtype=torch.uint8, device=device).view(dtype) for _ in range(2)),
+                   *(torch.ones(shape[:3], dtype=torch.float32, device=device) for _ in range(2)))
+
+
+_CACHE_STRUCT = struct.Struct("@4P6q5i4x")
+
+
+def _cache(cache):
+    """(lora_cache_t as bytes, n_heads, head_dim, tensors) of a KVCache or a tuple laid out as one."""
+    import torch
+    k, v, ks, vs = cache if len(cache) == 4 else (*cache, None, None)
+    if len(k.shape) != 4:
+        raise ValueError("a cache's keys must have four dimensions, got %d" % len(k.shape))
+    pages, heads, rows, D = k.shape
+    st = k.stride()
+    if v.shape != k.shape or v.dtype is not k.dtype or v.stride() != st:
+        raise ValueError("a cache's keys and values must have one shape, type and layout")
+    if st[3] != 1:
+        raise ValueError("a cache's rows must have unit stride")
+    if k.dtype is torch.bfloat16:
+        if ks is not None or vs is not None:
+            raise ValueError("a cache in 16 bits has no scales")
+        return (_CACHE_STRUCT.pack(k.data_ptr(), v.data_ptr(), 0, 0, st[0], st[1], st[2], 0, 0, 0, pages, heads, rows, D, 0),
+                heads, D, (k, v))
+    if k.dtype is not torch.float8_e4m3fn:
+        raise TypeError("a cache holds bfloat16 or float8_e4m3fn, got %s" % k.dtype)
+    if ks is None or vs is None:
+        raise ValueError("a cache in 8 bits needs k_scales and v_scales")
+    if ks.dtype is not torch.float32 or vs.dtype is not torch.float32:
+        raise TypeError("a cache's scales must be float32")
+    zt = ks.stride()
+    if ks.shape != k.shape[:3] or vs.shape != ks.shape or vs.stride() != zt:
+        raise ValueError("a cache's scales must be [pages, heads, rows of a page], in one layout")
+    return (_CACHE_STRUCT.pack(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), st[0], st[1], st[2], zt[0], zt[1],
+                               zt[2], pages, heads, rows, D, 1), heads, D, (k, v, ks, vs))
+
+
+def rotary_turns(rot_dim, base=10000.0, frequencies=None, device="cuda"):
+    """The frequencies of rotary positions as the calls below take them, int64 [rot_dim / 2]: turns a position in units of
+    2^-64.  They are base^(-2 i / rot_dim) (radians a position), or the `frequencies` given (scaled ones, for instance)."""
+    import torch
+    if rot_dim % 16:
+        raise ValueError("rot_dim must be a multiple of 16, got %d" % rot_dim)
+    if frequencies is None:
+        frequencies = [base ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
+    if len(frequencies) != rot_dim // 2:
+        raise ValueError("%d frequencies needed, got %d" % (rot_dim // 2, len(frequencies)))
+    turns = [round(float(f) / (2.0 * math.pi) * 2.0 ** 64) % 2 ** 64 for f in frequencies]
+    return torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
+
+
+_ROTARY_STRUCT = struct.Struct("@3P5if")
+
+
+def _rotary(cols, turns, n_heads, n_kv_heads, q_weight, k_weight, eps, interleaved, dtype):
+    """(lora_rotary_t as bytes, head size) for rows of `cols` elements."""
+    import torch
+    H = n_heads + n_kv_heads
+    if n_heads < 1 or n_kv_heads < 1 or cols % H:
+        raise ValueError("rows of %d elements do not hold %d query and %d key heads" % (cols, n_heads, n_kv_heads))
+    D = cols // H
+    if turns is not None:
+        _vector(turns, "turns", torch.int64, turns.numel())
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _vector(w, name, dtype, D)
+    return _ROTARY_STRUCT.pack(_ptr(turns) or 0, _ptr(q_weight) or 0, _ptr(k_weight) or 0, n_heads, n_kv_heads, D,
+                               0 if turns is None else 2 * turns.numel(), 1 if interleaved else 0, eps), D
+
+
+def _positions(positions, turns, T):
+    import torch
+    if positions is not None:
+        _vector(positions, "positions", torch.int64, T)
+    elif turns is not None:
+        raise ValueError("turns need positions")
+
+
+@_on_stream
+def rotary_forward(x, positions, turns, n_heads, n_kv_heads, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                   v=None, cache=None, slots=None, keep_keys=False, out=None):
+    """Query and key heads x [T, (n_heads + n_kv_heads) D] (bf16 or float32; the first columns of a fused q|k|v, for
+    instance) normalised where a weight [D] of x's type is given (root mean square over the head, eps), and turned by
+    positions [T] (int64) times `turns` (rotary_turns; None: no rotation).  Pairs are (i, i + R/2), or neighbours with
+    interleaved=True; elements past the first R = 2 len(turns) are not turned.
+
+    Without a cache: returns queries and keys, as x lies.  With one, the keys and v [T, n_kv_heads D] go to the cache's
+    slots [T] (int64; a slot outside it, such as -1, is not written; no slot twice), and the queries are returned, with
+    keep_keys the keys after them.  out may be x itself."""
+    import torch
+    code, ld = _dtype_code(x), _matrix(x, "x")
+    T, cols = x.shape
+    r, D = _rotary(cols, turns, n_heads, n_kv_heads, q_weight, k_weight, eps, interleaved, x.dtype)
+    _positions(positions, turns, T)
+    c, ldv, held = None, 0, ()
+    if cache is not None:
+        c, heads, size, held = _cache(cache)
+        if heads != n_kv_heads or size != D:
+            raise ValueError("the cache holds %d heads of %d, the keys are %d of %d" % (heads, size, n_kv_heads, D))
+        if v is None or slots is None:
+            raise ValueError("a cache needs v and slots")
+        ldv = _matrix(v, "v", x.dtype, T, n_kv_heads * D)
+        _vector(slots, "slots", torch.int64, T)
+        if not keep_keys:
+            cols = n_heads * D
+    elif v is not None or slots is not None:
+        raise ValueError("v and slots need a cache")
+    if out is None:
+        out, ldo = torch.empty((T, cols), dtype=x.dtype, device=x.device), cols
+    else:
+        ldo = _matrix(out, "out", x.dtype, T, cols)
+    _one_device(x, positions, turns, q_weight, k_weight, v, slots, out, *held)
+    rc = library().lora_rotary_forward(T, code, r, x.data_ptr(), ld, _ptr(positions), out.data_ptr(), ldo, _ptr(v), ldv, c,
+                                       _ptr(slots), 1 if keep_keys else 0, _stream_ptr(None))
+    if rc != 0:
+        _check(rc)
+    return out
+
+
+@_on_stream
+def rotary_backward(x, positions, turns, n_heads, n_kv_heads, dout, q_weight=None, k_weight=None, eps=1e-6,
+                    interleaved=False, weight_grads=False, dx=None, workspace=None):
+    """Gradient of rotary_forward's x from dout [T, (n_heads + n_kv_heads) D], the gradient of queries and keys; x is the
+    forward's input (None where no weight is given).  dx may be dout itself.  weight_grads: returns (dx, dq_weight,
+    dk_weight), float32 [D] (None for a weight that is not given)."""
+    import torch
+    code, ldd = _dtype_code(dout), _matrix(dout, "dout")
+    T, cols = dout.shape
+    r, D = _rotary(cols, turns, n_heads, n_kv_heads, q_weight, k_weight, eps, interleaved, dout.dtype)
+    _positions(positions, turns, T)
+    ld = 0
+    if q_weight is not None or k_weight is not None:
+        if x is None:
+            raise ValueError("the gradient of a norm needs its input x")
+        ld = _matrix(x, "x", dout.dtype, T, cols)
+    else:
+        x = None
+    if dx is None:
+        dx, ldx = torch.empty((T, cols), dtype=dout.dtype, device=dout.device), cols
+    else:
+        ldx = _matrix(dx, "dx", dout.dtype, T, cols)
+    dq = dk = None
+    if weight_grads:
+        if q_weight is not None:
+            dq = torch.empty(D, dtype=torch.float32, device=dout.device)
+        if k_weight is not None:
+            dk = torch.empty(D, dtype=torch.float32, device=dout.device)
+        if workspace is None and x is not None:
+            n = library().lora_rotary_workspace_size(T, r)
+            if n == 0:
+                raise LoraError(-1, library().lora_last_error().decode())
+            workspace = torch.empty(n, dtype=torch.uint8, device=dout.device)
+    _one_device(dout, x, positions, turns, q_weight, k_weight, dx, workspace)
+    rc = library().lora_rotary_backward(T, code, r, _ptr(x), ld, _ptr(positions), dout.data_ptr(), ldd, dx.data_ptr(), ldx,
+                                        _ptr(dq), _ptr(dk), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                                        _stream_ptr(None))
+    if rc != 0:
+        _check(rc)
+    return (dx, dq, dk) if weight_grads else dx
+
+
+@_on_stream
+def cache_write(k, v, cache, slots):
+    """Rows k and v [T, n_kv_heads D] (bf16 or float32) to the cache's slots [T] (int64; a slot outside the cache is not
+    written, no slot may come twice), quantized on the way into 8 bits."""
+    import torch
+    code, ldk = _dtype_code(k), _matrix(k, "k")
+    c, heads, D, held = _cache(cache)
+    T = k.shape[0]
+    _matrix(k, "k", k.dtype, T, heads * D)
+    ldv = _matrix(v, "v", k.dtype, T, heads * D)
+    _vector(slots, "slots", torch.int64, T)
+    _one_device(k, v, slots, *held)
+    rc = library().lora_cache_write(T, code, k.data_ptr(), ldk, v.data_ptr(), ldv, c, slots.data_ptr(), _stream_ptr(None))
+    if rc != 0:
+        _check(rc)
+
+
+@_on_stream
+def cache_read(cache, slots, dtype=None, k=None, v=None):
+    """(k, v) [T, n_kv_heads D] of the cache's slots [T] (int64; a slot outside the cache gives zeros), in bf16 (the
+    default) or float32."""
+    import torch
+    c, heads, D, held = _cache(cache)
+    T, cols = slots.numel(), heads * D
+    _vector(slots, "slots", torch.int64, T)
+    if dtype is None:
+        dtype = torch.bfloat16 if k is None else k.dtype
+    if k is None:
+        k = torch.empty((T, cols), dtype=dtype, device=slots.device)
+    if v is None:
+        v = torch.empty((T, cols), dtype=dtype, device=slots.device)
+    code, ldk, ldv = _dtype_code(k), _matrix(k, "k", dtype, T, cols), _matrix(v, "v", dtype, T, cols)
+    _one_device(slots, k, v, *held)
+    rc = library().lora_cache_read(T, code, c, slots.data_ptr(), k.data_ptr(), ldk, v.data_ptr(), ldv, _stream_ptr(None))
+    if rc != 0:
+        _check(rc)
+    return k, v
+
+
+def decode_workspace_size(n_heads, cache):
+    """Bytes of workspace that decode_attention needs for n_heads query heads over this cache, on the current device."""
+    import torch
+    k = cache[0]
+    return _decode_size(n_heads, k.shape[1], k.shape[3], k.dtype is torch.float8_e4m3fn, torch._C._cuda_getDevice())
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_size(n_heads, kv_heads, D, e4m3, device):
+    c = _CACHE_STRUCT.pack(0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, kv_heads, 1, D, 1 if e4m3 else 0)
+    n = library().lora_decode_workspace_size(n_heads, c)
+    if n == 0:
+        raise LoraError(-1, library().lora_last_error().decode())
+    return int(n)
+
+
+_DECODE_COUNTER_BYTES = 8192
+_decode_workspaces = {}
+
+
+def _decode_workspace(n, stream_ptr, device):
+    """A stream's own workspace of at least n bytes: calls on one stream run one after another and leave its counters
+    zero.  While a CUDA graph is captured, a new one, whose counters the graph itself clears: its replays may run beside
+    the stream's later calls."""
+    import torch
+    capturing = torch._C._cuda_isCurrentStreamCapturing()
+    key = (device.index, stream_ptr)
+    ws = None if capturing else _decode_workspaces.get(key)
+    if ws is None or ws.numel() < n:
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        ws[:_DECODE_COUNTER_BYTES].zero_()
+        if not capturing:
+            _decode_workspaces[key] = ws
+    return ws
+
+
+@_on_stream
+def decode_attention(q, cache, page_table, lengths, scale=None, window=0, softcap=0.0, want_lse=False, out=None,
+                     workspace=None):
+    """Attention of one new token of each sequence over its cached rows: q [B, n_heads D] (bf16), page_table [B, pages]
+    and lengths [B] (int32; the new token's row among them).  Query head h attends with the cache's head h // (n_heads /
+    n_kv_heads), over the last `window` rows (0: all), with scores scale q.k (default D^-1/2), capped to softcap
+    tanh(score / softcap) where softcap > 0.
+
+    Returns out [B, n_heads D], with want_lse (out, lse [B, n_heads] float32).  A length of zero gives zeros and -infinity;
+    a sequence longer than its table's row, or a page outside the cache, gives NaN.  workspace: decode_workspace_size
+    bytes, the first 8192 zero before its first use; not for two calls at once."""
+    import torch
+    c, kv_heads, D, held = _cache(cache)
+    ldq = _matrix(q, "q", torch.bfloat16)
+    B, cols = q.shape
+    if cols % D or cols // D % kv_heads or cols == 0:
+        raise ValueError("rows of %d elements do not hold query heads of %d in groups of %d" % (cols, D, kv_heads))
+    n_heads = cols // D
+    ldt = _matrix(page_table, "page_table", torch.int32)
+    if page_table.shape[0] != B:
+        raise ValueError("page_table must have a row for each of %d sequences, got %d" % (B, page_table.shape[0]))
+    _vector(lengths, "lengths", torch.int32, B)
+    if out is None:
+        out, ldo = torch.empty((B, cols), dtype=q.dtype, device=q.device), cols
+    else:
+        ldo = _matrix(out, "out", torch.bfloat16, B, cols)
+    lse = torch.empty((B, n_heads), dtype=torch.float32, device=q.device) if want_lse else None
+    _one_device(q, page_table, lengths, out, workspace, *held)
+    st = _stream_ptr(None)
+    if workspace is None:
+        workspace = _decode_workspace(_decode_size(n_heads, kv_heads, D, len(held) == 4, q.get_device()), st, q.device)
+    rc = library().lora_decode_attention(B, n_heads, q.data_ptr(), ldq, c, page_table.data_ptr(), ldt, page_table.shape[1],
+                                         lengths.data_ptr(), window, D ** -0.5 if scale is None else scale, softcap,
+                                         out.data_ptr(), ldo, _ptr(lse), workspace.data_ptr(), workspace.numel(), st)
+    if rc != 0:
+        _check(rc)
+    return (out, lse) if want_lse else out
