@@ -21,7 +21,8 @@
  * float32 scale for each head's row, k_scales and v_scales at page * scale_page_stride + head * scale_head_stride +
  * row * scale_row_stride.  A value is its code times its row's scale.  The functions here choose the smallest power of two
  * that brings the row within 448, e4m3's largest value (and at least 2^-108), as the 8-bit rows of lora_fp8.h; a row that
- * holds an infinity or a NaN gets the scale NaN.  lora_decode_attention and lora_cache_read accept any scales.
+ * holds an infinity or a NaN gets the scale NaN.  lora_cache_read accepts any scales,
+ * lora_decode_attention any that are not negative (a negative value scale gives NaN).
  * The place of a row is its slot, page * page_size + row in the page.
  *
  * The conventions of lora_mixed.h hold: device pointers unless marked HOST; the caller owns every buffer; everything
@@ -130,7 +131,8 @@ size_t lora_decode_workspace_size(int32_t n_heads, const lora_cache_t* cache /* 
  * A length of zero or less gives out = 0 and lse = -infinity.  A sequence that is longer than its table's row, or one of
  * whose pages lies outside the cache, gives NaN; nothing outside the cache is read.  Rows outside the range, and table
  * entries past it, are not read.  An infinite element of a value row in the range gives an infinity or NaN there.
- * n_heads a multiple of the cache's heads.  workspace: 256-byte aligned, >= lora_decode_workspace_size bytes, its first
+ * n_heads a multiple of the cache's heads; the cache's last row at most 2^32 units from its first, of the largest power of
+ * two that divides page_stride and row_stride in bytes (LORA_ERR_LIMIT).  workspace: 256-byte aligned, >= lora_decode_workspace_size bytes, its first
  * LORA_DECODE_COUNTER_BYTES zero before its first use; every call leaves them zero.  Calls that share a workspace must not
  * overlap on the GPU. */
 #define LORA_DECODE_COUNTER_BYTES 8192

@@ -8,10 +8,10 @@
 //           the B operand of two MMAs (four in 8 bits), if the query's elements are taken in the same order;
 //   output  B needs a pair of tokens of one element in a register: a lane loads the same 16 bytes of a pair's two value
 //           rows and interleaves them; which element is which output column is free, too.
-// Work is counted in tiles of 64 tokens of one sequence and one cache head.  All tiles of a call form one line, and each
-// CTA takes an equal piece of it, whatever the lengths are; a CTA's warps take 16 tokens of a tile each, with a running
-// maximum and sum of their own.  A sequence and head whose tiles lie in several CTAs is joined by the last of them to
-// arrive, in the order of the tiles.
+// Work is counted in tiles of 32 to 128 tokens of one sequence and one cache head.  All tiles of a call form one line, and
+// each CTA takes an equal piece of it, whatever the lengths are; a CTA's warps take 16 or 32 tokens of a tile each, with a
+// running maximum and sum of their own.  A sequence and head whose tiles lie in several CTAs is joined by the last of them
+// to arrive, in the order of the tiles.
 #include <algorithm>
 #include <type_traits>
 
@@ -24,8 +24,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kWarpTokens = 16;
-constexpr int kTileTokens = kWarps * kWarpTokens;
+constexpr int kMaxCtas = 912;        // of a launch: six on each SM
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 // A running maximum is raised only when a score exceeds it by a factor of 2^kSlack: probabilities stay below that.
@@ -95,6 +94,7 @@ struct Decode {
     int32_t parts, rows;     // a group is taken in `parts` of up to `rows` (<= 8 or 16) query heads
     int32_t table_width, window;
     PageDivision pages;
+    uint32_t unit, page_units, row_units;      // bytes that divide the cache's strides; the strides in these units
     float scale, softcap;
     int32_t* counters;
     float* ws;
@@ -104,143 +104,171 @@ __device__ __forceinline__ Range range_of(const Decode& a, int32_t b) {
     return Range(a.lengths[b], a.window, a.table_width, a.cache.page_size);
 }
 
-// A warp's 16 tokens: where each token's row lies, one token a lane (and once more in lanes 16 to 31)
-struct Rows {
-    int64_t at;              // bytes from head 0 of the cache; -1: no token, or no page
-    float scale;             // 8 bits: the token's key scale (lanes 16 to 31: value scale)
+// Shapes of a kernel for cache heads of up to kD elements and kRows query heads at a time.  A warp holds kPart elements of
+// each row: 128 at most, so that its sums, its share of the queries and one step's pieces stay in registers; heads of 256
+// are taken by two warps, which add up their scores.
+template <bool kE4m3_, int kD_, int kRows_>
+struct Shapes {
+    static constexpr bool kE4m3 = kE4m3_;
+    static constexpr int kD = kD_, kRows = kRows_;
+    static constexpr int kSplit = kD > 128 ? 2 : 1, kPart = kD / kSplit;
+    static constexpr int kTeams = kWarps / kSplit;                         // groups of warps with tokens of their own
+    static constexpr int kBytes = kPart * (kE4m3 ? 1 : 2);                 // of a row in a warp
+    static constexpr int kTokens = kBytes > 128 ? 16 : 32;                 // of a warp's step: 8 KB of keys and values
+    static constexpr int kTile = kTeams * kTokens;
+    static constexpr int kKeyTiles = kTokens / 8, kPairs = kTokens / 16;
+    static constexpr int kKeyLoads = kBytes / 64;                          // 16-byte pieces of a key row in a lane
+    static constexpr bool kNarrow = kBytes == 64;                          // value pieces of 8 bytes
+    static constexpr int kValueLoads = kNarrow ? 1 : kBytes / 128;         // pieces of a value row
+    static constexpr int kPerPiece = kE4m3 && !kNarrow ? 16 : 8;           // elements of a value piece
+    static constexpr int kOut = kPart / 8;                                 // column tiles of the output
+    static constexpr int kHalves = kRows > 8 ? 2 : 1;                      // rows g and g + 8 of the MMAs' 16
+    static constexpr int kStaged = kPart + 4;                              // a row of sums in shared memory
+    static constexpr int kTeamFloats = kRows * kSplit * kStaged;
+    static_assert(kSplit == 1 || kTeamFloats >= 2 * 2 * kKeyTiles * 4 * 32, "a team's scores pass through its place for sums");
+    static constexpr int kSlot = kRows * (kD + 2);                         // floats of a part of an item: m, l; sums
 };
 
-template <bool kE4m3, int kD, int kRows>
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;
+
+template <class S>
 struct Warp {
-    static constexpr int kKeyLoads = kE4m3 ? kD / 64 : kD / 32;            // 16-byte pieces of a key row in a lane
-    static constexpr int kValueLoads = kE4m3 ? (kD + 127) / 128 : kD / 64; // pieces of a value row
-    static constexpr bool kNarrow = kE4m3 && kD == 64;                     // value pieces of 8 bytes
-    static constexpr int kOut = kD / 8;                                    // column tiles of the output
-    static constexpr int kPerPiece = kE4m3 && !kNarrow ? 16 : 8;           // elements of a value piece
+    uint4 key[S::kKeyTiles][S::kKeyLoads];
+    uint4 value[2 * S::kKeyTiles][S::kValueLoads];
+    float o[S::kOut][4];
 
-    uint4 key[2][kKeyLoads];
-    uint4 value[4][kValueLoads];
-    float o[kOut][4];
-
-    __device__ __forceinline__ void load_keys(const char* base, int64_t at, int D) {
+    // rows: where the row of token `lane` of the step lies, in units of a.unit bytes; bytes: of a row, from base
+    __device__ __forceinline__ void load_keys(const char* base, uint32_t rows, uint32_t unit, int bytes) {
         const int lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int64_t off = __shfl_sync(0xffffffffu, at, 8 * j + g);
+        for (int j = 0; j < S::kKeyTiles; ++j) {
+            const uint32_t at = __shfl_sync(0xffffffffu, rows, 8 * j + g);
+            const char* row = base + (uint64_t)at * unit + 16 * c;
 #pragma unroll
-            for (int i = 0; i < kKeyLoads; ++i) {
-                const int byte = 64 * i + 16 * c;
-                key[j][i] = off >= 0 && byte < (kE4m3 ? D : 2 * D) ? *reinterpret_cast<const uint4*>(base + off + byte)
-                                                                  : make_uint4(0, 0, 0, 0);
-            }
+            for (int i = 0; i < S::kKeyLoads; ++i)
+                key[j][i] = at != kNoRow && 64 * i + 16 * c < bytes ? *reinterpret_cast<const uint4*>(row + 64 * i)
+                                                                   : make_uint4(0, 0, 0, 0);
         }
     }
-    __device__ __forceinline__ void load_values(const char* base, int64_t at, int D) {
+    __device__ __forceinline__ void load_values(const char* base, uint32_t rows, uint32_t unit, int bytes) {
         const int lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t off = __shfl_sync(0xffffffffu, at, 8 * (j / 2) + 2 * c + j % 2);
+        for (int j = 0; j < 2 * S::kKeyTiles; ++j) {
+            const uint32_t at = __shfl_sync(0xffffffffu, rows, 8 * (j / 2) + 2 * c + j % 2);
+            const char* row = base + (uint64_t)at * unit + (S::kNarrow ? 8 : 16) * g;
 #pragma unroll
-            for (int i = 0; i < kValueLoads; ++i) {
+            for (int i = 0; i < S::kValueLoads; ++i) {
                 value[j][i] = make_uint4(0, 0, 0, 0);
-                if constexpr (kNarrow) {
-                    if (off >= 0 && 8 * g < D) {
-                        const uint2 w = *reinterpret_cast<const uint2*>(base + off + 8 * g);
+                if constexpr (S::kNarrow) {
+                    if (at != kNoRow && 8 * g < bytes) {
+                        const uint2 w = *reinterpret_cast<const uint2*>(row);
                         value[j][i].x = w.x;
                         value[j][i].y = w.y;
                     }
                 } else {
-                    const int byte = 128 * i + 16 * g;
-                    if (off >= 0 && byte < (kE4m3 ? D : 2 * D))
-                        value[j][i] = *reinterpret_cast<const uint4*>(base + off + byte);
+                    if (at != kNoRow && 128 * i + 16 * g < bytes) value[j][i] = *reinterpret_cast<const uint4*>(row + 128 * i);
                 }
             }
         }
     }
     // s[j]: products of this lane's queries (rows g, g + 8) with tokens 8 j + 2 c and the next one
     template <class Query>
-    __device__ __forceinline__ void scores(const Query& q, float (&s)[2][4]) {
+    __device__ __forceinline__ void scores(const Query& q, float (&s)[S::kKeyTiles][4]) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < S::kKeyTiles; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
 #pragma unroll
-        for (int i = 0; i < kKeyLoads; ++i)
+        for (int i = 0; i < S::kKeyLoads; ++i)
 #pragma unroll
-            for (int m = 0; m < (kE4m3 ? 4 : 2); ++m)
+            for (int m = 0; m < (S::kE4m3 ? 4 : 2); ++m)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+                for (int j = 0; j < S::kKeyTiles; ++j) {
                     const uint32_t w[4] = {key[j][i].x, key[j][i].y, key[j][i].z, key[j][i].w};
-                    const int k = i * (kE4m3 ? 4 : 2) + m;
-                    const uint32_t b0 = kE4m3 ? codes_to_half(w[m]) : w[2 * m % 4];
-                    const uint32_t b1 = kE4m3 ? codes_to_half(w[m] >> 16) : w[(2 * m + 1) % 4];
-                    mma<kE4m3>(s[j], q.lo[2 * k], kRows > 8 ? q.hi[2 * k] : 0u, q.lo[2 * k + 1],
-                               kRows > 8 ? q.hi[2 * k + 1] : 0u, b0, b1);
+                    const int k = i * (S::kE4m3 ? 4 : 2) + m;
+                    const uint32_t b0 = S::kE4m3 ? codes_to_half(w[m]) : w[2 * m % 4];
+                    const uint32_t b1 = S::kE4m3 ? codes_to_half(w[m] >> 16) : w[(2 * m + 1) % 4];
+                    mma<S::kE4m3>(s[j], q.lo[2 * k], S::kRows > 8 ? q.hi[2 * k] : 0u, q.lo[2 * k + 1],
+                                  S::kRows > 8 ? q.hi[2 * k + 1] : 0u, b0, b1);
                 }
     }
     // o += p v.  p[j]: as scores.  Probabilities go in as a number of 16 bits and one for the rest of it.  With up to 8
     // queries the rest takes the place of rows 8 to 15.
-    __device__ __forceinline__ void accumulate(const float (&p)[2][4]) {
-        uint32_t hi[2][2], lo[2][2];
+    __device__ __forceinline__ void accumulate(const float (&p)[S::kKeyTiles][4]) {
+        uint32_t hi[S::kKeyTiles][2], lo[S::kKeyTiles][2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            split<kE4m3>(p[j][0], p[j][1], hi[j][0], lo[j][0]);
-            if constexpr (kRows > 8) split<kE4m3>(p[j][2], p[j][3], hi[j][1], lo[j][1]);
+        for (int j = 0; j < S::kKeyTiles; ++j) {
+            split<S::kE4m3>(p[j][0], p[j][1], hi[j][0], lo[j][0]);
+            if constexpr (S::kRows > 8) split<S::kE4m3>(p[j][2], p[j][3], hi[j][1], lo[j][1]);
         }
 #pragma unroll
-        for (int i = 0; i < kValueLoads; ++i)
+        for (int k = 0; k < S::kPairs; ++k)
 #pragma unroll
-            for (int e = 0; e < kPerPiece; ++e) {
-                uint32_t b[2];
+            for (int i = 0; i < S::kValueLoads; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint32_t u[4] = {value[2 * j][i].x, value[2 * j][i].y, value[2 * j][i].z, value[2 * j][i].w};
-                    const uint32_t w[4] = {value[2 * j + 1][i].x, value[2 * j + 1][i].y, value[2 * j + 1][i].z,
-                                           value[2 * j + 1][i].w};
-                    if constexpr (kE4m3) {
-                        const uint32_t x = __byte_perm(u[e / 4], w[e / 4], e % 4 < 2 ? 0x5140 : 0x7362);
-                        b[j] = codes_to_half(e % 2 ? x >> 16 : x);
+                for (int e = 0; e < S::kPerPiece; ++e) {
+                    uint32_t b[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint4 x = value[4 * k + 2 * j][i], y = value[4 * k + 2 * j + 1][i];
+                        const uint32_t u[4] = {x.x, x.y, x.z, x.w}, w[4] = {y.x, y.y, y.z, y.w};
+                        if constexpr (S::kE4m3) {
+                            const uint32_t z = __byte_perm(u[e / 4], w[e / 4], e % 4 < 2 ? 0x5140 : 0x7362);
+                            b[j] = codes_to_half(e % 2 ? z >> 16 : z);
+                        } else {
+                            b[j] = __byte_perm(u[e / 2 % 4], w[e / 2 % 4], e % 2 ? 0x7632 : 0x5410);
+                        }
+                    }
+                    float(&t)[4] = o[i * S::kPerPiece + e];
+                    const int j = 2 * k;
+                    if constexpr (S::kRows > 8) {
+                        mma<S::kE4m3>(t, hi[j][0], hi[j][1], hi[j + 1][0], hi[j + 1][1], b[0], b[1]);
+                        mma<S::kE4m3>(t, lo[j][0], lo[j][1], lo[j + 1][0], lo[j + 1][1], b[0], b[1]);
                     } else {
-                        b[j] = __byte_perm(u[e / 2 % 4], w[e / 2 % 4], e % 2 ? 0x7632 : 0x5410);
+                        mma<S::kE4m3>(t, hi[j][0], lo[j][0], hi[j + 1][0], lo[j + 1][0], b[0], b[1]);
                     }
                 }
-                float(&t)[4] = o[i * kPerPiece + e];
-                if constexpr (kRows > 8) {
-                    mma<kE4m3>(t, hi[0][0], hi[0][1], hi[1][0], hi[1][1], b[0], b[1]);
-                    mma<kE4m3>(t, lo[0][0], lo[0][1], lo[1][0], lo[1][1], b[0], b[1]);
-                } else {
-                    mma<kE4m3>(t, hi[0][0], lo[0][0], hi[1][0], lo[1][0], b[0], b[1]);
-                }
-            }
     }
-    // element of a head that o[t][e] belongs to (e = 0, 1 of row g; 2, 3 of row g + 8)
-    static __device__ __forceinline__ int element(int t, int e) {
+    // this lane's sums of row g (h = 1: row g + 8) times `by`, to a row in shared memory.  o[t][e] with e % 2 = f belongs
+    // to element (t / kPerPiece) 8 kPerPiece + (2 c + f) kPerPiece + t % kPerPiece.
+    __device__ __forceinline__ void stage(float* row, int h, float by) const {
         const int c = threadIdx.x % 4;
-        return (t / kPerPiece) * 8 * kPerPiece + (2 * c + (e & 1)) * kPerPiece + t % kPerPiece;
+#pragma unroll
+        for (int t = 0; t < S::kOut; t += 4)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[i] = (S::kRows > 8 ? o[t + i][2 * h + f] : o[t + i][f] + o[t + i][2 + f]) * by;
+                *reinterpret_cast<float4*>(row + t / S::kPerPiece * 8 * S::kPerPiece + (2 * c + f) * S::kPerPiece +
+                                           t % S::kPerPiece) = make_float4(v[0], v[1], v[2], v[3]);
+            }
     }
 };
 
 // A group's queries as A operands, in the order of elements that Warp::scores takes; 8-bit caches: as fp16, scaled by a
 // power of two that brings the largest element to 2^14, so that what 16 bits of bf16 hold stays exact over 31 binades
-template <bool kE4m3, int kD, int kRows>
+template <class S>
 struct Query {
-    static constexpr int kRegs = kD / 8;
-    uint32_t lo[kRegs], hi[kRows > 8 ? kRegs : 1];
-    float unit[2];           // what a product of rows g, g + 8 has to be multiplied by
+    static constexpr int kRegs = S::kPart / 8;
+    uint32_t lo[kRegs], hi[S::kRows > 8 ? kRegs : 1];
+    float unit[S::kHalves];  // what a product of rows g, g + 8 has to be multiplied by
 
-    __device__ __forceinline__ void load_row(const __nv_bfloat16* row, bool in, int D, uint32_t* to, float* unit_) {
+    // row: a query head's elements from this warp's first one on, of which `left` are there
+    __device__ __forceinline__ void load_row(const __nv_bfloat16* row, bool in, int left, uint32_t* to, float* unit_) {
         const int c = threadIdx.x % 4;
-        constexpr int kPieces = kD / 32;
+        constexpr int kPieces = S::kPart / 32;
         uint4 w[kPieces];
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             // 8-bit keys: a lane's 16 elements are two of these pieces
-            const int at = kE4m3 ? 64 * (i / 2) + 16 * c + 8 * (i % 2) : 32 * i + 8 * c;
-            w[i] = in && at < D ? *reinterpret_cast<const uint4*>(row + at) : make_uint4(0, 0, 0, 0);
+            const int at = S::kE4m3 ? 64 * (i / 2) + 16 * c + 8 * (i % 2) : 32 * i + 8 * c;
+            w[i] = in && at < left ? *reinterpret_cast<const uint4*>(row + at) : make_uint4(0, 0, 0, 0);
         }
         float inv = 1.f;
         *unit_ = 1.f;
-        if constexpr (kE4m3) {
+        if constexpr (S::kE4m3) {
             uint32_t a = 0;
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
@@ -259,42 +287,82 @@ struct Query {
             const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                to[4 * i + k] = kE4m3 ? pack_half(__uint_as_float(u[k] << 16) * inv, __uint_as_float(u[k] & 0xFFFF0000u) * inv)
-                                      : u[k];
+                to[4 * i + k] = S::kE4m3
+                                    ? pack_half(__uint_as_float(u[k] << 16) * inv, __uint_as_float(u[k] & 0xFFFF0000u) * inv)
+                                    : u[k];
         }
     }
-    __device__ __forceinline__ void load(const Decode& a, int b, int head0, int rows) {
+    __device__ __forceinline__ void load(const Decode& a, int b, int head0, int rows, int first) {
         const int g = threadIdx.x % 32 / 4;
-        const __nv_bfloat16* q = a.q + b * a.ld_q + (int64_t)head0 * a.D;
-        load_row(q + g * a.D, g < rows, a.D, lo, &unit[0]);
-        if constexpr (kRows > 8) load_row(q + (g + 8) * a.D, g + 8 < rows, a.D, hi, &unit[1]);
+        const __nv_bfloat16* q = a.q + b * a.ld_q + (int64_t)head0 * a.D + first;
+        load_row(q + g * a.D, g < rows, a.D - first, lo, &unit[0]);
+        if constexpr (S::kRows > 8) load_row(q + (g + 8) * a.D, g + 8 < rows, a.D - first, hi, &unit[S::kHalves - 1]);
     }
 };
 
-// Running maximum and sum of a row of scores.  With a scale for each value row (8 bits), the numerators e^s * scale have
-// a maximum of their own, in log2: what a large scale does to it leaves the sum alone.
+// Running maximum m and sum l of a row of scores, in log2.  With a scale for each value row (8 bits) the numerators
+// e^s * scale have a maximum of their own: what a large scale does to it leaves the sum alone.
 struct Stats {
     float m, l, top;
 };
 
-template <bool kE4m3, int kD, int kRows, int kCtas>
+// Sums of one row and four elements over parts that are relative to maxima of their own
+struct Joined {
+    float m, l;
+    float4 o;
+    __device__ __forceinline__ void add(float f, float pl, float4 x) {
+        l = fmaf(pl, f, l);
+        o.x = fmaf(x.x, f, o.x); o.y = fmaf(x.y, f, o.y); o.z = fmaf(x.z, f, o.z); o.w = fmaf(x.w, f, o.w);
+    }
+    static __device__ __forceinline__ float weight(float from, float to) { return from == to ? 1.f : exp2_fast(from - to); }
+};
+// parts k = 0 .. n - 1, at(k): [kRows] pairs of m and l, then [kRows, kD] sums.  Eight are loaded at a time.
+template <class S, class At>
+__device__ __forceinline__ Joined join_parts(int n, int row, int d, At at) {
+    Joined r{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    constexpr int kAhead = 8;
+    for (int k0 = 0; k0 < n; k0 += kAhead) {
+        float2 ml[kAhead];
+        float4 x[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const float* from = at(min(k0 + k, n - 1));
+            ml[k] = *reinterpret_cast<const float2*>(from + 2 * row);
+            x[k] = *reinterpret_cast<const float4*>(from + 2 * S::kRows + row * S::kD + d);
+        }
+        float m = r.m;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) m = fmaxf(m, ml[k].x);
+        const float f = Joined::weight(r.m, m);
+        r.m = m;
+        r.l *= f;
+        r.o.x *= f; r.o.y *= f; r.o.z *= f; r.o.w *= f;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (k0 + k < n) r.add(Joined::weight(ml[k].x, m), ml[k].y, x[k]);
+    }
+    return r;
+}
+
+template <class S, int kCtas>
 __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a) {
-    extern __shared__ __align__(16) float smem[];
+    extern __shared__ __align__(16) float smem[];        // a place for sums, [kRows][kSplit][kStaged], for each team
     __shared__ int32_t sh_seq;
     __shared__ int64_t sh_before;
     __shared__ int64_t warp_sum[kWarps];
-    __shared__ float sh_m[kWarps][kRows], sh_l[kWarps][kRows];
+    __shared__ float sh_m[S::kTeams][S::kRows], sh_l[S::kTeams][S::kRows];
     __shared__ int32_t sh_last;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g = lane / 4, c = lane % 4;
+    const int team = warp / S::kSplit, side = warp % S::kSplit;
     grid_dep_launch();
     grid_dep_wait();
 
-    // ---- this CTA's piece of the line of tiles: [p0, p1) of W, and the sequence that p0 lies in
+    // ---- this CTA's piece of the line of tiles, [p0, p1), and the sequence that p0 lies in
     const int heads = a.kv_heads * a.parts;           // lines of tiles of one sequence
     const int per = (a.B + kThreads - 1) / kThreads;  // sequences of a thread
     const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += range_of(a, b).tiles(kTileTokens);
+    for (int b = b0; b < b1; ++b) mine += range_of(a, b).tiles(S::kTile);
     int64_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -303,30 +371,30 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
     }
     if (lane == 31) warp_sum[warp] = upto;
     __syncthreads();
-    int64_t W = 0;
+    int64_t total = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) upto += warp_sum[w];
-        W += warp_sum[w];
+        total += warp_sum[w];
     }
-    W *= heads;
-    const Line all{W, min((int64_t)gridDim.x, W)};
-    const int64_t p0 = blockIdx.x < all.ctas ? all.first_tile(blockIdx.x) : W;
-    const int64_t p1 = blockIdx.x < all.ctas ? all.first_tile(blockIdx.x + 1) : W;
+    total *= heads;
+    const Line all{total, min((int64_t)gridDim.x, total)};
+    const int64_t p0 = blockIdx.x < all.ctas ? all.first_tile(blockIdx.x) : total;
+    const int64_t p1 = blockIdx.x < all.ctas ? all.first_tile(blockIdx.x + 1) : total;
     if (p0 < p1 && (upto - mine) * heads <= p0 && p0 < upto * heads) {
         int64_t before = upto - mine;
         int b = b0;
         for (;; ++b) {
-            const int n = range_of(a, b).tiles(kTileTokens);
+            const int n = range_of(a, b).tiles(S::kTile);
             if (p0 < (before + n) * heads) break;
             before += n;
         }
         sh_seq = b;
         sh_before = before * heads;
     }
-    // sequences without rows: no tile, so the CTAs share them out
+    // sequences without rows have no tile, so the CTAs share them out
     for (int b = blockIdx.x * kWarps + warp; b < a.B; b += gridDim.x * kWarps) {
-        if (range_of(a, b).tiles(kTileTokens) > 0) continue;
+        if (range_of(a, b).tiles(S::kTile) > 0) continue;
         for (int i = lane; i < a.n_heads * a.D / 8; i += 32)
             reinterpret_cast<uint4*>(a.out + b * a.ld_out)[i] = make_uint4(0, 0, 0, 0);
         if (a.lse)
@@ -337,11 +405,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
     int b = sh_seq;
     int64_t before = sh_before;
 
+    const int first = side * S::kPart;                // this warp's elements of a row
+    const int bytes = (a.D - first) * (S::kE4m3 ? 1 : 2);
     int64_t p = p0;
     while (p < p1) {
         // ---- the next item: a sequence and a line of its tiles
         const Range range = range_of(a, b);
-        const int n_tiles = range.tiles(kTileTokens);
+        const int n_tiles = range.tiles(S::kTile);
         if (p >= before + (int64_t)n_tiles * heads) {
             before += (int64_t)n_tiles * heads;
             ++b;
@@ -352,217 +422,237 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
         const int kv = line / a.parts, part = line % a.parts;
         const int head0 = kv * a.group + part * a.rows, rows = min(a.rows, a.group - part * a.rows);
         const int t0 = (int)(p - i0), t1 = (int)(min(p1, i1) - i0);
-        const char* kbase = a.cache.k + kv * a.cache.head_stride;
-        const char* vbase = a.cache.v + kv * a.cache.head_stride;
+        const char* kbase = a.cache.k + kv * a.cache.head_stride + first * (S::kE4m3 ? 1 : 2);
+        const char* vbase = a.cache.v + kv * a.cache.head_stride + first * (S::kE4m3 ? 1 : 2);
         const int32_t* table = a.table + b * a.ld_table;
 
-        Warp<kE4m3, kD, kRows> w;
-        Query<kE4m3, kD, kRows> q;
-        Stats st[kRows > 8 ? 2 : 1];
+        Warp<S> w;
+        Query<S> q;
+        Stats st[S::kHalves];
         for (auto& x : st) x = Stats{-INFINITY, 0.f, -INFINITY};
 #pragma unroll
-        for (int t = 0; t < kD / 8; ++t)
+        for (int t = 0; t < S::kOut; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) w.o[t][e] = 0.f;
         bool bad = range.poisoned;
 
-        // this warp's first token of tile t, and the page of this lane's (-1: a negative one, -2: no such token)
-        auto token = [&](int t) { return (uint32_t)range.start + (uint32_t)t * kTileTokens + warp * kWarpTokens; };
+        // this warp's first token of tile t; the page of this lane's (-1: a negative one, -2: no such token); its row
+        auto token = [&](int t) { return (uint32_t)range.start + (uint32_t)t * S::kTile + team * S::kTokens; };
         auto page_at = [&](int t) -> int32_t {
-            const uint32_t tok = token(t) + lane % 16;
+            const uint32_t tok = token(t) + lane % S::kTokens;
             return t < t1 && tok < (uint32_t)range.end ? max(table[a.pages.page_of(tok)], -1) : -2;
         };
-        auto rows_at = [&](int t, int32_t page) -> Rows {
-            Rows r{-1, 0.f};
-            if (page == -2) return r;
+        float ks = 0.f, vs = 0.f;        // 8 bits: the next step's token's key scale, and log2 of its value scale
+        auto row_at = [&](int t, int32_t page) -> uint32_t {
+            if (page == -2) return kNoRow;
             if (page == -1 || page >= a.cache.n_pages) {
                 bad = true;
-                return r;
+                return kNoRow;
             }
-            const uint32_t tok = token(t) + lane % 16;
-            const int64_t row = tok - a.pages.page_of(tok) * (uint32_t)a.cache.page_size;
-            r.at = page * a.cache.page_stride + row * a.cache.row_stride;
-            if (kE4m3)
-                r.scale = (lane < 16 ? a.cache.ks : a.cache.vs)[page * a.cache.s_page + row * a.cache.s_row +
-                                                               kv * a.cache.s_head];
-            return r;
+            const uint32_t tok = token(t) + lane % S::kTokens;
+            const uint32_t row = tok - a.pages.page_of(tok) * (uint32_t)a.cache.page_size;
+            if (S::kE4m3) {
+                const int64_t at = page * a.cache.s_page + row * a.cache.s_row + kv * a.cache.s_head;
+                ks = a.cache.ks[at];
+                vs = a.cache.vs[at];
+            }
+            return (uint32_t)page * a.page_units + row * a.row_units;
         };
         int32_t page = page_at(t0);
-        Rows now = rows_at(t0, page);
+        uint32_t at = row_at(t0, page);
         page = page_at(t0 + 1);
-        w.load_keys(kbase, now.at, a.D);
-        w.load_values(vbase, now.at, a.D);
-        q.load(a, b, head0, rows);
-        for (int t = t0; t < t1; ++t) {
-            const Rows next = rows_at(t + 1, page);
-            page = page_at(t + 2);
-            float s[2][4];
-            w.scores(q, s);
-            if (t + 1 < t1) w.load_keys(kbase, next.at, a.D);
-            // scores in log2, -infinity where there is no token
-            const uint32_t tok = token(t) + 2 * c;
-            float top[2][4], vs[2][2];
+        w.load_keys(kbase, at, a.unit, bytes);
+        w.load_values(vbase, at, a.unit, bytes);
+        q.load(a, b, head0, rows, first);
+        float factor[S::kHalves];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+        for (int h = 0; h < S::kHalves; ++h)
+            factor[h] = (S::kSplit > 1 ? 1.f : q.unit[h]) * (a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e);
+        for (int t = t0; t < t1; ++t) {
+            const float now_ks = ks, now_vs = S::kE4m3 ? log2_fast(vs) : 0.f;
+            at = row_at(t + 1, page);
+            page = page_at(t + 2);
+            float s[S::kKeyTiles][4];
+            w.scores(q, s);
+            if (t + 1 < t1) w.load_keys(kbase, at, a.unit, bytes);
+            if constexpr (S::kSplit > 1) {
+                // both warps of a team add the two halves in one order; they pass through the team's place for sums
+                auto place = [&](int of, int j, int e) -> float& {
+                    return smem[team * S::kTeamFloats + (((t & 1) * 2 + of) * S::kKeyTiles * 4 + 4 * j + e) * 32 + lane];
+                };
+#pragma unroll
+                for (int j = 0; j < S::kKeyTiles; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2 * S::kHalves; ++e) place(side, j, e) = s[j][e] * q.unit[e / 2];
+                asm volatile("bar.sync %0, 64;" ::"r"(team + 1) : "memory");
+#pragma unroll
+                for (int j = 0; j < S::kKeyTiles; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2 * S::kHalves; ++e)
+                        s[j][e] = place(0, j, e) + place(1, j, e);
+            }
+            // scores in log2, -infinity where there is no token; top: with the value's scale
+            const uint32_t tok = token(t) + 2 * c;
+            const bool all_in = token(t) + S::kTokens <= (uint32_t)range.end;
+            float lv[S::kKeyTiles][2];
+#pragma unroll
+            for (int j = 0; j < S::kKeyTiles; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const bool in = tok + 8 * j + e < (uint32_t)range.end;
-                    float ks = 1.f;
-                    if (kE4m3) {
-                        ks = __shfl_sync(0xffffffffu, now.scale, 8 * j + 2 * c + e);
-                        vs[j][e] = __shfl_sync(0xffffffffu, now.scale, 16 + 8 * j + 2 * c + e);
+                    float f = 1.f;
+                    if (S::kE4m3) {
+                        f = __shfl_sync(0xffffffffu, now_ks, 8 * j + 2 * c + e);
+                        lv[j][e] = __shfl_sync(0xffffffffu, now_vs, 8 * j + 2 * c + e);
                     }
 #pragma unroll
-                    for (int h = 0; h < (kRows > 8 ? 2 : 1); ++h) {
+                    for (int h = 0; h < S::kHalves; ++h) {
                         float& x = s[j][2 * h + e];
-                        if (kE4m3) x *= ks * q.unit[h];
-                        x *= a.scale;
-                        if (a.softcap > 0.f) x = a.softcap * tanhf(x / a.softcap);
-                        x = in ? x * kLog2e : -INFINITY;
-                        if (kE4m3) top[j][2 * h + e] = x + log2_fast(fabsf(vs[j][e]));
+                        x *= S::kE4m3 ? f * factor[h] : factor[h];
+                        if (a.softcap > 0.f) x = a.softcap * kLog2e * tanhf(x);
+                        if (!all_in && tok + 8 * j + e >= (uint32_t)range.end) x = -INFINITY;
                     }
                 }
             bool raise = false;
-            float to[kRows > 8 ? 2 : 1][2];
+            float most[S::kHalves][2];
 #pragma unroll
-            for (int h = 0; h < (kRows > 8 ? 2 : 1); ++h) {
-                float m = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+            for (int h = 0; h < S::kHalves; ++h) {
+                float m = -INFINITY, u = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < S::kKeyTiles; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        m = fmaxf(m, s[j][2 * h + e]);
+                        if (S::kE4m3) u = fmaxf(u, s[j][2 * h + e] + lv[j][e]);
+                    }
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                to[h][0] = m;
-                if (kE4m3) {
-                    float u = fmaxf(fmaxf(top[0][2 * h], top[0][2 * h + 1]), fmaxf(top[1][2 * h], top[1][2 * h + 1]));
+                most[h][0] = m;
+                raise |= m > st[h].m + kSlack;
+                if (S::kE4m3) {
                     u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, 1));
                     u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, 2));
-                    to[h][1] = u;
+                    most[h][1] = u;
                     raise |= u > st[h].top + kSlack;
                 }
-                raise |= m > st[h].m + kSlack;
             }
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-                for (int h = 0; h < (kRows > 8 ? 2 : 1); ++h) {
-                    const float m = fmaxf(st[h].m, to[h][0]);
-                    const float fl = st[h].m == m ? 1.f : exp2_fast(st[h].m - m);
-                    st[h].l *= fl;
+                for (int h = 0; h < S::kHalves; ++h) {
+                    const float m = fmaxf(st[h].m, most[h][0]);
+                    float f = Joined::weight(st[h].m, m);
+                    st[h].l *= f;
                     st[h].m = m;
-                    float fo = fl;
-                    if (kE4m3) {
-                        const float u = fmaxf(st[h].top, to[h][1]);
-                        fo = st[h].top == u ? 1.f : exp2_fast(st[h].top - u);
+                    if (S::kE4m3) {
+                        const float u = fmaxf(st[h].top, most[h][1]);
+                        f = Joined::weight(st[h].top, u);
                         st[h].top = u;
                     }
                     // rows 8 to 15 belong to the same queries where there are up to 8
 #pragma unroll
-                    for (int i = 0; i < kD / 8; ++i)
+                    for (int i = 0; i < S::kOut; ++i)
 #pragma unroll
-                        for (int e = 0; e < (kRows > 8 ? 2 : 4); ++e) w.o[i][2 * h + e] *= fo;
+                        for (int e = 0; e < (S::kRows > 8 ? 2 : 4); ++e) w.o[i][2 * h + e] *= f;
                 }
             }
 #pragma unroll
-            for (int h = 0; h < (kRows > 8 ? 2 : 1); ++h) {
+            for (int h = 0; h < S::kHalves; ++h) {
                 const float m = st[h].m == -INFINITY ? 0.f : st[h].m;
-                const float u = st[h].top == -INFINITY ? 0.f : st[h].top;
+                // 2^7 (2^15 with the slack) is the largest numerator in 8 bits: what fp16 loses below 2^-24 is 2^-31 of it
+                const float u = st[h].top == -INFINITY ? -7.f : st[h].top - 7.f;
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < S::kKeyTiles; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float& x = s[j][2 * h + e];
                         const float pr = exp2_fast(x - m);
                         st[h].l += pr;
-                        // 2^7 (2^15 with the slack) is the largest numerator: what is lost below 2^-24 is 2^-31 of it
-                        x = kE4m3 ? copysignf(exp2_fast(top[j][2 * h + e] - u + 7.f), vs[j][e]) : pr;
-                        if (kE4m3 && pr != pr) x = pr;
+                        x = S::kE4m3 ? exp2_fast(x + lv[j][e] - u) : pr;
                     }
             }
             w.accumulate(s);
-            if (t + 1 < t1) w.load_values(vbase, next.at, a.D);
-            now = next;
+            if (t + 1 < t1) w.load_values(vbase, at, a.unit, bytes);
         }
         bad = __any_sync(0xffffffffu, bad);
+        if constexpr (S::kSplit > 1) asm volatile("bar.sync %0, 64;" ::"r"(team + 1) : "memory");
 
         // ---- the warps' rows together: m and l of each, then the elements
-        float* so = smem;        // [kWarps][kRows][kD]
 #pragma unroll
-        for (int h = 0; h < (kRows > 8 ? 2 : 1); ++h) {
+        for (int h = 0; h < S::kHalves; ++h) {
             float l = st[h].l;
             l += __shfl_xor_sync(0xffffffffu, l, 1);
             l += __shfl_xor_sync(0xffffffffu, l, 2);
             if (bad) l = NAN;
             const int row = g + 8 * h;
-            if (c == 0) {
-                sh_m[warp][row] = st[h].m;
-                sh_l[warp][row] = l;
+            if (c == 0 && side == 0) {
+                sh_m[team][row] = st[h].m;
+                sh_l[team][row] = l;
             }
-            float unit = 1.f;
-            if (kE4m3) unit = st[h].top == -INFINITY ? 1.f : exp2_fast(st[h].top - 7.f - st[h].m);
-#pragma unroll
-            for (int i = 0; i < kD / 8; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    so[(warp * kRows + row) * kD + w.element(i, e)] =
-                        (kRows > 8 ? w.o[i][2 * h + e] : w.o[i][e] + w.o[i][2 + e]) * unit;
+            float by = 1.f;
+            if (S::kE4m3) by = st[h].top == -INFINITY ? 1.f : exp2_fast(st[h].top - 7.f - st[h].m);
+            w.stage(smem + team * S::kTeamFloats + (row * S::kSplit + side) * S::kStaged, h, by);
         }
         __syncthreads();
         const bool whole = t0 == 0 && t1 == n_tiles;
-        const int slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
-        constexpr int kSlot = kRows * (kD + 2);
-        for (int i = tid; i < rows * (kD / 4); i += kThreads) {
-            const int row = i / (kD / 4), d = i % (kD / 4) * 4;
-            float m = -INFINITY, l = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto slot = [&](int cta, bool begins) { return a.ws + (int64_t)(2 * cta + (begins ? 1 : 0)) * S::kSlot; };
+        auto write_out = [&](int row, int d, const Joined& r) {
+            if (d >= a.D) return;
+            const float f = 1.f / r.l;
+            *reinterpret_cast<uint2*>(a.out + b * a.ld_out + (int64_t)(head0 + row) * a.D + d) =
+                make_uint2(pack_bf16(r.o.x * f, r.o.y * f), pack_bf16(r.o.z * f, r.o.w * f));
+            if (d == 0 && a.lse) a.lse[(int64_t)b * a.n_heads + head0 + row] = (r.m + log2f(r.l)) * kLn2;
+        };
+        auto write_part = [&](float* to, int row, int d, const Joined& r) {
+            if (d == 0) *reinterpret_cast<float2*>(to + 2 * row) = make_float2(r.m, r.l);
+            *reinterpret_cast<float4*>(to + 2 * S::kRows + row * S::kD + d) = r.o;
+        };
+        for (int i = tid; i < rows * (S::kD / 4); i += kThreads) {
+            const int row = i / (S::kD / 4), d = i % (S::kD / 4) * 4;
+            Joined r{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) m = fmaxf(m, sh_m[k][row]);
+            for (int k = 0; k < S::kTeams; ++k) r.m = fmaxf(r.m, sh_m[k][row]);
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-                const float f = sh_m[k][row] == m ? 1.f : exp2_fast(sh_m[k][row] - m);
-                const float4 x = *reinterpret_cast<const float4*>(so + (k * kRows + row) * kD + d);
-                l = fmaf(sh_l[k][row], f, l);
-                o.x = fmaf(x.x, f, o.x); o.y = fmaf(x.y, f, o.y); o.z = fmaf(x.z, f, o.z); o.w = fmaf(x.w, f, o.w);
-            }
-            if (!whole) {
-                float* to = a.ws + (int64_t)slot * kSlot;
-                if (d == 0) {
-                    to[2 * row] = m;
-                    to[2 * row + 1] = l;
-                }
-                *reinterpret_cast<float4*>(to + 2 * kRows + row * kD + d) = o;
-            } else if (d < a.D) {
-                const float r = 1.f / l;
-                *reinterpret_cast<uint2*>(a.out + b * a.ld_out + (int64_t)(head0 + row) * a.D + d) =
-                    make_uint2(pack_bf16(o.x * r, o.y * r), pack_bf16(o.z * r, o.w * r));
-                if (d == 0 && a.lse) a.lse[(int64_t)b * a.n_heads + head0 + row] = (m + log2f(l)) * kLn2;
-            }
+            for (int k = 0; k < S::kTeams; ++k)
+                r.add(Joined::weight(sh_m[k][row], r.m), sh_l[k][row],
+                      *reinterpret_cast<const float4*>(smem + k * S::kTeamFloats + (row * S::kSplit + d / S::kPart) * S::kStaged +
+                                                       d % S::kPart));
+            if (whole) write_out(row, d, r);
+            else write_part(slot(blockIdx.x, t0 == 0), row, d, r);
         }
         if (!whole) {
-            // ---- joined by the last CTA of the item to arrive, in the order of the CTAs
-            const int first = (int)all.owner(i0), last = (int)all.owner(i1 - 1);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) sh_last = atomicAdd(a.counters + first, 1) == last - first;
-            __syncthreads();
-            if (sh_last) {
+            // ---- the item's parts, in the order of its CTAs: those of each eight neighbouring CTAs are joined by the last
+            // of them to arrive, and what they leave by the last eight to be done.
+            const int c0 = (int)all.owner(i0), c1 = (int)all.owner(i1 - 1), eight = blockIdx.x / 8;
+            const int e0 = max(c0, 8 * eight), e1 = min(c1, 8 * eight + 7);
+            auto part_of = [&](int cta) { return slot(cta, cta == c0); };
+            auto arrive = [&](int counter, int expected) -> bool {
                 __threadfence();
-                if (tid == 0) a.counters[first] = 0;
-                for (int i = tid; i < rows * (kD / 4); i += kThreads) {
-                    const int row = i / (kD / 4), d = i % (kD / 4) * 4;
-                    float m = -INFINITY, l = 0.f;
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int k = first; k <= last; ++k)
-                        m = fmaxf(m, a.ws[(int64_t)(2 * k + (k == first)) * kSlot + 2 * row]);
-                    for (int k = first; k <= last; ++k) {
-                        const float* from = a.ws + (int64_t)(2 * k + (k == first)) * kSlot;
-                        const float f = from[2 * row] == m ? 1.f : exp2_fast(from[2 * row] - m);
-                        const float4 x = *reinterpret_cast<const float4*>(from + 2 * kRows + row * kD + d);
-                        l = fmaf(from[2 * row + 1], f, l);
-                        o.x = fmaf(x.x, f, o.x); o.y = fmaf(x.y, f, o.y); o.z = fmaf(x.z, f, o.z); o.w = fmaf(x.w, f, o.w);
-                    }
-                    if (d >= a.D) continue;
-                    const float r = 1.f / l;
-                    *reinterpret_cast<uint2*>(a.out + b * a.ld_out + (int64_t)(head0 + row) * a.D + d) =
-                        make_uint2(pack_bf16(o.x * r, o.y * r), pack_bf16(o.z * r, o.w * r));
-                    if (d == 0 && a.lse) a.lse[(int64_t)b * a.n_heads + head0 + row] = (m + log2f(l)) * kLn2;
+                __syncthreads();
+                if (tid == 0) {
+                    const bool last = atomicAdd(a.counters + counter, 1) == expected - 1;
+                    if (last) a.counters[counter] = 0;
+                    sh_last = last;
                 }
+                __syncthreads();
+                if (sh_last) __threadfence();
+                return sh_last;
+            };
+            // the first eight of an item count at its first CTA, the others, which begin with it, at their own number
+            if (arrive(e0 == c0 ? c0 : kMaxCtas + eight, e1 - e0 + 1)) {
+                const int n = c1 / 8 - c0 / 8 + 1;
+                const bool only = n == 1;
+                for (int i = tid; i < rows * (S::kD / 4); i += kThreads) {
+                    const int row = i / (S::kD / 4), d = i % (S::kD / 4) * 4;
+                    const Joined r = join_parts<S>(e1 - e0 + 1, row, d, [&](int k) { return part_of(e0 + k); });
+                    if (only) write_out(row, d, r);
+                    else write_part(a.ws + (int64_t)(2 * gridDim.x + 2 * eight + (e0 == c0)) * S::kSlot, row, d, r);
+                }
+                if (!only && arrive(kMaxCtas + kMaxCtas / 8 + c0, n))
+                    for (int i = tid; i < rows * (S::kD / 4); i += kThreads) {
+                        const int row = i / (S::kD / 4), d = i % (S::kD / 4) * 4;
+                        write_out(row, d, join_parts<S>(n, row, d, [&](int k) {
+                            return a.ws + (int64_t)(2 * gridDim.x + 2 * (c0 / 8 + k) + (k == 0)) * S::kSlot;
+                        }));
+                    }
             }
         }
         __syncthreads();
@@ -571,10 +661,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
 }
 
 // ---------------------------------------------------------------------------------------------------------- host
+// counters of the items' first CTAs and of each eight; of an item's eights, at its first CTA
 constexpr size_t kCounterBytes = LORA_DECODE_COUNTER_BYTES;
+static_assert((2 * kMaxCtas + kMaxCtas / 8) * sizeof(int32_t) <= kCounterBytes, "counters");
 
 // CTAs on an SM: as many as the registers of a lane's pieces and sums leave room for
-constexpr int ctas_of(bool e4m3, int kD, int kRows) { return kD == 256 ? 2 : kRows > 8 ? (e4m3 ? 3 : 2) : (e4m3 ? 4 : 3); }
+template <class S>
+constexpr int ctas_of() { return S::kRows > 8 ? 2 : 3; }
 
 int sm_count() {
     int dev = 0, n = 0;
@@ -586,7 +679,9 @@ int sm_count() {
 template <class Go>
 auto by_shape(bool e4m3, int D, int rows, Go go) {
     auto with_rows = [&](auto t, auto d) {
-        return rows <= 8 ? go(t, d, std::integral_constant<int, 8>()) : go(t, d, std::integral_constant<int, 16>());
+        constexpr bool kE4m3 = decltype(t)::value;
+        constexpr int kD = decltype(d)::value;
+        return rows <= 8 ? go(Shapes<kE4m3, kD, 8>()) : go(Shapes<kE4m3, kD, 16>());
     };
     auto with_size = [&](auto t) {
         return D <= 64 ? with_rows(t, std::integral_constant<int, 64>())
@@ -602,15 +697,15 @@ int rows_of(int group) {
     return (group + parts - 1) / parts;
 }
 
-struct Shape {
+struct Launch {
     int grid;
     size_t bytes;
 };
-Shape shape_of(bool e4m3, int D, int group) {
-    return by_shape(e4m3, D, rows_of(group), [&](auto t, auto d, auto r) {
-        const int grid = std::min<int>(sm_count() * ctas_of(decltype(t)::value, decltype(d)::value, decltype(r)::value),
-                                       kCounterBytes / sizeof(int32_t));
-        return Shape{grid, kCounterBytes + (size_t)grid * 2 * decltype(r)::value * (decltype(d)::value + 2) * sizeof(float)};
+Launch launch_of(bool e4m3, int D, int group) {
+    return by_shape(e4m3, D, rows_of(group), [&](auto shapes) {
+        using S = decltype(shapes);
+        const int grid = std::min(sm_count() * ctas_of<S>(), kMaxCtas);
+        return Launch{grid, kCounterBytes + (size_t)(2 * grid + 2 * (grid / 8 + 1)) * S::kSlot * sizeof(float)};
     });
 }
 
@@ -631,7 +726,7 @@ extern "C" size_t lora_decode_workspace_size(int32_t n_heads, const lora_cache_t
         const char* fn = "lora_decode_workspace_size";
         CacheView view;
         if (check_cache(fn, cache, &view) != LORA_OK || check_heads(fn, n_heads, cache) != LORA_OK) return 0;
-        const Shape s = shape_of(cache->dtype == LORA_CACHE_E4M3, cache->head_dim, n_heads / cache->n_heads);
+        const Launch s = launch_of(cache->dtype == LORA_CACHE_E4M3, cache->head_dim, n_heads / cache->n_heads);
         if (s.grid == 0) {
             refuse(LORA_ERR_CUDA, std::string(fn) + ": no CUDA device");
             return 0;
@@ -665,9 +760,9 @@ extern "C" int lora_decode_attention(int32_t B, int32_t n_heads, const void* q, 
             return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": table, lengths and lse must be 4-byte aligned");
         const bool e4m3 = cache->dtype == LORA_CACHE_E4M3;
         a.group = n_heads / cache->n_heads;
-        const Shape shape = shape_of(e4m3, cache->head_dim, a.group);
-        if (shape.grid == 0) return refuse(LORA_ERR_CUDA, std::string(fn) + ": no CUDA device");
-        if (!workspace || !is_aligned(workspace, 256) || ws_bytes < shape.bytes)
+        const Launch launch = launch_of(e4m3, cache->head_dim, a.group);
+        if (launch.grid == 0) return refuse(LORA_ERR_CUDA, std::string(fn) + ": no CUDA device");
+        if (!workspace || !is_aligned(workspace, 256) || ws_bytes < launch.bytes)
             return refuse(LORA_ERR_WORKSPACE, std::string(fn) + ": workspace missing, too small or not 256-byte aligned");
         a.q = static_cast<const __nv_bfloat16*>(q); a.ld_q = ld_q;
         a.out = static_cast<__nv_bfloat16*>(out); a.ld_out = ld_out; a.lse = lse;
@@ -677,19 +772,25 @@ extern "C" int lora_decode_attention(int32_t B, int32_t n_heads, const void* q, 
         a.parts = (a.group + a.rows - 1) / a.rows;
         a.window = window; a.scale = scale; a.softcap = softcap;
         a.pages = page_division((uint32_t)cache->page_size);
+        // rows are found by 32-bit numbers of the largest unit that divides both strides
+        a.unit = 16;
+        while (a.unit < (1u << 30) && (a.cache.page_stride | a.cache.row_stride) % (2ll * a.unit) == 0) a.unit *= 2;
+        const int64_t pu = a.cache.page_stride / a.unit, ru = a.cache.row_stride / a.unit;
+        if (cache->n_pages > 0 && (pu >= (1ll << 32) || ru >= (1ll << 32) ||
+                                   (double)pu * (cache->n_pages - 1) + (double)ru * (cache->page_size - 1) >= 4294967295.0))
+            return refuse(LORA_ERR_LIMIT, std::string(fn) + ": the cache's rows lie more than 2^32 units apart (the largest "
+                                                            "power of two that divides the strides of pages and rows)");
+        a.page_units = (uint32_t)pu;
+        a.row_units = (uint32_t)ru;
         a.counters = static_cast<int32_t*>(workspace);
         a.ws = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
         cudaStream_t st = static_cast<cudaStream_t>(stream);
-        return enqueued(fn, by_shape(e4m3, a.D, a.rows, [&](auto t, auto kd, auto r) -> cudaError_t {
-            constexpr bool kE4m3 = decltype(t)::value;
-            constexpr int kD = decltype(kd)::value, kRows = decltype(r)::value;
-            const auto kernel = decode_kernel<kE4m3, kD, kRows, ctas_of(kE4m3, kD, kRows)>;
-            constexpr size_t smem = sizeof(float) * kWarps * kRows * kD;
-            if (smem > 48 * 1024) {
-                const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-                if (e != cudaSuccess) return e;
-            }
-            return launch_pdl(kernel, dim3((unsigned)shape.grid), dim3(kThreads), smem, st, a);
+        return enqueued(fn, by_shape(e4m3, a.D, a.rows, [&](auto shapes) -> cudaError_t {
+            using S = decltype(shapes);
+            const auto kernel = decode_kernel<S, ctas_of<S>()>;
+            constexpr size_t smem = sizeof(float) * S::kTeams * S::kTeamFloats;
+            static_assert(smem <= 36 * 1024, "static and dynamic shared memory fit 48 KB");
+            return launch_pdl(kernel, dim3((unsigned)launch.grid), dim3(kThreads), smem, st, a);
         }));
     });
 }
