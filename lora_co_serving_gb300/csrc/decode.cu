@@ -2,12 +2,13 @@
 //
 // What bounds it: each cached element is used by the n query heads of its group only, 4 n operations for 2 bytes (or one).
 // The cache's bytes bound the call at any matrix rate above some 100 TFLOP/s, so the products are small register-to-
-// register MMAs (m16n8k16) whose operands come straight from global memory: rows of scores are queries, columns cached
-// tokens.  Both products can take the cache as it lies, without a way through shared memory:
-//   scores  the sum over a head's elements may be taken in any order, so a lane's 16 bytes of a key row are its share of
-//           the B operand of two MMAs (four in 8 bits), if the query's elements are taken in the same order;
-//   output  B needs a pair of tokens of one element in a register: a lane loads the same 16 bytes of a pair's two value
-//           rows and interleaves them; which element is which output column is free, too.
+// register MMAs (m16n8k16) whose operands come straight from global memory: the cache's side has the 16 rows, up to 8
+// query heads the 8 columns.  Both products can take the cache as it lies, without a way through shared memory:
+//   scores  rows are tokens.  The sum over a head's elements may be taken in any order, so a lane's 16 bytes of a key row
+//           are its share of two MMAs (four in 8 bits), if the query's elements are taken in the same order;
+//   output  rows are elements, the sum goes over tokens, a pair of them in a register: a lane loads the same 16 bytes of a
+//           pair's two value rows and interleaves them.  Which element is which row is free, too.  The probabilities, whose
+//           tokens are rows, are turned around by the transposing move of 8 x 8 numbers.
 // Work is counted in tiles of 32 to 128 tokens of one sequence and one cache head.  All tiles of a call form one line, and
 // each CTA takes an equal piece of it, whatever the lengths are; a CTA's warps take 16 or 32 tokens of a tile each, with a
 // running maximum and sum of their own.  A sequence and head whose tiles lie in several CTAs is joined by the last of them
@@ -61,17 +62,11 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-// two numbers in 16 bits, and what that rounding leaves in 16 bits more
-template <bool kHalf>
-__device__ __forceinline__ void split(float a, float b, uint32_t& hi, uint32_t& lo) {
-    if constexpr (kHalf) {
-        hi = pack_half(a, b);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-        lo = pack_half(a - f.x, b - f.y);
-    } else {
-        hi = pack_bf16(a, b);
-        lo = pack_bf16(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
-    }
+// the transpose of 8 x 8 numbers of 16 bits: row lane / 4, columns 2 (lane % 4) and the next
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 // two e4m3 codes (the low 16 bits) as fp16, exactly
 __device__ __forceinline__ uint32_t codes_to_half(uint32_t q) {
@@ -116,16 +111,16 @@ struct Shapes {
     static constexpr int kBytes = kPart * (kE4m3 ? 1 : 2);                 // of a row in a warp
     static constexpr int kTokens = kBytes > 128 ? 16 : 32;                 // of a warp's step: 8 KB of keys and values
     static constexpr int kTile = kTeams * kTokens;
-    static constexpr int kKeyTiles = kTokens / 8, kPairs = kTokens / 16;
+    static constexpr int kMmas = kTokens / 16;                             // MMAs' worth of tokens in a step
     static constexpr int kKeyLoads = kBytes / 64;                          // 16-byte pieces of a key row in a lane
     static constexpr bool kNarrow = kBytes == 64;                          // value pieces of 8 bytes
     static constexpr int kValueLoads = kNarrow ? 1 : kBytes / 128;         // pieces of a value row
     static constexpr int kPerPiece = kE4m3 && !kNarrow ? 16 : 8;           // elements of a value piece
-    static constexpr int kOut = kPart / 8;                                 // column tiles of the output
-    static constexpr int kHalves = kRows > 8 ? 2 : 1;                      // rows g and g + 8 of the MMAs' 16
+    static constexpr int kOut = kPart / 16;                                // MMAs' worth of elements of the output
+    static constexpr int kCols = kRows / 8;                                // MMAs' worth of queries
     static constexpr int kStaged = kPart + 4;                              // a row of sums in shared memory
     static constexpr int kTeamFloats = kRows * kSplit * kStaged;
-    static_assert(kSplit == 1 || kTeamFloats >= 2 * 2 * kKeyTiles * 4 * 32, "a team's scores pass through its place for sums");
+    static_assert(kSplit == 1 || kTeamFloats >= 2 * 2 * kMmas * kCols * 4 * 32, "a team's scores pass through its place for sums");
     static constexpr int kSlot = kRows * (kD + 2);                         // floats of a part of an item: m, l; sums
 };
 
@@ -133,15 +128,15 @@ constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 
 template <class S>
 struct Warp {
-    uint4 key[S::kKeyTiles][S::kKeyLoads];
-    uint4 value[2 * S::kKeyTiles][S::kValueLoads];
-    float o[S::kOut][4];
+    uint4 key[2 * S::kMmas][S::kKeyLoads];         // rows of tokens 8 j + g
+    uint4 value[4 * S::kMmas][S::kValueLoads];     // rows of tokens 8 (j / 2) + 2 c + j % 2
+    float o[S::kOut][S::kCols][4];
 
     // rows: where the row of token `lane` of the step lies, in units of a.unit bytes; bytes: of a row, from base
     __device__ __forceinline__ void load_keys(const char* base, uint32_t rows, uint32_t unit, int bytes) {
         const int lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
 #pragma unroll
-        for (int j = 0; j < S::kKeyTiles; ++j) {
+        for (int j = 0; j < 2 * S::kMmas; ++j) {
             const uint32_t at = __shfl_sync(0xffffffffu, rows, 8 * j + g);
             const char* row = base + (uint64_t)at * unit + 16 * c;
 #pragma unroll
@@ -153,7 +148,7 @@ struct Warp {
     __device__ __forceinline__ void load_values(const char* base, uint32_t rows, uint32_t unit, int bytes) {
         const int lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
 #pragma unroll
-        for (int j = 0; j < 2 * S::kKeyTiles; ++j) {
+        for (int j = 0; j < 4 * S::kMmas; ++j) {
             const uint32_t at = __shfl_sync(0xffffffffu, rows, 8 * (j / 2) + 2 * c + j % 2);
             const char* row = base + (uint64_t)at * unit + (S::kNarrow ? 8 : 16) * g;
 #pragma unroll
@@ -171,89 +166,98 @@ struct Warp {
             }
         }
     }
-    // s[j]: products of this lane's queries (rows g, g + 8) with tokens 8 j + 2 c and the next one
+    // s[n][m][2 h + f]: the product of token 16 m + 8 h + g with query 8 n + 2 c + f
     template <class Query>
-    __device__ __forceinline__ void scores(const Query& q, float (&s)[S::kKeyTiles][4]) {
+    __device__ __forceinline__ void scores(const Query& q, float (&s)[S::kCols][S::kMmas][4]) {
 #pragma unroll
-        for (int j = 0; j < S::kKeyTiles; ++j)
+        for (int n = 0; n < S::kCols; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+            for (int m = 0; m < S::kMmas; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][m][e] = 0.f;
 #pragma unroll
         for (int i = 0; i < S::kKeyLoads; ++i)
 #pragma unroll
-            for (int m = 0; m < (S::kE4m3 ? 4 : 2); ++m)
+            for (int k = 0; k < (S::kE4m3 ? 4 : 2); ++k)
 #pragma unroll
-                for (int j = 0; j < S::kKeyTiles; ++j) {
-                    const uint32_t w[4] = {key[j][i].x, key[j][i].y, key[j][i].z, key[j][i].w};
-                    const int k = i * (S::kE4m3 ? 4 : 2) + m;
-                    const uint32_t b0 = S::kE4m3 ? codes_to_half(w[m]) : w[2 * m % 4];
-                    const uint32_t b1 = S::kE4m3 ? codes_to_half(w[m] >> 16) : w[(2 * m + 1) % 4];
-                    mma<S::kE4m3>(s[j], q.lo[2 * k], S::kRows > 8 ? q.hi[2 * k] : 0u, q.lo[2 * k + 1],
-                                  S::kRows > 8 ? q.hi[2 * k + 1] : 0u, b0, b1);
+                for (int m = 0; m < S::kMmas; ++m) {
+                    const uint4 x = key[2 * m][i], y = key[2 * m + 1][i];
+                    const uint32_t u[4] = {x.x, x.y, x.z, x.w}, w[4] = {y.x, y.y, y.z, y.w};
+                    const uint32_t a0 = S::kE4m3 ? codes_to_half(u[k]) : u[2 * k % 4];
+                    const uint32_t a1 = S::kE4m3 ? codes_to_half(w[k]) : w[2 * k % 4];
+                    const uint32_t a2 = S::kE4m3 ? codes_to_half(u[k] >> 16) : u[(2 * k + 1) % 4];
+                    const uint32_t a3 = S::kE4m3 ? codes_to_half(w[k] >> 16) : w[(2 * k + 1) % 4];
+                    const int at = 2 * (i * (S::kE4m3 ? 4 : 2) + k);
+#pragma unroll
+                    for (int n = 0; n < S::kCols; ++n) mma<S::kE4m3>(s[n][m], a0, a1, a2, a3, q.reg[n][at], q.reg[n][at + 1]);
                 }
     }
-    // o += p v.  p[j]: as scores.  Probabilities go in as a number of 16 bits and one for the rest of it.  With up to 8
-    // queries the rest takes the place of rows 8 to 15.
-    __device__ __forceinline__ void accumulate(const float (&p)[S::kKeyTiles][4]) {
-        uint32_t hi[S::kKeyTiles][2], lo[S::kKeyTiles][2];
+    // o += v p, p as scores gives them.  With bf16 values a probability goes in as a number of 8 bits and one for the rest
+    // of it: 8 bits alone would double the square of what rounding the output costs.  With 8-bit values the MMAs take
+    // fp16, whose 11 bits cost a fiftieth of that.
+    __device__ __forceinline__ void accumulate(const float (&p)[S::kCols][S::kMmas][4]) {
+        uint32_t hi[S::kCols][S::kMmas][2], lo[S::kE4m3 ? 1 : S::kCols][S::kMmas][2];
 #pragma unroll
-        for (int j = 0; j < S::kKeyTiles; ++j) {
-            split<S::kE4m3>(p[j][0], p[j][1], hi[j][0], lo[j][0]);
-            if constexpr (S::kRows > 8) split<S::kE4m3>(p[j][2], p[j][3], hi[j][1], lo[j][1]);
-        }
+        for (int n = 0; n < S::kCols; ++n)
 #pragma unroll
-        for (int k = 0; k < S::kPairs; ++k)
+            for (int m = 0; m < S::kMmas; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float x = p[n][m][2 * h], y = p[n][m][2 * h + 1];
+                    if constexpr (S::kE4m3) {
+                        hi[n][m][h] = transposed(pack_half(x, y));
+                    } else {
+                        const uint32_t v = pack_bf16(x, y);
+                        hi[n][m][h] = transposed(v);
+                        lo[n][m][h] =
+                            transposed(pack_bf16(x - __uint_as_float(v << 16), y - __uint_as_float(v & 0xFFFF0000u)));
+                    }
+                }
+#pragma unroll
+        for (int m = 0; m < S::kMmas; ++m)
 #pragma unroll
             for (int i = 0; i < S::kValueLoads; ++i)
 #pragma unroll
-                for (int e = 0; e < S::kPerPiece; ++e) {
-                    uint32_t b[2];
+                for (int e = 0; e < S::kPerPiece / 2; ++e) {       // elements 2 e and 2 e + 1 of the piece
+                    uint32_t a[4];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint4 x = value[4 * k + 2 * j][i], y = value[4 * k + 2 * j + 1][i];
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 x = value[4 * m + 2 * h][i], y = value[4 * m + 2 * h + 1][i];
                         const uint32_t u[4] = {x.x, x.y, x.z, x.w}, w[4] = {y.x, y.y, y.z, y.w};
                         if constexpr (S::kE4m3) {
-                            const uint32_t z = __byte_perm(u[e / 4], w[e / 4], e % 4 < 2 ? 0x5140 : 0x7362);
-                            b[j] = codes_to_half(e % 2 ? z >> 16 : z);
+                            const uint32_t z = __byte_perm(u[e / 2], w[e / 2], e % 2 ? 0x7362 : 0x5140);
+                            a[2 * h] = codes_to_half(z);
+                            a[2 * h + 1] = codes_to_half(z >> 16);
                         } else {
-                            b[j] = __byte_perm(u[e / 2 % 4], w[e / 2 % 4], e % 2 ? 0x7632 : 0x5410);
+                            a[2 * h] = __byte_perm(u[e % 4], w[e % 4], 0x5410);
+                            a[2 * h + 1] = __byte_perm(u[e % 4], w[e % 4], 0x7632);
                         }
                     }
-                    float(&t)[4] = o[i * S::kPerPiece + e];
-                    const int j = 2 * k;
-                    if constexpr (S::kRows > 8) {
-                        mma<S::kE4m3>(t, hi[j][0], hi[j][1], hi[j + 1][0], hi[j + 1][1], b[0], b[1]);
-                        mma<S::kE4m3>(t, lo[j][0], lo[j][1], lo[j + 1][0], lo[j + 1][1], b[0], b[1]);
-                    } else {
-                        mma<S::kE4m3>(t, hi[j][0], lo[j][0], hi[j + 1][0], lo[j + 1][0], b[0], b[1]);
+#pragma unroll
+                    for (int n = 0; n < S::kCols; ++n) {
+                        float(&t)[4] = o[i * S::kPerPiece / 2 + e][n];
+                        mma<S::kE4m3>(t, a[0], a[1], a[2], a[3], hi[n][m][0], hi[n][m][1]);
+                        if constexpr (!S::kE4m3) mma<S::kE4m3>(t, a[0], a[1], a[2], a[3], lo[n][m][0], lo[n][m][1]);
                     }
                 }
     }
-    // this lane's sums of row g (h = 1: row g + 8) times `by`, to a row in shared memory.  o[t][e] with e % 2 = f belongs
-    // to element (t / kPerPiece) 8 kPerPiece + (2 c + f) kPerPiece + t % kPerPiece.
-    __device__ __forceinline__ void stage(float* row, int h, float by) const {
-        const int c = threadIdx.x % 4;
+    // this lane's sums of query 8 n + 2 c + f, times `by`, to the query's row in shared memory
+    __device__ __forceinline__ void stage(float* row, int n, int f, float by) const {
+        const int g = threadIdx.x % 32 / 4;
+        constexpr int kHalf = S::kPerPiece / 2;
 #pragma unroll
-        for (int t = 0; t < S::kOut; t += 4)
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                float v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    v[i] = (S::kRows > 8 ? o[t + i][2 * h + f] : o[t + i][f] + o[t + i][2 + f]) * by;
-                *reinterpret_cast<float4*>(row + t / S::kPerPiece * 8 * S::kPerPiece + (2 * c + f) * S::kPerPiece +
-                                           t % S::kPerPiece) = make_float4(v[0], v[1], v[2], v[3]);
-            }
+        for (int t = 0; t < S::kOut; t += 2)
+            *reinterpret_cast<float4*>(row + (t / kHalf * 8 + g) * S::kPerPiece + t % kHalf * 2) =
+                make_float4(o[t][n][f] * by, o[t][n][2 + f] * by, o[t + 1][n][f] * by, o[t + 1][n][2 + f] * by);
     }
 };
 
-// A group's queries as A operands, in the order of elements that Warp::scores takes; 8-bit caches: as fp16, scaled by a
+// A group's queries as B operands, in the order of elements that Warp::scores takes; 8-bit caches: as fp16, scaled by a
 // power of two that brings the largest element to 2^14, so that what 16 bits of bf16 hold stays exact over 31 binades
 template <class S>
 struct Query {
-    static constexpr int kRegs = S::kPart / 8;
-    uint32_t lo[kRegs], hi[S::kRows > 8 ? kRegs : 1];
-    float unit[S::kHalves];  // what a product of rows g, g + 8 has to be multiplied by
+    uint32_t reg[S::kCols][S::kPart / 8];
+    float unit[S::kCols];    // what a product of query 8 n + g has to be multiplied by
 
     // row: a query head's elements from this warp's first one on, of which `left` are there
     __device__ __forceinline__ void load_row(const __nv_bfloat16* row, bool in, int left, uint32_t* to, float* unit_) {
@@ -295,8 +299,8 @@ struct Query {
     __device__ __forceinline__ void load(const Decode& a, int b, int head0, int rows, int first) {
         const int g = threadIdx.x % 32 / 4;
         const __nv_bfloat16* q = a.q + b * a.ld_q + (int64_t)head0 * a.D + first;
-        load_row(q + g * a.D, g < rows, a.D - first, lo, &unit[0]);
-        if constexpr (S::kRows > 8) load_row(q + (g + 8) * a.D, g + 8 < rows, a.D - first, hi, &unit[S::kHalves - 1]);
+#pragma unroll
+        for (int n = 0; n < S::kCols; ++n) load_row(q + (g + 8 * n) * a.D, g + 8 * n < rows, a.D - first, reg[n], &unit[n]);
     }
 };
 
@@ -428,12 +432,17 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
 
         Warp<S> w;
         Query<S> q;
-        Stats st[S::kHalves];
-        for (auto& x : st) x = Stats{-INFINITY, 0.f, -INFINITY};
+        Stats st[S::kCols][2];       // of queries 8 n + 2 c + f
+#pragma unroll
+        for (int n = 0; n < S::kCols; ++n)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) st[n][f] = Stats{-INFINITY, 0.f, -INFINITY};
 #pragma unroll
         for (int t = 0; t < S::kOut; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w.o[t][e] = 0.f;
+            for (int n = 0; n < S::kCols; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w.o[t][n][e] = 0.f;
         bool bad = range.poisoned;
 
         // this warp's first token of tile t; the page of this lane's (-1: a negative one, -2: no such token); its row
@@ -464,111 +473,116 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
         w.load_keys(kbase, at, a.unit, bytes);
         w.load_values(vbase, at, a.unit, bytes);
         q.load(a, b, head0, rows, first);
-        float factor[S::kHalves];
+        // what a score is multiplied by: its query's unit, the scale, and the change to powers of two
+        float factor[S::kCols][2], unit[S::kCols][2];
 #pragma unroll
-        for (int h = 0; h < S::kHalves; ++h)
-            factor[h] = (S::kSplit > 1 ? 1.f : q.unit[h]) * (a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e);
+        for (int n = 0; n < S::kCols; ++n)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                unit[n][f] = __shfl_sync(0xffffffffu, q.unit[n], 4 * (2 * c + f));
+                factor[n][f] = (S::kSplit > 1 ? 1.f : unit[n][f]) * (a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e);
+            }
         for (int t = t0; t < t1; ++t) {
             const float now_ks = ks, now_vs = S::kE4m3 ? log2_fast(vs) : 0.f;
             at = row_at(t + 1, page);
             page = page_at(t + 2);
-            float s[S::kKeyTiles][4];
+            float s[S::kCols][S::kMmas][4];
             w.scores(q, s);
             if (t + 1 < t1) w.load_keys(kbase, at, a.unit, bytes);
             if constexpr (S::kSplit > 1) {
                 // both warps of a team add the two halves in one order; they pass through the team's place for sums
-                auto place = [&](int of, int j, int e) -> float& {
-                    return smem[team * S::kTeamFloats + (((t & 1) * 2 + of) * S::kKeyTiles * 4 + 4 * j + e) * 32 + lane];
+                auto place = [&](int of, int i, int e) -> float& {
+                    return smem[team * S::kTeamFloats + (((t & 1) * 2 + of) * S::kMmas * S::kCols * 4 + 4 * i + e) * 32 + lane];
                 };
 #pragma unroll
-                for (int j = 0; j < S::kKeyTiles; ++j)
+                for (int n = 0; n < S::kCols; ++n)
 #pragma unroll
-                    for (int e = 0; e < 2 * S::kHalves; ++e) place(side, j, e) = s[j][e] * q.unit[e / 2];
+                    for (int m = 0; m < S::kMmas; ++m)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) place(side, n * S::kMmas + m, e) = s[n][m][e] * unit[n][e % 2];
                 asm volatile("bar.sync %0, 64;" ::"r"(team + 1) : "memory");
 #pragma unroll
-                for (int j = 0; j < S::kKeyTiles; ++j)
+                for (int n = 0; n < S::kCols; ++n)
 #pragma unroll
-                    for (int e = 0; e < 2 * S::kHalves; ++e)
-                        s[j][e] = place(0, j, e) + place(1, j, e);
+                    for (int m = 0; m < S::kMmas; ++m)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            s[n][m][e] = place(0, n * S::kMmas + m, e) + place(1, n * S::kMmas + m, e);
             }
-            // scores in log2, -infinity where there is no token; top: with the value's scale
-            const uint32_t tok = token(t) + 2 * c;
-            const bool all_in = token(t) + S::kTokens <= (uint32_t)range.end;
-            float lv[S::kKeyTiles][2];
-#pragma unroll
-            for (int j = 0; j < S::kKeyTiles; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float f = 1.f;
-                    if (S::kE4m3) {
-                        f = __shfl_sync(0xffffffffu, now_ks, 8 * j + 2 * c + e);
-                        lv[j][e] = __shfl_sync(0xffffffffu, now_vs, 8 * j + 2 * c + e);
-                    }
-#pragma unroll
-                    for (int h = 0; h < S::kHalves; ++h) {
-                        float& x = s[j][2 * h + e];
-                        x *= S::kE4m3 ? f * factor[h] : factor[h];
-                        if (a.softcap > 0.f) x = a.softcap * kLog2e * tanhf(x);
-                        if (!all_in && tok + 8 * j + e >= (uint32_t)range.end) x = -INFINITY;
-                    }
-                }
+            // scores in log2, -infinity where there is no token; lv: log2 of their tokens' value scales
+            const uint32_t tok = token(t);
+            const bool all_in = tok + S::kTokens <= (uint32_t)range.end;
+            float lv[S::kMmas][2];
             bool raise = false;
-            float most[S::kHalves][2];
 #pragma unroll
-            for (int h = 0; h < S::kHalves; ++h) {
-                float m = -INFINITY, u = -INFINITY;
+            for (int m = 0; m < S::kMmas; ++m)
 #pragma unroll
-                for (int j = 0; j < S::kKeyTiles; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        m = fmaxf(m, s[j][2 * h + e]);
-                        if (S::kE4m3) u = fmaxf(u, s[j][2 * h + e] + lv[j][e]);
+                for (int h = 0; h < 2; ++h) {
+                    float k = 1.f;
+                    if (S::kE4m3) {
+                        k = __shfl_sync(0xffffffffu, now_ks, 16 * m + 8 * h + g);
+                        lv[m][h] = __shfl_sync(0xffffffffu, now_vs, 16 * m + 8 * h + g);
                     }
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                most[h][0] = m;
-                raise |= m > st[h].m + kSlack;
-                if (S::kE4m3) {
-                    u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, 1));
-                    u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, 2));
-                    most[h][1] = u;
-                    raise |= u > st[h].top + kSlack;
+#pragma unroll
+                    for (int n = 0; n < S::kCols; ++n)
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) {
+                            float& x = s[n][m][2 * h + f];
+                            x *= S::kE4m3 ? k * factor[n][f] : factor[n][f];
+                            if (a.softcap > 0.f) x = a.softcap * kLog2e * tanhf(x);
+                            if (!all_in && tok + 16 * m + 8 * h + g >= (uint32_t)range.end) x = -INFINITY;
+                            raise |= x > st[n][f].m + kSlack;
+                            if (S::kE4m3) raise |= x + lv[m][h] > st[n][f].top + kSlack;
+                        }
                 }
-            }
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-                for (int h = 0; h < S::kHalves; ++h) {
-                    const float m = fmaxf(st[h].m, most[h][0]);
-                    float f = Joined::weight(st[h].m, m);
-                    st[h].l *= f;
-                    st[h].m = m;
-                    if (S::kE4m3) {
-                        const float u = fmaxf(st[h].top, most[h][1]);
-                        f = Joined::weight(st[h].top, u);
-                        st[h].top = u;
+                for (int n = 0; n < S::kCols; ++n)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        Stats& r = st[n][f];
+                        float most = r.m, top = r.top;
+#pragma unroll
+                        for (int m = 0; m < S::kMmas; ++m)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                most = fmaxf(most, s[n][m][2 * h + f]);
+                                if (S::kE4m3) top = fmaxf(top, s[n][m][2 * h + f] + lv[m][h]);
+                            }
+#pragma unroll
+                        for (int d = 4; d < 32; d *= 2) {
+                            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+                            if (S::kE4m3) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        }
+                        float by = Joined::weight(r.m, most);
+                        r.l *= by;
+                        if (S::kE4m3) by = Joined::weight(r.top, top);
+                        r.m = most;
+                        r.top = top;
+#pragma unroll
+                        for (int i = 0; i < S::kOut; ++i) {
+                            w.o[i][n][f] *= by;
+                            w.o[i][n][2 + f] *= by;
+                        }
                     }
-                    // rows 8 to 15 belong to the same queries where there are up to 8
+            }
 #pragma unroll
-                    for (int i = 0; i < S::kOut; ++i)
+            for (int n = 0; n < S::kCols; ++n)
 #pragma unroll
-                        for (int e = 0; e < (S::kRows > 8 ? 2 : 4); ++e) w.o[i][2 * h + e] *= f;
+                for (int f = 0; f < 2; ++f) {
+                    const float less = st[n][f].m == -INFINITY ? 0.f : st[n][f].m;
+                    // 2^7 (2^15 with the slack) is the largest numerator in 8 bits: what fp16 loses below 2^-24 is 2^-31 of it
+                    const float top = st[n][f].top == -INFINITY ? -7.f : st[n][f].top - 7.f;
+#pragma unroll
+                    for (int m = 0; m < S::kMmas; ++m)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float& x = s[n][m][2 * h + f];
+                            const float pr = exp2_fast(x - less);
+                            st[n][f].l += pr;
+                            x = S::kE4m3 ? exp2_fast(x + lv[m][h] - top) : pr;
+                        }
                 }
-            }
-#pragma unroll
-            for (int h = 0; h < S::kHalves; ++h) {
-                const float m = st[h].m == -INFINITY ? 0.f : st[h].m;
-                // 2^7 (2^15 with the slack) is the largest numerator in 8 bits: what fp16 loses below 2^-24 is 2^-31 of it
-                const float u = st[h].top == -INFINITY ? -7.f : st[h].top - 7.f;
-#pragma unroll
-                for (int j = 0; j < S::kKeyTiles; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float& x = s[j][2 * h + e];
-                        const float pr = exp2_fast(x - m);
-                        st[h].l += pr;
-                        x = S::kE4m3 ? exp2_fast(x + lv[j][e] - u) : pr;
-                    }
-            }
             w.accumulate(s);
             if (t + 1 < t1) w.load_values(vbase, at, a.unit, bytes);
         }
@@ -577,20 +591,22 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
 
         // ---- the warps' rows together: m and l of each, then the elements
 #pragma unroll
-        for (int h = 0; h < S::kHalves; ++h) {
-            float l = st[h].l;
-            l += __shfl_xor_sync(0xffffffffu, l, 1);
-            l += __shfl_xor_sync(0xffffffffu, l, 2);
-            if (bad) l = NAN;
-            const int row = g + 8 * h;
-            if (c == 0 && side == 0) {
-                sh_m[team][row] = st[h].m;
-                sh_l[team][row] = l;
+        for (int n = 0; n < S::kCols; ++n)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                const Stats& r = st[n][f];
+                float l = r.l;
+#pragma unroll
+                for (int d = 4; d < 32; d *= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
+                if (bad) l = NAN;
+                const int row = 8 * n + 2 * c + f;
+                if (g == 0 && side == 0) {
+                    sh_m[team][row] = r.m;
+                    sh_l[team][row] = l;
+                }
+                const float by = !S::kE4m3 || r.top == -INFINITY ? 1.f : exp2_fast(r.top - 7.f - r.m);
+                w.stage(smem + team * S::kTeamFloats + (row * S::kSplit + side) * S::kStaged, n, f, by);
             }
-            float by = 1.f;
-            if (S::kE4m3) by = st[h].top == -INFINITY ? 1.f : exp2_fast(st[h].top - 7.f - st[h].m);
-            w.stage(smem + team * S::kTeamFloats + (row * S::kSplit + side) * S::kStaged, h, by);
-        }
         __syncthreads();
         const bool whole = t0 == 0 && t1 == n_tiles;
         auto slot = [&](int cta, bool begins) { return a.ws + (int64_t)(2 * cta + (begins ? 1 : 0)) * S::kSlot; };

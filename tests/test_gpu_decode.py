@@ -5,9 +5,9 @@ Tolerances, with S the largest scale sum_d |q_d k_d| of a row and u = 2^-24:
               of two and, where scores are capped, the tangent (2 units) and two more: 8 u of |score| + 4 u of the cap.
               Capping does not enlarge an error.  delta = D 2^-23 S + 2^-20 (|score| + cap)
   weight      e^s: delta and the exponential's 2 units: delta + 2^-21, and the same for the sum it is divided by
-  product     a probability in 16 bits and 16 bits more: 2^-16 of it (fp16: 2^-22); L terms and their joins added in
-              float32: (L + 64) 2^-23
-  out         (2 (delta + 2^-21) + 2^-16 + (L + 64) 2^-23) sum_j p_j |v_j|, then half a step of bf16
+  product     a probability in bf16 and its rest in bf16: half a step of half a step, 2^-16 of it; 8-bit caches: in fp16,
+              half a step, 2^-11; L terms and their joins added in float32: (L + 64) 2^-23
+  out         (2 (delta + 2^-21) + 2^-16 or 2^-11 + (L + 64) 2^-23) sum_j p_j |v_j|, then half a step of bf16
   lse         delta + 2^-21 + (L + 64) 2^-23, and 2^-22 of itself
 """
 import math
@@ -96,7 +96,8 @@ class Case:
                 most = (q.abs() @ k.abs().t()).amax() * abs(scale)
                 delta = D * 2.0 ** -23 * most + 2.0 ** -20 * (s.abs().amax() + softcap)
                 join = (len(t) + 64) * 2.0 ** -23
-                tol = (2 * (delta + 2.0 ** -21) + 2.0 ** -16 + join) * (p @ v.abs()) + BF * o.abs()
+                weight = 2.0 ** (-11 if self.e4m3 else -16)
+                tol = (2 * (delta + 2.0 ** -21) + weight + join) * (p @ v.abs()) + BF * o.abs()
                 err = (out[b, h] - o).abs()
                 assert (err <= tol).all(), "sequence %d head %d: %.3g times the tolerance" % (b, h, (err / tol).max())
                 zerr = (lse[b, h] - z).abs()
