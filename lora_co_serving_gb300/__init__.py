@@ -1093,7 +1093,7 @@ def _decode_size(n_heads, kv_heads, D, e4m3, device):
     return int(n)
 
 
-_DECODE_COUNTER_BYTES = 8192
+DECODE_COUNTER_BYTES = 8192    # of a decode workspace: zero before its first use
 _decode_workspaces = {}
 
 
@@ -1107,7 +1107,7 @@ def _decode_workspace(n, stream_ptr, device):
     ws = None if capturing else _decode_workspaces.get(key)
     if ws is None or ws.numel() < n:
         ws = torch.empty(n, dtype=torch.uint8, device=device)
-        ws[:_DECODE_COUNTER_BYTES].zero_()
+        ws[:DECODE_COUNTER_BYTES].zero_()
         if not capturing:
             _decode_workspaces[key] = ws
     return ws
@@ -1123,7 +1123,7 @@ def decode_attention(q, cache, page_table, lengths, scale=None, window=0, softca
 
     Returns out [B, n_heads D], with want_lse (out, lse [B, n_heads] float32).  A length of zero gives zeros and -infinity;
     a sequence longer than its table's row, or a page outside the cache, gives NaN.  workspace: decode_workspace_size
-    bytes, the first 8192 zero before its first use; not for two calls at once."""
+    bytes, the first DECODE_COUNTER_BYTES zero before its first use; not for two calls at once."""
     import torch
     c, kv_heads, D, held = _cache(cache)
     ldq = _matrix(q, "q", torch.bfloat16)

@@ -1,18 +1,22 @@
 // decode.cu -- attention of one new token of each sequence over the paged cache (include/lora_attention.h).
 //
 // What bounds it: each cached element is used by the n query heads of its group only, 4 n operations for 2 bytes (or one).
-// The cache's bytes bound the call at any matrix rate above some 100 TFLOP/s, so the products are small register-to-
-// register MMAs (m16n8k16) whose operands come straight from global memory: the cache's side has the 16 rows, up to 8
-// query heads the 8 columns.  Both products can take the cache as it lies, without a way through shared memory:
+// The cache's bytes bound the call at any matrix rate above some 100 TFLOP/s, so the products are small MMAs of a warp
+// (m16n8k16): the cache's side has the 16 rows, up to 8 query heads the 8 columns.  Both take the cache as it lies, with
+// no exchange between lanes:
 //   scores  rows are tokens.  The sum over a head's elements may be taken in any order, so a lane's 16 bytes of a key row
-//           are its share of two MMAs (four in 8 bits), if the query's elements are taken in the same order;
-//   output  rows are elements, the sum goes over tokens, a pair of them in a register: a lane loads the same 16 bytes of a
+//           are its share of two MMAs, if the query's elements are taken in the same order;
+//   output  rows are elements, the sum goes over tokens, a pair of them in a register: a lane takes the same 16 bytes of a
 //           pair's two value rows and interleaves them.  Which element is which row is free, too.  The probabilities, whose
 //           tokens are rows, are turned around by the transposing move of 8 x 8 numbers.
+// Every warp copies its rows into shared memory two steps ahead of their use, asynchronously, 512 neighbouring bytes at a
+// time, and reads them back as its lanes need them: a barrier within the warp is all that it takes.  (Lanes that copied
+// their own pieces, 64 bytes of 8 rows at a time, needed one and a half times the requests to L2: 236 us instead of @ for
+// 64 x 8192 tokens in bf16.)
 // Work is counted in tiles of 32 to 128 tokens of one sequence and one cache head.  All tiles of a call form one line, and
 // each CTA takes an equal piece of it, whatever the lengths are; a CTA's warps take 16 or 32 tokens of a tile each, with a
-// running maximum and sum of their own.  A sequence and head whose tiles lie in several CTAs is joined by the last of them
-// to arrive, in the order of the tiles.
+// running maximum and sum of their own, and the copies run on from one sequence into the next.  A sequence and head whose
+// tiles lie in several CTAs is joined by the last of them to arrive, in the order of the tiles.
 #include <algorithm>
 #include <type_traits>
 
@@ -62,6 +66,30 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
+// c += a b for e4m3 operands, m16n8k32: half the time of the fp16 form for twice the sum
+__device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                     uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// An asynchronous copy of kBytes to shared memory; where `in` is false, zeros
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, bool in) {
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(kBytes), "r"(in ? kBytes : 0)
+                     : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// waits until at most kPending of the thread's latest groups are under way
+template <int kPending>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
 // the transpose of 8 x 8 numbers of 16 bits: row lane / 4, columns 2 (lane % 4) and the next
 __device__ __forceinline__ uint32_t transposed(uint32_t v) {
     uint32_t r;
@@ -100,8 +128,8 @@ __device__ __forceinline__ Range range_of(const Decode& a, int32_t b) {
 }
 
 // Shapes of a kernel for cache heads of up to kD elements and kRows query heads at a time.  A warp holds kPart elements of
-// each row: 128 at most, so that its sums, its share of the queries and one step's pieces stay in registers; heads of 256
-// are taken by two warps, which add up their scores.
+// each row: 128 at most, so that its sums and its share of the queries stay in registers; heads of 256 are taken by two
+// warps, which add up their scores.
 template <bool kE4m3_, int kD_, int kRows_>
 struct Shapes {
     static constexpr bool kE4m3 = kE4m3_;
@@ -113,89 +141,109 @@ struct Shapes {
     static constexpr int kTile = kTeams * kTokens;
     static constexpr int kMmas = kTokens / 16;                             // MMAs' worth of tokens in a step
     static constexpr int kKeyLoads = kBytes / 64;                          // 16-byte pieces of a key row in a lane
-    static constexpr bool kNarrow = kBytes == 64;                          // value pieces of 8 bytes
-    static constexpr int kValueLoads = kNarrow ? 1 : kBytes / 128;         // pieces of a value row
-    static constexpr int kPerPiece = kE4m3 && !kNarrow ? 16 : 8;           // elements of a value piece
+    static constexpr int kPieceBytes = kBytes == 64 ? 8 : 16;              // a lane's piece of a value row
+    static constexpr int kValueLoads = kBytes == 64 ? 1 : kBytes / 128;    // such pieces
+    static constexpr int kPerPiece = kE4m3 ? kPieceBytes : kPieceBytes / 2;   // elements of one
     static constexpr int kOut = kPart / 16;                                // MMAs' worth of elements of the output
     static constexpr int kCols = kRows / 8;                                // MMAs' worth of queries
-    static constexpr int kStaged = kPart + 4;                              // a row of sums in shared memory
-    static constexpr int kTeamFloats = kRows * kSplit * kStaged;
-    static_assert(kSplit == 1 || kTeamFloats >= 2 * 2 * kMmas * kCols * 4 * 32, "a team's scores pass through its place for sums");
+    // shared memory of a warp: two steps' keys, values and scales; after an item's last step its place holds the item's
+    // sums, [kRows][kPart]
+    static constexpr int kKeyBytes = kTokens * kBytes, kStepBytes = 2 * kKeyBytes;
+    static_assert(kRows * kPart * 4 <= kStepBytes, "a warp's sums fit a step's place");
+    static constexpr int kScaleBytes = kE4m3 ? 2 * 32 * 4 : 0;
+    static constexpr int kWarpBytes = 2 * (kStepBytes + kScaleBytes);
+    static constexpr int kExchangeFloats = kSplit > 1 ? 2 * kCols * kMmas * 4 * 32 : 0;      // a warp's scores, twice
+    static constexpr int kSmem = kWarps * (kWarpBytes + 4 * kExchangeFloats);
     static constexpr int kSlot = kRows * (kD + 2);                         // floats of a part of an item: m, l; sums
 };
 
-constexpr uint32_t kNoRow = 0xFFFFFFFFu;
-
 template <class S>
 struct Warp {
-    uint4 key[2 * S::kMmas][S::kKeyLoads];         // rows of tokens 8 j + g
-    uint4 value[4 * S::kMmas][S::kValueLoads];     // rows of tokens 8 (j / 2) + 2 c + j % 2
     float o[S::kOut][S::kCols][4];
 
-    // rows: where the row of token `lane` of the step lies, in units of a.unit bytes; bytes: of a row, from base
-    __device__ __forceinline__ void load_keys(const char* base, uint32_t rows, uint32_t unit, int bytes) {
-        const int lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
+    // Copies of a step's rows, [kTokens][kBytes] of keys, then of values.  rows: where the row of token `lane` of the step
+    // lies, in units of a.unit bytes, from `keys`; bytes: of a row.  Pieces of 16 bytes lie in an order of their own in each
+    // row, so that the lanes that read them at once (rows g, pieces c of the keys; rows 2 c, pieces g of the values) fall on
+    // different banks.
+    static constexpr int kAcross = S::kBytes / 16;                         // pieces of a row
+    static __device__ __forceinline__ void copy(uint32_t to, const char* keys, int64_t to_values, uint32_t rows, uint32_t unit,
+                                                int bytes) {
+        const int lane = threadIdx.x % 32, row0 = lane / kAcross, col = lane % kAcross;
+        const bool in = 16 * col < bytes;
+        const int at_k = (col ^ (kAcross >= 8 ? 4 * (row0 & 1) : 0)) * 16 + row0 * S::kBytes;
+        const int at_v = (col ^ (kAcross >= 8 ? row0 & 6 : (row0 >> 1) & 3)) * 16 + row0 * S::kBytes;
 #pragma unroll
-        for (int j = 0; j < 2 * S::kMmas; ++j) {
-            const uint32_t at = __shfl_sync(0xffffffffu, rows, 8 * j + g);
-            const char* row = base + (uint64_t)at * unit + 16 * c;
-#pragma unroll
-            for (int i = 0; i < S::kKeyLoads; ++i)
-                key[j][i] = at != kNoRow && 64 * i + 16 * c < bytes ? *reinterpret_cast<const uint4*>(row + 64 * i)
-                                                                   : make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < S::kKeyBytes / 512; ++k) {
+            const uint32_t at = __shfl_sync(0xffffffffu, rows, k * (32 / kAcross) + row0);
+            const char* from = in ? keys + (uint64_t)at * unit + 16 * col : keys;
+            copy_async<16>(to + 512 * k + at_k, from, in);
+            const int turn = kAcross >= 8 ? k * (32 / kAcross) & 6 : 0;
+            copy_async<16>(to + S::kKeyBytes + 512 * k + (at_v ^ (16 * turn)), from + to_values, in);
         }
     }
-    __device__ __forceinline__ void load_values(const char* base, uint32_t rows, uint32_t unit, int bytes) {
-        const int lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
-#pragma unroll
-        for (int j = 0; j < 4 * S::kMmas; ++j) {
-            const uint32_t at = __shfl_sync(0xffffffffu, rows, 8 * (j / 2) + 2 * c + j % 2);
-            const char* row = base + (uint64_t)at * unit + (S::kNarrow ? 8 : 16) * g;
-#pragma unroll
-            for (int i = 0; i < S::kValueLoads; ++i) {
-                value[j][i] = make_uint4(0, 0, 0, 0);
-                if constexpr (S::kNarrow) {
-                    if (at != kNoRow && 8 * g < bytes) {
-                        const uint2 w = *reinterpret_cast<const uint2*>(row);
-                        value[j][i].x = w.x;
-                        value[j][i].y = w.y;
-                    }
-                } else {
-                    if (at != kNoRow && 128 * i + 16 * g < bytes) value[j][i] = *reinterpret_cast<const uint4*>(row + 128 * i);
-                }
-            }
-        }
+    // the 16 bytes 4 i + c of the key row of token 8 j + g
+    static __device__ __forceinline__ uint4 key(const char* at, int j, int i) {
+        const int g = threadIdx.x % 32 / 4, c = threadIdx.x % 4;
+        const int off = g * S::kBytes + ((kAcross >= 8 ? 4 * (g & 1) : 0) + c) * 16;
+        return *reinterpret_cast<const uint4*>(at + 8 * j * S::kBytes + (off ^ (64 * i)));
+    }
+    // piece 8 i + g of the value row of token 8 (j / 2) + 2 c + j % 2
+    static __device__ __forceinline__ uint4 value(const char* at, int j, int i) {
+        const int g = threadIdx.x % 32 / 4, c = threadIdx.x % 4;
+        const char* row = at + (8 * (j / 2) + j % 2 + 2 * c) * S::kBytes;
+        if constexpr (S::kPieceBytes == 16) return *reinterpret_cast<const uint4*>(row + 128 * i + (g ^ (2 * c)) * 16);
+        const uint2 v = *reinterpret_cast<const uint2*>(row + ((g / 2) ^ c) * 16 + g % 2 * 8);
+        return make_uint4(v.x, v.y, 0, 0);
     }
     // s[n][m][2 h + f]: the product of token 16 m + 8 h + g with query 8 n + 2 c + f
     template <class Query>
-    __device__ __forceinline__ void scores(const Query& q, float (&s)[S::kCols][S::kMmas][4]) {
+    static __device__ __forceinline__ void scores(const char* keys, const Query& q, float (&s)[S::kCols][S::kMmas][4]) {
 #pragma unroll
         for (int n = 0; n < S::kCols; ++n)
 #pragma unroll
             for (int m = 0; m < S::kMmas; ++m)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[n][m][e] = 0.f;
+        float rest[S::kE4m3 ? S::kCols : 1][S::kMmas][4];
+        if constexpr (S::kE4m3)
+#pragma unroll
+            for (int n = 0; n < S::kCols; ++n)
+#pragma unroll
+                for (int m = 0; m < S::kMmas; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) rest[n][m][e] = 0.f;
 #pragma unroll
         for (int i = 0; i < S::kKeyLoads; ++i)
 #pragma unroll
-            for (int k = 0; k < (S::kE4m3 ? 4 : 2); ++k)
+            for (int m = 0; m < S::kMmas; ++m) {
+                const uint4 x = key(keys, 2 * m, i), y = key(keys, 2 * m + 1, i);
 #pragma unroll
-                for (int m = 0; m < S::kMmas; ++m) {
-                    const uint4 x = key[2 * m][i], y = key[2 * m + 1][i];
-                    const uint32_t u[4] = {x.x, x.y, x.z, x.w}, w[4] = {y.x, y.y, y.z, y.w};
-                    const uint32_t a0 = S::kE4m3 ? codes_to_half(u[k]) : u[2 * k % 4];
-                    const uint32_t a1 = S::kE4m3 ? codes_to_half(w[k]) : w[2 * k % 4];
-                    const uint32_t a2 = S::kE4m3 ? codes_to_half(u[k] >> 16) : u[(2 * k + 1) % 4];
-                    const uint32_t a3 = S::kE4m3 ? codes_to_half(w[k] >> 16) : w[(2 * k + 1) % 4];
-                    const int at = 2 * (i * (S::kE4m3 ? 4 : 2) + k);
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t a0 = k ? x.z : x.x, a1 = k ? y.z : y.x, a2 = k ? x.w : x.y, a3 = k ? y.w : y.y;
+                    const int at = 4 * i + 2 * k;
 #pragma unroll
-                    for (int n = 0; n < S::kCols; ++n) mma<S::kE4m3>(s[n][m], a0, a1, a2, a3, q.reg[n][at], q.reg[n][at + 1]);
+                    for (int n = 0; n < S::kCols; ++n) {
+                        if constexpr (S::kE4m3) {
+                            mma8(s[n][m], a0, a1, a2, a3, q.reg[n][at], q.reg[n][at + 1]);
+                            mma8(rest[n][m], a0, a1, a2, a3, q.reg[n][S::kPart / 16 + at], q.reg[n][S::kPart / 16 + at + 1]);
+                        } else {
+                            mma<false>(s[n][m], a0, a1, a2, a3, q.reg[n][at], q.reg[n][at + 1]);
+                        }
+                    }
                 }
+            }
+        if constexpr (S::kE4m3)
+#pragma unroll
+            for (int n = 0; n < S::kCols; ++n)
+#pragma unroll
+                for (int m = 0; m < S::kMmas; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[n][m][e] = fmaf(rest[n][m][e], 0x1p-4f, s[n][m][e]);
     }
     // o += v p, p as scores gives them.  With bf16 values a probability goes in as a number of 8 bits and one for the rest
     // of it: 8 bits alone would double the square of what rounding the output costs.  With 8-bit values the MMAs take
     // fp16, whose 11 bits cost a fiftieth of that.
-    __device__ __forceinline__ void accumulate(const float (&p)[S::kCols][S::kMmas][4]) {
+    __device__ __forceinline__ void accumulate(const char* values, const float (&p)[S::kCols][S::kMmas][4]) {
         uint32_t hi[S::kCols][S::kMmas][2], lo[S::kE4m3 ? 1 : S::kCols][S::kMmas][2];
 #pragma unroll
         for (int n = 0; n < S::kCols; ++n)
@@ -216,21 +264,25 @@ struct Warp {
 #pragma unroll
         for (int m = 0; m < S::kMmas; ++m)
 #pragma unroll
-            for (int i = 0; i < S::kValueLoads; ++i)
+            for (int i = 0; i < S::kValueLoads; ++i) {
+                uint32_t v[4][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 x = value(values, 4 * m + j, i);
+                    v[j][0] = x.x; v[j][1] = x.y; v[j][2] = x.z; v[j][3] = x.w;
+                }
 #pragma unroll
                 for (int e = 0; e < S::kPerPiece / 2; ++e) {       // elements 2 e and 2 e + 1 of the piece
                     uint32_t a[4];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint4 x = value[4 * m + 2 * h][i], y = value[4 * m + 2 * h + 1][i];
-                        const uint32_t u[4] = {x.x, x.y, x.z, x.w}, w[4] = {y.x, y.y, y.z, y.w};
                         if constexpr (S::kE4m3) {
-                            const uint32_t z = __byte_perm(u[e / 2], w[e / 2], e % 2 ? 0x7362 : 0x5140);
+                            const uint32_t z = __byte_perm(v[2 * h][e / 2], v[2 * h + 1][e / 2], e % 2 ? 0x7362 : 0x5140);
                             a[2 * h] = codes_to_half(z);
                             a[2 * h + 1] = codes_to_half(z >> 16);
                         } else {
-                            a[2 * h] = __byte_perm(u[e % 4], w[e % 4], 0x5410);
-                            a[2 * h + 1] = __byte_perm(u[e % 4], w[e % 4], 0x7632);
+                            a[2 * h] = __byte_perm(v[2 * h][e], v[2 * h + 1][e], 0x5410);
+                            a[2 * h + 1] = __byte_perm(v[2 * h][e], v[2 * h + 1][e], 0x7632);
                         }
                     }
 #pragma unroll
@@ -240,20 +292,28 @@ struct Warp {
                         if constexpr (!S::kE4m3) mma<S::kE4m3>(t, a[0], a[1], a[2], a[3], lo[n][m][0], lo[n][m][1]);
                     }
                 }
+            }
     }
-    // this lane's sums of query 8 n + 2 c + f, times `by`, to the query's row in shared memory
-    __device__ __forceinline__ void stage(float* row, int n, int f, float by) const {
-        const int g = threadIdx.x % 32 / 4;
+    // Where four neighbouring sums of a row, from `element`, lie among a warp's staged sums; turned about by the row, so that
+    // lanes of different rows fall on different banks
+    static __device__ __forceinline__ int staged(int row, int element) {
+        return row * S::kPart + ((element / 4) ^ (row & 7)) * 4;
+    }
+    // this lane's sums of query row 8 n + 2 c + f, times `by`
+    __device__ __forceinline__ void stage(float* to, int n, int f, float by) const {
+        const int g = threadIdx.x % 32 / 4, row = 8 * n + 2 * (threadIdx.x % 4) + f;
         constexpr int kHalf = S::kPerPiece / 2;
 #pragma unroll
         for (int t = 0; t < S::kOut; t += 2)
-            *reinterpret_cast<float4*>(row + (t / kHalf * 8 + g) * S::kPerPiece + t % kHalf * 2) =
+            *reinterpret_cast<float4*>(to + staged(row, (t / kHalf * 8 + g) * S::kPerPiece + t % kHalf * 2)) =
                 make_float4(o[t][n][f] * by, o[t][n][2 + f] * by, o[t + 1][n][f] * by, o[t + 1][n][2 + f] * by);
     }
 };
 
-// A group's queries as B operands, in the order of elements that Warp::scores takes; 8-bit caches: as fp16, scaled by a
-// power of two that brings the largest element to 2^14, so that what 16 bits of bf16 hold stays exact over 31 binades
+// A group's queries as B operands, in the order of elements that Warp::scores takes.  8-bit caches: as e4m3 codes, like the
+// keys, so that these need no change: a query of 8 bits is an e4m3 number of 4 bits and 2^-4 times one for the
+// 4 that are left.  They are scaled by a power of two that brings the largest element to between 2^7 and 2^8: what is rounded lies
+// below 2^-14, which is 2^-21 of that element.
 template <class S>
 struct Query {
     uint32_t reg[S::kCols][S::kPart / 8];
@@ -282,18 +342,33 @@ struct Query {
             }
             a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
             a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-            const int e = min(max((int)(a >> 23) - 127, -112), 127);
-            inv = a >= 0x7F800000u ? NAN : __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-            *unit_ = a >= 0x7F800000u ? NAN : __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+            const int e = min(max((int)(a >> 23) - 127, -118), 127);
+            inv = a >= 0x7F800000u ? NAN : __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+            *unit_ = a >= 0x7F800000u ? NAN : __uint_as_float((uint32_t)(127 - 7 + e) << 23);
         }
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            if constexpr (S::kE4m3) {
+                Row8Bf16 r;
+                float v[8];
+                r.q = w[i];
+                r.get(v);
+                const uint2 hi = encode8(v, inv);
+                float back[8];
+                decode8(hi, 1.f, back);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                to[4 * i + k] = S::kE4m3
-                                    ? pack_half(__uint_as_float(u[k] << 16) * inv, __uint_as_float(u[k] & 0xFFFF0000u) * inv)
-                                    : u[k];
+                for (int k = 0; k < 8; ++k) v[k] = (v[k] * inv - back[k]) * 16.f;
+                const uint2 lo = encode8(v, 1.f);
+                to[2 * i] = hi.x;
+                to[2 * i + 1] = hi.y;
+                to[S::kPart / 16 + 2 * i] = lo.x;
+                to[S::kPart / 16 + 2 * i + 1] = lo.y;
+            } else {
+                to[4 * i] = w[i].x;
+                to[4 * i + 1] = w[i].y;
+                to[4 * i + 2] = w[i].z;
+                to[4 * i + 3] = w[i].w;
+            }
         }
     }
     __device__ __forceinline__ void load(const Decode& a, int b, int head0, int rows, int first) {
@@ -348,9 +423,34 @@ __device__ __forceinline__ Joined join_parts(int n, int row, int d, At at) {
     return r;
 }
 
+// A tile of the line: tile t of one of the lines of sequence b.  A line belongs to a cache head, or a part of its group.
+template <class S>
+struct Cursor {
+    int32_t b, line, t, n_tiles;
+    uint32_t start, end;
+    bool poisoned;
+    __device__ __forceinline__ void enter(const Decode& a) {
+        const Range r = range_of(a, b);
+        start = r.start;
+        end = r.end;
+        poisoned = r.poisoned;
+        n_tiles = r.tiles(S::kTile);
+    }
+    // the next line's first tile; there is one
+    __device__ __forceinline__ void next_line(const Decode& a) {
+        t = 0;
+        if (++line < a.kv_heads * a.parts) return;
+        line = 0;
+        do {
+            ++b;
+            enter(a);
+        } while (n_tiles == 0);
+    }
+};
+
 template <class S, int kCtas>
 __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a) {
-    extern __shared__ __align__(16) float smem[];        // a place for sums, [kRows][kSplit][kStaged], for each team
+    extern __shared__ __align__(128) char smem[];
     __shared__ int32_t sh_seq;
     __shared__ int64_t sh_before;
     __shared__ int64_t warp_sum[kWarps];
@@ -406,30 +506,67 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
     }
     __syncthreads();
     if (p0 >= p1) return;
-    int b = sh_seq;
-    int64_t before = sh_before;
 
+    // ---- the copies, two tiles ahead: `ahead` is the tile to be copied next, whose pages are on their way
     const int first = side * S::kPart;                // this warp's elements of a row
     const int bytes = (a.D - first) * (S::kE4m3 ? 1 : 2);
-    int64_t p = p0;
-    while (p < p1) {
-        // ---- the next item: a sequence and a line of its tiles
-        const Range range = range_of(a, b);
-        const int n_tiles = range.tiles(S::kTile);
-        if (p >= before + (int64_t)n_tiles * heads) {
-            before += (int64_t)n_tiles * heads;
-            ++b;
-            continue;
+    char* const mine_at = smem + warp * S::kWarpBytes;
+    const uint32_t mine_u32 = smem_u32(mine_at);
+    Cursor<S> at;
+    at.b = sh_seq;
+    at.enter(a);
+    at.line = (int)((p0 - sh_before) / at.n_tiles);
+    at.t = (int)((p0 - sh_before) % at.n_tiles);
+    Cursor<S> ahead = at;
+    int64_t to_copy = p1 - p0, to_do = p1 - p0;
+    int32_t page = 0;
+    uint32_t bad_steps = 0;                           // bit i: step i's tile has a page outside the cache
+    auto token = [&](const Cursor<S>& x) { return x.start + (uint32_t)x.t * S::kTile + team * S::kTokens; };
+    // Lanes past the last token take that token's row once more: their scores become -infinity, and 0 times a value of the
+    // range adds nothing.
+    auto my_token = [&](const Cursor<S>& x) { return min(token(x) + lane % S::kTokens, x.end - 1); };
+    auto read_page = [&]() {
+        if (to_copy > 0) page = a.table[ahead.b * a.ld_table + a.pages.page_of(my_token(ahead))];
+    };
+    auto copy = [&](int step) {
+        if (to_copy > 0) {
+            // a page outside the cache is taken as its first; the result becomes NaN
+            const bool bad = (uint32_t)page >= (uint32_t)a.cache.n_pages;
+            if (bad) page = 0;
+            bad_steps = (bad_steps & ~(1u << step)) | (__any_sync(0xffffffffu, bad) ? 1u << step : 0);
+            if (token(ahead) < ahead.end && a.cache.n_pages > 0) {
+                const int kv = ahead.line / a.parts;
+                const uint32_t tok = my_token(ahead);
+                const uint32_t row = tok - a.pages.page_of(tok) * (uint32_t)a.cache.page_size;
+                Warp<S>::copy(mine_u32 + step * S::kStepBytes,
+                              a.cache.k + kv * a.cache.head_stride + first * (S::kE4m3 ? 1 : 2), a.cache.v - a.cache.k,
+                              (uint32_t)page * a.page_units + row * a.row_units, a.unit, bytes);
+                if (S::kE4m3) {
+                    const int64_t z = page * a.cache.s_page + row * a.cache.s_row + kv * a.cache.s_head;
+                    const uint32_t sc = mine_u32 + 2 * S::kStepBytes + step * S::kScaleBytes + lane * 4;
+                    copy_async<4>(sc, a.cache.ks + z, true);
+                    copy_async<4>(sc + 128, a.cache.vs + z, true);
+                }
+            }
+            if (--to_copy > 0) {
+                if (++ahead.t == ahead.n_tiles) ahead.next_line(a);
+                read_page();
+            }
         }
-        const int line = (int)((p - before) / n_tiles);      // a cache head, or a part of its group
-        const int64_t i0 = before + (int64_t)line * n_tiles, i1 = i0 + n_tiles;
-        const int kv = line / a.parts, part = line % a.parts;
-        const int head0 = kv * a.group + part * a.rows, rows = min(a.rows, a.group - part * a.rows);
-        const int t0 = (int)(p - i0), t1 = (int)(min(p1, i1) - i0);
-        const char* kbase = a.cache.k + kv * a.cache.head_stride + first * (S::kE4m3 ? 1 : 2);
-        const char* vbase = a.cache.v + kv * a.cache.head_stride + first * (S::kE4m3 ? 1 : 2);
-        const int32_t* table = a.table + b * a.ld_table;
+        copies_commit();
+    };
+    read_page();
+    copy(0);
+    copy(1);
 
+    int step = 0;
+    int64_t p = p0;
+    while (to_do > 0) {
+        // ---- the next item: a sequence and a line of its tiles
+        const int b = at.b, n_tiles = at.n_tiles, t0 = at.t, t1 = (int)min((int64_t)n_tiles, t0 + to_do);
+        const int64_t i0 = p - t0, i1 = i0 + n_tiles;
+        const int kv = at.line / a.parts, part = at.line % a.parts;
+        const int head0 = kv * a.group + part * a.rows, n_rows = min(a.rows, a.group - part * a.rows);
         Warp<S> w;
         Query<S> q;
         Stats st[S::kCols][2];       // of queries 8 n + 2 c + f
@@ -443,36 +580,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
             for (int n = 0; n < S::kCols; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w.o[t][n][e] = 0.f;
-        bool bad = range.poisoned;
-
-        // this warp's first token of tile t; the page of this lane's (-1: a negative one, -2: no such token); its row
-        auto token = [&](int t) { return (uint32_t)range.start + (uint32_t)t * S::kTile + team * S::kTokens; };
-        auto page_at = [&](int t) -> int32_t {
-            const uint32_t tok = token(t) + lane % S::kTokens;
-            return t < t1 && tok < (uint32_t)range.end ? max(table[a.pages.page_of(tok)], -1) : -2;
-        };
-        float ks = 0.f, vs = 0.f;        // 8 bits: the next step's token's key scale, and log2 of its value scale
-        auto row_at = [&](int t, int32_t page) -> uint32_t {
-            if (page == -2) return kNoRow;
-            if (page == -1 || page >= a.cache.n_pages) {
-                bad = true;
-                return kNoRow;
-            }
-            const uint32_t tok = token(t) + lane % S::kTokens;
-            const uint32_t row = tok - a.pages.page_of(tok) * (uint32_t)a.cache.page_size;
-            if (S::kE4m3) {
-                const int64_t at = page * a.cache.s_page + row * a.cache.s_row + kv * a.cache.s_head;
-                ks = a.cache.ks[at];
-                vs = a.cache.vs[at];
-            }
-            return (uint32_t)page * a.page_units + row * a.row_units;
-        };
-        int32_t page = page_at(t0);
-        uint32_t at = row_at(t0, page);
-        page = page_at(t0 + 1);
-        w.load_keys(kbase, at, a.unit, bytes);
-        w.load_values(vbase, at, a.unit, bytes);
-        q.load(a, b, head0, rows, first);
+        bool bad = at.poisoned;
+        q.load(a, b, head0, n_rows, first);
         // what a score is multiplied by: its query's unit, the scale, and the change to powers of two
         float factor[S::kCols][2], unit[S::kCols][2];
 #pragma unroll
@@ -482,112 +591,133 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
                 unit[n][f] = __shfl_sync(0xffffffffu, q.unit[n], 4 * (2 * c + f));
                 factor[n][f] = (S::kSplit > 1 ? 1.f : unit[n][f]) * (a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e);
             }
-        for (int t = t0; t < t1; ++t) {
-            const float now_ks = ks, now_vs = S::kE4m3 ? log2_fast(vs) : 0.f;
-            at = row_at(t + 1, page);
-            page = page_at(t + 2);
-            float s[S::kCols][S::kMmas][4];
-            w.scores(q, s);
-            if (t + 1 < t1) w.load_keys(kbase, at, a.unit, bytes);
-            if constexpr (S::kSplit > 1) {
-                // both warps of a team add the two halves in one order; they pass through the team's place for sums
-                auto place = [&](int of, int i, int e) -> float& {
-                    return smem[team * S::kTeamFloats + (((t & 1) * 2 + of) * S::kMmas * S::kCols * 4 + 4 * i + e) * 32 + lane];
-                };
-#pragma unroll
-                for (int n = 0; n < S::kCols; ++n)
-#pragma unroll
-                    for (int m = 0; m < S::kMmas; ++m)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) place(side, n * S::kMmas + m, e) = s[n][m][e] * unit[n][e % 2];
-                asm volatile("bar.sync %0, 64;" ::"r"(team + 1) : "memory");
-#pragma unroll
-                for (int n = 0; n < S::kCols; ++n)
-#pragma unroll
-                    for (int m = 0; m < S::kMmas; ++m)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            s[n][m][e] = place(0, n * S::kMmas + m, e) + place(1, n * S::kMmas + m, e);
-            }
-            // scores in log2, -infinity where there is no token; lv: log2 of their tokens' value scales
-            const uint32_t tok = token(t);
-            const bool all_in = tok + S::kTokens <= (uint32_t)range.end;
-            float lv[S::kMmas][2];
-            bool raise = false;
-#pragma unroll
-            for (int m = 0; m < S::kMmas; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float k = 1.f;
-                    if (S::kE4m3) {
-                        k = __shfl_sync(0xffffffffu, now_ks, 16 * m + 8 * h + g);
-                        lv[m][h] = __shfl_sync(0xffffffffu, now_vs, 16 * m + 8 * h + g);
-                    }
-#pragma unroll
-                    for (int n = 0; n < S::kCols; ++n)
-#pragma unroll
-                        for (int f = 0; f < 2; ++f) {
-                            float& x = s[n][m][2 * h + f];
-                            x *= S::kE4m3 ? k * factor[n][f] : factor[n][f];
-                            if (a.softcap > 0.f) x = a.softcap * kLog2e * tanhf(x);
-                            if (!all_in && tok + 16 * m + 8 * h + g >= (uint32_t)range.end) x = -INFINITY;
-                            raise |= x > st[n][f].m + kSlack;
-                            if (S::kE4m3) raise |= x + lv[m][h] > st[n][f].top + kSlack;
-                        }
-                }
-            if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-                for (int n = 0; n < S::kCols; ++n)
-#pragma unroll
-                    for (int f = 0; f < 2; ++f) {
-                        Stats& r = st[n][f];
-                        float most = r.m, top = r.top;
-#pragma unroll
-                        for (int m = 0; m < S::kMmas; ++m)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                most = fmaxf(most, s[n][m][2 * h + f]);
-                                if (S::kE4m3) top = fmaxf(top, s[n][m][2 * h + f] + lv[m][h]);
-                            }
-#pragma unroll
-                        for (int d = 4; d < 32; d *= 2) {
-                            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-                            if (S::kE4m3) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                        }
-                        float by = Joined::weight(r.m, most);
-                        r.l *= by;
-                        if (S::kE4m3) by = Joined::weight(r.top, top);
-                        r.m = most;
-                        r.top = top;
-#pragma unroll
-                        for (int i = 0; i < S::kOut; ++i) {
-                            w.o[i][n][f] *= by;
-                            w.o[i][n][2 + f] *= by;
-                        }
-                    }
-            }
-#pragma unroll
-            for (int n = 0; n < S::kCols; ++n)
-#pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    const float less = st[n][f].m == -INFINITY ? 0.f : st[n][f].m;
-                    // 2^7 (2^15 with the slack) is the largest numerator in 8 bits: what fp16 loses below 2^-24 is 2^-31 of it
-                    const float top = st[n][f].top == -INFINITY ? -7.f : st[n][f].top - 7.f;
+        for (;; ++at.t, step ^= 1) {
+            const bool last = at.t + 1 == t1;            // the next step's copies then wait: its place takes the item's sums
+            const uint32_t tok = token(at);
+            bad |= (bad_steps >> step) & 1;
+            const char* keys = mine_at + step * S::kStepBytes;
+            if (tok < at.end && a.cache.n_pages > 0) {
+                copies_wait<1>();
+                __syncwarp();
+                float s[S::kCols][S::kMmas][4];
+                Warp<S>::scores(keys, q, s);
+                float ks[S::kMmas][2], lv[S::kMmas][2] = {};       // key scales; log2 of value scales
+                if constexpr (S::kE4m3) {
+                    const float* sc = reinterpret_cast<const float*>(mine_at + 2 * S::kStepBytes + step * S::kScaleBytes);
 #pragma unroll
                     for (int m = 0; m < S::kMmas; ++m)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            float& x = s[n][m][2 * h + f];
-                            const float pr = exp2_fast(x - less);
-                            st[n][f].l += pr;
-                            x = S::kE4m3 ? exp2_fast(x + lv[m][h] - top) : pr;
+                            ks[m][h] = sc[16 * m + 8 * h + g];
+                            lv[m][h] = log2_fast(sc[32 + 16 * m + 8 * h + g]);
                         }
                 }
-            w.accumulate(s);
-            if (t + 1 < t1) w.load_values(vbase, at, a.unit, bytes);
+                if constexpr (S::kSplit > 1) {
+                    // both warps of a team add the two halves in one order
+                    float* const exchange = reinterpret_cast<float*>(smem + kWarps * S::kWarpBytes);
+                    auto place = [&](int of, int i, int e) -> float& {
+                        return exchange[(2 * team + of) * S::kExchangeFloats + ((step * S::kMmas * S::kCols + i) * 4 + e) * 32 + lane];
+                    };
+#pragma unroll
+                    for (int n = 0; n < S::kCols; ++n)
+#pragma unroll
+                        for (int m = 0; m < S::kMmas; ++m)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) place(side, n * S::kMmas + m, e) = s[n][m][e] * unit[n][e % 2];
+                    asm volatile("bar.sync %0, 64;" ::"r"(team + 1) : "memory");
+#pragma unroll
+                    for (int n = 0; n < S::kCols; ++n)
+#pragma unroll
+                        for (int m = 0; m < S::kMmas; ++m)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                s[n][m][e] = place(0, n * S::kMmas + m, e) + place(1, n * S::kMmas + m, e);
+                }
+                // scores in log2, -infinity where there is no token
+                const bool all_in = tok + S::kTokens <= at.end;
+#pragma unroll
+                for (int m = 0; m < S::kMmas; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int n = 0; n < S::kCols; ++n)
+#pragma unroll
+                            for (int f = 0; f < 2; ++f) {
+                                float& x = s[n][m][2 * h + f];
+                                x *= S::kE4m3 ? ks[m][h] * factor[n][f] : factor[n][f];
+                                if (a.softcap > 0.f) x = a.softcap * kLog2e * tanhf(x);
+                                if (!all_in && tok + 16 * m + 8 * h + g >= at.end) x = -INFINITY;
+                            }
+                bool raise = false;
+#pragma unroll
+                for (int n = 0; n < S::kCols; ++n)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        float most = s[n][0][f], top = most + lv[0][0];
+#pragma unroll
+                        for (int i = 1; i < 2 * S::kMmas; ++i) {
+                            most = fmaxf(most, s[n][i / 2][2 * (i % 2) + f]);
+                            if (S::kE4m3) top = fmaxf(top, s[n][i / 2][2 * (i % 2) + f] + lv[i / 2][i % 2]);
+                        }
+                        raise |= most > st[n][f].m + kSlack;
+                        if (S::kE4m3) raise |= top > st[n][f].top + kSlack;
+                    }
+                if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                    for (int n = 0; n < S::kCols; ++n)
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) {
+                            Stats& r = st[n][f];
+                            float most = r.m, top = r.top;
+#pragma unroll
+                            for (int m = 0; m < S::kMmas; ++m)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    most = fmaxf(most, s[n][m][2 * h + f]);
+                                    if (S::kE4m3) top = fmaxf(top, s[n][m][2 * h + f] + lv[m][h]);
+                                }
+#pragma unroll
+                            for (int d = 4; d < 32; d *= 2) {
+                                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+                                if (S::kE4m3) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                            }
+                            float by = Joined::weight(r.m, most);
+                            r.l *= by;
+                            if (S::kE4m3) by = Joined::weight(r.top, top);
+                            r.m = most;
+                            r.top = top;
+#pragma unroll
+                            for (int i = 0; i < S::kOut; ++i) {
+                                w.o[i][n][f] *= by;
+                                w.o[i][n][2 + f] *= by;
+                            }
+                        }
+                }
+#pragma unroll
+                for (int n = 0; n < S::kCols; ++n)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        const float less = st[n][f].m == -INFINITY ? 0.f : st[n][f].m;
+                        // 2^7 (2^15 with the slack) is the largest numerator in 8 bits: what fp16 loses below 2^-24 is
+                        // 2^-31 of it
+                        const float top = st[n][f].top == -INFINITY ? -7.f : st[n][f].top - 7.f;
+#pragma unroll
+                        for (int m = 0; m < S::kMmas; ++m)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float& x = s[n][m][2 * h + f];
+                                const float pr = exp2_fast(x - less);
+                                st[n][f].l += pr;
+                                x = S::kE4m3 ? exp2_fast(x + lv[m][h] - top) : pr;
+                            }
+                    }
+                w.accumulate(keys + S::kKeyBytes, s);
+                __syncwarp();       // the next copies take the place of what was read
+            }
+            if (last) break;
+            copy(step);
         }
         bad = __any_sync(0xffffffffu, bad);
-        if constexpr (S::kSplit > 1) asm volatile("bar.sync %0, 64;" ::"r"(team + 1) : "memory");
 
         // ---- the warps' rows together: m and l of each, then the elements
 #pragma unroll
@@ -605,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
                     sh_l[team][row] = l;
                 }
                 const float by = !S::kE4m3 || r.top == -INFINITY ? 1.f : exp2_fast(r.top - 7.f - r.m);
-                w.stage(smem + team * S::kTeamFloats + (row * S::kSplit + side) * S::kStaged, n, f, by);
+                w.stage(reinterpret_cast<float*>(mine_at + step * S::kStepBytes), n, f, by);
             }
         __syncthreads();
         const bool whole = t0 == 0 && t1 == n_tiles;
@@ -621,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
             if (d == 0) *reinterpret_cast<float2*>(to + 2 * row) = make_float2(r.m, r.l);
             *reinterpret_cast<float4*>(to + 2 * S::kRows + row * S::kD + d) = r.o;
         };
-        for (int i = tid; i < rows * (S::kD / 4); i += kThreads) {
+        for (int i = tid; i < n_rows * (S::kD / 4); i += kThreads) {
             const int row = i / (S::kD / 4), d = i % (S::kD / 4) * 4;
             Joined r{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll
@@ -629,8 +759,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
 #pragma unroll
             for (int k = 0; k < S::kTeams; ++k)
                 r.add(Joined::weight(sh_m[k][row], r.m), sh_l[k][row],
-                      *reinterpret_cast<const float4*>(smem + k * S::kTeamFloats + (row * S::kSplit + d / S::kPart) * S::kStaged +
-                                                       d % S::kPart));
+                      *reinterpret_cast<const float4*>(
+                          reinterpret_cast<const float*>(smem + (k * S::kSplit + d / S::kPart) * S::kWarpBytes +
+                                                         step * S::kStepBytes) +
+                          Warp<S>::staged(row, d % S::kPart)));
             if (whole) write_out(row, d, r);
             else write_part(slot(blockIdx.x, t0 == 0), row, d, r);
         }
@@ -656,14 +788,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
             if (arrive(e0 == c0 ? c0 : kMaxCtas + eight, e1 - e0 + 1)) {
                 const int n = c1 / 8 - c0 / 8 + 1;
                 const bool only = n == 1;
-                for (int i = tid; i < rows * (S::kD / 4); i += kThreads) {
+                for (int i = tid; i < n_rows * (S::kD / 4); i += kThreads) {
                     const int row = i / (S::kD / 4), d = i % (S::kD / 4) * 4;
                     const Joined r = join_parts<S>(e1 - e0 + 1, row, d, [&](int k) { return part_of(e0 + k); });
                     if (only) write_out(row, d, r);
                     else write_part(a.ws + (int64_t)(2 * gridDim.x + 2 * eight + (e0 == c0)) * S::kSlot, row, d, r);
                 }
                 if (!only && arrive(kMaxCtas + kMaxCtas / 8 + c0, n))
-                    for (int i = tid; i < rows * (S::kD / 4); i += kThreads) {
+                    for (int i = tid; i < n_rows * (S::kD / 4); i += kThreads) {
                         const int row = i / (S::kD / 4), d = i % (S::kD / 4) * 4;
                         write_out(row, d, join_parts<S>(n, row, d, [&](int k) {
                             return a.ws + (int64_t)(2 * gridDim.x + 2 * (c0 / 8 + k) + (k == 0)) * S::kSlot;
@@ -672,18 +804,27 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
             }
         }
         __syncthreads();
-        p = min(p1, i1);
+        // the copies that waited, and on to the next item
+        copy(step);
+        step ^= 1;
+        to_do -= t1 - t0;
+        p += t1 - t0;
+        if (to_do > 0) at.next_line(a);
     }
+    copies_wait<0>();
 }
+
 
 // ---------------------------------------------------------------------------------------------------------- host
 // counters of the items' first CTAs and of each eight; of an item's eights, at its first CTA
 constexpr size_t kCounterBytes = LORA_DECODE_COUNTER_BYTES;
 static_assert((2 * kMaxCtas + kMaxCtas / 8) * sizeof(int32_t) <= kCounterBytes, "counters");
 
-// CTAs on an SM: as many as the registers of a lane's pieces and sums leave room for
+// CTAs on an SM: as many as registers and shared memory leave room for
 template <class S>
-constexpr int ctas_of() { return S::kRows > 8 ? 2 : 3; }
+constexpr int ctas_of() {
+    return std::min(S::kRows > 8 ? 2 : 3, 227 * 1024 / (S::kSmem + 2048));
+}
 
 int sm_count() {
     int dev = 0, n = 0;
@@ -697,7 +838,7 @@ auto by_shape(bool e4m3, int D, int rows, Go go) {
     auto with_rows = [&](auto t, auto d) {
         constexpr bool kE4m3 = decltype(t)::value;
         constexpr int kD = decltype(d)::value;
-        return rows <= 8 ? go(Shapes<kE4m3, kD, 8>()) : go(Shapes<kE4m3, kD, 16>());
+                return rows <= 8 ? go(Shapes<kE4m3, kD, 8>()) : go(Shapes<kE4m3, kD, 16>());
     };
     auto with_size = [&](auto t) {
         return D <= 64 ? with_rows(t, std::integral_constant<int, 64>())
@@ -804,9 +945,9 @@ extern "C" int lora_decode_attention(int32_t B, int32_t n_heads, const void* q, 
         return enqueued(fn, by_shape(e4m3, a.D, a.rows, [&](auto shapes) -> cudaError_t {
             using S = decltype(shapes);
             const auto kernel = decode_kernel<S, ctas_of<S>()>;
-            constexpr size_t smem = sizeof(float) * S::kTeams * S::kTeamFloats;
-            static_assert(smem <= 36 * 1024, "static and dynamic shared memory fit 48 KB");
-            return launch_pdl(kernel, dim3((unsigned)launch.grid), dim3(kThreads), smem, st, a);
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+            if (e != cudaSuccess) return e;
+            return launch_pdl(kernel, dim3((unsigned)launch.grid), dim3(kThreads), S::kSmem, st, a);
         }));
     });
 }

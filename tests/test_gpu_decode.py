@@ -234,7 +234,7 @@ def test_repeated_calls_and_streams():
     ws = torch.zeros(lm.decode_workspace_size(32, c.cache), dtype=torch.uint8, device="cuda")
     for _ in range(3):
         assert all(torch.equal(a, b) for a, b in zip(first, c.run(workspace=ws)))
-    assert (ws[:8192] == 0).all()
+    assert (ws[:lm.DECODE_COUNTER_BYTES] == 0).all()
     small = torch.zeros(lm.decode_workspace_size(32, c.cache) - 1, dtype=torch.uint8, device="cuda")
     with pytest.raises(lm.LoraError, match="workspace"):
         c.run(workspace=small)
