@@ -175,7 +175,7 @@ struct Warp {
 #pragma unroll
         for (int k = 0; k < S::kKeyBytes / 512; ++k) {
             const uint32_t at = __shfl_sync(0xffffffffu, rows, k * (32 / kAcross) + row0);
-            const char* from = in ? keys + (uint64_t)at * unit + 16 * col : keys;
+            const char* from = keys + (uint64_t)(in ? at : 0) * unit + 16 * col;      // not read where !in
             copy_async<16>(to + 512 * k + at_k, from, in);
             const int turn = kAcross >= 8 ? k * (32 / kAcross) & 6 : 0;
             copy_async<16>(to + S::kKeyBytes + 512 * k + (at_v ^ (16 * turn)), from + to_values, in);
@@ -319,17 +319,28 @@ struct Query {
     uint32_t reg[S::kCols][S::kPart / 8];
     float unit[S::kCols];    // what a product of query 8 n + g has to be multiplied by
 
-    // row: a query head's elements from this warp's first one on, of which `left` are there
-    __device__ __forceinline__ void load_row(const __nv_bfloat16* row, bool in, int left, uint32_t* to, float* unit_) {
-        const int c = threadIdx.x % 4;
-        constexpr int kPieces = S::kPart / 32;
-        uint4 w[kPieces];
+    // the rows as they are, from this warp's first element on; then the operands
+    uint4 raw[S::kCols][S::kPart / 32];
+    __device__ __forceinline__ void fetch(const Decode& a, int b, int head0, int rows, int first) {
+        const int g = threadIdx.x % 32 / 4, c = threadIdx.x % 4;
+        const __nv_bfloat16* q = a.q + b * a.ld_q + (int64_t)head0 * a.D + first;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            // 8-bit keys: a lane's 16 elements are two of these pieces
-            const int at = S::kE4m3 ? 64 * (i / 2) + 16 * c + 8 * (i % 2) : 32 * i + 8 * c;
-            w[i] = in && at < left ? *reinterpret_cast<const uint4*>(row + at) : make_uint4(0, 0, 0, 0);
-        }
+        for (int n = 0; n < S::kCols; ++n)
+#pragma unroll
+            for (int i = 0; i < S::kPart / 32; ++i) {
+                // 8-bit keys: a lane's 16 elements are two of these pieces
+                const int at = S::kE4m3 ? 64 * (i / 2) + 16 * c + 8 * (i % 2) : 32 * i + 8 * c;
+                raw[n][i] = g + 8 * n < rows && at < a.D - first
+                                ? *reinterpret_cast<const uint4*>(q + (g + 8 * n) * a.D + at)
+                                : make_uint4(0, 0, 0, 0);
+            }
+    }
+    __device__ __forceinline__ void convert() {
+#pragma unroll
+        for (int n = 0; n < S::kCols; ++n) convert_row(raw[n], reg[n], &unit[n]);
+    }
+    __device__ __forceinline__ void convert_row(const uint4 (&w)[S::kPart / 32], uint32_t* to, float* unit_) {
+        constexpr int kPieces = S::kPart / 32;
         float inv = 1.f;
         *unit_ = 1.f;
         if constexpr (S::kE4m3) {
@@ -370,12 +381,6 @@ struct Query {
                 to[4 * i + 3] = w[i].w;
             }
         }
-    }
-    __device__ __forceinline__ void load(const Decode& a, int b, int head0, int rows, int first) {
-        const int g = threadIdx.x % 32 / 4;
-        const __nv_bfloat16* q = a.q + b * a.ld_q + (int64_t)head0 * a.D + first;
-#pragma unroll
-        for (int n = 0; n < S::kCols; ++n) load_row(q + (g + 8 * n) * a.D, g + 8 * n < rows, a.D - first, reg[n], &unit[n]);
     }
 };
 
@@ -515,8 +520,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
     Cursor<S> at;
     at.b = sh_seq;
     at.enter(a);
-    at.line = (int)((p0 - sh_before) / at.n_tiles);
-    at.t = (int)((p0 - sh_before) % at.n_tiles);
+    at.line = (int)quotient(p0 - sh_before, at.n_tiles);
+    at.t = (int)(p0 - sh_before - (int64_t)at.line * at.n_tiles);
     Cursor<S> ahead = at;
     int64_t to_copy = p1 - p0, to_do = p1 - p0;
     int32_t page = 0;
@@ -559,6 +564,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
     copy(0);
     copy(1);
 
+    Query<S> q;
+    auto fetch_queries = [&]() {
+        const int kv = at.line / a.parts, part = at.line % a.parts;
+        q.fetch(a, at.b, kv * a.group + part * a.rows, min(a.rows, a.group - part * a.rows), first);
+    };
+    fetch_queries();
     int step = 0;
     int64_t p = p0;
     while (to_do > 0) {
@@ -568,7 +579,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
         const int kv = at.line / a.parts, part = at.line % a.parts;
         const int head0 = kv * a.group + part * a.rows, n_rows = min(a.rows, a.group - part * a.rows);
         Warp<S> w;
-        Query<S> q;
         Stats st[S::kCols][2];       // of queries 8 n + 2 c + f
 #pragma unroll
         for (int n = 0; n < S::kCols; ++n)
@@ -581,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w.o[t][n][e] = 0.f;
         bool bad = at.poisoned;
-        q.load(a, b, head0, n_rows, first);
+        q.convert();
         // what a score is multiplied by: its query's unit, the scale, and the change to powers of two
         float factor[S::kCols][2], unit[S::kCols][2];
 #pragma unroll
@@ -634,7 +644,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
                                 s[n][m][e] = place(0, n * S::kMmas + m, e) + place(1, n * S::kMmas + m, e);
                 }
                 // scores in log2, -infinity where there is no token
-                const bool all_in = tok + S::kTokens <= at.end;
 #pragma unroll
                 for (int m = 0; m < S::kMmas; ++m)
 #pragma unroll
@@ -645,9 +654,24 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
                             for (int f = 0; f < 2; ++f) {
                                 float& x = s[n][m][2 * h + f];
                                 x *= S::kE4m3 ? ks[m][h] * factor[n][f] : factor[n][f];
-                                if (a.softcap > 0.f) x = a.softcap * kLog2e * tanhf(x);
-                                if (!all_in && tok + 16 * m + 8 * h + g >= at.end) x = -INFINITY;
                             }
+                if (a.softcap > 0.f) {
+#pragma unroll
+                    for (int n = 0; n < S::kCols; ++n)
+#pragma unroll
+                        for (int m = 0; m < S::kMmas; ++m)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) s[n][m][e] = a.softcap * kLog2e * tanhf(s[n][m][e]);
+                }
+                if (tok + S::kTokens > at.end) {
+#pragma unroll
+                    for (int n = 0; n < S::kCols; ++n)
+#pragma unroll
+                        for (int m = 0; m < S::kMmas; ++m)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (tok + 16 * m + 8 * (e / 2) + g >= at.end) s[n][m][e] = -INFINITY;
+                }
                 bool raise = false;
 #pragma unroll
                 for (int n = 0; n < S::kCols; ++n)
@@ -737,6 +761,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
                 const float by = !S::kE4m3 || r.top == -INFINITY ? 1.f : exp2_fast(r.top - 7.f - r.m);
                 w.stage(reinterpret_cast<float*>(mine_at + step * S::kStepBytes), n, f, by);
             }
+        to_do -= t1 - t0;
+        p += t1 - t0;
+        if (to_do > 0) {             // the next item's queries come while this one is joined
+            at.next_line(a);
+            fetch_queries();
+        }
         __syncthreads();
         const bool whole = t0 == 0 && t1 == n_tiles;
         auto slot = [&](int cta, bool begins) { return a.ws + (int64_t)(2 * cta + (begins ? 1 : 0)) * S::kSlot; };
@@ -772,16 +802,19 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
             const int c0 = (int)all.owner(i0), c1 = (int)all.owner(i1 - 1), eight = blockIdx.x / 8;
             const int e0 = max(c0, 8 * eight), e1 = min(c1, 8 * eight + 7);
             auto part_of = [&](int cta) { return slot(cta, cta == c0); };
+            // the barriers order the CTA's writes before its one thread's release, and its acquire before the CTA's reads
             auto arrive = [&](int counter, int expected) -> bool {
-                __threadfence();
                 __syncthreads();
                 if (tid == 0) {
-                    const bool last = atomicAdd(a.counters + counter, 1) == expected - 1;
-                    if (last) a.counters[counter] = 0;
-                    sh_last = last;
+                    int before;
+                    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
+                                 : "=r"(before)
+                                 : "l"(a.counters + counter)
+                                 : "memory");
+                    if (before == expected - 1) a.counters[counter] = 0;
+                    sh_last = before == expected - 1;
                 }
                 __syncthreads();
-                if (sh_last) __threadfence();
                 return sh_last;
             };
             // the first eight of an item count at its first CTA, the others, which begin with it, at their own number
@@ -807,9 +840,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
         // the copies that waited, and on to the next item
         copy(step);
         step ^= 1;
-        to_do -= t1 - t0;
-        p += t1 - t0;
-        if (to_do > 0) at.next_line(a);
     }
     copies_wait<0>();
 }
