@@ -66,14 +66,6 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-// c += a b for e4m3 operands, m16n8k32: half the time of the fp16 form for twice the sum
-__device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                     uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 // An asynchronous copy of kBytes to shared memory; where `in` is false, zeros
 template <int kBytes>
 __device__ __forceinline__ void copy_async(uint32_t to, const void* from, bool in) {
@@ -96,10 +88,11 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-// two e4m3 codes (the low 16 bits) as fp16, exactly
-__device__ __forceinline__ uint32_t codes_to_half(uint32_t q) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)q, __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// four e4m3 codes as two pairs of fp16, exactly
+__device__ __forceinline__ void codes_to_half(uint32_t q, uint32_t& low, uint32_t& high) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(low), "=r"(high)
+        : "r"(q));
 }
 
 struct Decode {
@@ -204,41 +197,28 @@ struct Warp {
             for (int m = 0; m < S::kMmas; ++m)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[n][m][e] = 0.f;
-        float rest[S::kE4m3 ? S::kCols : 1][S::kMmas][4];
-        if constexpr (S::kE4m3)
-#pragma unroll
-            for (int n = 0; n < S::kCols; ++n)
-#pragma unroll
-                for (int m = 0; m < S::kMmas; ++m)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) rest[n][m][e] = 0.f;
 #pragma unroll
         for (int i = 0; i < S::kKeyLoads; ++i)
 #pragma unroll
             for (int m = 0; m < S::kMmas; ++m) {
                 const uint4 x = key(keys, 2 * m, i), y = key(keys, 2 * m + 1, i);
+                const uint32_t u[4] = {x.x, x.y, x.z, x.w}, w[4] = {y.x, y.y, y.z, y.w};
+                constexpr int kSums = S::kE4m3 ? 4 : 2;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t a0 = k ? x.z : x.x, a1 = k ? y.z : y.x, a2 = k ? x.w : x.y, a3 = k ? y.w : y.y;
-                    const int at = 4 * i + 2 * k;
-#pragma unroll
-                    for (int n = 0; n < S::kCols; ++n) {
-                        if constexpr (S::kE4m3) {
-                            mma8(s[n][m], a0, a1, a2, a3, q.reg[n][at], q.reg[n][at + 1]);
-                            mma8(rest[n][m], a0, a1, a2, a3, q.reg[n][S::kPart / 16 + at], q.reg[n][S::kPart / 16 + at + 1]);
-                        } else {
-                            mma<false>(s[n][m], a0, a1, a2, a3, q.reg[n][at], q.reg[n][at + 1]);
-                        }
+                for (int k = 0; k < kSums; ++k) {
+                    uint32_t v[4];
+                    if constexpr (S::kE4m3) {
+                        codes_to_half(u[k], v[0], v[2]);
+                        codes_to_half(w[k], v[1], v[3]);
+                    } else {
+                        v[0] = u[2 * k]; v[1] = w[2 * k]; v[2] = u[2 * k + 1]; v[3] = w[2 * k + 1];
                     }
+                    const int at = 2 * (i * kSums + k);
+#pragma unroll
+                    for (int n = 0; n < S::kCols; ++n)
+                        mma<S::kE4m3>(s[n][m], v[0], v[1], v[2], v[3], q.reg[n][at], q.reg[n][at + 1]);
                 }
             }
-        if constexpr (S::kE4m3)
-#pragma unroll
-            for (int n = 0; n < S::kCols; ++n)
-#pragma unroll
-                for (int m = 0; m < S::kMmas; ++m)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[n][m][e] = fmaf(rest[n][m][e], 0x1p-4f, s[n][m][e]);
     }
     // o += v p, p as scores gives them.  With bf16 values a probability goes in as a number of 8 bits and one for the rest
     // of it: 8 bits alone would double the square of what rounding the output costs.  With 8-bit values the MMAs take
@@ -278,8 +258,7 @@ struct Warp {
                     for (int h = 0; h < 2; ++h) {
                         if constexpr (S::kE4m3) {
                             const uint32_t z = __byte_perm(v[2 * h][e / 2], v[2 * h + 1][e / 2], e % 2 ? 0x7362 : 0x5140);
-                            a[2 * h] = codes_to_half(z);
-                            a[2 * h + 1] = codes_to_half(z >> 16);
+                            codes_to_half(z, a[2 * h], a[2 * h + 1]);
                         } else {
                             a[2 * h] = __byte_perm(v[2 * h][e], v[2 * h + 1][e], 0x5410);
                             a[2 * h + 1] = __byte_perm(v[2 * h][e], v[2 * h + 1][e], 0x7632);
@@ -310,10 +289,10 @@ struct Warp {
     }
 };
 
-// A group's queries as B operands, in the order of elements that Warp::scores takes.  8-bit caches: as e4m3 codes, like the
-// keys, so that these need no change: a query of 8 bits is an e4m3 number of 4 bits and 2^-4 times one for the
-// 4 that are left.  They are scaled by a power of two that brings the largest element to between 2^7 and 2^8: what is rounded lies
-// below 2^-14, which is 2^-21 of that element.
+// A group's queries as B operands, in the order of elements that Warp::scores takes; 8-bit caches: as fp16, scaled by a
+// power of two that brings the largest element to between 2^14 and 2^15, so that what bf16 holds stays exact down to 2^-31
+// of it.  (The MMAs that take e4m3 convert to fp16 themselves, and again for each call: queries split into two e4m3 numbers
+// took 135 us instead of @ for 256 x 2048 tokens.)
 template <class S>
 struct Query {
     uint32_t reg[S::kCols][S::kPart / 8];
@@ -353,33 +332,18 @@ struct Query {
             }
             a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
             a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-            const int e = min(max((int)(a >> 23) - 127, -118), 127);
-            inv = a >= 0x7F800000u ? NAN : __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-            *unit_ = a >= 0x7F800000u ? NAN : __uint_as_float((uint32_t)(127 - 7 + e) << 23);
+            const int e = min(max((int)(a >> 23) - 127, -112), 127);
+            inv = a >= 0x7F800000u ? NAN : __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+            *unit_ = a >= 0x7F800000u ? NAN : __uint_as_float((uint32_t)(127 - 14 + e) << 23);
         }
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-            if constexpr (S::kE4m3) {
-                Row8Bf16 r;
-                float v[8];
-                r.q = w[i];
-                r.get(v);
-                const uint2 hi = encode8(v, inv);
-                float back[8];
-                decode8(hi, 1.f, back);
+            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = (v[k] * inv - back[k]) * 16.f;
-                const uint2 lo = encode8(v, 1.f);
-                to[2 * i] = hi.x;
-                to[2 * i + 1] = hi.y;
-                to[S::kPart / 16 + 2 * i] = lo.x;
-                to[S::kPart / 16 + 2 * i + 1] = lo.y;
-            } else {
-                to[4 * i] = w[i].x;
-                to[4 * i + 1] = w[i].y;
-                to[4 * i + 2] = w[i].z;
-                to[4 * i + 3] = w[i].w;
-            }
+            for (int k = 0; k < 4; ++k)
+                to[4 * i + k] = S::kE4m3
+                                    ? pack_half(__uint_as_float(u[k] << 16) * inv, __uint_as_float(u[k] & 0xFFFF0000u) * inv)
+                                    : u[k];
         }
     }
 };
