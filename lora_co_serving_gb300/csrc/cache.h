@@ -7,6 +7,7 @@
 
 #include <string>
 
+#include "decode_split.h"
 #include "fp8.h"
 #include "lora_attention.h"
 
@@ -23,15 +24,14 @@ struct CacheView {
     int64_t s_page, s_head, s_row;
     int64_t slots;           // n_pages * page_size
     int32_t n_pages, page_size;
+    PageDivision pages;
 };
 
 // Where a slot's row lies in head 0, in bytes and in scales; the slot is inside the cache
 struct RowPlace {
     int64_t row, scale;
     __device__ __forceinline__ RowPlace(const CacheView& c, int64_t slot) {
-        int64_t page;
-        if ((slot >> 32) == 0) page = (uint32_t)slot / (uint32_t)c.page_size;
-        else page = slot / c.page_size;
+        const int64_t page = (slot >> 31) == 0 ? (int64_t)c.pages.page_of((uint32_t)slot) : slot / c.page_size;
         const int64_t r = slot - page * c.page_size;
         row = page * c.page_stride + r * c.row_stride;
         scale = page * c.s_page + r * c.s_row;
@@ -75,6 +75,7 @@ inline int check_cache(const char* fn, const lora_cache_t* c, CacheView* out) {
     out->n_pages = c->n_pages;
     out->page_size = c->page_size;
     out->slots = (int64_t)c->n_pages * c->page_size;
+    out->pages = page_division((uint32_t)c->page_size);
     return LORA_OK;
 }
 

@@ -109,7 +109,6 @@ struct Decode {
     int32_t group;           // query heads of a cache head
     int32_t parts, rows;     // a group is taken in `parts` of up to `rows` (<= 8 or 16) query heads
     int32_t table_width, window;
-    PageDivision pages;
     uint32_t unit, page_units, row_units;      // bytes that divide the cache's strides; the strides in these units
     float scale, softcap;
     int32_t* counters;
@@ -495,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
     // range adds nothing.
     auto my_token = [&](const Cursor<S>& x) { return min(token(x) + lane % S::kTokens, x.end - 1); };
     auto read_page = [&]() {
-        if (to_copy > 0) page = a.table[ahead.b * a.ld_table + a.pages.page_of(my_token(ahead))];
+        if (to_copy > 0) page = a.table[ahead.b * a.ld_table + a.cache.pages.page_of(my_token(ahead))];
     };
     auto copy = [&](int step) {
         if (to_copy > 0) {
@@ -506,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
             if (token(ahead) < ahead.end && a.cache.n_pages > 0) {
                 const int kv = ahead.line / a.parts;
                 const uint32_t tok = my_token(ahead);
-                const uint32_t row = tok - a.pages.page_of(tok) * (uint32_t)a.cache.page_size;
+                const uint32_t row = tok - a.cache.pages.page_of(tok) * (uint32_t)a.cache.page_size;
                 Warp<S>::copy(mine_u32 + step * S::kStepBytes,
                               a.cache.k + kv * a.cache.head_stride + first * (S::kE4m3 ? 1 : 2), a.cache.v - a.cache.k,
                               (uint32_t)page * a.page_units + row * a.row_units, a.unit, bytes);
@@ -922,7 +921,6 @@ extern "C" int lora_decode_attention(int32_t B, int32_t n_heads, const void* q, 
         a.rows = rows_of(a.group);
         a.parts = (a.group + a.rows - 1) / a.rows;
         a.window = window; a.scale = scale; a.softcap = softcap;
-        a.pages = page_division((uint32_t)cache->page_size);
         // rows are found by 32-bit numbers of the largest unit that divides both strides
         a.unit = 16;
         while (a.unit < (1u << 30) && (a.cache.page_stride | a.cache.row_stride) % (2ll * a.unit) == 0) a.unit *= 2;

@@ -1,11 +1,13 @@
 // rotary.cu -- norm and rotary positions of query and key heads, forward and backward, and rows of the paged cache
 // (include/lora_attention.h).
 //
-// Every kernel here moves each byte once and computes little per byte: the memory rate bounds them.  A head's row of D
-// elements belongs to D / 16 neighbouring lanes (of the next power of two, at least four), 16 elements each: two pieces of 8.  Where the
-// row is turned in halves, a lane's two pieces are the two members of its 8 pairs, so the rotation stays in the lane; a
-// row's sum of squares, or its largest magnitude, is at most four shuffles away.  The angles of a CTA's rows are
-// computed once, by all its threads, into shared memory, while the rows are on their way: their heads share them.
+// Every kernel here moves each byte once and computes little per byte: the memory rate bounds them, if the instructions
+// do not.  A head's row of D elements belongs to D / 16 neighbouring lanes (of the next power of two, at least four), 16
+// elements each: two pieces of 8.  Where the row is turned in halves, a lane's two pieces are the two members of its 8
+// pairs, so the rotation stays in the lane; a row's sum of squares, or its largest magnitude, is at most four shuffles
+// away.  A lane keeps its head and takes several rows of it, so that what depends on the head (its weights, where it lies)
+// is found once: numbering (row, head) units instead took twice the instructions and 61 us for 8192 rows of 72 heads, @ now.
+// The angles of a CTA's rows are computed once, by all its threads, into shared memory, while the rows are on their way.
 #include <algorithm>
 #include <type_traits>
 
@@ -15,7 +17,25 @@
 namespace lora {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kMaxThreads = 256;
+
+// How a CTA's warps lie over heads and rows: `across` warps take neighbouring heads, `down` of such rows of warps take
+// neighbouring rows of the matrix.  A lane takes kRows rows, `down` apart.
+struct Shape {
+    int32_t across, down;
+};
+template <int kLanes, int kRows>
+struct Spot {
+    int lane, head, row;         // lane within the head; head; first of the lane's rows in the CTA
+    int64_t t0;                  // the CTA's first row
+    __device__ __forceinline__ Spot(const Shape& s, int64_t block) {
+        const int warp = threadIdx.x / 32;
+        lane = threadIdx.x % kLanes;
+        head = ((int)blockIdx.y * s.across + warp % s.across) * (32 / kLanes) + threadIdx.x % 32 / kLanes;
+        row = warp / s.across;
+        t0 = block * (int64_t)(s.down * kRows);
+    }
+};
 
 struct Turns {
     const int64_t* positions;
@@ -43,7 +63,7 @@ struct Angles {
     __device__ __forceinline__ Angles(const Turns& a, float* smem, int n_rows)
         : cos_(smem), sin_(smem + n_rows * (a.rot / 2)), half(a.rot / 2) {}
     __device__ __forceinline__ void fill(const Turns& a, int64_t t0, int n_rows, int64_t T) {
-        for (int i = threadIdx.x; i < n_rows * half; i += kThreads) {
+        for (int i = threadIdx.x; i < n_rows * half; i += (int)blockDim.x) {
             const int64_t t = t0 + i / half;
             if (t >= T) break;
             const float2 v = cos_sin((uint64_t)a.positions[t] * (uint64_t)a.turns[i % half]);
@@ -113,7 +133,7 @@ __device__ __forceinline__ uint32_t max_over_lanes(uint32_t v) {
 }
 
 // ------------------------------------------------------------------------------------------------------- forward
-// A unit is a head of a row: query heads, key heads, and with a cache the value heads.
+// Heads are query heads, key heads, and with a cache the value heads.
 struct Forward {
     const void* x;
     int64_t ld_x;
@@ -126,93 +146,102 @@ struct Forward {
     Turns turns;
     CacheView cache;
     int64_t T;
-    int32_t hq, hk, heads;   // query heads, key heads, units of a row
+    Shape shape;
+    int32_t hq, hk, heads;   // query heads, key heads, all
     int32_t out_heads;       // the first of them that go to out
-    int32_t D, max_rows;     // rows that a CTA's units may lie in
+    int32_t D;
     float eps, inv_d;
 };
 
-template <class Row8, int kLanes, int kUnits, int kCache /* -1: none */>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const Forward a) {
+template <class Row8, int kLanes, int kRows, int kCache /* -1: none */>
+__global__ void __launch_bounds__(kMaxThreads) rotary_kernel(const Forward a) {
     extern __shared__ __align__(16) float smem[];
     grid_dep_launch();
     grid_dep_wait();
-    constexpr int kGroups = kThreads / kLanes;
-    const int lane = threadIdx.x % kLanes;
-    const LanePieces p(lane, a.D, a.turns);
-    const int64_t u0 = (int64_t)blockIdx.x * (kGroups * kUnits);
-    const int64_t t0 = u0 / a.heads;
-    const int first = (int)(u0 - t0 * a.heads) + threadIdx.x / kLanes;      // unit of row t0
-    Row8 r[kUnits][2];
+    const Spot<kLanes, kRows> at(a.shape, blockIdx.x);
+    const LanePieces p(at.lane, a.D, a.turns);
+    const bool key = at.head >= a.hq, value = at.head >= a.hq + a.hk, in = p.in && at.head < a.heads;
+    const void* from = value ? a.v : a.x;
+    const int64_t ld = value ? a.ld_v : a.ld_x;
+    const int64_t head_at = (int64_t)(value ? at.head - a.hq - a.hk : at.head) * a.D;
+    Row8 r[kRows][2], w[2];
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-        const int u = first + k * kGroups;
-        const int64_t t = t0 + u / a.heads;
-        const int h = u % a.heads;
+    for (int k = 0; k < kRows; ++k) {
+        const int64_t t = at.t0 + at.row + k * a.shape.down;
         r[k][0].zero();
         r[k][1].zero();
-        if (t < a.T && p.in) {
-            const bool value = h >= a.hq + a.hk;
-            const void* from = value ? a.v : a.x;
-            const int64_t at = value ? t * a.ld_v + (int64_t)(h - a.hq - a.hk) * a.D : t * a.ld_x + (int64_t)h * a.D;
-            r[k][0].load(from, at + p.at0);
-            r[k][1].load(from, at + p.at1);
+        if (in && t < a.T) {
+            r[k][0].load(from, t * ld + head_at + p.at0);
+            r[k][1].load(from, t * ld + head_at + p.at1);
         }
     }
-    Angles angles(a.turns, smem, a.max_rows);
+    const void* weight = value ? nullptr : key ? a.wk : a.wq;
+    w[0].zero();
+    w[1].zero();
+    if (weight && in) {
+        w[0].load(weight, p.at0);
+        w[1].load(weight, p.at1);
+    }
+    Angles angles(a.turns, smem, a.shape.down * kRows);
     if (a.turns.rot) {
-        angles.fill(a.turns, t0, a.max_rows, a.T);
+        angles.fill(a.turns, at.t0, a.shape.down * kRows, a.T);
         __syncthreads();
     }
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-        const int u = first + k * kGroups;
-        const int row = u / a.heads, h = u % a.heads;
-        const int64_t t = t0 + row;
-        float y[8], z[8];
+    for (int k = 0; k < kRows; ++k) {
+        const int row = at.row + k * a.shape.down;
+        const int64_t t = at.t0 + row;
+        float y[8], z[8], f = 1.f;
         r[k][0].get(y);
         r[k][1].get(z);
-        const bool key = h >= a.hq, value = h >= a.hq + a.hk;
-        const void* w = value ? nullptr : key ? a.wk : a.wq;
-        float ss = 0.f;
         if (a.wq || a.wk) {
+            float ss = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], fmaf(z[i], z[i], ss));
             ss = sum_over_lanes<kLanes>(ss);
-        }
-        if (w && p.in) {
-            const float f = rsqrtf(ss * a.inv_d + a.eps);
-            Row8 w0, w1;
-            float g[8];
-            w0.load(w, p.at0);
-            w1.load(w, p.at1);
-            w0.get(g);
+            if (weight) {
+                f = rsqrtf(ss * a.inv_d + a.eps);
+                float g[8];
+                w[0].get(g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] *= f * g[i];
-            w1.get(g);
+                for (int i = 0; i < 8; ++i) y[i] *= g[i];
+                w[1].get(g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] *= f * g[i];
+                for (int i = 0; i < 8; ++i) z[i] *= g[i];
+            }
         }
         if (p.turned && !value && t < a.T) {
             float c[8], s[8];
-            angles.get(row, lane, c, s);
+            angles.get(row, at.lane, c, s);
+            if (weight) {            // the row's factor goes into its angles' cosines and sines
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    c[i] *= f;
+                    s[i] *= f;
+                }
+            }
             turn(y, z, c, s, a.turns.interleaved);
+        } else if (weight) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                y[i] *= f;
+                z[i] *= f;
+            }
         }
-        const bool in = p.in && t < a.T;
-        if (in && h < a.out_heads) {
-            const int64_t at = t * a.ld_out + (int64_t)h * a.D;
-            Row8::store(a.out, at + p.at0, y);
-            Row8::store(a.out, at + p.at1, z);
+        const bool here = in && t < a.T;
+        if (here && at.head < a.out_heads) {
+            Row8::store(a.out, t * a.ld_out + head_at + p.at0, y);
+            Row8::store(a.out, t * a.ld_out + head_at + p.at1, z);
         }
         if (kCache < 0) continue;
         uint32_t amax = 0;
         if (kCache == LORA_CACHE_E4M3) amax = max_over_lanes<kLanes>(max(abs_bits_max(y), abs_bits_max(z)));
-        if (!in || !key) continue;
+        if (!here || !key) continue;
         const int64_t slot = a.slots[t];
         if (slot < 0 || slot >= a.cache.slots) continue;
-        const RowPlace at(a.cache, slot);
-        const int head = h - a.hq - (value ? a.hk : 0);
-        char* to = (value ? a.cache.v : a.cache.k) + at.row + head * a.cache.head_stride;
+        const RowPlace place(a.cache, slot);
+        const int head = at.head - a.hq - (value ? a.hk : 0);
+        char* to = (value ? a.cache.v : a.cache.k) + place.row + head * a.cache.head_stride;
         if (kCache == LORA_CACHE_BF16) {
             Row8Bf16::store(to, p.at0, y);
             Row8Bf16::store(to, p.at1, z);
@@ -221,7 +250,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const Forward a) {
             const float sc = block_scale(amax, &inv);
             *reinterpret_cast<uint2*>(to + p.at0) = encode8(y, inv);
             *reinterpret_cast<uint2*>(to + p.at1) = encode8(z, inv);
-            if (lane == 0) (value ? a.cache.vs : a.cache.ks)[at.scale + head * a.cache.s_head] = sc;
+            if (at.lane == 0) (value ? a.cache.vs : a.cache.ks)[place.scale + head * a.cache.s_head] = sc;
         }
     }
 }
@@ -237,53 +266,57 @@ struct Backward {
     const void *wq, *wk;
     float* parts;            // [CTAs, 2, D]: each CTA's sums of the weights' gradients; null: not wanted
     Turns turns;
-    int64_t T, n_chunks;     // units are taken kGroups * kUnits at a time
-    int32_t hq, heads, D, max_rows;
+    int64_t T, n_blocks;     // rows are taken shape.down * kRows at a time
+    Shape shape;
+    int32_t hq, heads, D;
     float eps, inv_d;
 };
 
-template <class Row8, int kLanes, int kUnits, bool kNorm, bool kWeights>
-__global__ void __launch_bounds__(kThreads) rotary_backward_kernel(const Backward a) {
+template <class Row8, int kLanes, int kRows, bool kNorm, bool kWeights>
+__global__ void __launch_bounds__(kMaxThreads) rotary_backward_kernel(const Backward a) {
     extern __shared__ __align__(16) float smem[];
     grid_dep_launch();
     grid_dep_wait();
-    constexpr int kGroups = kThreads / kLanes;
     const int lane = threadIdx.x % kLanes;
     const LanePieces p(lane, a.D, a.turns);
-    Angles angles(a.turns, smem, a.max_rows);
-    float sum[kWeights ? 2 : 1][16] = {};
-    for (int64_t chunk = blockIdx.x; chunk < a.n_chunks; chunk += gridDim.x) {
-        const int64_t u0 = chunk * (kGroups * kUnits);
-        const int64_t t0 = u0 / a.heads;
-        const int first = (int)(u0 - t0 * a.heads) + threadIdx.x / kLanes;
-        Row8 r[kUnits][2], d[kUnits][2];
+    const Spot<kLanes, kRows> spot(a.shape, 0);
+    const bool key = spot.head >= a.hq, in = p.in && spot.head < a.heads;
+    const int64_t head_at = (int64_t)spot.head * a.D;
+    const void* weight = key ? a.wk : a.wq;
+    Row8 w[2];
+    if (kNorm && weight && in) {
+        w[0].load(weight, p.at0);
+        w[1].load(weight, p.at1);
+    }
+    Angles angles(a.turns, smem, a.shape.down * kRows);
+    float sum[kWeights ? 16 : 1] = {};
+    for (int64_t block = blockIdx.x; block < a.n_blocks; block += gridDim.x) {
+        const int64_t t0 = block * (int64_t)(a.shape.down * kRows);
+        Row8 r[kRows][2], d[kRows][2];
 #pragma unroll
-        for (int k = 0; k < kUnits; ++k) {
-            const int u = first + k * kGroups;
-            const int64_t t = t0 + u / a.heads;
-            const int64_t h = u % a.heads;
+        for (int k = 0; k < kRows; ++k) {
+            const int64_t t = t0 + spot.row + k * a.shape.down;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 r[k][i].zero();
                 d[k][i].zero();
             }
-            if (t < a.T && p.in) {
-                d[k][0].load(a.dout, t * a.ld_dout + h * a.D + p.at0);
-                d[k][1].load(a.dout, t * a.ld_dout + h * a.D + p.at1);
+            if (in && t < a.T) {
+                d[k][0].load(a.dout, t * a.ld_dout + head_at + p.at0);
+                d[k][1].load(a.dout, t * a.ld_dout + head_at + p.at1);
                 if (kNorm) {
-                    r[k][0].load(a.x, t * a.ld_x + h * a.D + p.at0);
-                    r[k][1].load(a.x, t * a.ld_x + h * a.D + p.at1);
+                    r[k][0].load(a.x, t * a.ld_x + head_at + p.at0);
+                    r[k][1].load(a.x, t * a.ld_x + head_at + p.at1);
                 }
             }
         }
         if (a.turns.rot) {
-            angles.fill(a.turns, t0, a.max_rows, a.T);
+            angles.fill(a.turns, t0, a.shape.down * kRows, a.T);
             __syncthreads();
         }
 #pragma unroll
-        for (int k = 0; k < kUnits; ++k) {
-            const int u = first + k * kGroups;
-            const int row = u / a.heads, h = u % a.heads;
+        for (int k = 0; k < kRows; ++k) {
+            const int row = spot.row + k * a.shape.down;
             const int64_t t = t0 + row;
             float y[8], z[8];
             d[k][0].get(y);
@@ -299,8 +332,6 @@ __global__ void __launch_bounds__(kThreads) rotary_backward_kernel(const Backwar
                 float v[8], x[8];
                 r[k][0].get(v);
                 r[k][1].get(x);
-                const bool key = h >= a.hq;
-                const void* w = key ? a.wk : a.wq;
                 float ss = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], fmaf(x[i], x[i], ss));
@@ -310,29 +341,22 @@ __global__ void __launch_bounds__(kThreads) rotary_backward_kernel(const Backwar
                     v[i] *= f;
                     x[i] *= f;
                 }
-                if (kWeights) {
+                if constexpr (kWeights)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float g0 = y[i] * v[i], g1 = z[i] * x[i];
-                        sum[0][i] += key ? 0.f : g0;
-                        sum[0][8 + i] += key ? 0.f : g1;
-                        sum[1][i] += key ? g0 : 0.f;
-                        sum[1][8 + i] += key ? g1 : 0.f;
+                        sum[i] = fmaf(y[i], v[i], sum[i]);
+                        sum[8 + i] = fmaf(z[i], x[i], sum[8 + i]);
                     }
-                }
                 float along = 0.f;
-                if (w && p.in) {
-                    Row8 w0, w1;
+                if (weight && in) {
                     float g[8];
-                    w0.load(w, p.at0);
-                    w1.load(w, p.at1);
-                    w0.get(g);
+                    w[0].get(g);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         y[i] *= g[i];
                         along = fmaf(y[i], v[i], along);
                     }
-                    w1.get(g);
+                    w[1].get(g);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         z[i] *= g[i];
@@ -340,44 +364,41 @@ __global__ void __launch_bounds__(kThreads) rotary_backward_kernel(const Backwar
                     }
                 }
                 along = sum_over_lanes<kLanes>(along) * a.inv_d;
-                if (w) {
+                if (weight) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        y[i] = f * (y[i] - v[i] * along);
-                        z[i] = f * (z[i] - x[i] * along);
+                        y[i] = f * fmaf(-v[i], along, y[i]);
+                        z[i] = f * fmaf(-x[i], along, z[i]);
                     }
                 }
             }
-            if (p.in && t < a.T) {
-                const int64_t at = t * a.ld_dx + (int64_t)h * a.D;
-                Row8::store(a.dx, at + p.at0, y);
-                Row8::store(a.dx, at + p.at1, z);
+            if (in && t < a.T) {
+                Row8::store(a.dx, t * a.ld_dx + head_at + p.at0, y);
+                Row8::store(a.dx, t * a.ld_dx + head_at + p.at1, z);
             }
         }
         if (a.turns.rot) __syncthreads();      // the next rows' angles take these rows' place
     }
     if constexpr (kWeights) {
-        // lanes that hold the same elements: within the warp, then over the warps
-        __shared__ float total[kThreads / 32][2][kLanes * 16];
+        // every head's sums, then the query heads' and the key heads' together
+        constexpr int kHeads = kMaxThreads / kLanes;
+        __shared__ float total[kHeads][kLanes * 16];
+        const int group = threadIdx.x / kLanes;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float v = sum[j][i];
-#pragma unroll
-                for (int o = 16; o >= kLanes; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (threadIdx.x % 32 < kLanes) total[threadIdx.x / 32][j][lane * 16 + i] = v;
-            }
+        for (int i = 0; i < 16; ++i) total[group][lane * 16 + i] = sum[i];
         __syncthreads();
-        for (int e = threadIdx.x; e < 2 * kLanes * 16; e += kThreads) {
+        const int groups = (int)blockDim.x / kLanes, across = a.shape.across * (32 / kLanes);
+        for (int e = threadIdx.x; e < 2 * kLanes * 16; e += (int)blockDim.x) {
             const int j = e / (kLanes * 16), i = e % (kLanes * 16);
             const LanePieces q(i / 16, a.D, a.turns);
             if (!q.in) continue;
             float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < kThreads / 32; ++w) v += total[w][j][i];
+            for (int k = 0; k < groups; ++k) {
+                const int head = (int)blockIdx.y * across + k % across;
+                if (head < a.heads && (head >= a.hq) == (j == 1)) v += total[k][i];
+            }
             const int d = i % 16 < 8 ? q.at0 + i % 16 : q.at1 + i % 16 - 8;
-            a.parts[((int64_t)blockIdx.x * 2 + j) * a.D + d] = v;
+            a.parts[(((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 + j) * a.D + d] = v;
         }
     }
 }
@@ -409,63 +430,57 @@ struct Read {
     void *k, *v;
     int64_t ld_k, ld_v;
     int64_t T;
+    Shape shape;
     int32_t n_heads, D;
 };
 
-// Units are heads of a row, keys then values; a lane takes 16 neighbouring elements.
-template <class Row8, int kLanes, int kUnits, int kCache>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const Read a) {
+// Heads are key heads, then value heads; a lane takes 16 neighbouring elements.
+template <class Row8, int kLanes, int kRows, int kCache>
+__global__ void __launch_bounds__(kMaxThreads) cache_read_kernel(const Read a) {
     grid_dep_launch();
     grid_dep_wait();
-    constexpr int kGroups = kThreads / kLanes;
-    const int lane = threadIdx.x % kLanes, heads = 2 * a.n_heads;
-    const int64_t u0 = (int64_t)blockIdx.x * (kGroups * kUnits);
-    const int64_t t0 = u0 / heads;
-    const int first = (int)(u0 - t0 * heads) + threadIdx.x / kLanes;
-    uint4 q[kUnits][kCache == LORA_CACHE_E4M3 ? 1 : 2];
-    float sc[kUnits];
+    constexpr bool kE4m3 = kCache == LORA_CACHE_E4M3;
+    const Spot<kLanes, kRows> spot(a.shape, blockIdx.x);
+    const bool value = spot.head >= a.n_heads;
+    const int head = value ? spot.head - a.n_heads : spot.head;
+    if (head >= a.n_heads || 16 * spot.lane >= a.D) return;
+    const char* from = (value ? a.cache.v : a.cache.k) + head * a.cache.head_stride + (kE4m3 ? 16 : 32) * spot.lane;
+    const float* scales = kE4m3 ? (value ? a.cache.vs : a.cache.ks) + head * a.cache.s_head : nullptr;
+    uint4 q[kRows][kE4m3 ? 1 : 2];
+    float sc[kRows];
+    int64_t slot[kRows];
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-        const int u = first + k * kGroups;
-        const int64_t t = t0 + u / heads;
-        const int h = u % heads;
-        const bool value = h >= a.n_heads;
-        const int head = value ? h - a.n_heads : h;
-        sc[k] = 0.f;
-        for (auto& w : q[k]) w = make_uint4(0, 0, 0, 0);
-        if (t >= a.T || 16 * lane >= a.D) continue;
-        const int64_t slot = a.slots[t];
-        if (slot < 0 || slot >= a.cache.slots) continue;
-        const RowPlace at(a.cache, slot);
-        const char* from = (value ? a.cache.v : a.cache.k) + at.row + head * a.cache.head_stride;
-        if (kCache == LORA_CACHE_E4M3) {
-            sc[k] = (value ? a.cache.vs : a.cache.ks)[at.scale + head * a.cache.s_head];
-            q[k][0] = *reinterpret_cast<const uint4*>(from + 16 * lane);
-        } else {
-            q[k][0] = *reinterpret_cast<const uint4*>(from + 32 * lane);
-            q[k][1] = *reinterpret_cast<const uint4*>(from + 32 * lane + 16);
-        }
+    for (int k = 0; k < kRows; ++k) {
+        const int64_t t = spot.t0 + spot.row + k * a.shape.down;
+        slot[k] = t < a.T ? a.slots[t] : -1;
     }
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-        const int u = first + k * kGroups;
-        const int64_t t = t0 + u / heads;
-        const int h = u % heads;
-        const bool value = h >= a.n_heads;
-        if (t >= a.T || 16 * lane >= a.D) continue;
-        void* to = value ? a.v : a.k;
-        const int64_t at = t * (value ? a.ld_v : a.ld_k) + (int64_t)(value ? h - a.n_heads : h) * a.D + 16 * lane;
+    for (int k = 0; k < kRows; ++k) {
+        sc[k] = 0.f;
+        for (auto& w : q[k]) w = make_uint4(0, 0, 0, 0);
+        if (slot[k] < 0 || slot[k] >= a.cache.slots) continue;
+        const RowPlace place(a.cache, slot[k]);
+        if (kE4m3) sc[k] = scales[place.scale];
+        q[k][0] = *reinterpret_cast<const uint4*>(from + place.row);
+        if (!kE4m3) q[k][kE4m3 ? 0 : 1] = *reinterpret_cast<const uint4*>(from + place.row + 16);
+    }
+    void* to = value ? a.v : a.k;
+    const int64_t ld = value ? a.ld_v : a.ld_k, col = (int64_t)head * a.D + 16 * spot.lane;
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+        const int64_t t = spot.t0 + spot.row + k * a.shape.down;
+        if (t >= a.T) continue;
         float x[8];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            if (kCache == LORA_CACHE_E4M3) {
+            if (kE4m3) {
                 decode8(i ? make_uint2(q[k][0].z, q[k][0].w) : make_uint2(q[k][0].x, q[k][0].y), sc[k], x);
             } else {
                 Row8Bf16 b;
-                b.q = q[k][i];
+                b.q = q[k][kE4m3 ? 0 : i];
                 b.get(x);
             }
-            Row8::store(to, at + 8 * i, x);
+            Row8::store(to, t * ld + col + 8 * i, x);
         }
     }
 }
@@ -486,16 +501,24 @@ cudaError_t by_type(lora_dtype_t dt, Go go) {
     return dt == LORA_BF16 ? go(Row8Bf16()) : go(Row8F32());
 }
 
-// Units that a thread takes: one where all of them fit one round of CTAs, four else.
-int units_of(int64_t units, int D) { return units * lanes_of(D) <= 152ll * 2 * kThreads ? 1 : 4; }
-
-int64_t chunks(int64_t units, int D, int per_thread) {
-    const int64_t n = (int64_t)(kThreads / lanes_of(D)) * per_thread;
-    return (units + n - 1) / n;
+// CTAs of up to eight warps: the heads in equal shares across, and as many rows of warps as are left room for.
+struct Launch {
+    Shape shape;
+    unsigned y;
+};
+Launch launch_of(int heads, int D, int64_t T) {
+    const int per_warp = 32 / lanes_of(D), all = (heads + per_warp - 1) / per_warp;
+    Launch l;
+    l.y = (unsigned)((all + 7) / 8);
+    l.shape.across = (all + (int)l.y - 1) / (int)l.y;
+    l.shape.down = (int)std::min<int64_t>(8 / l.shape.across, T);
+    return l;
 }
-// Rows that a CTA's units may lie in, and the shared memory of their angles
-int rows_of(int D, int per_thread, int heads) { return kThreads / lanes_of(D) * per_thread / heads + 2; }
-size_t angle_bytes(int rows, int rot) { return (size_t)rows * rot * sizeof(float); }
+unsigned threads_of(const Launch& l) { return (unsigned)(32 * l.shape.across * l.shape.down); }
+// Rows that a lane takes: one where all CTAs fit a round on the SMs, `most` else.
+bool one_row(const Launch& l, int64_t T) { return T * l.y * threads_of(l) <= 152ll * 1024 * l.shape.down; }
+int64_t blocks(const Launch& l, int64_t T, int rows) { return (T + l.shape.down * rows - 1) / (l.shape.down * rows); }
+size_t angle_bytes(const Launch& l, int rows, int rot) { return (size_t)l.shape.down * rows * rot * sizeof(float); }
 
 int check_rotary(const char* fn, int32_t T, lora_dtype_t dt, const lora_rotary_t* r) {
     const std::string f(fn);
@@ -526,17 +549,15 @@ int check_slots(const char* fn, const int64_t* slots) {
 template <class Row8, int kCache>
 cudaError_t launch_forward(Forward a, cudaStream_t st) {
     return by_lanes(a.D, [&](auto lanes) {
-        constexpr int kLanes = decltype(lanes)::value;
-        const int64_t units = a.T * a.heads;
-        auto go = [&](auto per) {
-            constexpr int kUnits = decltype(per)::value;
-            a.max_rows = rows_of(a.D, kUnits, a.heads);
-            const int64_t n = chunks(units, a.D, kUnits);
-            if (n > INT32_MAX) return cudaErrorInvalidConfiguration;
-            return launch_pdl(rotary_kernel<Row8, kLanes, kUnits, kCache>, dim3((unsigned)n), dim3(kThreads),
-                              angle_bytes(a.max_rows, a.turns.rot), st, a);
+        const Launch l = launch_of(a.heads, a.D, a.T);
+        a.shape = l.shape;
+        auto go = [&](auto rows) {
+            constexpr int kRows = decltype(rows)::value;
+            return launch_pdl(rotary_kernel<Row8, decltype(lanes)::value, kRows, kCache>,
+                              dim3((unsigned)blocks(l, a.T, kRows), l.y), dim3(threads_of(l)),
+                              angle_bytes(l, kRows, a.turns.rot), st, a);
         };
-        return units_of(units, a.D) == 1 ? go(std::integral_constant<int, 1>()) : go(std::integral_constant<int, 4>());
+        return one_row(l, a.T) ? go(std::integral_constant<int, 1>()) : go(std::integral_constant<int, 4>());
     });
 }
 cudaError_t forward(lora_dtype_t dt, int cache, const Forward& a, cudaStream_t st) {
@@ -548,7 +569,7 @@ cudaError_t forward(lora_dtype_t dt, int cache, const Forward& a, cudaStream_t s
     });
 }
 
-constexpr int kMaxParts = 608;       // CTAs of a backward that sums the weights' gradients: four on each SM
+constexpr unsigned kMaxParts = 608;  // CTAs of a backward that sums the weights' gradients: four on each SM
 
 }  // namespace
 }  // namespace lora
@@ -644,21 +665,22 @@ extern "C" int lora_rotary_backward(int32_t T, lora_dtype_t dt, const lora_rotar
             e = by_type(dt, [&](auto row) {
                 using Row8 = decltype(row);
                 return by_lanes(a.D, [&](auto lanes) {
-                    constexpr int kLanes = decltype(lanes)::value;
-                    const int64_t units = a.T * a.heads;
-                    auto go = [&](auto per, auto nrm, auto wts) {
-                        constexpr int kUnits = decltype(per)::value;
-                        a.max_rows = rows_of(a.D, kUnits, a.heads);
-                        a.n_chunks = chunks(units, a.D, kUnits);
-                        const int64_t n = std::min<int64_t>(a.n_chunks, decltype(wts)::value ? kMaxParts : INT32_MAX);
-                        parts = (int)n;
-                        return launch_pdl(rotary_backward_kernel<Row8, kLanes, kUnits, decltype(nrm)::value,
-                                                                 decltype(wts)::value>,
-                                          dim3((unsigned)n), dim3(kThreads), angle_bytes(a.max_rows, a.turns.rot), st, a);
+                    const Launch l = launch_of(a.heads, a.D, a.T);
+                    a.shape = l.shape;
+                    auto go = [&](auto rows, auto nrm, auto wts) {
+                        constexpr int kRows = decltype(rows)::value;
+                        constexpr bool kWeights = decltype(wts)::value;
+                        a.n_blocks = blocks(l, a.T, kRows);
+                        const int64_t n = kWeights ? std::min<int64_t>(a.n_blocks, std::max(1u, kMaxParts / l.y)) : a.n_blocks;
+                        parts = (int)(n * l.y);
+                        return launch_pdl(rotary_backward_kernel<Row8, decltype(lanes)::value, kRows, decltype(nrm)::value,
+                                                                 kWeights>,
+                                          dim3((unsigned)n, l.y), dim3(threads_of(l)), angle_bytes(l, kRows, a.turns.rot), st,
+                                          a);
                     };
                     auto sized = [&](auto nrm, auto wts) {
-                        return units_of(units, a.D) == 1 ? go(std::integral_constant<int, 1>(), nrm, wts)
-                                                         : go(std::integral_constant<int, 2>(), nrm, wts);
+                        return one_row(l, a.T) ? go(std::integral_constant<int, 1>(), nrm, wts)
+                                               : go(std::integral_constant<int, 2>(), nrm, wts);
                     };
                     return !norm ? sized(std::false_type(), std::false_type())
                                  : !weights ? sized(std::true_type(), std::false_type())
@@ -714,18 +736,16 @@ extern "C" int lora_cache_read(int32_t T, lora_dtype_t dt, const lora_cache_t* c
         return enqueued(fn, by_type(dt, [&](auto row) {
             using Row8 = decltype(row);
             return by_lanes(a.D, [&](auto lanes) {
-                constexpr int kLanes = decltype(lanes)::value;
-                const int64_t units = a.T * 2 * a.n_heads;
-                auto go = [&](auto per, auto c) {
-                    constexpr int kUnits = decltype(per)::value;
-                    const int64_t n = chunks(units, a.D, kUnits);
-                    if (n > INT32_MAX) return cudaErrorInvalidConfiguration;
-                    return launch_pdl(cache_read_kernel<Row8, kLanes, kUnits, decltype(c)::value>, dim3((unsigned)n),
-                                      dim3(kThreads), 0, st, a);
+                const Launch l = launch_of(2 * a.n_heads, a.D, a.T);
+                a.shape = l.shape;
+                auto go = [&](auto rows, auto c) {
+                    constexpr int kRows = decltype(rows)::value;
+                    return launch_pdl(cache_read_kernel<Row8, decltype(lanes)::value, kRows, decltype(c)::value>,
+                                      dim3((unsigned)blocks(l, a.T, kRows), l.y), dim3(threads_of(l)), 0, st, a);
                 };
                 auto sized = [&](auto c) {
-                    return units_of(units, a.D) == 1 ? go(std::integral_constant<int, 1>(), c)
-                                                     : go(std::integral_constant<int, 4>(), c);
+                    return one_row(l, a.T) ? go(std::integral_constant<int, 1>(), c)
+                                           : go(std::integral_constant<int, 4>(), c);
                 };
                 return cache->dtype == LORA_CACHE_BF16 ? sized(std::integral_constant<int, LORA_CACHE_BF16>())
                                                        : sized(std::integral_constant<int, LORA_CACHE_E4M3>());
