@@ -29,7 +29,8 @@ struct CacheView {
 
 // Where a slot's row lies in head 0, in bytes and in scales; the slot is inside the cache
 struct RowPlace {
-    int64_t row, scale;
+    int64_t row = 0, scale = 0;
+    __device__ __forceinline__ RowPlace() {}
     __device__ __forceinline__ RowPlace(const CacheView& c, int64_t slot) {
         const int64_t page = (slot >> 31) == 0 ? (int64_t)c.pages.page_of((uint32_t)slot) : slot / c.page_size;
         const int64_t r = slot - page * c.page_size;

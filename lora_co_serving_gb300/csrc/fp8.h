@@ -64,6 +64,8 @@ __device__ __forceinline__ void decode8(uint2 q, float s, float (&v)[8]) {
 // 8 elements of a row in either element type
 struct Row8Bf16 {
     uint4 q;
+    static __device__ __forceinline__ const void* at(const void* p, int64_t i) { return static_cast<const __nv_bfloat16*>(p) + i; }
+    static __device__ __forceinline__ void* at(void* p, int64_t i) { return static_cast<__nv_bfloat16*>(p) + i; }
     __device__ __forceinline__ void load(const void* p, int64_t i) {
         q = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
     }
@@ -96,6 +98,8 @@ struct Row8Bf16 {
 };
 struct Row8F32 {
     float4 a, b;
+    static __device__ __forceinline__ const void* at(const void* p, int64_t i) { return static_cast<const float*>(p) + i; }
+    static __device__ __forceinline__ void* at(void* p, int64_t i) { return static_cast<float*>(p) + i; }
     __device__ __forceinline__ void load(const void* p, int64_t i) {
         const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
         a = s[0];

@@ -5,9 +5,10 @@
 // do not.  A head's row of D elements belongs to D / 16 neighbouring lanes (of the next power of two, at least four), 16
 // elements each: two pieces of 8.  Where the row is turned in halves, a lane's two pieces are the two members of its 8
 // pairs, so the rotation stays in the lane; a row's sum of squares, or its largest magnitude, is at most four shuffles
-// away.  A lane keeps its head and takes several rows of it, so that what depends on the head (its weights, where it lies)
-// is found once: numbering (row, head) units instead took twice the instructions and 61 us for 8192 rows of 72 heads, @ now.
-// The angles of a CTA's rows are computed once, by all its threads, into shared memory, while the rows are on their way.
+// away.  A warp takes a chunk of the heads of one row after another and shares nothing with other warps: it computes the
+// row's angles, and copies the next row's pieces into shared memory, asynchronously, while it works on this one's.  (CTAs
+// of a few rows each, whose loads, arithmetic and stores follow one another, took 56 us at best for 8192 rows of 72 heads,
+// 54 now; a copy of these rows takes 46.)
 #include <algorithm>
 #include <type_traits>
 
@@ -19,21 +20,23 @@ namespace {
 
 constexpr int kMaxThreads = 256;
 
-// How a CTA's warps lie over heads and rows: `across` warps take neighbouring heads, `down` of such rows of warps take
-// neighbouring rows of the matrix.  A lane takes kRows rows, `down` apart.
-struct Shape {
-    int32_t across, down;
+constexpr int kMaxWarps = kMaxThreads / 32;
+constexpr int kCtas = 2;      // CTAs on an SM: with three, or four, registers spill and 8192 rows of 72 heads take 61 and 78 us
+
+// The heads of a row, in chunks of one kind each; a warp takes a chunk
+enum Kind { kQuery, kKey, kValue };
+struct Chunks {
+    int32_t heads[3];        // of each kind
+    int32_t per;             // heads of a chunk, the last of a kind may have fewer
+    __host__ __device__ int32_t of(int kind) const { return (heads[kind] + per - 1) / per; }
+    __host__ __device__ int32_t all() const { return of(kQuery) + of(kKey) + of(kValue); }
 };
-template <int kLanes, int kRows>
-struct Spot {
-    int lane, head, row;         // lane within the head; head; first of the lane's rows in the CTA
-    int64_t t0;                  // the CTA's first row
-    __device__ __forceinline__ Spot(const Shape& s, int64_t block) {
-        const int warp = threadIdx.x / 32;
-        lane = threadIdx.x % kLanes;
-        head = ((int)blockIdx.y * s.across + warp % s.across) * (32 / kLanes) + threadIdx.x % 32 / kLanes;
-        row = warp / s.across;
-        t0 = block * (int64_t)(s.down * kRows);
+struct Chunk {
+    int kind, first, heads;
+    __device__ __forceinline__ Chunk(const Chunks& c, int i) : kind(kQuery) {
+        while (kind < kValue && i >= c.of(kind)) i -= c.of(kind++);
+        first = i * c.per;
+        heads = min(c.per, c.heads[kind] - first);
     }
 };
 
@@ -45,47 +48,113 @@ struct Turns {
 };
 
 // cos and sin of a phase in units of 2^-64 turns.  The quarter turn nearest to it is taken off in whole numbers: what is
-// left is at most an eighth, so that its float32 value is 5e-8 off in angle at the most, and its sine and cosine a few
-// units of 2^-24.
+// left, an angle of at most pi / 4, is 5e-8 off in float32, and the two Taylor series break off at x^9 and x^8, 2e-9 and
+// 2.5e-8 off there.
 __device__ __forceinline__ float2 cos_sin(uint64_t phase) {
     const uint32_t quarter = (uint32_t)((phase + (1ull << 61)) >> 62);
     const int32_t rest = (int32_t)(uint32_t)((phase - ((uint64_t)quarter << 62)) >> 32);      // in 2^-32 turns
-    float s, c;
-    sincospif((float)rest * 0x1p-31f, &s, &c);
+    const float x = (float)rest * (float)(6.283185307179586 * 0x1p-32), q = x * x;
+    const float s = fmaf(x * q, fmaf(q, fmaf(q, fmaf(q, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), x);
+    const float c = fmaf(q, fmaf(q, fmaf(q, fmaf(q, 1.f / 40320.f, -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
     const float c1 = quarter & 1 ? -s : c, s1 = quarter & 1 ? c : s;
     return quarter & 2 ? make_float2(-c1, -s1) : make_float2(c1, s1);
 }
 
-// Angles of rows [t0, t0 + n_rows) of this CTA: cosines [n_rows, rot / 2], then sines
-struct Angles {
-    float *cos_, *sin_;
-    int half;
-    __device__ __forceinline__ Angles(const Turns& a, float* smem, int n_rows)
-        : cos_(smem), sin_(smem + n_rows * (a.rot / 2)), half(a.rot / 2) {}
-    __device__ __forceinline__ void fill(const Turns& a, int64_t t0, int n_rows, int64_t T) {
-        for (int i = threadIdx.x; i < n_rows * half; i += (int)blockDim.x) {
-            const int64_t t = t0 + i / half;
-            if (t >= T) break;
-            const float2 v = cos_sin((uint64_t)a.positions[t] * (uint64_t)a.turns[i % half]);
-            cos_[i] = v.x;
-            sin_[i] = v.y;
-        }
-    }
-    // of a lane's 8 pairs
-    __device__ __forceinline__ void get(int row, int lane, float (&c)[8], float (&s)[8]) const {
-        const float4* pc = reinterpret_cast<const float4*>(cos_ + row * half + 8 * lane);
-        const float4* ps = reinterpret_cast<const float4*>(sin_ + row * half + 8 * lane);
+// Two products, or two fused sums, in one instruction
+__device__ __forceinline__ void mul2(float (&d)[8], const float (&a)[8], const float (&b)[8]) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float4 x = pc[i], y = ps[i];
-            c[4 * i] = x.x; c[4 * i + 1] = x.y; c[4 * i + 2] = x.z; c[4 * i + 3] = x.w;
-            s[4 * i] = y.x; s[4 * i + 1] = y.y; s[4 * i + 2] = y.z; s[4 * i + 3] = y.w;
-        }
+    for (int i = 0; i < 8; i += 2)
+        asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\tmov.b64 "
+            "{%0, %1}, d;\n\t}"
+            : "=f"(d[i]), "=f"(d[i + 1])
+            : "f"(a[i]), "f"(a[i + 1]), "f"(b[i]), "f"(b[i + 1]));
+}
+__device__ __forceinline__ void mul2(float (&d)[8], const float (&a)[8], float b) {
+    const float all[8] = {b, b, b, b, b, b, b, b};
+    mul2(d, a, all);
+}
+// d = a b + c
+__device__ __forceinline__ void fma2(float (&d)[8], const float (&a)[8], const float (&b)[8], const float (&c)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+        asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\tfma.rn.f32x2 "
+            "d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+            : "=f"(d[i]), "=f"(d[i + 1])
+            : "f"(a[i]), "f"(a[i + 1]), "f"(b[i]), "f"(b[i + 1]), "f"(c[i]), "f"(c[i + 1]));
+}
+__device__ __forceinline__ float sum8(const float (&v)[8]) {
+    return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+}
+// a . b + c . d
+__device__ __forceinline__ float dot(const float (&a)[8], const float (&b)[8], const float (&c)[8], const float (&d)[8]) {
+    float v[8];
+    mul2(v, a, b);
+    fma2(v, c, d, v);
+    return sum8(v);
+}
+
+// The angles of a warp's row: cosines [rot / 2], then sines, by all its lanes
+__device__ __forceinline__ void fill_angles(const Turns& a, uint64_t position, float* to) {
+    const int half = a.rot / 2;
+    for (int i = threadIdx.x % 32; i < half; i += 32) {
+        const float2 v = cos_sin(position * (uint64_t)a.turns[i]);
+        to[i] = v.x;
+        to[half + i] = v.y;
     }
+}
+__device__ __forceinline__ void read8(const float* from, float (&v)[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(from), b = *reinterpret_cast<const float4*>(from + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+// A warp's place in shared memory: two rows of a chunk's pieces, [piece][lane] of 16 bytes, so that each lane reads back what
+// it copied; the rows' positions and slots; a row's angles.
+constexpr int kRowBytes = 3072;      // 8192 rows of 72 heads: 1024 bytes 64 us, 2048 and 3072 54, 4096 57
+struct WarpPlace {
+    uint4 piece[2][kRowBytes / 16];
+    int64_t position[2], slot[2];
+    float angles[kMaxHeadDim];
 };
+__device__ __forceinline__ void copy_async16(void* to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_async8(void* to, const void* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+// 8 elements of a row, as one or two pieces from number `at` on
+template <class Row8>
+__device__ __forceinline__ void copy8(uint4* pieces, int at, const void* from) {
+    constexpr int kPieces = sizeof(Row8) / 16;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+        copy_async16(pieces + (at * kPieces + i) * 32 + threadIdx.x % 32, static_cast<const char*>(from) + 16 * i);
+}
+template <class Row8>
+__device__ __forceinline__ void read_pieces(const uint4* pieces, int at, float (&v)[8]) {
+    constexpr int kPieces = sizeof(Row8) / 16;
+    uint4 q[kPieces];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) q[i] = pieces[(at * kPieces + i) * 32 + threadIdx.x % 32];
+    reinterpret_cast<const Row8*>(q)->get(v);
+}
+
+// What is known of a head beforehand: nothing; that it fills its lanes (D = 16 kLanes) and is turned whole, in halves; or
+// that it fills them and is not turned.  The known forms take two thirds of the instructions.
+enum Form { kAny, kTurned, kPlain };
 
 // The two pieces of a head's row that a lane holds: from elements at0 and at1
 struct LanePieces {
+    template <int kLanes, int kForm>
+    static __device__ __forceinline__ LanePieces of(int lane, int D, const Turns& a) {
+        LanePieces p(lane, D, a);
+        if (kForm == kAny) return p;
+        p.in = true;
+        p.turned = kForm == kTurned;
+        p.at0 = kForm == kTurned ? 8 * lane : 16 * lane;
+        p.at1 = p.at0 + (kForm == kTurned ? 8 * kLanes : 8);
+        return p;
+    }
     int at0, at1;
     bool in, turned;
     __device__ __forceinline__ LanePieces(int lane, int D, const Turns& a) {
@@ -97,25 +166,32 @@ struct LanePieces {
     }
 };
 
-// turns 8 pairs: (u[i], w[i]), or neighbours within u and within w
-__device__ __forceinline__ void turn(float (&u)[8], float (&w)[8], const float (&c)[8], const float (&s)[8],
+// turns 8 pairs, (u[i], w[i]) or neighbours within u and within w, by its angles (back: by their negatives), and multiplies by f
+__device__ __forceinline__ void turn(float (&u)[8], float (&w)[8], const float* cosines, const float* sines, float f, bool back,
                                      bool interleaved) {
+    float c[8], s[8], less[8];
+    read8(sines, s);
+    mul2(less, s, back ? f : -f);
+    mul2(s, s, back ? -f : f);
+    read8(cosines, c);
+    mul2(c, c, f);
     if (interleaved) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float a = u[2 * i], b = u[2 * i + 1], d = w[2 * i], e = w[2 * i + 1];
-            u[2 * i] = a * c[i] - b * s[i];
-            u[2 * i + 1] = b * c[i] + a * s[i];
-            w[2 * i] = d * c[4 + i] - e * s[4 + i];
-            w[2 * i + 1] = e * c[4 + i] + d * s[4 + i];
+            u[2 * i] = fmaf(b, less[i], a * c[i]);
+            u[2 * i + 1] = fmaf(a, s[i], b * c[i]);
+            w[2 * i] = fmaf(e, less[4 + i], d * c[4 + i]);
+            w[2 * i + 1] = fmaf(d, s[4 + i], e * c[4 + i]);
         }
     } else {
+        float p[8], q[8];
+        mul2(p, u, c);
+        mul2(q, w, c);
+        fma2(q, u, s, q);
+        fma2(u, w, less, p);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float a = u[i], b = w[i];
-            u[i] = a * c[i] - b * s[i];
-            w[i] = b * c[i] + a * s[i];
-        }
+        for (int i = 0; i < 8; ++i) w[i] = q[i];
     }
 }
 
@@ -133,9 +209,8 @@ __device__ __forceinline__ uint32_t max_over_lanes(uint32_t v) {
 }
 
 // ------------------------------------------------------------------------------------------------------- forward
-// Heads are query heads, key heads, and with a cache the value heads.
 struct Forward {
-    const void* x;
+    const void* x;           // query heads, then key heads
     int64_t ld_x;
     const void* v;
     int64_t ld_v;
@@ -146,113 +221,115 @@ struct Forward {
     Turns turns;
     CacheView cache;
     int64_t T;
-    Shape shape;
-    int32_t hq, hk, heads;   // query heads, key heads, all
-    int32_t out_heads;       // the first of them that go to out
+    Chunks chunks;
+    bool out_keys;           // keys go to out
     int32_t D;
     float eps, inv_d;
 };
 
-template <class Row8, int kLanes, int kRows, int kCache /* -1: none */>
-__global__ void __launch_bounds__(kMaxThreads) rotary_kernel(const Forward a) {
-    extern __shared__ __align__(16) float smem[];
+template <class Row8, int kLanes, int kForm, int kCache /* -1: none */>
+__global__ void __launch_bounds__(kMaxThreads, kCtas) rotary_kernel(const Forward a) {
+    extern __shared__ __align__(16) char smem[];
+    WarpPlace& mine = reinterpret_cast<WarpPlace*>(smem)[threadIdx.x / 32];
     grid_dep_launch();
     grid_dep_wait();
-    const Spot<kLanes, kRows> at(a.shape, blockIdx.x);
-    const LanePieces p(at.lane, a.D, a.turns);
-    const bool key = at.head >= a.hq, value = at.head >= a.hq + a.hk, in = p.in && at.head < a.heads;
-    const void* from = value ? a.v : a.x;
-    const int64_t ld = value ? a.ld_v : a.ld_x;
-    const int64_t head_at = (int64_t)(value ? at.head - a.hq - a.hk : at.head) * a.D;
-    Row8 r[kRows][2], w[2];
-#pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-        const int64_t t = at.t0 + at.row + k * a.shape.down;
-        r[k][0].zero();
-        r[k][1].zero();
-        if (in && t < a.T) {
-            r[k][0].load(from, t * ld + head_at + p.at0);
-            r[k][1].load(from, t * ld + head_at + p.at1);
-        }
-    }
-    const void* weight = value ? nullptr : key ? a.wk : a.wq;
-    w[0].zero();
-    w[1].zero();
-    if (weight && in) {
+    constexpr int kAcross = 32 / kLanes;
+    const int64_t t0 = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32, by = (int64_t)gridDim.x * (blockDim.x / 32);
+    if (t0 >= a.T) return;
+    const Chunk chunk(a.chunks, blockIdx.y);
+    const int lane = threadIdx.x % kLanes, sub = threadIdx.x % 32 / kLanes;
+    const bool value = chunk.kind == kValue, keeps = kCache >= 0 && chunk.kind != kQuery;
+    const bool to_out = chunk.kind == kQuery || (chunk.kind == kKey && a.out_keys), turned = kForm != kPlain && a.turns.rot > 0 && !value;
+    const int D = kForm != kAny ? 16 * kLanes : a.D, steps = (chunk.heads + kAcross - 1) / kAcross;
+    const LanePieces p = LanePieces::of<kLanes, kForm>(lane, D, a.turns);
+    const int heads = p.in ? chunk.heads - sub : 0;      // this lane's are 0, kAcross, 2 kAcross, .. below that
+    const int64_t head_at = (int64_t)(chunk.first + (chunk.kind == kKey ? a.chunks.heads[kQuery] : 0) + sub) * D;
+    const void* weight = value ? nullptr : chunk.kind == kKey ? a.wk : a.wq;
+    float g0[8] = {}, g1[8] = {};
+    if (weight && (p.in)) {
+        Row8 w[2];
         w[0].load(weight, p.at0);
         w[1].load(weight, p.at1);
+        w[0].get(g0);
+        w[1].get(g1);
     }
-    Angles angles(a.turns, smem, a.shape.down * kRows);
-    if (a.turns.rot) {
-        angles.fill(a.turns, at.t0, a.shape.down * kRows, a.T);
-        __syncthreads();
-    }
-#pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-        const int row = at.row + k * a.shape.down;
-        const int64_t t = at.t0 + row;
-        float y[8], z[8], f = 1.f;
-        r[k][0].get(y);
-        r[k][1].get(z);
-        if (a.wq || a.wk) {
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], fmaf(z[i], z[i], ss));
-            ss = sum_over_lanes<kLanes>(ss);
-            if (weight) {
-                f = rsqrtf(ss * a.inv_d + a.eps);
-                float g[8];
-                w[0].get(g);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] *= g[i];
-                w[1].get(g);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) z[i] *= g[i];
+    // a lane's pieces that are not there are read as what the place held before: numbers that go nowhere
+    auto copy = [&](int64_t t, int to) {
+        if (t < a.T) {
+            const char* from = static_cast<const char*>(Row8::at(value ? a.v : a.x, t * (value ? a.ld_v : a.ld_x) + head_at));
+            for (int k = 0; k < steps; ++k) {
+                if (k * kAcross >= heads) break;
+                copy8<Row8>(mine.piece[to], 2 * k, Row8::at(static_cast<const void*>(from), k * kAcross * D + p.at0));
+                copy8<Row8>(mine.piece[to], 2 * k + 1, Row8::at(static_cast<const void*>(from), k * kAcross * D + p.at1));
+            }
+            if (threadIdx.x % 32 == 0) {
+                if (turned) copy_async8(&mine.position[to], a.turns.positions + t);
+                if (keeps) copy_async8(&mine.slot[to], a.slots + t);
             }
         }
-        if (p.turned && !value && t < a.T) {
-            float c[8], s[8];
-            angles.get(row, at.lane, c, s);
-            if (weight) {            // the row's factor goes into its angles' cosines and sines
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    c[i] *= f;
-                    s[i] *= f;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    copy(t0, 0);
+    int now = 0;
+    for (int64_t t = t0; t < a.T; t += by, now ^= 1) {
+        copy(t + by, now ^ 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+        if (turned) {
+            fill_angles(a.turns, (uint64_t)mine.position[now], mine.angles);
+            __syncwarp();
+        }
+        void* const out = Row8::at(a.out, t * a.ld_out + head_at);
+        const int64_t slot = keeps ? mine.slot[now] : -1;
+        const bool cached = slot >= 0 && slot < a.cache.slots;
+        const RowPlace place = cached ? RowPlace(a.cache, slot) : RowPlace();
+#pragma unroll 2
+        for (int k = 0; k < steps; ++k) {
+            float y[8], z[8], f = 1.f;
+            read_pieces<Row8>(mine.piece[now], 2 * k, y);
+            read_pieces<Row8>(mine.piece[now], 2 * k + 1, z);
+            const bool in = k * kAcross < heads;
+            if (weight) {
+                const float ss = p.in ? dot(y, y, z, z) : 0.f;
+                f = rsqrtf(sum_over_lanes<kLanes>(ss) * a.inv_d + a.eps);
+                mul2(y, y, g0);
+                mul2(z, z, g1);
+            }
+            if (turned && p.turned) {
+                turn(y, z, mine.angles + 8 * lane, mine.angles + (kForm == kTurned ? 8 * kLanes : a.turns.rot / 2) + 8 * lane, f, false, kForm == kAny && a.turns.interleaved);
+            } else if (weight) {
+                mul2(y, y, f);
+                mul2(z, z, f);
+            }
+            if (in && to_out) {
+                Row8::store(out, k * kAcross * D + p.at0, y);
+                Row8::store(out, k * kAcross * D + p.at1, z);
+            }
+            if constexpr (kCache >= 0) {
+                if (keeps) {
+                    uint32_t amax = 0;
+                    if (kCache == LORA_CACHE_E4M3)
+                        amax = max_over_lanes<kLanes>(p.in ? max(abs_bits_max(y), abs_bits_max(z)) : 0);
+                    if (in && cached) {
+                        const int head = chunk.first + k * kAcross + sub;
+                        char* to = (value ? a.cache.v : a.cache.k) + place.row + head * a.cache.head_stride;
+                        if (kCache == LORA_CACHE_BF16) {
+                            Row8Bf16::store(to, p.at0, y);
+                            Row8Bf16::store(to, p.at1, z);
+                        } else {
+                            float inv;
+                            const float sc = block_scale(amax, &inv);
+                            *reinterpret_cast<uint2*>(to + p.at0) = encode8(y, inv);
+                            *reinterpret_cast<uint2*>(to + p.at1) = encode8(z, inv);
+                            if (lane == 0) (value ? a.cache.vs : a.cache.ks)[place.scale + head * a.cache.s_head] = sc;
+                        }
+                    }
                 }
             }
-            turn(y, z, c, s, a.turns.interleaved);
-        } else if (weight) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                y[i] *= f;
-                z[i] *= f;
-            }
         }
-        const bool here = in && t < a.T;
-        if (here && at.head < a.out_heads) {
-            Row8::store(a.out, t * a.ld_out + head_at + p.at0, y);
-            Row8::store(a.out, t * a.ld_out + head_at + p.at1, z);
-        }
-        if (kCache < 0) continue;
-        uint32_t amax = 0;
-        if (kCache == LORA_CACHE_E4M3) amax = max_over_lanes<kLanes>(max(abs_bits_max(y), abs_bits_max(z)));
-        if (!here || !key) continue;
-        const int64_t slot = a.slots[t];
-        if (slot < 0 || slot >= a.cache.slots) continue;
-        const RowPlace place(a.cache, slot);
-        const int head = at.head - a.hq - (value ? a.hk : 0);
-        char* to = (value ? a.cache.v : a.cache.k) + place.row + head * a.cache.head_stride;
-        if (kCache == LORA_CACHE_BF16) {
-            Row8Bf16::store(to, p.at0, y);
-            Row8Bf16::store(to, p.at1, z);
-        } else {
-            float inv;
-            const float sc = block_scale(amax, &inv);
-            *reinterpret_cast<uint2*>(to + p.at0) = encode8(y, inv);
-            *reinterpret_cast<uint2*>(to + p.at1) = encode8(z, inv);
-            if (at.lane == 0) (value ? a.cache.vs : a.cache.ks)[place.scale + head * a.cache.s_head] = sc;
-        }
+        __syncwarp();        // what this row's copies and angles were in is written anew
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // ------------------------------------------------------------------------------------------------------ backward
@@ -264,155 +341,141 @@ struct Backward {
     void* dx;
     int64_t ld_dx;
     const void *wq, *wk;
-    float* parts;            // [CTAs, 2, D]: each CTA's sums of the weights' gradients; null: not wanted
+    float* parts;            // [chunks, CTAs across the rows, D]: each CTA's sums of the weights' gradients
     Turns turns;
-    int64_t T, n_blocks;     // rows are taken shape.down * kRows at a time
-    Shape shape;
-    int32_t hq, heads, D;
+    int64_t T;
+    Chunks chunks;
+    int32_t D;
     float eps, inv_d;
 };
 
-template <class Row8, int kLanes, int kRows, bool kNorm, bool kWeights>
-__global__ void __launch_bounds__(kMaxThreads) rotary_backward_kernel(const Backward a) {
-    extern __shared__ __align__(16) float smem[];
+template <class Row8, int kLanes, int kForm, bool kNorm, bool kWeights>
+__global__ void __launch_bounds__(kMaxThreads, kCtas) rotary_backward_kernel(const Backward a) {
+    extern __shared__ __align__(16) char smem[];
+    WarpPlace* const places = reinterpret_cast<WarpPlace*>(smem);
+    WarpPlace& mine = places[threadIdx.x / 32];
     grid_dep_launch();
     grid_dep_wait();
-    const int lane = threadIdx.x % kLanes;
-    const LanePieces p(lane, a.D, a.turns);
-    const Spot<kLanes, kRows> spot(a.shape, 0);
-    const bool key = spot.head >= a.hq, in = p.in && spot.head < a.heads;
-    const int64_t head_at = (int64_t)spot.head * a.D;
-    const void* weight = key ? a.wk : a.wq;
-    Row8 w[2];
-    if (kNorm && weight && in) {
+    constexpr int kAcross = 32 / kLanes;
+    const int warps = (int)blockDim.x / 32, warp = threadIdx.x / 32;
+    const Chunk chunk(a.chunks, blockIdx.y);
+    const int lane = threadIdx.x % kLanes, sub = threadIdx.x % 32 / kLanes;
+    const int D = kForm != kAny ? 16 * kLanes : a.D, steps = (chunk.heads + kAcross - 1) / kAcross;
+    const LanePieces p = LanePieces::of<kLanes, kForm>(lane, D, a.turns);
+    const int heads = p.in ? chunk.heads - sub : 0;
+    const int64_t head_at = (int64_t)(chunk.first + (chunk.kind == kKey ? a.chunks.heads[kQuery] : 0) + sub) * D;
+    const void* weight = chunk.kind == kKey ? a.wk : a.wq;
+    float g0[8] = {}, g1[8] = {};
+    if (kNorm && weight && (p.in)) {
+        Row8 w[2];
         w[0].load(weight, p.at0);
         w[1].load(weight, p.at1);
+        w[0].get(g0);
+        w[1].get(g1);
     }
-    Angles angles(a.turns, smem, a.shape.down * kRows);
-    float sum[kWeights ? 16 : 1] = {};
-    for (int64_t block = blockIdx.x; block < a.n_blocks; block += gridDim.x) {
-        const int64_t t0 = block * (int64_t)(a.shape.down * kRows);
-        Row8 r[kRows][2], d[kRows][2];
-#pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-            const int64_t t = t0 + spot.row + k * a.shape.down;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                r[k][i].zero();
-                d[k][i].zero();
-            }
-            if (in && t < a.T) {
-                d[k][0].load(a.dout, t * a.ld_dout + head_at + p.at0);
-                d[k][1].load(a.dout, t * a.ld_dout + head_at + p.at1);
-                if (kNorm) {
-                    r[k][0].load(a.x, t * a.ld_x + head_at + p.at0);
-                    r[k][1].load(a.x, t * a.ld_x + head_at + p.at1);
+    float sum[2][8] = {};
+    const int64_t t0 = (int64_t)blockIdx.x * warps + warp, by = (int64_t)gridDim.x * warps;
+    // pieces of dout, and with a norm of x, in turn
+    constexpr int kEach = kNorm ? 4 : 2;
+    auto copy = [&](int64_t t, int to) {
+        if (t < a.T) {
+            for (int k = 0; k < steps; ++k) {
+                if (k * kAcross >= heads) break;
+                const int64_t at = head_at + k * kAcross * D;
+                copy8<Row8>(mine.piece[to], kEach * k, Row8::at(a.dout, t * a.ld_dout + at + p.at0));
+                copy8<Row8>(mine.piece[to], kEach * k + 1, Row8::at(a.dout, t * a.ld_dout + at + p.at1));
+                if (kNorm && weight) {
+                    copy8<Row8>(mine.piece[to], kEach * k + 2, Row8::at(a.x, t * a.ld_x + at + p.at0));
+                    copy8<Row8>(mine.piece[to], kEach * k + 3, Row8::at(a.x, t * a.ld_x + at + p.at1));
                 }
             }
+            if (threadIdx.x % 32 == 0 && a.turns.rot) copy_async8(&mine.position[to], a.turns.positions + t);
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    copy(t0, 0);
+    int now = 0;
+    for (int64_t t = t0; t < a.T; t += by, now ^= 1) {
+        copy(t + by, now ^ 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
         if (a.turns.rot) {
-            angles.fill(a.turns, t0, a.shape.down * kRows, a.T);
-            __syncthreads();
+            fill_angles(a.turns, (uint64_t)mine.position[now], mine.angles);
+            __syncwarp();
         }
-#pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-            const int row = spot.row + k * a.shape.down;
-            const int64_t t = t0 + row;
+        for (int k = 0; k < steps; ++k) {
             float y[8], z[8];
-            d[k][0].get(y);
-            d[k][1].get(z);
-            if (p.turned && t < a.T) {
-                float c[8], s[8];
-                angles.get(row, lane, c, s);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s[i] = -s[i];
-                turn(y, z, c, s, a.turns.interleaved);
-            }
-            if (kNorm) {
+            read_pieces<Row8>(mine.piece[now], kEach * k, y);
+            read_pieces<Row8>(mine.piece[now], kEach * k + 1, z);
+            const bool in = k * kAcross < heads;
+            if (p.turned)
+                turn(y, z, mine.angles + 8 * lane, mine.angles + (kForm == kTurned ? 8 * kLanes : a.turns.rot / 2) + 8 * lane, 1.f, true, kForm == kAny && a.turns.interleaved);
+            if (kNorm && weight) {
                 float v[8], x[8];
-                r[k][0].get(v);
-                r[k][1].get(x);
-                float ss = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], fmaf(x[i], x[i], ss));
+                read_pieces<Row8>(mine.piece[now], kEach * k + 2, v);
+                read_pieces<Row8>(mine.piece[now], kEach * k + 3, x);
+                const float ss = p.in ? dot(v, v, x, x) : 0.f;
                 const float f = rsqrtf(sum_over_lanes<kLanes>(ss) * a.inv_d + a.eps);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    v[i] *= f;
-                    x[i] *= f;
+                mul2(v, v, f);
+                mul2(x, x, f);
+                if (kWeights && in) {
+                    fma2(sum[0], y, v, sum[0]);
+                    fma2(sum[1], z, x, sum[1]);
                 }
-                if constexpr (kWeights)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        sum[i] = fmaf(y[i], v[i], sum[i]);
-                        sum[8 + i] = fmaf(z[i], x[i], sum[8 + i]);
-                    }
-                float along = 0.f;
-                if (weight && in) {
-                    float g[8];
-                    w[0].get(g);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        y[i] *= g[i];
-                        along = fmaf(y[i], v[i], along);
-                    }
-                    w[1].get(g);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        z[i] *= g[i];
-                        along = fmaf(z[i], x[i], along);
-                    }
-                }
-                along = sum_over_lanes<kLanes>(along) * a.inv_d;
-                if (weight) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        y[i] = f * fmaf(-v[i], along, y[i]);
-                        z[i] = f * fmaf(-x[i], along, z[i]);
-                    }
-                }
+                mul2(y, y, g0);
+                mul2(z, z, g1);
+                const float yx = p.in ? dot(y, v, z, x) : 0.f;
+                const float along = -a.inv_d * sum_over_lanes<kLanes>(yx);
+                const float all[8] = {along, along, along, along, along, along, along, along};
+                fma2(y, v, all, y);
+                fma2(z, x, all, z);
+                mul2(y, y, f);
+                mul2(z, z, f);
             }
-            if (in && t < a.T) {
-                Row8::store(a.dx, t * a.ld_dx + head_at + p.at0, y);
-                Row8::store(a.dx, t * a.ld_dx + head_at + p.at1, z);
+            if (in) {
+                void* const to = Row8::at(a.dx, t * a.ld_dx + head_at);
+                Row8::store(to, k * kAcross * D + p.at0, y);
+                Row8::store(to, k * kAcross * D + p.at1, z);
             }
         }
-        if (a.turns.rot) __syncthreads();      // the next rows' angles take these rows' place
+        __syncwarp();        // what this row's copies and angles were in is written anew
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     if constexpr (kWeights) {
-        // every head's sums, then the query heads' and the key heads' together
-        constexpr int kHeads = kMaxThreads / kLanes;
-        __shared__ float total[kHeads][kLanes * 16];
-        const int group = threadIdx.x / kLanes;
+        // each lane's 16 sums, then those of all lanes and warps that hold the same elements
+        float* const to = reinterpret_cast<float*>(&mine);
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) total[group][lane * 16 + i] = sum[i];
+        for (int i = 0; i < 16; ++i) to[threadIdx.x % 32 * 16 + i] = sum[i / 8][i % 8];
         __syncthreads();
-        const int groups = (int)blockDim.x / kLanes, across = a.shape.across * (32 / kLanes);
-        for (int e = threadIdx.x; e < 2 * kLanes * 16; e += (int)blockDim.x) {
-            const int j = e / (kLanes * 16), i = e % (kLanes * 16);
-            const LanePieces q(i / 16, a.D, a.turns);
+        for (int i = threadIdx.x; i < kLanes * 16; i += (int)blockDim.x) {
+            const LanePieces q = LanePieces::of<kLanes, kForm>(i / 16, D, a.turns);
             if (!q.in) continue;
             float v = 0.f;
-            for (int k = 0; k < groups; ++k) {
-                const int head = (int)blockIdx.y * across + k % across;
-                if (head < a.heads && (head >= a.hq) == (j == 1)) v += total[k][i];
-            }
+            for (int k = 0; k < warps; ++k)
+#pragma unroll
+                for (int j = 0; j < kAcross; ++j) v += reinterpret_cast<const float*>(places + k)[j * kLanes * 16 + i];
             const int d = i % 16 < 8 ? q.at0 + i % 16 : q.at1 + i % 16 - 8;
-            a.parts[(((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 + j) * a.D + d] = v;
+            a.parts[((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * D + d] = v;
         }
     }
 }
 
-// Sums of the CTAs' parts [n, 2 D], in a fixed order; 32 columns a CTA
-__global__ void __launch_bounds__(1024) weight_grad_kernel(const float* parts, int n, int D, float* dq, float* dk) {
+// Sums of the CTAs' parts, nq of the query weight's, then nk of the key weight's, [D] each, in a fixed order; 32 columns of
+// [2 D] a CTA
+__global__ void __launch_bounds__(1024) weight_grad_kernel(const float* parts, int nq, int nk, int D, float* dq, float* dk) {
     __shared__ float s[32][33];
     grid_dep_launch();
     grid_dep_wait();
     const int col = blockIdx.x * 32 + threadIdx.x % 32, y = threadIdx.x / 32;
     float v = 0.f;
-    if (col < 2 * D)
+    if (col < 2 * D) {
+        const bool key = col >= D;
+        const float* from = key ? parts + (int64_t)nq * D + col - D : parts + col;
+        const int n = key ? nk : nq;
 #pragma unroll 4
-        for (int i = y; i < n; i += 32) v += parts[(int64_t)i * 2 * D + col];
+        for (int i = y; i < n; i += 32) v += from[(int64_t)i * D];
+    }
     s[y][threadIdx.x % 32] = v;
     __syncthreads();
     if (y > 0 || col >= 2 * D) return;
@@ -424,34 +487,39 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const float* parts, i
 }
 
 // ---------------------------------------------------------------------------------------------------- cache read
+constexpr int kReadWarps = 4;        // of a CTA (8: 37 us for 32768 rows of 8 heads in 8 bits, 4: 35)
 struct Read {
     CacheView cache;
     const int64_t* slots;
     void *k, *v;
     int64_t ld_k, ld_v;
     int64_t T;
-    Shape shape;
+    int32_t across, down;
     int32_t n_heads, D;
 };
 
-// Heads are key heads, then value heads; a lane takes 16 neighbouring elements.
+// How a CTA's warps lie over heads (key heads, then value heads) and rows: `across` warps take neighbouring heads, `down` of
+// such rows of warps take neighbouring rows.  A lane takes 8 elements of each half of a head of kRows rows, `down`
+// apart.
 template <class Row8, int kLanes, int kRows, int kCache>
-__global__ void __launch_bounds__(kMaxThreads) cache_read_kernel(const Read a) {
+__global__ void __launch_bounds__(32 * kReadWarps) cache_read_kernel(const Read a) {
     grid_dep_launch();
     grid_dep_wait();
     constexpr bool kE4m3 = kCache == LORA_CACHE_E4M3;
-    const Spot<kLanes, kRows> spot(a.shape, blockIdx.x);
-    const bool value = spot.head >= a.n_heads;
-    const int head = value ? spot.head - a.n_heads : spot.head;
-    if (head >= a.n_heads || 16 * spot.lane >= a.D) return;
-    const char* from = (value ? a.cache.v : a.cache.k) + head * a.cache.head_stride + (kE4m3 ? 16 : 32) * spot.lane;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % kLanes;
+    const int both = ((int)blockIdx.y * a.across + warp % a.across) * (32 / kLanes) + threadIdx.x % 32 / kLanes;
+    const int64_t t0 = (int64_t)blockIdx.x * (a.down * kRows) + warp / a.across;
+    const bool value = both >= a.n_heads;
+    const int head = value ? both - a.n_heads : both;
+    if (head >= a.n_heads || 16 * lane >= a.D) return;
+    const char* from = (value ? a.cache.v : a.cache.k) + head * a.cache.head_stride + (kE4m3 ? 8 : 16) * lane;
     const float* scales = kE4m3 ? (value ? a.cache.vs : a.cache.ks) + head * a.cache.s_head : nullptr;
     uint4 q[kRows][kE4m3 ? 1 : 2];
     float sc[kRows];
     int64_t slot[kRows];
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
-        const int64_t t = spot.t0 + spot.row + k * a.shape.down;
+        const int64_t t = t0 + k * a.down;
         slot[k] = t < a.T ? a.slots[t] : -1;
     }
 #pragma unroll
@@ -461,14 +529,20 @@ __global__ void __launch_bounds__(kMaxThreads) cache_read_kernel(const Read a) {
         if (slot[k] < 0 || slot[k] >= a.cache.slots) continue;
         const RowPlace place(a.cache, slot[k]);
         if (kE4m3) sc[k] = scales[place.scale];
-        q[k][0] = *reinterpret_cast<const uint4*>(from + place.row);
-        if (!kE4m3) q[k][kE4m3 ? 0 : 1] = *reinterpret_cast<const uint4*>(from + place.row + 16);
+        if (kE4m3) {
+            const uint2 lo = *reinterpret_cast<const uint2*>(from + place.row);
+            const uint2 hi = *reinterpret_cast<const uint2*>(from + place.row + a.D / 2);
+            q[k][0] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        } else {
+            q[k][0] = *reinterpret_cast<const uint4*>(from + place.row);
+            q[k][kE4m3 ? 0 : 1] = *reinterpret_cast<const uint4*>(from + place.row + a.D);
+        }
     }
     void* to = value ? a.v : a.k;
-    const int64_t ld = value ? a.ld_v : a.ld_k, col = (int64_t)head * a.D + 16 * spot.lane;
+    const int64_t ld = value ? a.ld_v : a.ld_k, col = (int64_t)head * a.D + 8 * lane;
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
-        const int64_t t = spot.t0 + spot.row + k * a.shape.down;
+        const int64_t t = t0 + k * a.down;
         if (t >= a.T) continue;
         float x[8];
 #pragma unroll
@@ -480,7 +554,7 @@ __global__ void __launch_bounds__(kMaxThreads) cache_read_kernel(const Read a) {
                 b.q = q[k][kE4m3 ? 0 : i];
                 b.get(x);
             }
-            Row8::store(to, t * ld + col + 8 * i, x);
+            Row8::store(to, t * ld + col + (i ? a.D / 2 : 0), x);
         }
     }
 }
@@ -501,24 +575,48 @@ cudaError_t by_type(lora_dtype_t dt, Go go) {
     return dt == LORA_BF16 ? go(Row8Bf16()) : go(Row8F32());
 }
 
-// CTAs of up to eight warps: the heads in equal shares across, and as many rows of warps as are left room for.
-struct Launch {
-    Shape shape;
-    unsigned y;
-};
-Launch launch_of(int heads, int D, int64_t T) {
-    const int per_warp = 32 / lanes_of(D), all = (heads + per_warp - 1) / per_warp;
-    Launch l;
-    l.y = (unsigned)((all + 7) / 8);
-    l.shape.across = (all + (int)l.y - 1) / (int)l.y;
-    l.shape.down = (int)std::min<int64_t>(8 / l.shape.across, T);
-    return l;
+constexpr unsigned kMaxParts = kCtas * 152 + kMaxHeads;   // CTAs of a backward that sums the weights' gradients
+
+// Chunks of one step of heads where all warps then fit the SMs at once.  Else as many steps, of those that fit a row's place,
+// as waste the least: an empty head costs as much as a full one, and a chunk's angles as much as 0.6 steps.
+Chunks chunks_of(int hq, int hk, int hv, int D, int64_t T, int bytes_per_head) {
+    const int across = 32 / lanes_of(D);
+    Chunks c{{hq, hk, hv}, across};
+    if (T * c.all() <= 152ll * kCtas * kMaxWarps) return c;
+    Chunks best = c;
+    double least = 1e30;
+    for (int steps = 1; steps * across * bytes_per_head <= kRowBytes; ++steps) {
+        c.per = steps * across;
+        const double cost = c.all() * (steps + 0.6);
+        if (cost < least) {
+            least = cost;
+            best = c;
+        }
+    }
+    return best;
 }
-unsigned threads_of(const Launch& l) { return (unsigned)(32 * l.shape.across * l.shape.down); }
-// Rows that a lane takes: one where all CTAs fit a round on the SMs, `most` else.
-bool one_row(const Launch& l, int64_t T) { return T * l.y * threads_of(l) <= 152ll * 1024 * l.shape.down; }
-int64_t blocks(const Launch& l, int64_t T, int rows) { return (T + l.shape.down * rows - 1) / (l.shape.down * rows); }
-size_t angle_bytes(const Launch& l, int rows, int rot) { return (size_t)l.shape.down * rows * rot * sizeof(float); }
+// A launch's grid: across the rows as many CTAs as the SMs hold at once, or as there are rows for
+struct Launch {
+    dim3 grid;
+    unsigned threads;
+    size_t smem;
+};
+Launch launch_of(const Chunks& c, int64_t T) {
+    const unsigned w = (unsigned)std::min<int64_t>(kMaxWarps, T), y = (unsigned)c.all();
+    const unsigned n = (unsigned)std::min<int64_t>((T + w - 1) / w, std::max(1u, 152u * kCtas / y));
+    return Launch{dim3(n, y), 32 * w, w * sizeof(WarpPlace)};
+}
+template <class K, class A>
+cudaError_t launch_rows(K kernel, const Launch& l, cudaStream_t st, const A& a) {
+    if (l.smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)l.smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(kernel, l.grid, dim3(l.threads), l.smem, st, a);
+}
+bool turned_whole(int D, int lanes, const Turns& t) { return D == 16 * lanes && t.rot == D && !t.interleaved; }
+// what a head's lanes take of a row's place, in bytes: 16 elements each
+int bytes_of(lora_dtype_t dt, int D) { return 16 * lanes_of(D) * elem_size(dt); }
 
 int check_rotary(const char* fn, int32_t T, lora_dtype_t dt, const lora_rotary_t* r) {
     const std::string f(fn);
@@ -547,20 +645,20 @@ int check_slots(const char* fn, const int64_t* slots) {
 }
 
 template <class Row8, int kCache>
-cudaError_t launch_forward(Forward a, cudaStream_t st) {
+cudaError_t launch_forward(const Forward& a, cudaStream_t st) {
     return by_lanes(a.D, [&](auto lanes) {
-        const Launch l = launch_of(a.heads, a.D, a.T);
-        a.shape = l.shape;
-        auto go = [&](auto rows) {
-            constexpr int kRows = decltype(rows)::value;
-            return launch_pdl(rotary_kernel<Row8, decltype(lanes)::value, kRows, kCache>,
-                              dim3((unsigned)blocks(l, a.T, kRows), l.y), dim3(threads_of(l)),
-                              angle_bytes(l, kRows, a.turns.rot), st, a);
-        };
-        return one_row(l, a.T) ? go(std::integral_constant<int, 1>()) : go(std::integral_constant<int, 4>());
+        constexpr int kLanes = decltype(lanes)::value;
+        const Launch l = launch_of(a.chunks, a.T);
+        if (turned_whole(a.D, kLanes, a.turns)) return launch_rows(rotary_kernel<Row8, kLanes, kTurned, kCache>, l, st, a);
+        if constexpr (kCache >= 0)
+            if (a.D == 16 * kLanes && a.turns.rot == 0)
+                return launch_rows(rotary_kernel<Row8, kLanes, kPlain, kCache>, l, st, a);
+        return launch_rows(rotary_kernel<Row8, kLanes, kAny, kCache>, l, st, a);
     });
 }
-cudaError_t forward(lora_dtype_t dt, int cache, const Forward& a, cudaStream_t st) {
+cudaError_t forward(lora_dtype_t dt, int cache, Forward a, cudaStream_t st) {
+    const int32_t* h = a.chunks.heads;
+    a.chunks = chunks_of(h[kQuery], h[kKey], h[kValue], a.D, a.T, bytes_of(dt, a.D));
     return by_type(dt, [&](auto row) {
         using Row8 = decltype(row);
         return cache < 0 ? launch_forward<Row8, -1>(a, st)
@@ -568,8 +666,6 @@ cudaError_t forward(lora_dtype_t dt, int cache, const Forward& a, cudaStream_t s
                                                     : launch_forward<Row8, LORA_CACHE_E4M3>(a, st);
     });
 }
-
-constexpr unsigned kMaxParts = 608;  // CTAs of a backward that sums the weights' gradients: four on each SM
 
 }  // namespace
 }  // namespace lora
@@ -592,10 +688,10 @@ extern "C" int lora_rotary_forward(int32_t T, lora_dtype_t dt, const lora_rotary
         }
         if (T == 0) return LORA_OK;
         const int64_t D = r->head_dim, all = (int64_t)(r->n_heads + r->n_kv_heads) * D;
-        a.out_heads = cache && !keep_keys ? r->n_heads : r->n_heads + r->n_kv_heads;
+        a.out_keys = !cache || keep_keys;
         const int es = elem_size(dt);
         if ((rc = check_matrix(fn, "x", x, all, ld_x, es)) != LORA_OK) return rc;
-        if ((rc = check_matrix(fn, "out", out, a.out_heads * D, ld_out, es)) != LORA_OK) return rc;
+        if ((rc = check_matrix(fn, "out", out, a.out_keys ? all : r->n_heads * D, ld_out, es)) != LORA_OK) return rc;
         if (T > 1 && out == x && ld_out != ld_x)
             return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": in place, ld_out must be ld_x");
         if (cache) {
@@ -608,8 +704,8 @@ extern "C" int lora_rotary_forward(int32_t T, lora_dtype_t dt, const lora_rotary
         a.x = x; a.ld_x = ld_x; a.v = v; a.ld_v = ld_v; a.out = out; a.ld_out = ld_out;
         a.wq = r->q_weight; a.wk = r->k_weight; a.slots = slots;
         a.turns = Turns{positions, r->turns, r->rot_dim, r->interleaved != 0};
-        a.T = T; a.hq = r->n_heads; a.hk = r->n_kv_heads;
-        a.heads = r->n_heads + r->n_kv_heads * (cache ? 2 : 1);
+        a.T = T;
+        a.chunks = Chunks{{r->n_heads, r->n_kv_heads, cache ? r->n_kv_heads : 0}, 0};
         a.D = (int32_t)D; a.eps = r->eps; a.inv_d = 1.f / (float)D;
         return enqueued(fn, forward(dt, cache ? cache->dtype : -1, a, static_cast<cudaStream_t>(stream)));
     });
@@ -618,7 +714,7 @@ extern "C" int lora_rotary_forward(int32_t T, lora_dtype_t dt, const lora_rotary
 extern "C" size_t lora_rotary_workspace_size(int32_t T, const lora_rotary_t* r) {
     const int64_t n = guarded([&]() -> int64_t {
         if (check_rotary("lora_rotary_workspace_size", T, LORA_BF16, r) != LORA_OK) return 0;
-        return (int64_t)kMaxParts * 2 * r->head_dim * sizeof(float);
+        return (int64_t)kMaxParts * r->head_dim * sizeof(float);
     });
     return n > 0 ? (size_t)n : 0;
 }
@@ -636,7 +732,7 @@ extern "C" int lora_rotary_backward(int32_t T, lora_dtype_t dt, const lora_rotar
         if ((dq_weight && !r->q_weight) || (dk_weight && !r->k_weight))
             return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": the gradient of a weight that is not given");
         if (weights && (!workspace || !is_aligned(workspace, 16) ||
-                        ws_bytes < (size_t)kMaxParts * 2 * D * sizeof(float)))
+                        ws_bytes < (size_t)kMaxParts * D * sizeof(float)))
             return refuse(LORA_ERR_WORKSPACE, std::string(fn) + ": workspace missing, too small or not 16-byte aligned");
         cudaStream_t st = static_cast<cudaStream_t>(stream);
         const int es = elem_size(dt);
@@ -657,39 +753,32 @@ extern "C" int lora_rotary_backward(int32_t T, lora_dtype_t dt, const lora_rotar
         a.x = x; a.ld_x = ld_x; a.dout = dout; a.ld_dout = ld_dout; a.dx = dx; a.ld_dx = ld_dx;
         a.wq = r->q_weight; a.wk = r->k_weight; a.parts = static_cast<float*>(workspace);
         a.turns = Turns{positions, r->turns, r->rot_dim, r->interleaved != 0};
-        a.T = T; a.hq = r->n_heads; a.heads = r->n_heads + r->n_kv_heads;
+        a.T = T;
         a.D = (int32_t)D; a.eps = r->eps; a.inv_d = 1.f / (float)D;
-        int parts = 0;
+        int nq = 0, nk = 0;
         cudaError_t e = cudaSuccess;
         if (T > 0)
             e = by_type(dt, [&](auto row) {
                 using Row8 = decltype(row);
                 return by_lanes(a.D, [&](auto lanes) {
-                    const Launch l = launch_of(a.heads, a.D, a.T);
-                    a.shape = l.shape;
-                    auto go = [&](auto rows, auto nrm, auto wts) {
-                        constexpr int kRows = decltype(rows)::value;
-                        constexpr bool kWeights = decltype(wts)::value;
-                        a.n_blocks = blocks(l, a.T, kRows);
-                        const int64_t n = kWeights ? std::min<int64_t>(a.n_blocks, std::max(1u, kMaxParts / l.y)) : a.n_blocks;
-                        parts = (int)(n * l.y);
-                        return launch_pdl(rotary_backward_kernel<Row8, decltype(lanes)::value, kRows, decltype(nrm)::value,
-                                                                 kWeights>,
-                                          dim3((unsigned)n, l.y), dim3(threads_of(l)), angle_bytes(l, kRows, a.turns.rot), st,
-                                          a);
+                    constexpr int kLanes = decltype(lanes)::value;
+                    a.chunks = chunks_of(r->n_heads, r->n_kv_heads, 0, a.D, T, (norm ? 2 : 1) * bytes_of(dt, a.D));
+                    const Launch l = launch_of(a.chunks, T);
+                    nq = (int)l.grid.x * a.chunks.of(kQuery);
+                    nk = (int)l.grid.x * a.chunks.of(kKey);
+                    auto go = [&](auto nrm, auto wts) {
+                        constexpr bool kNorm = decltype(nrm)::value, kWeights = decltype(wts)::value;
+                        return turned_whole(a.D, kLanes, a.turns)
+                                   ? launch_rows(rotary_backward_kernel<Row8, kLanes, kTurned, kNorm, kWeights>, l, st, a)
+                                   : launch_rows(rotary_backward_kernel<Row8, kLanes, kAny, kNorm, kWeights>, l, st, a);
                     };
-                    auto sized = [&](auto nrm, auto wts) {
-                        return one_row(l, a.T) ? go(std::integral_constant<int, 1>(), nrm, wts)
-                                               : go(std::integral_constant<int, 2>(), nrm, wts);
-                    };
-                    return !norm ? sized(std::false_type(), std::false_type())
-                                 : !weights ? sized(std::true_type(), std::false_type())
-                                            : sized(std::true_type(), std::true_type());
+                    return !norm ? go(std::false_type(), std::false_type())
+                                 : !weights ? go(std::true_type(), std::false_type()) : go(std::true_type(), std::true_type());
                 });
             });
         if (e == cudaSuccess && weights)
             e = launch_pdl(weight_grad_kernel, dim3((unsigned)((2 * D + 31) / 32)), dim3(1024), 0, st,
-                           static_cast<const float*>(workspace), parts, (int)D, dq_weight, dk_weight);
+                           static_cast<const float*>(workspace), nq, nk, (int)D, dq_weight, dk_weight);
         return enqueued(fn, e);
     });
 }
@@ -710,7 +799,7 @@ extern "C" int lora_cache_write(int32_t T, lora_dtype_t dt, const void* k, int64
         if ((rc = check_matrix(fn, "v", v, cols, ld_v, elem_size(dt))) != LORA_OK) return rc;
         if ((rc = check_slots(fn, slots)) != LORA_OK) return rc;
         a.x = k; a.ld_x = ld_k; a.v = v; a.ld_v = ld_v; a.slots = slots;
-        a.T = T; a.hk = cache->n_heads; a.heads = 2 * cache->n_heads; a.D = cache->head_dim;
+        a.T = T; a.chunks = Chunks{{0, cache->n_heads, cache->n_heads}, 0}; a.D = cache->head_dim;
         return enqueued(fn, forward(dt, cache->dtype, a, static_cast<cudaStream_t>(stream)));
     });
 }
@@ -736,16 +825,21 @@ extern "C" int lora_cache_read(int32_t T, lora_dtype_t dt, const lora_cache_t* c
         return enqueued(fn, by_type(dt, [&](auto row) {
             using Row8 = decltype(row);
             return by_lanes(a.D, [&](auto lanes) {
-                const Launch l = launch_of(2 * a.n_heads, a.D, a.T);
-                a.shape = l.shape;
+                // the heads in equal shares across, and as many rows of warps as are left room for
+                const int per_warp = 32 / decltype(lanes)::value, all = (2 * a.n_heads + per_warp - 1) / per_warp;
+                const int y = (all + kReadWarps - 1) / kReadWarps;
+                a.across = (all + y - 1) / y;
+                a.down = (int)std::min<int64_t>(kReadWarps / a.across, T);
                 auto go = [&](auto rows, auto c) {
                     constexpr int kRows = decltype(rows)::value;
+                    const int64_t n = (T + a.down * kRows - 1) / (a.down * kRows);
                     return launch_pdl(cache_read_kernel<Row8, decltype(lanes)::value, kRows, decltype(c)::value>,
-                                      dim3((unsigned)blocks(l, a.T, kRows), l.y), dim3(threads_of(l)), 0, st, a);
+                                      dim3((unsigned)n, (unsigned)y), dim3((unsigned)(32 * a.across * a.down)), 0, st, a);
                 };
+                // a row a lane where all of them fit the SMs at once, else four
                 auto sized = [&](auto c) {
-                    return one_row(l, a.T) ? go(std::integral_constant<int, 1>(), c)
-                                           : go(std::integral_constant<int, 4>(), c);
+                    return a.T * y * a.across <= 152ll * 32 ? go(std::integral_constant<int, 1>(), c)
+                                                            : go(std::integral_constant<int, 4>(), c);
                 };
                 return cache->dtype == LORA_CACHE_BF16 ? sized(std::integral_constant<int, LORA_CACHE_BF16>())
                                                        : sized(std::integral_constant<int, LORA_CACHE_E4M3>());
