@@ -1028,7 +1028,7 @@ def rotary_backward(x, positions, turns, n_heads, n_kv_heads, dout, q_weight=Non
             n = library().lora_rotary_workspace_size(T, r)
             if n == 0:
                 raise LoraError(-1, library().lora_last_error().decode())
-            workspace = torch.empty(n, dtype=torch.uint8, device=dout.device)
+            workspace = _stream_workspace("rotary", n, 0, _stream_ptr(None), dout.device)
     _one_device(dout, x, positions, turns, q_weight, k_weight, dx, workspace)
     rc = library().lora_rotary_backward(T, code, r, _ptr(x), ld, _ptr(positions), dout.data_ptr(), ldd, dx.data_ptr(), ldx,
                                         _ptr(dq), _ptr(dk), _ptr(workspace), 0 if workspace is None else workspace.numel(),
@@ -1093,23 +1093,24 @@ def _decode_size(n_heads, kv_heads, D, e4m3, device):
     return int(n)
 
 
-DECODE_COUNTER_BYTES = 8192    # of a decode workspace: zero before its first use
-_decode_workspaces = {}
+DECODE_COUNTER_BYTES = 8192     # of a decode workspace: zero before its first use
+_stream_workspaces = {}
 
 
-def _decode_workspace(n, stream_ptr, device):
-    """A stream's own workspace of at least n bytes: calls on one stream run one after another and leave its counters
-    zero.  While a CUDA graph is captured, a new one, whose counters the graph itself clears: its replays may run beside
-    the stream's later calls."""
+def _stream_workspace(kind, n, zero, stream_ptr, device):
+    """A stream's own workspace of at least n bytes for calls of one kind, its first `zero` bytes zero at first: calls on
+    one stream run one after another.  While a CUDA graph is captured, a new one, which the graph itself clears: its replays
+    may run beside the stream's later calls."""
     import torch
     capturing = torch._C._cuda_isCurrentStreamCapturing()
-    key = (device.index, stream_ptr)
-    ws = None if capturing else _decode_workspaces.get(key)
+    key = (kind, device.index, stream_ptr)
+    ws = None if capturing else _stream_workspaces.get(key)
     if ws is None or ws.numel() < n:
         ws = torch.empty(n, dtype=torch.uint8, device=device)
-        ws[:DECODE_COUNTER_BYTES].zero_()
+        if zero:
+            ws[:zero].zero_()
         if not capturing:
-            _decode_workspaces[key] = ws
+            _stream_workspaces[key] = ws
     return ws
 
 
@@ -1143,7 +1144,8 @@ def decode_attention(q, cache, page_table, lengths, scale=None, window=0, softca
     _one_device(q, page_table, lengths, out, workspace, *held)
     st = _stream_ptr(None)
     if workspace is None:
-        workspace = _decode_workspace(_decode_size(n_heads, kv_heads, D, len(held) == 4, q.get_device()), st, q.device)
+        workspace = _stream_workspace("decode", _decode_size(n_heads, kv_heads, D, len(held) == 4, q.get_device()),
+                                      DECODE_COUNTER_BYTES, st, q.device)
     rc = library().lora_decode_attention(B, n_heads, q.data_ptr(), ldq, c, page_table.data_ptr(), ldt, page_table.shape[1],
                                          lengths.data_ptr(), window, D ** -0.5 if scale is None else scale, softcap,
                                          out.data_ptr(), ldo, _ptr(lse), workspace.data_ptr(), workspace.numel(), st)
