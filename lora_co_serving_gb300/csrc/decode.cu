@@ -11,8 +11,8 @@
 //           tokens are rows, are turned around by the transposing move of 8 x 8 numbers.
 // Every warp copies its rows into shared memory two steps ahead of their use, asynchronously, 512 neighbouring bytes at a
 // time, and reads them back as its lanes need them: a barrier within the warp is all that it takes.  (Lanes that copied
-// their own pieces, 64 bytes of 8 rows at a time, needed one and a half times the requests to L2: 236 us instead of @ for
-// 64 x 8192 tokens in bf16.)
+// their own pieces, 64 bytes of 8 rows at a time, needed one and a half times the requests to L2: 236 us instead of 188
+// for 64 x 8192 tokens in bf16.)
 // Work is counted in tiles of 32 to 128 tokens of one sequence and one cache head.  All tiles of a call form one line, and
 // each CTA takes an equal piece of it, whatever the lengths are; a CTA's warps take 16 or 32 tokens of a tile each, with a
 // running maximum and sum of their own, and the copies run on from one sequence into the next.  A sequence and head whose
@@ -291,7 +291,7 @@ struct Warp {
 // A group's queries as B operands, in the order of elements that Warp::scores takes; 8-bit caches: as fp16, scaled by a
 // power of two that brings the largest element to between 2^14 and 2^15, so that what bf16 holds stays exact down to 2^-31
 // of it.  (The MMAs that take e4m3 convert to fp16 themselves, and again for each call: queries split into two e4m3 numbers
-// took 135 us instead of @ for 256 x 2048 tokens.)
+// took 135 us instead of 110 for 256 x 2048 tokens.)
 template <class S>
 struct Query {
     uint32_t reg[S::kCols][S::kPart / 8];
@@ -374,8 +374,8 @@ __device__ __forceinline__ Joined join_parts(int n, int row, int d, At at) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             const float* from = at(min(k0 + k, n - 1));
-            ml[k] = *reinterpret_cast<const float2*>(from + 2 * row);
-            x[k] = *reinterpret_cast<const float4*>(from + 2 * S::kRows + row * S::kD + d);
+            ml[k] = __ldcg(reinterpret_cast<const float2*>(from + 2 * row));      // other CTAs' writes: not from L1
+            x[k] = __ldcg(reinterpret_cast<const float4*>(from + 2 * S::kRows + row * S::kD + d));
         }
         float m = r.m;
 #pragma unroll
@@ -807,7 +807,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
     copies_wait<0>();
 }
 
-
 // ---------------------------------------------------------------------------------------------------------- host
 // counters of the items' first CTAs and of each eight; of an item's eights, at its first CTA
 constexpr size_t kCounterBytes = LORA_DECODE_COUNTER_BYTES;
@@ -831,7 +830,7 @@ auto by_shape(bool e4m3, int D, int rows, Go go) {
     auto with_rows = [&](auto t, auto d) {
         constexpr bool kE4m3 = decltype(t)::value;
         constexpr int kD = decltype(d)::value;
-                return rows <= 8 ? go(Shapes<kE4m3, kD, 8>()) : go(Shapes<kE4m3, kD, 16>());
+        return rows <= 8 ? go(Shapes<kE4m3, kD, 8>()) : go(Shapes<kE4m3, kD, 16>());
     };
     auto with_size = [&](auto t) {
         return D <= 64 ? with_rows(t, std::integral_constant<int, 64>())

@@ -110,7 +110,9 @@ __device__ __forceinline__ void read8(const float* from, float (&v)[8]) {
 
 // A warp's place in shared memory: two rows of a chunk's pieces, [piece][lane] of 16 bytes, so that each lane reads back what
 // it copied; the rows' positions and slots; a row's angles.
-constexpr int kRowBytes = 3072;      // 8192 rows of 72 heads: 1024 bytes 64 us, 2048 and 3072 54, 4096 57
+constexpr int kRowBytes = 4096;       // a step of float32 heads, with their gradients, at the most
+constexpr int kChunkBytes = 3072;     // that chunks of more steps take (8192 rows of 72 heads: 1024 64 us, 2048 and 3072 54,
+                                      // 4096 57)
 struct WarpPlace {
     uint4 piece[2][kRowBytes / 16];
     int64_t position[2], slot[2];
@@ -584,8 +586,8 @@ Chunks chunks_of(int hq, int hk, int hv, int D, int64_t T, int bytes_per_head) {
     Chunks c{{hq, hk, hv}, across};
     if (T * c.all() <= 152ll * kCtas * kMaxWarps) return c;
     Chunks best = c;
-    double least = 1e30;
-    for (int steps = 1; steps * across * bytes_per_head <= kRowBytes; ++steps) {
+    double least = c.all() * 1.6;
+    for (int steps = 2; steps * across * bytes_per_head <= kChunkBytes; ++steps) {
         c.per = steps * across;
         const double cost = c.all() * (steps + 0.6);
         if (cost < least) {
@@ -615,7 +617,9 @@ cudaError_t launch_rows(K kernel, const Launch& l, cudaStream_t st, const A& a) 
     return launch_pdl(kernel, l.grid, dim3(l.threads), l.smem, st, a);
 }
 bool turned_whole(int D, int lanes, const Turns& t) { return D == 16 * lanes && t.rot == D && !t.interleaved; }
-// what a head's lanes take of a row's place, in bytes: 16 elements each
+// what a head's lanes take of a row's place, in bytes: 16 elements each; a step of 32 lanes is 4 KB with x in float32 beside
+// the gradient
+static_assert(2 * 32 * 16 * sizeof(float) <= kRowBytes, "a step fits a row's place");
 int bytes_of(lora_dtype_t dt, int D) { return 16 * lanes_of(D) * elem_size(dt); }
 
 int check_rotary(const char* fn, int32_t T, lora_dtype_t dt, const lora_rotary_t* r) {

@@ -255,6 +255,33 @@ class TestBinding:
         self.refused("one CUDA device", d, q, c, table, n)
 
 
+def test_other_devices_are_refused(monkeypatch):
+    """As if every tensor lay on a device that is not the current one: no call reaches the library."""
+    class NoCalls:
+        def __getattr__(self, name):
+            if name in ("lora_rotary_workspace_size", "lora_last_error"):          # host functions
+                return getattr(real, name)
+            raise AssertionError(name + " was called")
+
+    lm.build()
+    real = lm.library()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: False, raising=False)
+    monkeypatch.setattr(lm, "_stream_ptr", lambda stream: 0)
+    monkeypatch.setattr(lm, "library", lambda: NoCalls())
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 1)
+    bf = torch.bfloat16
+    x, pos, w = torch.zeros(3, 128, dtype=bf), torch.zeros(3, dtype=torch.int64), torch.ones(32, dtype=bf)
+    turns, c = lm.rotary_turns(32, device="cpu"), lm.kv_cache(4, 2, 8, 32, device="cpu")
+    n = torch.ones(3, dtype=torch.int32)
+    for call in (lambda: lm.rotary_forward(x, pos, turns, 2, 2), lambda: lm.rotary_backward(None, pos, turns, 2, 2, x),
+                 lambda: lm.rotary_backward(x, pos, turns, 2, 2, x, q_weight=w, weight_grads=True),
+                 lambda: lm.cache_write(x[:, :64], x[:, :64], c, pos), lambda: lm.cache_read(c, pos),
+                 lambda: lm.decode_attention(x, c, torch.zeros(3, 2, dtype=torch.int32), n)):
+        with pytest.raises(ValueError, match="the current one"):
+            call()
+
+
 def test_turns_are_the_frequencies():
     """Whole-number turns against the angles of float64 products, where those are good: positions below 2^20."""
     from attention_oracle import angles, frequencies

@@ -268,3 +268,16 @@ def test_graphs():
     graphs[1].replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for o in outs for a, b in zip(eager, o))
+
+
+def test_a_cache_without_pages():
+    """Sequences that claim rows of a cache that has none get NaN, those without rows zeros; nothing is read."""
+    for dtype in (bf16, torch.float8_e4m3fn):
+        cache = lm.kv_cache(0, 2, 16, 64, dtype)
+        q = torch.ones(3, 256, dtype=bf16, device="cuda")
+        n = torch.tensor([0, 5, 300], dtype=torch.int32).cuda()
+        out, lse = lm.decode_attention(q, cache, torch.zeros(3, 20, dtype=torch.int32).cuda(), n, want_lse=True)
+        assert (out[0] == 0).all() and out[1:].isnan().all() and lse[1:].isnan().all()
+        slots = torch.tensor([0, -1, 7]).cuda()
+        assert (lm.cache_read(cache, slots)[0] == 0).all()
+        lm.cache_write(q[:, :128], q[:, :128], cache, slots)

@@ -6,8 +6,8 @@ Tolerances, in half steps u = 2^-24 of float32, before the one rounding to the o
   angle     a whole number of 2^-32 turns of at most an eighth: 1.5e-9 + half a step of pi / 4, 1 u; sine and cosine 2 units
             (4 u): 5 u; three roundings in a c - b s.  Together 26 u (|a| + |b|).  REACH = 32.
   gradient  the same for g; then w g, its sum with x r (21), and f (w g - x r mean): 64 u of f (|w g| + |x r| mean |w g x r|)
-  weights   a term g x r is 50 u off; a thread adds at most 40 of them in the cases here, then at most 5 shuffles, 8 warps,
-            19 + 32 CTAs: 104 u.  Together 160 u of the sum of magnitudes.
+  weights   a term g x r is 50 u off; a lane adds at most 40 of them in the cases here, then come the 8 x 8 lanes and warps
+            of a CTA, and 10 + 32 of the CTAs: at most 110 u, of a sum that has as many.  Together 160 u of the magnitudes.
 """
 import pytest
 import torch
@@ -118,6 +118,21 @@ def test_forward(c):
     assert torch.equal(k.x, before)
     again = lm.rotary_forward(k.x, *k.args, **k.kw, out=k.x)       # in place, in its wider rows
     assert again.data_ptr() == k.x.data_ptr() and torch.equal(out, k.x)
+
+
+# rows and heads enough that a warp takes several rows, and chunks of several steps
+MANY = [dict(T=3000, hq=12, hk=4, D=128, dtype=F32), dict(T=2500, hq=30, hk=3, D=64, dtype=BF), dict(T=1500, hq=6, hk=6, D=256, dtype=F32),
+        dict(T=2600, hq=9, hk=2, D=80, dtype=F32, interleaved=True, pad=16), dict(T=1700, hq=72, hk=1, D=96, dtype=BF, rot=32)]
+
+
+@pytest.mark.parametrize("c", MANY, ids=ids)
+def test_forward_of_many_rows(c):
+    test_forward(c)
+
+
+@pytest.mark.parametrize("c", MANY, ids=ids)
+def test_backward_of_many_rows(c):
+    test_backward(c)
 
 
 @pytest.mark.parametrize("c", CASES, ids=ids)
