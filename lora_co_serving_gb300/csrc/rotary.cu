@@ -141,9 +141,8 @@ __device__ __forceinline__ void read_pieces(const uint4* pieces, int at, float (
     reinterpret_cast<const Row8*>(q)->get(v);
 }
 
-// What is known of a head beforehand: nothing; that it fills its lanes (D = 16 kLanes) and is turned whole, in halves; or
-// that it fills them and is not turned.  The known forms take two thirds of the instructions.
-enum Form { kAny, kTurned, kPlain };
+// What is known of a head beforehand: nothing, or that it fills its lanes (D = 16 kLanes) and is turned whole, in halves.
+enum Form { kAny, kTurned };
 
 // The two pieces of a head's row that a lane holds: from elements at0 and at1
 struct LanePieces {
@@ -151,10 +150,9 @@ struct LanePieces {
     static __device__ __forceinline__ LanePieces of(int lane, int D, const Turns& a) {
         LanePieces p(lane, D, a);
         if (kForm == kAny) return p;
-        p.in = true;
-        p.turned = kForm == kTurned;
-        p.at0 = kForm == kTurned ? 8 * lane : 16 * lane;
-        p.at1 = p.at0 + (kForm == kTurned ? 8 * kLanes : 8);
+        p.in = p.turned = true;
+        p.at0 = 8 * lane;
+        p.at1 = 8 * (kLanes + lane);
         return p;
     }
     int at0, at1;
@@ -241,7 +239,7 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) rotary_kernel(const Forwar
     const Chunk chunk(a.chunks, blockIdx.y);
     const int lane = threadIdx.x % kLanes, sub = threadIdx.x % 32 / kLanes;
     const bool value = chunk.kind == kValue, keeps = kCache >= 0 && chunk.kind != kQuery;
-    const bool to_out = chunk.kind == kQuery || (chunk.kind == kKey && a.out_keys), turned = kForm != kPlain && a.turns.rot > 0 && !value;
+    const bool to_out = chunk.kind == kQuery || (chunk.kind == kKey && a.out_keys), turned = a.turns.rot > 0 && !value;
     const int D = kForm != kAny ? 16 * kLanes : a.D, steps = (chunk.heads + kAcross - 1) / kAcross;
     const LanePieces p = LanePieces::of<kLanes, kForm>(lane, D, a.turns);
     const int heads = p.in ? chunk.heads - sub : 0;      // this lane's are 0, kAcross, 2 kAcross, .. below that
@@ -488,9 +486,9 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const float* parts, i
     if (to) to[col % D] = v;
 }
 
-// ---------------------------------------------------------------------------------------------------- cache read
-constexpr int kReadWarps = 4;        // of a CTA (8: 37 us for 32768 rows of 8 heads in 8 bits, 4: 35)
-struct Read {
+// ------------------------------------------------------------------------------------------------------ cache rows
+constexpr int kCacheWarps = 4;        // of a CTA (8: 37 us to read 32768 rows of 8 heads in 8 bits, 4: 34)
+struct Rows {
     CacheView cache;
     const int64_t* slots;
     void *k, *v;
@@ -504,7 +502,7 @@ struct Read {
 // such rows of warps take neighbouring rows.  A lane takes 8 elements of each half of a head of kRows rows, `down`
 // apart.
 template <class Row8, int kLanes, int kRows, int kCache>
-__global__ void __launch_bounds__(32 * kReadWarps) cache_read_kernel(const Read a) {
+__global__ void __launch_bounds__(32 * kCacheWarps) cache_read_kernel(const Rows a) {
     grid_dep_launch();
     grid_dep_wait();
     constexpr bool kE4m3 = kCache == LORA_CACHE_E4M3;
@@ -557,6 +555,58 @@ __global__ void __launch_bounds__(32 * kReadWarps) cache_read_kernel(const Read 
                 b.get(x);
             }
             Row8::store(to, t * ld + col + (i ? a.D / 2 : 0), x);
+        }
+    }
+}
+
+// The same the other way: rows are rounded, or quantized by the head's lanes together, and written to their slots.
+template <class Row8, int kLanes, int kRows, int kCache>
+__global__ void __launch_bounds__(32 * kCacheWarps) cache_write_kernel(const Rows a) {
+    grid_dep_launch();
+    grid_dep_wait();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % kLanes;
+    const int both = ((int)blockIdx.y * a.across + warp % a.across) * (32 / kLanes) + threadIdx.x % 32 / kLanes;
+    const int64_t t0 = (int64_t)blockIdx.x * (a.down * kRows) + warp / a.across;
+    const bool value = both >= a.n_heads;
+    const int head = value ? both - a.n_heads : both;
+    const bool in = head < a.n_heads && 16 * lane < a.D;
+    const void* from = value ? a.v : a.k;
+    const int64_t ld = value ? a.ld_v : a.ld_k, col = (int64_t)head * a.D + 8 * lane;
+    Row8 r[kRows][2];
+    int64_t slot[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+        const int64_t t = t0 + k * a.down;
+        r[k][0].zero();
+        r[k][1].zero();
+        slot[k] = -1;
+        if (in && t < a.T) {
+            r[k][0].load(from, t * ld + col);
+            r[k][1].load(from, t * ld + col + a.D / 2);
+            slot[k] = a.slots[t];
+        }
+    }
+    constexpr int kElement = kCache == LORA_CACHE_E4M3 ? 1 : 2;
+    char* const to = (value ? a.cache.v : a.cache.k) + head * a.cache.head_stride + 8 * lane * kElement;
+    float* const scales = kCache == LORA_CACHE_E4M3 ? (value ? a.cache.vs : a.cache.ks) + head * a.cache.s_head : nullptr;
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+        uint32_t amax = 0;
+        if (kCache == LORA_CACHE_E4M3) amax = max_over_lanes<kLanes>(max(r[k][0].abs_max(), r[k][1].abs_max()));
+        if (slot[k] < 0 || slot[k] >= a.cache.slots) continue;
+        const RowPlace place(a.cache, slot[k]);
+        float y[8], z[8];
+        r[k][0].get(y);
+        r[k][1].get(z);
+        if (kCache == LORA_CACHE_BF16) {
+            Row8Bf16::store(to + place.row, 0, y);
+            Row8Bf16::store(to + place.row, a.D / 2, z);
+        } else {
+            float inv;
+            const float sc = block_scale(amax, &inv);
+            *reinterpret_cast<uint2*>(to + place.row) = encode8(y, inv);
+            *reinterpret_cast<uint2*>(to + place.row + a.D / 2) = encode8(z, inv);
+            if (lane == 0) scales[place.scale] = sc;
         }
     }
 }
@@ -622,6 +672,32 @@ bool turned_whole(int D, int lanes, const Turns& t) { return D == 16 * lanes && 
 static_assert(2 * 32 * 16 * sizeof(float) <= kRowBytes, "a step fits a row's place");
 int bytes_of(lora_dtype_t dt, int D) { return 16 * lanes_of(D) * elem_size(dt); }
 
+// kernel(type, lanes, rows a lane, cache's type) over the rows of a cache
+template <class Kernel>
+cudaError_t launch_cache_rows(lora_dtype_t dt, int cache, Rows a, Kernel kernel, cudaStream_t st) {
+    return by_type(dt, [&](auto row) {
+        return by_lanes(a.D, [&](auto lanes) {
+            // the heads in equal shares across, and as many rows of warps as are left room for
+            const int per_warp = 32 / decltype(lanes)::value, all = (2 * a.n_heads + per_warp - 1) / per_warp;
+            const int y = (all + kCacheWarps - 1) / kCacheWarps;
+            a.across = (all + y - 1) / y;
+            a.down = (int)std::min<int64_t>(kCacheWarps / a.across, a.T);
+            auto go = [&](auto rows, auto c) {
+                const int64_t per = (int64_t)a.down * decltype(rows)::value;
+                return launch_pdl(kernel(row, lanes, rows, c), dim3((unsigned)((a.T + per - 1) / per), (unsigned)y),
+                                  dim3((unsigned)(32 * a.across * a.down)), 0, st, a);
+            };
+            // a row a lane where all of them fit the SMs at once, else four
+            auto sized = [&](auto c) {
+                return a.T * y * a.across <= 152ll * 32 ? go(std::integral_constant<int, 1>(), c)
+                                                        : go(std::integral_constant<int, 4>(), c);
+            };
+            return cache == LORA_CACHE_BF16 ? sized(std::integral_constant<int, LORA_CACHE_BF16>())
+                                            : sized(std::integral_constant<int, LORA_CACHE_E4M3>());
+        });
+    });
+}
+
 int check_rotary(const char* fn, int32_t T, lora_dtype_t dt, const lora_rotary_t* r) {
     const std::string f(fn);
     if (!r) return refuse(LORA_ERR_INVALID_ARG, f + ": rotary is NULL");
@@ -654,9 +730,6 @@ cudaError_t launch_forward(const Forward& a, cudaStream_t st) {
         constexpr int kLanes = decltype(lanes)::value;
         const Launch l = launch_of(a.chunks, a.T);
         if (turned_whole(a.D, kLanes, a.turns)) return launch_rows(rotary_kernel<Row8, kLanes, kTurned, kCache>, l, st, a);
-        if constexpr (kCache >= 0)
-            if (a.D == 16 * kLanes && a.turns.rot == 0)
-                return launch_rows(rotary_kernel<Row8, kLanes, kPlain, kCache>, l, st, a);
         return launch_rows(rotary_kernel<Row8, kLanes, kAny, kCache>, l, st, a);
     });
 }
@@ -791,7 +864,7 @@ extern "C" int lora_cache_write(int32_t T, lora_dtype_t dt, const void* k, int64
                                 const lora_cache_t* cache, const int64_t* slots, void* stream) {
     return guarded([&]() -> int {
         const char* fn = "lora_cache_write";
-        Forward a = {};
+        Rows a = {};
         if (dt != LORA_BF16 && dt != LORA_F32) return refuse(LORA_ERR_DTYPE, "unknown dtype");
         int rc = check_cache(fn, cache, &a.cache);
         if (rc != LORA_OK) return rc;
@@ -802,9 +875,11 @@ extern "C" int lora_cache_write(int32_t T, lora_dtype_t dt, const void* k, int64
         if ((rc = check_matrix(fn, "k", k, cols, ld_k, elem_size(dt))) != LORA_OK) return rc;
         if ((rc = check_matrix(fn, "v", v, cols, ld_v, elem_size(dt))) != LORA_OK) return rc;
         if ((rc = check_slots(fn, slots)) != LORA_OK) return rc;
-        a.x = k; a.ld_x = ld_k; a.v = v; a.ld_v = ld_v; a.slots = slots;
-        a.T = T; a.chunks = Chunks{{0, cache->n_heads, cache->n_heads}, 0}; a.D = cache->head_dim;
-        return enqueued(fn, forward(dt, cache->dtype, a, static_cast<cudaStream_t>(stream)));
+        a.slots = slots; a.k = const_cast<void*>(k); a.v = const_cast<void*>(v); a.ld_k = ld_k; a.ld_v = ld_v;
+        a.T = T; a.n_heads = cache->n_heads; a.D = cache->head_dim;
+        return enqueued(fn, launch_cache_rows(dt, cache->dtype, a, [](auto row, auto lanes, auto rows, auto c) {
+            return cache_write_kernel<decltype(row), decltype(lanes)::value, decltype(rows)::value, decltype(c)::value>;
+        }, static_cast<cudaStream_t>(stream)));
     });
 }
 
@@ -812,7 +887,7 @@ extern "C" int lora_cache_read(int32_t T, lora_dtype_t dt, const lora_cache_t* c
                                int64_t ld_k, void* v, int64_t ld_v, void* stream) {
     return guarded([&]() -> int {
         const char* fn = "lora_cache_read";
-        Read a = {};
+        Rows a = {};
         if (dt != LORA_BF16 && dt != LORA_F32) return refuse(LORA_ERR_DTYPE, "unknown dtype");
         int rc = check_cache(fn, cache, &a.cache);
         if (rc != LORA_OK) return rc;
@@ -825,29 +900,8 @@ extern "C" int lora_cache_read(int32_t T, lora_dtype_t dt, const lora_cache_t* c
         if ((rc = check_slots(fn, slots)) != LORA_OK) return rc;
         a.slots = slots; a.k = k; a.v = v; a.ld_k = ld_k; a.ld_v = ld_v;
         a.T = T; a.n_heads = cache->n_heads; a.D = cache->head_dim;
-        cudaStream_t st = static_cast<cudaStream_t>(stream);
-        return enqueued(fn, by_type(dt, [&](auto row) {
-            using Row8 = decltype(row);
-            return by_lanes(a.D, [&](auto lanes) {
-                // the heads in equal shares across, and as many rows of warps as are left room for
-                const int per_warp = 32 / decltype(lanes)::value, all = (2 * a.n_heads + per_warp - 1) / per_warp;
-                const int y = (all + kReadWarps - 1) / kReadWarps;
-                a.across = (all + y - 1) / y;
-                a.down = (int)std::min<int64_t>(kReadWarps / a.across, T);
-                auto go = [&](auto rows, auto c) {
-                    constexpr int kRows = decltype(rows)::value;
-                    const int64_t n = (T + a.down * kRows - 1) / (a.down * kRows);
-                    return launch_pdl(cache_read_kernel<Row8, decltype(lanes)::value, kRows, decltype(c)::value>,
-                                      dim3((unsigned)n, (unsigned)y), dim3((unsigned)(32 * a.across * a.down)), 0, st, a);
-                };
-                // a row a lane where all of them fit the SMs at once, else four
-                auto sized = [&](auto c) {
-                    return a.T * y * a.across <= 152ll * 32 ? go(std::integral_constant<int, 1>(), c)
-                                                            : go(std::integral_constant<int, 4>(), c);
-                };
-                return cache->dtype == LORA_CACHE_BF16 ? sized(std::integral_constant<int, LORA_CACHE_BF16>())
-                                                       : sized(std::integral_constant<int, LORA_CACHE_E4M3>());
-            });
-        }));
+        return enqueued(fn, launch_cache_rows(dt, cache->dtype, a, [](auto row, auto lanes, auto rows, auto c) {
+            return cache_read_kernel<decltype(row), decltype(lanes)::value, decltype(rows)::value, decltype(c)::value>;
+        }, static_cast<cudaStream_t>(stream)));
     });
 }
