@@ -18,9 +18,10 @@
 namespace lora {
 namespace {
 
-constexpr int kMaxThreads = 256;
 
-constexpr int kMaxWarps = kMaxThreads / 32;
+// Warps of a CTA: as many as two CTAs' registers leave room for (forward, 8192 rows of 72 heads: 8 warps 55.5 us, 10 53.6;
+// backward, 2048 rows of 40 heads: 18.5 and 21.8)
+constexpr int kForwardWarps = 10, kBackwardWarps = 8;
 constexpr int kCtas = 2;      // CTAs on an SM: with three, or four, registers spill and 8192 rows of 72 heads take 61 and 78 us
 
 // The heads of a row, in chunks of one kind each; a warp takes a chunk
@@ -228,7 +229,7 @@ struct Forward {
 };
 
 template <class Row8, int kLanes, int kForm, int kCache /* -1: none */>
-__global__ void __launch_bounds__(kMaxThreads, kCtas) rotary_kernel(const Forward a) {
+__global__ void __launch_bounds__(32 * kForwardWarps, kCtas) rotary_kernel(const Forward a) {
     extern __shared__ __align__(16) char smem[];
     WarpPlace& mine = reinterpret_cast<WarpPlace*>(smem)[threadIdx.x / 32];
     grid_dep_launch();
@@ -350,7 +351,7 @@ struct Backward {
 };
 
 template <class Row8, int kLanes, int kForm, bool kNorm, bool kWeights>
-__global__ void __launch_bounds__(kMaxThreads, kCtas) rotary_backward_kernel(const Backward a) {
+__global__ void __launch_bounds__(32 * kBackwardWarps, kCtas) rotary_backward_kernel(const Backward a) {
     extern __shared__ __align__(16) char smem[];
     WarpPlace* const places = reinterpret_cast<WarpPlace*>(smem);
     WarpPlace& mine = places[threadIdx.x / 32];
@@ -631,10 +632,10 @@ constexpr unsigned kMaxParts = kCtas * 152 + kMaxHeads;   // CTAs of a backward 
 
 // Chunks of one step of heads where all warps then fit the SMs at once.  Else as many steps, of those that fit a row's place,
 // as waste the least: an empty head costs as much as a full one, and a chunk's angles as much as 0.6 steps.
-Chunks chunks_of(int hq, int hk, int hv, int D, int64_t T, int bytes_per_head) {
+Chunks chunks_of(int hq, int hk, int hv, int D, int64_t T, int bytes_per_head, int warps) {
     const int across = 32 / lanes_of(D);
     Chunks c{{hq, hk, hv}, across};
-    if (T * c.all() <= 152ll * kCtas * kMaxWarps) return c;
+    if (T * c.all() <= 152ll * kCtas * warps) return c;
     Chunks best = c;
     double least = c.all() * 1.6;
     for (int steps = 2; steps * across * bytes_per_head <= kChunkBytes; ++steps) {
@@ -653,8 +654,8 @@ struct Launch {
     unsigned threads;
     size_t smem;
 };
-Launch launch_of(const Chunks& c, int64_t T) {
-    const unsigned w = (unsigned)std::min<int64_t>(kMaxWarps, T), y = (unsigned)c.all();
+Launch launch_of(const Chunks& c, int64_t T, int warps) {
+    const unsigned w = (unsigned)std::min<int64_t>(warps, T), y = (unsigned)c.all();
     const unsigned n = (unsigned)std::min<int64_t>((T + w - 1) / w, std::max(1u, 152u * kCtas / y));
     return Launch{dim3(n, y), 32 * w, w * sizeof(WarpPlace)};
 }
@@ -728,14 +729,14 @@ template <class Row8, int kCache>
 cudaError_t launch_forward(const Forward& a, cudaStream_t st) {
     return by_lanes(a.D, [&](auto lanes) {
         constexpr int kLanes = decltype(lanes)::value;
-        const Launch l = launch_of(a.chunks, a.T);
+        const Launch l = launch_of(a.chunks, a.T, kForwardWarps);
         if (turned_whole(a.D, kLanes, a.turns)) return launch_rows(rotary_kernel<Row8, kLanes, kTurned, kCache>, l, st, a);
         return launch_rows(rotary_kernel<Row8, kLanes, kAny, kCache>, l, st, a);
     });
 }
 cudaError_t forward(lora_dtype_t dt, int cache, Forward a, cudaStream_t st) {
     const int32_t* h = a.chunks.heads;
-    a.chunks = chunks_of(h[kQuery], h[kKey], h[kValue], a.D, a.T, bytes_of(dt, a.D));
+    a.chunks = chunks_of(h[kQuery], h[kKey], h[kValue], a.D, a.T, bytes_of(dt, a.D), kForwardWarps);
     return by_type(dt, [&](auto row) {
         using Row8 = decltype(row);
         return cache < 0 ? launch_forward<Row8, -1>(a, st)
@@ -839,8 +840,8 @@ extern "C" int lora_rotary_backward(int32_t T, lora_dtype_t dt, const lora_rotar
                 using Row8 = decltype(row);
                 return by_lanes(a.D, [&](auto lanes) {
                     constexpr int kLanes = decltype(lanes)::value;
-                    a.chunks = chunks_of(r->n_heads, r->n_kv_heads, 0, a.D, T, (norm ? 2 : 1) * bytes_of(dt, a.D));
-                    const Launch l = launch_of(a.chunks, T);
+                    a.chunks = chunks_of(r->n_heads, r->n_kv_heads, 0, a.D, T, (norm ? 2 : 1) * bytes_of(dt, a.D), kBackwardWarps);
+                    const Launch l = launch_of(a.chunks, T, kBackwardWarps);
                     nq = (int)l.grid.x * a.chunks.of(kQuery);
                     nk = (int)l.grid.x * a.chunks.of(kKey);
                     auto go = [&](auto nrm, auto wts) {

@@ -129,7 +129,8 @@ def test_pages(page, layout, e4m3):
 
 @pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
 @pytest.mark.parametrize("lengths", [[3000], [1], [0], [0, 0, 0], [2500, 1, 0, 700, 64], [5] * 70, list(range(200)),
-                                     [0] * 140 + [900] + [0] * 200 + [33]], ids=lambda v: "%d of %d" % (len(v), max(v)))
+                                     [0] * 140 + [900] + [0] * 200 + [33],
+                                     [i % 9 for i in range(2500)]], ids=lambda v: "%d of %d" % (len(v), max(v)))
 def test_lengths(lengths, e4m3):
     c = Case(lengths, 8, 2, 64, e4m3=e4m3)
     c.check(*c.run())
