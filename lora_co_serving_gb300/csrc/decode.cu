@@ -30,6 +30,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCtas = 912;        // of a launch: six on each SM
+constexpr int kJoined = 18;          // parts of an item that are joined in one stage
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 // A running maximum is raised only when a score exceeds it by a factor of 2^kSlack: probabilities stay below that.
@@ -404,7 +405,10 @@ struct Cursor {
         poisoned = r.poisoned;
         n_tiles = r.tiles(S::kTile);
     }
-    // the next line's first tile; there is one
+    // the next tile; the next line's first one; there is one
+    __device__ __forceinline__ void next(const Decode& a) {
+        if (++t == n_tiles) next_line(a);
+    }
     __device__ __forceinline__ void next_line(const Decode& a) {
         t = 0;
         if (++line < a.kv_heads * a.parts) return;
@@ -487,16 +491,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
     at.t = (int)(p0 - sh_before - (int64_t)at.line * at.n_tiles);
     Cursor<S> ahead = at;
     int64_t to_copy = p1 - p0, to_do = p1 - p0;
-    int32_t page = 0;
+    int32_t page = 0, following = 0;
     uint32_t bad_steps = 0;                           // bit i: step i's tile has a page outside the cache
     auto token = [&](const Cursor<S>& x) { return x.start + (uint32_t)x.t * S::kTile + team * S::kTokens; };
     // Lanes past the last token take that token's row once more: their scores become -infinity, and 0 times a value of the
     // range adds nothing.
     auto my_token = [&](const Cursor<S>& x) { return min(token(x) + lane % S::kTokens, x.end - 1); };
-    auto read_page = [&]() {
-        if (to_copy > 0) page = a.table[ahead.b * a.ld_table + a.cache.pages.page_of(my_token(ahead))];
-    };
-    auto copy = [&](int step) {
+    auto page_of = [&](const Cursor<S>& x) { return a.table[x.b * a.ld_table + a.cache.pages.page_of(my_token(x))]; };
+    auto copy = [&](int step, bool following_known = false) {
         if (to_copy > 0) {
             // a page outside the cache is taken as its first; the result becomes NaN
             const bool bad = (uint32_t)page >= (uint32_t)a.cache.n_pages;
@@ -517,14 +519,20 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
                 }
             }
             if (--to_copy > 0) {
-                if (++ahead.t == ahead.n_tiles) ahead.next_line(a);
-                read_page();
+                ahead.next(a);
+                page = following_known ? following : page_of(ahead);
             }
         }
         copies_commit();
     };
-    read_page();
-    copy(0);
+    // the first two tiles' pages are read at once
+    page = page_of(ahead);
+    if (to_copy > 1) {
+        Cursor<S> second = ahead;
+        second.next(a);
+        following = page_of(second);
+    }
+    copy(0, true);
     copy(1);
 
     Query<S> q;
@@ -760,10 +768,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
             else write_part(slot(blockIdx.x, t0 == 0), row, d, r);
         }
         if (!whole) {
-            // ---- the item's parts, in the order of its CTAs: those of each eight neighbouring CTAs are joined by the last
-            // of them to arrive, and what they leave by the last eight to be done.
+            // ---- the item's parts, in the order of its CTAs, are joined by the last CTA to arrive.  Where there are many,
+            // those of each eight neighbouring CTAs are, and what they leave by the last eight to be done: a second stage
+            // costs as much as ten parts more.
             const int c0 = (int)all.owner(i0), c1 = (int)all.owner(i1 - 1), eight = blockIdx.x / 8;
-            const int e0 = max(c0, 8 * eight), e1 = min(c1, 8 * eight + 7);
+            const bool only = c1 - c0 < kJoined;
+            const int e0 = only ? c0 : max(c0, 8 * eight), e1 = only ? c1 : min(c1, 8 * eight + 7);
             auto part_of = [&](int cta) { return slot(cta, cta == c0); };
             // the barriers order the CTA's writes before its one thread's release, and its acquire before the CTA's reads
             auto arrive = [&](int counter, int expected) -> bool {
@@ -783,7 +793,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
             // the first eight of an item count at its first CTA, the others, which begin with it, at their own number
             if (arrive(e0 == c0 ? c0 : kMaxCtas + eight, e1 - e0 + 1)) {
                 const int n = c1 / 8 - c0 / 8 + 1;
-                const bool only = n == 1;
                 for (int i = tid; i < n_rows * (S::kD / 4); i += kThreads) {
                     const int row = i / (S::kD / 4), d = i % (S::kD / 4) * 4;
                     const Joined r = join_parts<S>(e1 - e0 + 1, row, d, [&](int k) { return part_of(e0 + k); });
