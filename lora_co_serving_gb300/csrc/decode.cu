@@ -11,7 +11,7 @@
 //           tokens are rows, are turned around by the transposing move of 8 x 8 numbers.
 // Every warp copies its rows into shared memory two steps ahead of their use, asynchronously, 512 neighbouring bytes at a
 // time, and reads them back as its lanes need them: a barrier within the warp is all that it takes.  (Lanes that copied
-// their own pieces, 64 bytes of 8 rows at a time, needed one and a half times the requests to L2: 236 us instead of 188
+// their own pieces, 64 bytes of 8 rows at a time, needed one and a half times the requests to L2: 236 us instead of 187
 // for 64 x 8192 tokens in bf16.)
 // Work is counted in tiles of 32 to 128 tokens of one sequence and one cache head.  All tiles of a call form one line, and
 // each CTA takes an equal piece of it, whatever the lengths are; a CTA's warps take 16 or 32 tokens of a tile each, with a
