@@ -9,6 +9,7 @@
  *
  * Rotary positions.  A head's row x [D] is normalised (where a weight w [D] is given) and its first R elements turned:
  *     n = x w / sqrt(mean(x^2) + eps)
+ * (a row whose squares add up past float32's range counts as infinitely long: n = 0)
  *     pair i < R/2:  a = n[i], b = n[i + R/2]   (interleaved: n[2i], n[2i+1])
  *     y_a = a cos t - b sin t,  y_b = b cos t + a sin t,   t = 2 pi position turns_i
  * turns_i is the pair's frequency in turns a position, as a whole number of 2^-64 turns (an angular frequency f, base^

@@ -18,7 +18,6 @@
 namespace lora {
 namespace {
 
-
 // Warps of a CTA: as many as two CTAs' registers leave room for (forward, 8192 rows of 72 heads: 8 warps 55.5 us, 10 53.6;
 // backward, 2048 rows of 40 heads: 18.5 and 21.8)
 constexpr int kForwardWarps = 10, kBackwardWarps = 8;
@@ -62,10 +61,10 @@ __device__ __forceinline__ float2 cos_sin(uint64_t phase) {
     return quarter & 2 ? make_float2(-c1, -s1) : make_float2(c1, s1);
 }
 // 1 / sqrt(v), the fast one improved by a step of Newton's method: its error is that of every element of a row, and in 8 bits
-// a neighbouring code here and there
+// a neighbouring code here and there.  Infinity for 0, 0 for infinity.
 __device__ __forceinline__ float inverse_root(float v) {
-    const float f = rsqrtf(v);
-    return fmaf(0.5f * f, fmaf(-v * f, f, 1.f), f);
+    const float f = rsqrtf(v), better = fmaf(0.5f * f, fmaf(-v * f, f, 1.f), f);
+    return v > 0.f && v < INFINITY ? better : f;
 }
 
 // Two products, or two fused sums, in one instruction
@@ -254,7 +253,7 @@ __global__ void __launch_bounds__(32 * kForwardWarps, kCtas) rotary_kernel(const
     const int64_t head_at = (int64_t)(chunk.first + (chunk.kind == kKey ? a.chunks.heads[kQuery] : 0) + sub) * D;
     const void* weight = value ? nullptr : chunk.kind == kKey ? a.wk : a.wq;
     float g0[8] = {}, g1[8] = {};
-    if (weight && (p.in)) {
+    if (weight && p.in) {
         Row8 w[2];
         w[0].load(weight, p.at0);
         w[1].load(weight, p.at1);
@@ -304,7 +303,8 @@ __global__ void __launch_bounds__(32 * kForwardWarps, kCtas) rotary_kernel(const
                 mul2(z, z, g1);
             }
             if (turned && p.turned) {
-                turn(y, z, mine.angles + 8 * lane, mine.angles + (kForm == kTurned ? 8 * kLanes : a.turns.rot / 2) + 8 * lane, f, false, kForm == kAny && a.turns.interleaved);
+                const float* sines = mine.angles + (kForm == kTurned ? 8 * kLanes : a.turns.rot / 2);
+                turn(y, z, mine.angles + 8 * lane, sines + 8 * lane, f, false, kForm == kAny && a.turns.interleaved);
             } else if (weight) {
                 mul2(y, y, f);
                 mul2(z, z, f);
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(32 * kBackwardWarps, kCtas) rotary_backward_ke
     const int64_t head_at = (int64_t)(chunk.first + (chunk.kind == kKey ? a.chunks.heads[kQuery] : 0) + sub) * D;
     const void* weight = chunk.kind == kKey ? a.wk : a.wq;
     float g0[8] = {}, g1[8] = {};
-    if (kNorm && weight && (p.in)) {
+    if (kNorm && weight && p.in) {
         Row8 w[2];
         w[0].load(weight, p.at0);
         w[1].load(weight, p.at1);
@@ -416,8 +416,10 @@ __global__ void __launch_bounds__(32 * kBackwardWarps, kCtas) rotary_backward_ke
             read_pieces<Row8>(mine.piece[now], kEach * k, y);
             read_pieces<Row8>(mine.piece[now], kEach * k + 1, z);
             const bool in = k * kAcross < heads;
-            if (p.turned)
-                turn(y, z, mine.angles + 8 * lane, mine.angles + (kForm == kTurned ? 8 * kLanes : a.turns.rot / 2) + 8 * lane, 1.f, true, kForm == kAny && a.turns.interleaved);
+            if (p.turned) {
+                const float* sines = mine.angles + (kForm == kTurned ? 8 * kLanes : a.turns.rot / 2);
+                turn(y, z, mine.angles + 8 * lane, sines + 8 * lane, 1.f, true, kForm == kAny && a.turns.interleaved);
+            }
             if (kNorm && weight) {
                 float v[8], x[8];
                 read_pieces<Row8>(mine.piece[now], kEach * k + 2, v);

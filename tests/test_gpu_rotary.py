@@ -188,6 +188,24 @@ def test_positions_wrap_exactly():
     close(back, x.cpu().double().reshape(4, 2, 64), 2 * REACH * far)
 
 
+def test_rows_of_extreme_length():
+    """Squares past float32's range: zeros; an infinite or NaN element: its own row and head; zeros stay zeros; rows whose
+    squares vanish are as long as eps says."""
+    turns, w = lm.rotary_turns(64), torch.ones(64, device="cuda")
+    x = torch.randn(6, 3 * 64, generator=gen(1)).cuda()
+    x[0, :64], x[1, 70], x[2, 130], x[3, :64], x[4, 64:128] = 1e30, float("inf"), float("nan"), 0.0, 1e-30
+    p = torch.arange(6).cuda()
+    out = lm.rotary_forward(x, p, turns, 2, 1, q_weight=w, k_weight=w).reshape(6, 3, 64)
+    assert (out[0, 0] == 0).all() and (out[3, 0] == 0).all() and out[4, 1].abs().max() < 1e-25 and out[4, 1].abs().max() > 0
+    hit = torch.zeros(6, 3, dtype=torch.bool)
+    hit[1, 1] = hit[2, 2] = True
+    assert torch.equal(out.isfinite().all(-1).cpu(), ~hit) and out[2, 2].isnan().all() and out[1, 1].isnan().sum() == 2
+    cache = lm.kv_cache(1, 1, 8, 64, torch.float8_e4m3fn)
+    lm.rotary_forward(x, p, turns, 2, 1, q_weight=w, k_weight=w, v=x[:, :64], cache=cache, slots=p)
+    k, v = lm.cache_read(cache, p, dtype=F32)
+    assert k[2].isnan().all() and k[[0, 1, 3, 4, 5]].isfinite().all() and v.isfinite().all()
+
+
 def test_no_rows():
     turns = lm.rotary_turns(64)
     e = torch.empty(0, 128, dtype=BF, device="cuda")
