@@ -597,7 +597,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
                     // both warps of a team add the two halves in one order
                     float* const exchange = reinterpret_cast<float*>(smem + kWarps * S::kWarpBytes);
                     auto place = [&](int of, int i, int e) -> float& {
-                        return exchange[(2 * team + of) * S::kExchangeFloats + ((step * S::kMmas * S::kCols + i) * 4 + e) * 32 + lane];
+                        return exchange[(2 * team + of) * S::kExchangeFloats +
+                                        ((step * S::kMmas * S::kCols + i) * 4 + e) * 32 + lane];
                     };
 #pragma unroll
                     for (int n = 0; n < S::kCols; ++n)

@@ -849,7 +849,8 @@ extern "C" int lora_rotary_backward(int32_t T, lora_dtype_t dt, const lora_rotar
                 using Row8 = decltype(row);
                 return by_lanes(a.D, [&](auto lanes) {
                     constexpr int kLanes = decltype(lanes)::value;
-                    a.chunks = chunks_of(r->n_heads, r->n_kv_heads, 0, a.D, T, (norm ? 2 : 1) * bytes_of(dt, a.D), kBackwardWarps);
+                    a.chunks = chunks_of(r->n_heads, r->n_kv_heads, 0, a.D, T, (norm ? 2 : 1) * bytes_of(dt, a.D),
+                                         kBackwardWarps);
                     const Launch l = launch_of(a.chunks, T, kBackwardWarps);
                     nq = (int)l.grid.x * a.chunks.of(kQuery);
                     nk = (int)l.grid.x * a.chunks.of(kKey);
