@@ -118,8 +118,7 @@ __device__ __forceinline__ void read8(const float* from, float (&v)[8]) {
 // A warp's place in shared memory: two rows of a chunk's pieces, [piece][lane] of 16 bytes, so that each lane reads back what
 // it copied; the rows' positions and slots; a row's angles.
 constexpr int kRowBytes = 4096;       // a step of float32 heads, with their gradients, at the most
-constexpr int kChunkBytes = 3072;     // that chunks of more steps take (8192 rows of 72 heads: 1024 64 us, 2048 and 3072 54,
-                                      // 4096 57)
+constexpr int kChunkBytes = 2048;     // that chunks of more steps take (8192 rows of 72 heads: 1024 64 us, 2048 54, 4096 57)
 struct WarpPlace {
     uint4 piece[2][kRowBytes / 16];
     int64_t position[2], slot[2];
