@@ -667,10 +667,13 @@ Launch launch_of(const Chunks& c, int64_t T, int warps) {
     const unsigned n = (unsigned)std::min<int64_t>((T + w - 1) / w, std::max(1u, 152u * kCtas / y));
     return Launch{dim3(n, y), 32 * w, w * sizeof(WarpPlace)};
 }
-template <class K, class A>
+// The limit of shared memory is the kernel's, not the call's: every thread that launches it sets the same, that of kWarps
+// warps, so that none takes it from a call that another thread is about to launch.
+template <int kWarps, class K, class A>
 cudaError_t launch_rows(K kernel, const Launch& l, cudaStream_t st, const A& a) {
     if (l.smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)l.smem);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)(kWarps * sizeof(WarpPlace)));
         if (e != cudaSuccess) return e;
     }
     return launch_pdl(kernel, l.grid, dim3(l.threads), l.smem, st, a);
@@ -738,8 +741,9 @@ cudaError_t launch_forward(const Forward& a, cudaStream_t st) {
     return by_lanes(a.D, [&](auto lanes) {
         constexpr int kLanes = decltype(lanes)::value;
         const Launch l = launch_of(a.chunks, a.T, kForwardWarps);
-        if (turned_whole(a.D, kLanes, a.turns)) return launch_rows(rotary_kernel<Row8, kLanes, kTurned, kCache>, l, st, a);
-        return launch_rows(rotary_kernel<Row8, kLanes, kAny, kCache>, l, st, a);
+        if (turned_whole(a.D, kLanes, a.turns))
+            return launch_rows<kForwardWarps>(rotary_kernel<Row8, kLanes, kTurned, kCache>, l, st, a);
+        return launch_rows<kForwardWarps>(rotary_kernel<Row8, kLanes, kAny, kCache>, l, st, a);
     });
 }
 cudaError_t forward(lora_dtype_t dt, int cache, Forward a, cudaStream_t st) {
@@ -855,9 +859,10 @@ extern "C" int lora_rotary_backward(int32_t T, lora_dtype_t dt, const lora_rotar
                     nk = (int)l.grid.x * a.chunks.of(kKey);
                     auto go = [&](auto nrm, auto wts) {
                         constexpr bool kNorm = decltype(nrm)::value, kWeights = decltype(wts)::value;
-                        return turned_whole(a.D, kLanes, a.turns)
-                                   ? launch_rows(rotary_backward_kernel<Row8, kLanes, kTurned, kNorm, kWeights>, l, st, a)
-                                   : launch_rows(rotary_backward_kernel<Row8, kLanes, kAny, kNorm, kWeights>, l, st, a);
+                        const auto kernel = turned_whole(a.D, kLanes, a.turns)
+                                                ? rotary_backward_kernel<Row8, kLanes, kTurned, kNorm, kWeights>
+                                                : rotary_backward_kernel<Row8, kLanes, kAny, kNorm, kWeights>;
+                        return launch_rows<kBackwardWarps>(kernel, l, st, a);
                     };
                     return !norm ? go(std::false_type(), std::false_type())
                                  : !weights ? go(std::true_type(), std::false_type()) : go(std::true_type(), std::true_type());
