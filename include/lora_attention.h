@@ -125,7 +125,8 @@ size_t lora_decode_workspace_size(int32_t n_heads, const lora_cache_t* cache /* 
  * (window 0: [0, L_b)), row j in page table[b, j / page_size]:
  *     s_j = scale q.k_j       (softcap c > 0: c tanh(s_j / c))
  *     out = sum_j e^s_j v_j / sum_j e^s_j,   lse = log sum_j e^s_j
- *   q, out [B, n_heads D] (bf16, ld_q, ld_out); out may be q itself (same ld).   lse [B, n_heads] float32 or NULL.   lengths [B], table [B, ld_table].
+ *   q, out [B, n_heads D] (bf16, ld_q, ld_out); out may be q itself (same ld: another one is refused), and overlaps q in no
+ *   other way.   lse [B, n_heads] float32 or NULL.   lengths [B], table [B, ld_table].
  * Products are taken in 16 bits (for 8-bit codes and the probabilities with enough digits to lose none of the inputs'),
  * sums and statistics in 32, in an order that depends on the lengths of the call's sequences only: repeated calls give
  * identical bits.

@@ -912,6 +912,8 @@ extern "C" int lora_decode_attention(int32_t B, int32_t n_heads, const void* q, 
         const int64_t cols = (int64_t)n_heads * cache->head_dim;
         if ((rc = check_matrix(fn, "q", q, cols, ld_q, 2)) != LORA_OK) return rc;
         if ((rc = check_matrix(fn, "out", out, cols, ld_out, 2)) != LORA_OK) return rc;
+        if (B > 1 && out == q && ld_out != ld_q)
+            return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": in place, ld_out must be ld_q");
         if (!table || !lengths) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": table or lengths is NULL");
         if (table_width < 1 || ld_table < table_width)
             return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": rows of table are empty or overlap");
