@@ -1119,7 +1119,7 @@ def decode_attention(q, cache, page_table, lengths, scale=None, window=0, softca
                      workspace=None):
     """Attention of one new token of each sequence over its cached rows: q [B, n_heads D] (bf16), page_table [B, pages]
     and lengths [B] (int32; the new token's row among them).  Query head h attends with the cache's head h // (n_heads /
-    n_kv_heads), over the last `window` rows (0: all), with scores scale q.k (default D^-1/2), capped to softcap
+    n_kv_heads), over the last `window` rows (0: all; below 2^31), with scores scale q.k (default D^-1/2), capped to softcap
     tanh(score / softcap) where softcap > 0.
 
     Returns out [B, n_heads D], with want_lse (out, lse [B, n_heads] float32).  A length of zero gives zeros and -infinity;
@@ -1132,6 +1132,8 @@ def decode_attention(q, cache, page_table, lengths, scale=None, window=0, softca
     if cols % D or cols // D % kv_heads or cols == 0:
         raise ValueError("rows of %d elements do not hold query heads of %d in groups of %d" % (cols, D, kv_heads))
     n_heads = cols // D
+    if not -2 ** 31 <= window < 2 ** 31:        # a C int: ctypes would drop the higher bits
+        raise ValueError("window must be below 2^31, got %d" % window)
     ldt = _matrix(page_table, "page_table", torch.int32)
     if page_table.shape[0] != B:
         raise ValueError("page_table must have a row for each of %d sequences, got %d" % (B, page_table.shape[0]))

@@ -2,6 +2,7 @@
 import math
 
 import pytest
+import torch
 
 import lora_co_serving_gb300 as lm
 from test_attention_refusals import FAKE, cache, e4m3, error, lib  # noqa: F401  (lib: a fixture)
@@ -20,3 +21,22 @@ def test_decode_in_place_has_one_row_distance(lib, c):
     for kw in (dict(out=FAKE), dict(out=FAKE, ld_out=520, B=1), dict(ld_out=520)):
         rc, msg = decode(lib, c=c, **kw)
         assert "in place" not in msg
+
+
+@pytest.mark.parametrize("window", [2 ** 31, 2 ** 32, 2 ** 32 + 5, -2 ** 32, -2 ** 32 + 5, 2 ** 63])
+def test_window_is_not_cut_to_32_bits(monkeypatch, window):
+    """No call with such a window reaches the library, where 2^32 + 5 would be 5."""
+    bf, i32 = torch.bfloat16, torch.int32
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    monkeypatch.setattr(lm, "_stream_ptr", lambda stream: 0)
+
+    class Calls:
+        def __getattr__(self, name):
+            raise AssertionError(name + " was called")
+
+    monkeypatch.setattr(lm, "library", lambda: Calls())
+    q, c = torch.zeros(2, 128, dtype=bf), lm.kv_cache(4, 2, 8, 32, device="cpu")
+    with pytest.raises(ValueError, match="window"):
+        lm.decode_attention(q, c, torch.zeros(2, 3, dtype=i32), torch.zeros(2, dtype=i32), window=window,
+                            workspace=torch.zeros(8, dtype=torch.uint8))
