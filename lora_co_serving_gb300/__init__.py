@@ -557,6 +557,8 @@ def _matrix(t, name, dtype=None, rows=None, cols=None, contiguous=False):
     if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError("%s must be [%s, %s], got [%d, %d]" % (name, "T" if rows is None else rows,
                                                                 "K" if cols is None else cols, r, c))
+    if r >= 2 ** 31 or c >= 2 ** 31:            # C ints of the ABI: ctypes would drop the higher bits
+        raise ValueError("%s must have less than 2^31 rows and columns, got [%d, %d]" % (name, r, c))
     if dtype is not None and t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.is_contiguous():

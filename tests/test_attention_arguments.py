@@ -40,3 +40,19 @@ def test_window_is_not_cut_to_32_bits(monkeypatch, window):
     with pytest.raises(ValueError, match="window"):
         lm.decode_attention(q, c, torch.zeros(2, 3, dtype=i32), torch.zeros(2, dtype=i32), window=window,
                             workspace=torch.zeros(8, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("shape", [(2 ** 32 + 8, 32), (2 ** 31, 32), (8, 2 ** 32 + 32)])
+def test_sizes_are_not_cut_to_32_bits(monkeypatch, shape):
+    """Rows and columns cross the ABI as C ints: 2^32 + 8 rows would be 8."""
+    x = torch.empty(shape, dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError, match="2\\^31"):
+        lm._matrix(x, "x")
+    if shape[1] == 32:
+        slots = torch.empty(shape[0], dtype=torch.int64, device="meta")
+        c = lm.kv_cache(4, 1, 8, 32, device="meta")
+        monkeypatch.setattr(lm, "library", lambda: None)
+        for call in (lambda: lm.cache_write(x, x, c, slots), lambda: lm.cache_read(c, slots),
+                     lambda: lm.rotary_forward(x, slots, None, 1, 1), lambda: lm.fp8_quantize(x)):
+            with pytest.raises(ValueError, match="2\\^31"):
+                call()
