@@ -123,7 +123,8 @@ size_t lora_decode_workspace_size(int32_t n_heads, const lora_cache_t* cache /* 
 /* Attention of one new token of each of B sequences over its cached rows (its own among them).  With n = n_heads / the
  * cache's heads, head h of sequence b attends with the cache's head h / n, over the rows j of [max(0, L_b - window), L_b)
  * (window 0: [0, L_b)), row j in page table[b, j / page_size]:
- *     s_j = scale q.k_j       (softcap c > 0: c tanh(s_j / c))
+ *     s_j = scale q.k_j       (softcap c > 0: c tanh(s_j / c); scale / c and c log2(e), without a cap scale log2(e), must
+ *                             be finite in float32)
  *     out = sum_j e^s_j v_j / sum_j e^s_j,   lse = log sum_j e^s_j
  *   q, out [B, n_heads D] (bf16, ld_q, ld_out); out may be q itself (same ld: another one is refused), and overlaps q in no
  *   other way.   lse [B, n_heads] float32 or NULL.   lengths [B], table [B, ld_table].

@@ -908,6 +908,11 @@ extern "C" int lora_decode_attention(int32_t B, int32_t n_heads, const void* q, 
         if (B < 0 || window < 0) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": B and window must be >= 0");
         if (!(fabsf(scale) < INFINITY) || !(softcap >= 0.f && softcap < INFINITY))
             return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": scale must be finite, softcap finite and >= 0");
+        // what scores are multiplied by: an infinite factor would make NaN of a score of zero
+        if (softcap > 0.f ? !(fabsf(scale / softcap) < INFINITY && softcap * kLog2e < INFINITY)
+                          : !(fabsf(scale * kLog2e) < INFINITY))
+            return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": scale / softcap and softcap log2(e), without a softcap "
+                                                                  "scale log2(e), must be finite in float32");
         if (B == 0) return LORA_OK;
         const int64_t cols = (int64_t)n_heads * cache->head_dim;
         if ((rc = check_matrix(fn, "q", q, cols, ld_q, 2)) != LORA_OK) return rc;

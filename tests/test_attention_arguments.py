@@ -1,5 +1,4 @@
 """Arguments of the attention side's calls that would give a wrong answer without an error (no GPU is touched)."""
-import math
 
 import pytest
 import torch
@@ -56,3 +55,18 @@ def test_sizes_are_not_cut_to_32_bits(monkeypatch, shape):
                      lambda: lm.rotary_forward(x, slots, None, 1, 1), lambda: lm.fp8_quantize(x)):
             with pytest.raises(ValueError, match="2\\^31"):
                 call()
+
+
+@pytest.mark.parametrize("scale,softcap", [(0.1, 3e38), (0.1, 2.0 ** -140), (1e10, 1e-30), (3e38, 0.0), (-3e38, 0.0),
+                                           (3e38, 0.5)])
+def test_score_factors_stay_finite(lib, scale, softcap):
+    """The kernel forms scale log2(e), or scale / cap and cap log2(e), in float32: where one is infinite, scores of zero would
+    be NaN."""
+    rc, msg = decode(lib, scale=scale, softcap=softcap)
+    assert lm.ERRORS[rc] == "LORA_ERR_INVALID_ARG" and "softcap" in msg
+
+
+@pytest.mark.parametrize("scale,softcap", [(2e38, 0.0), (0.0, 1e-40), (1.0, 2e38), (2e38, 2e38), (1e-45, 1e-45), (-1.0, 30.0)])
+def test_other_score_factors_are_taken(lib, scale, softcap):
+    rc, msg = decode(lib, scale=scale, softcap=softcap)
+    assert "softcap" not in msg
