@@ -33,7 +33,7 @@
  * stride; ld_* is the distance of two rows in elements.  Zero rows are valid and launch nothing.
  *
  * Limits (LORA_ERR_LIMIT): D a multiple of 16, at most 256; R a multiple of 16, at most D; at most 1024 heads in all;
- * T <= 2^31 - 1025.  Data, weights and caches 16-byte aligned, their row distances and strides multiples of 16 bytes
+ * T and B <= 2^31 - 1025.  Data, weights and caches 16-byte aligned, their row distances and strides multiples of 16 bytes
  * (LORA_ERR_ALIGNMENT).
  */
 #ifndef LORA_ATTENTION_H

@@ -435,10 +435,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
 
     // ---- this CTA's piece of the line of tiles, [p0, p1), and the sequence that p0 lies in
     const int heads = a.kv_heads * a.parts;           // lines of tiles of one sequence
-    const int per = (a.B + kThreads - 1) / kThreads;  // sequences of a thread
-    const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+    const Share share(a.B, tid, kThreads);            // sequences of a thread
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += range_of(a, b).tiles(S::kTile);
+    for (int b = share.first; b < share.last; ++b) mine += range_of(a, b).tiles(S::kTile);
     int64_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -459,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
     const int64_t p1 = blockIdx.x < all.ctas ? all.first_tile(blockIdx.x + 1) : total;
     if (p0 < p1 && (upto - mine) * heads <= p0 && p0 < upto * heads) {
         int64_t before = upto - mine;
-        int b = b0;
+        int b = share.first;
         for (;; ++b) {
             const int n = range_of(a, b).tiles(S::kTile);
             if (p0 < (before + n) * heads) break;
@@ -469,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_kernel(const Decode a)
         sh_before = before * heads;
     }
     // sequences without rows have no tile, so the CTAs share them out
-    for (int b = blockIdx.x * kWarps + warp; b < a.B; b += gridDim.x * kWarps) {
+    for (uint32_t b = blockIdx.x * kWarps + warp; b < (uint32_t)a.B; b += gridDim.x * kWarps) {
         if (range_of(a, b).tiles(S::kTile) > 0) continue;
         for (int i = lane; i < a.n_heads * a.D / 8; i += 32)
             reinterpret_cast<uint4*>(a.out + b * a.ld_out)[i] = make_uint4(0, 0, 0, 0);
@@ -906,6 +905,7 @@ extern "C" int lora_decode_attention(int32_t B, int32_t n_heads, const void* q, 
         if (rc != LORA_OK) return rc;
         if ((rc = check_heads(fn, n_heads, cache)) != LORA_OK) return rc;
         if (B < 0 || window < 0) return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": B and window must be >= 0");
+        if (B > kMaxRowsOfX) return refuse(LORA_ERR_LIMIT, std::string(fn) + ": more than 2^31 - 1025 sequences");
         if (!(fabsf(scale) < INFINITY) || !(softcap >= 0.f && softcap < INFINITY))
             return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": scale must be finite, softcap finite and >= 0");
         // what scores are multiplied by: an infinite factor would make NaN of a score of zero

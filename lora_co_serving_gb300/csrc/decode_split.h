@@ -52,6 +52,16 @@ LORA_HD int64_t quotient(int64_t a, int64_t b) {
     return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
+// What the i-th of `of` takes of n, [first, last)
+struct Share {
+    int32_t first, last;
+    LORA_HD Share(int32_t n, int32_t i, int32_t of) {
+        const int64_t per = ((int64_t)n + of - 1) / of, from = i * per;
+        first = (int32_t)(from < n ? from : n);
+        last = (int32_t)(from + per < n ? from + per : n);
+    }
+};
+
 // `tiles` in one line, in equal pieces: CTA c takes [first_tile(c), first_tile(c + 1)).  ctas <= tiles.
 struct Line {
     int64_t tiles, ctas;

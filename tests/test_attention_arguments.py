@@ -1,9 +1,12 @@
 """Arguments of the attention side's calls that would give a wrong answer without an error (no GPU is touched)."""
 
+import subprocess
+
 import pytest
 import torch
 
 import lora_co_serving_gb300 as lm
+from lora_co_serving_gb300 import _build
 from test_attention_refusals import FAKE, cache, e4m3, error, lib  # noqa: F401  (lib: a fixture)
 
 
@@ -70,3 +73,37 @@ def test_score_factors_stay_finite(lib, scale, softcap):
 def test_other_score_factors_are_taken(lib, scale, softcap):
     rc, msg = decode(lib, scale=scale, softcap=softcap)
     assert "softcap" not in msg
+
+
+def test_more_sequences_than_the_limit(lib):
+    for B in (2 ** 31 - 1, 2 ** 31 - 1024):
+        rc, msg = decode(lib, B=B)
+        assert lm.ERRORS[rc] == "LORA_ERR_LIMIT" and "2^31 - 1025" in msg
+    assert lm.ERRORS[decode(lib, B=2 ** 31 - 1025)[0]] != "LORA_ERR_LIMIT"
+
+
+def test_shares_of_sequences(tmp_path):
+    """The sequences that a thread counts the tiles of: all of them once, in order, for any number that is accepted."""
+    src, exe = tmp_path / "t.cpp", str(tmp_path / "t")
+    src.write_text(r'''
+#include <cstdio>
+#include <initializer_list>
+#include "decode_split.h"
+using namespace lora;
+int main() {
+    for (int32_t B : {1, 2, 127, 128, 129, 1000, 2500, 1 << 24, (1 << 30) + 7, 2147483647 - 1024}) {
+        int32_t at = 0;
+        for (int32_t i = 0; i < 128; ++i) {
+            const Share s(B, i, 128);
+            if (s.first < 0 || s.last < s.first || s.last > B || (s.first < s.last && s.first != at)) return printf("%d %d\n", B, i), 1;
+            if (s.first < s.last) at = s.last;
+        }
+        if (at != B) return printf("%d\n", B), 1;
+    }
+    return 0;
+}
+''')
+    subprocess.run(["g++", "-std=c++17", "-O2", "-fsanitize=undefined", "-fno-sanitize-recover", "-I", _build.CSRC, str(src), "-o",
+                    exe], check=True)
+    res = subprocess.run([exe], capture_output=True, text=True)
+    assert res.returncode == 0, res.stdout + res.stderr
