@@ -298,6 +298,10 @@ __global__ void __launch_bounds__(32 * kForwardWarps, kCtas) rotary_kernel(const
             if (weight) {
                 const float ss = p.in ? dot(y, y, z, z) : 0.f;
                 f = inverse_root(sum_over_lanes<kLanes>(ss) * a.inv_d + a.eps);
+                if (f == 0.f) {          // infinitely long: zeros before the weight, whose product may be infinite
+                    mul2(y, y, f);
+                    mul2(z, z, f);
+                }
                 mul2(y, y, g0);
                 mul2(z, z, g1);
             }
