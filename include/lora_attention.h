@@ -128,8 +128,8 @@ size_t lora_decode_workspace_size(int32_t n_heads, const lora_cache_t* cache /* 
  *     out = sum_j e^s_j v_j / sum_j e^s_j,   lse = log sum_j e^s_j
  *   q, out [B, n_heads D] (bf16, ld_q, ld_out); out may be q itself (same ld: another one is refused), and overlaps q in no
  *   other way.   lse [B, n_heads] float32 or NULL.   lengths [B], table [B, ld_table].
- * Products are taken in 16 bits (for 8-bit codes and the probabilities with enough digits to lose none of the inputs'),
- * sums and statistics in 32, in an order that depends on the lengths of the call's sequences only: repeated calls give
+ * Products are of 16-bit numbers (8-bit codes exactly; a probability as two of them, 2^-16 of it off at most), sums and
+ * statistics in 32 bits, in an order that depends on the lengths of the call's sequences only: repeated calls give
  * identical bits.
  * A length of zero or less gives out = 0 and lse = -infinity.  A sequence that is longer than its table's row, or one of
  * whose pages lies outside the cache, gives NaN; nothing outside the cache is read.  Rows outside the range, and table

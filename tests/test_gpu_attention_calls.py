@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import lora_co_serving_gb300 as lm
+from attention_oracle import attention
 from test_gpu_decode import Case
 
 pytestmark = pytest.mark.gpu
@@ -27,3 +28,32 @@ def test_in_place_over_several_ctas(lengths, hq, hkv, D, e4m3):
         wide[:, :hq * D] = q
         got, z = lm.decode_attention(wide[:, :hq * D], c.cache, table, n, want_lse=True, out=wide[:, :hq * D])
         assert torch.equal(got, ref) and torch.equal(z, lse) and (wide[:, hq * D:] == 5).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,hkv,D", [(8, 2, 64), (16, 1, 128), (20, 2, 256), (71, 1, 64)])
+def test_probabilities_lose_none_of_the_outputs_digits(hq, hkv, D, e4m3):
+    """Few tokens and small scores, where the sums' bound is far below what one number of 11 bits would cost a probability:
+    outputs are the nearest bf16 numbers but for that bound.
+
+    A probability is two numbers of 16 bits: bf16 leaves half a step of half a step, 2^-16 of it, fp16 2^-22.  The products
+    and their sums as in test_gpu_decode.py; half a step of the output is taken at the output's own power of two."""
+    lengths = [2 + i % 7 for i in range(48)]
+    c = Case(lengths, hq, hkv, D, e4m3=e4m3, q_std=0.05, seed=11)
+    out, lse = c.run()
+    c.check(out, lse)
+    n = hq // hkv
+    out = out.cpu().double().reshape(-1, hkv, n, D)
+    for b, L in enumerate(lengths):
+        t = torch.arange(L)
+        pages = c.table[b].long()[t // c.page]
+        for h in range(hkv):
+            k, v = (c.kv[i, pages, h, t % c.page] for i in range(2))
+            q = c.q[b].double().reshape(hkv, n, D)[h]
+            o, _, p, s = attention(q, k, v, D ** -0.5)
+            most = (q.abs() @ k.abs().t()).amax() * D ** -0.5
+            delta = D * 2.0 ** -23 * most + 2.0 ** -20 * s.abs().amax()
+            bound = (2 * (delta + 2.0 ** -21) + 2.0 ** (-22 if e4m3 else -16) + (L + 64) * 2.0 ** -23) * (p @ v.abs())
+            half = torch.exp2(torch.floor(torch.log2(o.abs() + bound)) - 8.0)
+            err = (out[b, h] - o).abs()
+            assert (err <= half + bound).all(), "sequence %d head %d: %.3g of the bound" % (b, h, ((err - half) / bound).max())
