@@ -9,12 +9,14 @@
  *
  * Rotary positions.  A head's row x [D] is normalised (where a weight w [D] is given) and its first R elements turned:
  *     n = x w / sqrt(mean(x^2) + eps)
- * (a row whose squares add up past float32's range counts as infinitely long: n = 0)
+ * (a row whose squares add up past float32's range counts as infinitely long: n = 0; squares below 2^-126 lose digits, which
+ * shows where eps is no larger than they)
  *     pair i < R/2:  a = n[i], b = n[i + R/2]   (interleaved: n[2i], n[2i+1])
  *     y_a = a cos t - b sin t,  y_b = b cos t + a sin t,   t = 2 pi position turns_i
  * turns_i is the pair's frequency in turns a position, as a whole number of 2^-64 turns (an angular frequency f, base^
- * (-2i/R) for instance, is f / 2 pi turns).  position * turns_i is then taken modulo one turn exactly, in 64-bit whole
- * numbers: the angle of a position p is off by p 2^-65 turns at the most, for positions of any size.
+ * (-2i/R) for instance, is f / 2 pi turns).  position * turns_i is taken modulo one turn exactly, in 64-bit whole numbers,
+ * for positions of any size; then it is cut to a whole number of 2^-32 turns and goes on in float32.  What the given turns
+ * are off their frequency counts position times: p 2^-65 turns for the nearest whole numbers.
  *
  * Paged cache.  Keys and values lie in pages of page_size rows for each of n_heads heads.  Element (page, head, row, d)
  * is at page * page_stride + head * head_stride + row * row_stride + d, so a page may be [heads, rows, D] or

@@ -918,7 +918,9 @@ def _cache(cache):
 
 def rotary_turns(rot_dim, base=10000.0, frequencies=None, device="cuda"):
     """The frequencies of rotary positions as the calls below take them, int64 [rot_dim / 2]: turns a position in units of
-    2^-64.  They are base^(-2 i / rot_dim) (radians a position), or the `frequencies` given (scaled ones, for instance)."""
+    2^-64.  They are base^(-2 i / rot_dim) (radians a position), or the `frequencies` given (scaled ones, for instance).
+
+    Each is a float64 quotient, frequency / 2 pi: 2^-52 of itself off, which a position p makes p times as much of an angle."""
     import torch
     if rot_dim % 16:
         raise ValueError("rot_dim must be a multiple of 16, got %d" % rot_dim)

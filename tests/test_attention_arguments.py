@@ -1,6 +1,7 @@
 """Arguments of the attention side's calls that would give a wrong answer without an error (no GPU is touched)."""
-
+import math
 import subprocess
+from fractions import Fraction
 
 import pytest
 import torch
@@ -107,3 +108,21 @@ int main() {
                     exe], check=True)
     res = subprocess.run([exe], capture_output=True, text=True)
     assert res.returncode == 0, res.stdout + res.stderr
+
+
+PI = Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
+
+
+@pytest.mark.parametrize("rot,base,frequencies", [(128, 10000.0, None), (256, 500000.0, None), (64, 1e6, None), (16, 2.0, None),
+                                                  (16, 0.0, [1.0, math.pi, 3.0, 1e-5, 1e-15, 0.25, -0.75, 100.0])])
+def test_turns_against_many_digits(rot, base, frequencies):
+    """A float64 quotient f / 2 pi: its rounding is half a step, 2^-53, and float64's 2 pi is 2^-54 off: 2^-52 of the turns, then
+    half a unit.  (Not the nearest whole number: for a frequency of 1 it is 181 units off, of 2.9e18.)"""
+    given = [base ** (-2.0 * i / rot) for i in range(rot // 2)] if frequencies is None else frequencies
+    got = lm.rotary_turns(rot, base, frequencies, device="cpu")
+    for f, t in zip(given, got.tolist()):
+        exact = Fraction(f) * 2 ** 63 / PI
+        off = (t - exact + 2 ** 63) % 2 ** 64 - 2 ** 63          # whole turns count for nothing
+        assert abs(off) <= abs(exact) / 2 ** 52 + Fraction(1, 2)
+    one = lm.rotary_turns(16, 1.0, device="cpu").tolist()[0]
+    assert 180 < abs(one - 2 ** 63 / PI) < 182
