@@ -135,11 +135,13 @@ size_t lora_decode_workspace_size(int32_t n_heads, const lora_cache_t* cache /* 
  * identical bits.
  * A length of zero or less gives out = 0 and lse = -infinity.  A sequence that is longer than its table's row, or one of
  * whose pages lies outside the cache, gives NaN; nothing outside the cache is read.  Rows outside the range, and table
- * entries past it, are not read.  An infinite element of a value row in the range gives an infinity or NaN there.
+ * entries past it, are not read.  An infinite element of a value row in the range gives an infinity or NaN there, and so do
+ * finite ones where the sum before its division, of up to 2^8 e^(s_j - max s) |v_j|, passes float32's range (never while the
+ * elements are below 2^88).  Queries are bf16, as the cache holds 16 bits at most: a float32 layer rounds its own.
  * n_heads a multiple of the cache's heads; the cache's last row at most 2^32 units from its first, of the largest power of
- * two that divides page_stride and row_stride in bytes (LORA_ERR_LIMIT).  workspace: 256-byte aligned, >= lora_decode_workspace_size bytes, its first
- * LORA_DECODE_COUNTER_BYTES zero before its first use; every call leaves them zero.  Calls that share a workspace must not
- * overlap on the GPU. */
+ * two that divides page_stride and row_stride in bytes (LORA_ERR_LIMIT).
+ *   workspace: 256-byte aligned, >= lora_decode_workspace_size bytes, its first LORA_DECODE_COUNTER_BYTES zero before its first
+ *   use; every call leaves them zero.  Calls that share a workspace must not overlap on the GPU. */
 #define LORA_DECODE_COUNTER_BYTES 8192
 int lora_decode_attention(int32_t B, int32_t n_heads, const void* q, int64_t ld_q, const lora_cache_t* cache /* HOST */,
                           const int32_t* table, int64_t ld_table, int32_t table_width, const int32_t* lengths,

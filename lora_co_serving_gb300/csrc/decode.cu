@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxCtas = 912;        // of a launch: six on each SM
+constexpr int kMaxCtas = 912;        // of a launch, which the counters have room for; 152 SMs hold 456 (ctas_of)
 constexpr int kJoined = 18;          // parts of an item that are joined in one stage
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -295,8 +295,8 @@ struct Warp {
 
 // A group's queries as B operands, in the order of elements that Warp::scores takes; 8-bit caches: as fp16, scaled by a
 // power of two that brings the largest element to between 2^14 and 2^15, so that what bf16 holds stays exact down to 2^-31
-// of it.  (The MMAs that take e4m3 convert to fp16 themselves, and again for each call: queries split into two e4m3 numbers
-// took 135 us instead of 110 for 256 x 2048 tokens.)
+// of it.  (The MMAs that take e4m3 convert to fp16 themselves, and again for each call: with one number for a probability,
+// queries split into two e4m3 numbers took 135 us instead of 110 for 256 x 2048 tokens.)
 template <class S>
 struct Query {
     uint32_t reg[S::kCols][S::kPart / 8];

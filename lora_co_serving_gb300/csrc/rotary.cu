@@ -21,6 +21,7 @@ namespace {
 // Warps of a CTA: as many as two CTAs' registers leave room for (forward, 8192 rows of 72 heads: 8 warps 55.5 us, 10 53.6;
 // backward, 2048 rows of 40 heads: 18.5 and 21.8)
 constexpr int kForwardWarps = 10, kBackwardWarps = 8;
+constexpr int kSms = 152;     // the grids and chunks are made for
 constexpr int kCtas = 2;      // CTAs on an SM: with three, or four, registers spill and 8192 rows of 72 heads take 61 and 78 us
 
 // The heads of a row, in chunks of one kind each; a warp takes a chunk
@@ -118,7 +119,12 @@ __device__ __forceinline__ void read8(const float* from, float (&v)[8]) {
 // A warp's place in shared memory: two rows of a chunk's pieces, [piece][lane] of 16 bytes, so that each lane reads back what
 // it copied; the rows' positions and slots; a row's angles.
 constexpr int kRowBytes = 4096;       // a step of float32 heads, with their gradients, at the most
-constexpr int kChunkBytes = 2048;     // that chunks of more steps take (8192 rows of 72 heads: 1024 64 us, 2048 54, 4096 57)
+// Bytes that chunks of more steps take: half a row's place.  Forward in bf16, 8192 rows of 72 heads of 128: 1024 65 us, 2048
+// 54, 4096 57; 4718 rows of 72 neighbour-paired heads of 80 48, 42, 41.  Where a step takes more, 2048 is one step: float32
+// forward, 2301 rows of 51 heads of 96, 24 us and 27 with two; backward in bf16 with norms, 3027 rows of 40 neighbour-paired
+// heads 27.0 and 27.6.  The rule loses in that backward with more rows (8192: 48 and 44) and with heads of 256 (forward,
+// 2218 rows of 40: 21.3 and 19.9).
+constexpr int kChunkBytes = 2048;
 struct WarpPlace {
     uint4 piece[2][kRowBytes / 16];
     int64_t position[2], slot[2];
@@ -640,14 +646,14 @@ cudaError_t by_type(lora_dtype_t dt, Go go) {
     return dt == LORA_BF16 ? go(Row8Bf16()) : go(Row8F32());
 }
 
-constexpr unsigned kMaxParts = kCtas * 152 + kMaxHeads;   // CTAs of a backward that sums the weights' gradients
+constexpr unsigned kMaxParts = kCtas * kSms + kMaxHeads;   // CTAs of a backward that sums the weights' gradients
 
 // Chunks of one step of heads where all warps then fit the SMs at once.  Else as many steps, of those that fit a row's place,
 // as waste the least: an empty head costs as much as a full one, and a chunk's angles as much as 0.6 steps.
 Chunks chunks_of(int hq, int hk, int hv, int D, int64_t T, int bytes_per_head, int warps) {
     const int across = 32 / lanes_of(D);
     Chunks c{{hq, hk, hv}, across};
-    if (T * c.all() <= 152ll * kCtas * warps) return c;
+    if (T * c.all() <= (int64_t)kSms * kCtas * warps) return c;
     Chunks best = c;
     double least = c.all() * 1.6;
     for (int steps = 2; steps * across * bytes_per_head <= kChunkBytes; ++steps) {
@@ -668,7 +674,7 @@ struct Launch {
 };
 Launch launch_of(const Chunks& c, int64_t T, int warps) {
     const unsigned w = (unsigned)std::min<int64_t>(warps, T), y = (unsigned)c.all();
-    const unsigned n = (unsigned)std::min<int64_t>((T + w - 1) / w, std::max(1u, 152u * kCtas / y));
+    const unsigned n = (unsigned)std::min<int64_t>((T + w - 1) / w, std::max(1u, unsigned(kSms * kCtas) / y));
     return Launch{dim3(n, y), 32 * w, w * sizeof(WarpPlace)};
 }
 // The limit of shared memory is the kernel's, not the call's: every thread that launches it sets the same, that of kWarps
@@ -705,7 +711,7 @@ cudaError_t launch_cache_rows(lora_dtype_t dt, int cache, Rows a, Kernel kernel,
             };
             // a row a lane where all of them fit the SMs at once, else four
             auto sized = [&](auto c) {
-                return a.T * y * a.across <= 152ll * 32 ? go(std::integral_constant<int, 1>(), c)
+                return a.T * y * a.across <= kSms * 32 ? go(std::integral_constant<int, 1>(), c)
                                                         : go(std::integral_constant<int, 4>(), c);
             };
             return cache == LORA_CACHE_BF16 ? sized(std::integral_constant<int, LORA_CACHE_BF16>())
