@@ -102,8 +102,9 @@ size_t lora_rotary_workspace_size(int32_t T, const lora_rotary_t* rotary /* HOST
  *     dw = sum over rows and heads of g x r          dx = r (w g - x r^2 mean(w g x))
  *   x [T, (n_heads + n_kv_heads) D] (ld_x): the forward's input; NULL where neither weight is given.
  *   dx (element type dt, ld_dx): may be dout itself (same ld).
- *   dq_weight, dk_weight [D] float32: written where non-NULL; they need their weight, and a workspace (16-byte aligned,
- *   >= lora_rotary_workspace_size bytes).  Sums are float32 in a fixed order: repeated calls give identical bits. */
+ *   dq_weight, dk_weight [D] float32 (4-byte aligned): written where non-NULL; they need their weight, and a workspace
+ *   (16-byte aligned, >= lora_rotary_workspace_size bytes).  Sums are float32 in a fixed order: repeated calls give identical
+ *   bits. */
 int lora_rotary_backward(int32_t T, lora_dtype_t dt, const lora_rotary_t* rotary /* HOST */, const void* x, int64_t ld_x,
                          const int64_t* positions, const void* dout, int64_t ld_dout, void* dx, int64_t ld_dx,
                          float* dq_weight, float* dk_weight, void* workspace, size_t ws_bytes, void* stream);

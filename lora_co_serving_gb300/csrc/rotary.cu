@@ -831,6 +831,8 @@ extern "C" int lora_rotary_backward(int32_t T, lora_dtype_t dt, const lora_rotar
         const bool norm = r->q_weight || r->k_weight, weights = dq_weight || dk_weight;
         if ((dq_weight && !r->q_weight) || (dk_weight && !r->k_weight))
             return refuse(LORA_ERR_INVALID_ARG, std::string(fn) + ": the gradient of a weight that is not given");
+        if ((dq_weight && !is_aligned(dq_weight, 4)) || (dk_weight && !is_aligned(dk_weight, 4)))
+            return refuse(LORA_ERR_ALIGNMENT, std::string(fn) + ": the weights' gradients must be 4-byte aligned");
         if (weights && (!workspace || !is_aligned(workspace, 16) ||
                         ws_bytes < (size_t)kMaxParts * D * sizeof(float)))
             return refuse(LORA_ERR_WORKSPACE, std::string(fn) + ": workspace missing, too small or not 16-byte aligned");

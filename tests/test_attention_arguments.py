@@ -8,7 +8,7 @@ import torch
 
 import lora_co_serving_gb300 as lm
 from lora_co_serving_gb300 import _build
-from test_attention_refusals import FAKE, cache, e4m3, error, lib  # noqa: F401  (lib: a fixture)
+from test_attention_refusals import FAKE, cache, e4m3, error, lib, rotary  # noqa: F401  (lib: a fixture)
 
 
 def decode(lib, B=2, heads=8, q=FAKE, ld_q=512, c=None, width=4, window=0, scale=0.1, softcap=0.0, out=2 * FAKE, ld_out=512):
@@ -126,3 +126,12 @@ def test_turns_against_many_digits(rot, base, frequencies):
         assert abs(off) <= abs(exact) / 2 ** 52 + Fraction(1, 2)
     one = lm.rotary_turns(16, 1.0, device="cpu").tolist()[0]
     assert 180 < abs(one - 2 ** 63 / PI) < 182
+
+
+def test_weight_gradients_are_aligned(lib):
+    """A store of a float32 to an address that is no multiple of 4 would fault on the device."""
+    for dq, dk in ((FAKE + 2, None), (None, FAKE + 1), (FAKE, FAKE + 2)):
+        for T in (0, 4):
+            rc, msg = error(lib, lib.lora_rotary_backward(T, 0, rotary(qw=FAKE, kw=FAKE), FAKE, 768, FAKE, FAKE, 768, 2 * FAKE, 768,
+                                                          dq, dk, FAKE, 1 << 30, None))
+            assert lm.ERRORS[rc] == "LORA_ERR_ALIGNMENT" and "gradients" in msg
