@@ -1022,6 +1022,8 @@ def rotary_backward(x, positions, turns, n_heads, n_kv_heads, dout, q_weight=Non
         dx, ldx = torch.empty((T, cols), dtype=dout.dtype, device=dout.device), cols
     else:
         ldx = _matrix(dx, "dx", dout.dtype, T, cols)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     dq = dk = None
     if weight_grads:
         if q_weight is not None:
@@ -1146,6 +1148,8 @@ def decode_attention(q, cache, page_table, lengths, scale=None, window=0, softca
         out, ldo = torch.empty((B, cols), dtype=q.dtype, device=q.device), cols
     else:
         ldo = _matrix(out, "out", torch.bfloat16, B, cols)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     lse = torch.empty((B, n_heads), dtype=torch.float32, device=q.device) if want_lse else None
     _one_device(q, page_table, lengths, out, workspace, *held)
     st = _stream_ptr(None)

@@ -135,3 +135,24 @@ def test_weight_gradients_are_aligned(lib):
             rc, msg = error(lib, lib.lora_rotary_backward(T, 0, rotary(qw=FAKE, kw=FAKE), FAKE, 768, FAKE, FAKE, 768, 2 * FAKE, 768,
                                                           dq, dk, FAKE, 1 << 30, None))
             assert lm.ERRORS[rc] == "LORA_ERR_ALIGNMENT" and "gradients" in msg
+
+
+def test_workspaces_are_whole_bytes(monkeypatch):
+    """A workspace is as long as its bytes say: a view whose elements lie on one another, or apart, is none."""
+    i32, bf = torch.int32, torch.bfloat16
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    monkeypatch.setattr(lm, "_stream_ptr", lambda stream: 0)
+
+    class Calls:
+        def __getattr__(self, name):
+            raise AssertionError(name + " was called")
+
+    monkeypatch.setattr(lm, "library", lambda: Calls())
+    q, c = torch.zeros(2, 128, dtype=bf), lm.kv_cache(4, 2, 8, 32, device="cpu")
+    w, p, turns = torch.ones(32, dtype=bf), torch.zeros(2, dtype=torch.int64), lm.rotary_turns(32, device="cpu")
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 24), torch.zeros(64, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace must be contiguous"):
+            lm.decode_attention(q, c, torch.zeros(2, 3, dtype=i32), torch.zeros(2, dtype=i32), workspace=ws)
+        with pytest.raises(ValueError, match="workspace must be contiguous"):
+            lm.rotary_backward(q, p, turns, 2, 2, q, q_weight=w, weight_grads=True, workspace=ws)
