@@ -1130,7 +1130,8 @@ def decode_attention(q, cache, page_table, lengths, scale=None, window=0, softca
 
     Returns out [B, n_heads D], with want_lse (out, lse [B, n_heads] float32).  A length of zero gives zeros and -infinity;
     a sequence longer than its table's row, or a page outside the cache, gives NaN.  workspace: decode_workspace_size
-    bytes, the first DECODE_COUNTER_BYTES zero before its first use; not for two calls at once."""
+    bytes, the first DECODE_COUNTER_BYTES zero before its first use; not for two calls at once.  (A call without one that is
+    captured into a graph gets a new one, which the graph clears: a launch more.)"""
     import torch
     c, kv_heads, D, held = _cache(cache)
     ldq = _matrix(q, "q", torch.bfloat16)
