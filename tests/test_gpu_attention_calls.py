@@ -1,5 +1,7 @@
 """Decode attention called as its documentation allows and as few programs do; against float64, or bit by bit against the same
 call in its usual form.  Tolerances: test_gpu_decode.py's."""
+import threading
+
 import pytest
 import torch
 
@@ -57,3 +59,58 @@ def test_probabilities_lose_none_of_the_outputs_digits(hq, hkv, D, e4m3):
             half = torch.exp2(torch.floor(torch.log2(o.abs() + bound)) - 8.0)
             err = (out[b, h] - o).abs()
             assert (err <= half + bound).all(), "sequence %d head %d: %.3g of the bound" % (b, h, ((err - half) / bound).max())
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("power", [84, -84])
+def test_large_and_small_values(power, e4m3):
+    """Value rows near 2^84 (elements below 2^88) and 2^-84.  In 16 bits a power of two changes no digit of the result; in 8 it
+    goes into the exponent that a numerator is formed from."""
+    c = Case([700, 1, 33], 8, 2, 64, e4m3=e4m3, spread=0.2)
+    assert c.kv[1].nan_to_num().abs().max() < 16
+    ref, lse = c.run()
+    if e4m3:
+        c.cache.v_scales.mul_(2.0 ** power)
+    else:
+        c.cache.v.copy_((c.cache.v.double() * 2.0 ** power).to(bf16))
+    c.kv[1] *= 2.0 ** power
+    out, again = c.run()
+    c.check(out, again)
+    if not e4m3:
+        assert torch.equal(out.double(), ref.double() * 2.0 ** power) and torch.equal(again, lse)
+
+
+def test_threads_of_their_own():
+    """A thread that decodes few rows beside one with a long batch and its gradient, each on its own stream: what they give
+    alone, call after call."""
+    g = torch.Generator().manual_seed(5)
+    turns, w = lm.rotary_turns(64), torch.ones(64, device="cuda", dtype=bf16)
+    c = Case([300, 0, 900, 17, 64, 5, 1200], 8, 2, 64, page=64, e4m3=True)
+    q, table, n = c.dev
+
+    def serve(x, p):
+        y = lm.rotary_forward(x, p, turns, 8, 2, q_weight=w, k_weight=w)
+        return (y, *lm.rotary_backward(x, p, turns, 8, 2, y, q_weight=w, k_weight=w, weight_grads=True),
+                *lm.decode_attention(q, c.cache, table, n, want_lse=True))
+
+    batches = [(torch.randn(T, 640, generator=g).to(bf16).cuda(), torch.arange(T).cuda()) for T in (5000, 7, 3000, 6)]
+    alone = [serve(*b) for b in batches]
+    torch.cuda.synchronize()
+    errors = []
+
+    def run(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(150):
+                    got = serve(*batches[i])
+                    if not all(torch.equal(a, b) for a, b in zip(got, alone[i])):
+                        errors.append("batch %d differs" % i)
+        except Exception as e:
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors[:3]
