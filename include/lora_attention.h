@@ -130,7 +130,8 @@ size_t lora_decode_workspace_size(int32_t n_heads, const lora_cache_t* cache /* 
  *                             be finite in float32)
  *     out = sum_j e^s_j v_j / sum_j e^s_j,   lse = log sum_j e^s_j
  *   q, out [B, n_heads D] (bf16, ld_q, ld_out); out may be q itself (same ld: another one is refused), and overlaps q in no
- *   other way.   lse [B, n_heads] float32 or NULL.   lengths [B], table [B, ld_table].
+ *   other way.   lse [B, n_heads] float32 or NULL.   lengths [B], table [B, ld_table]: they stay as they are until the call's
+ *   kernel has run (they are read more than once).
  * Products are of 16-bit numbers (8-bit codes exactly; a probability as two of them, 2^-16 of it off at most), sums and
  * statistics in 32 bits, in an order that depends on the lengths of the call's sequences only: repeated calls give
  * identical bits.
